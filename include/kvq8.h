@@ -362,6 +362,195 @@ const void *kvq8_host_device_pointer(const void *host_ptr);
 kvq8_status kvq8_selftest_bounded_wait(uint32_t *dev_status, uint64_t timeout_ns,
                                        unsigned long long *waited_ns, void *stream);
 
+/* --------------------------- sliding window with first tokens (sinks) --- */
+
+/*
+ * kvq8_decode_attn_window -- kvq8_decode_attn over a sliding window and the
+ * first tokens: of a sequence of L = ctx_lens[b] tokens, token t is attended
+ * when t < sinks or t >= L - windows[b].  Only the 64-token stages that hold
+ * such a token are read: the block-table entries of blocks that hold none are
+ * not looked at, so those blocks may belong to others again (or the entries
+ * be -1).
+ *
+ *   windows   int32 [batch]: tokens in each row's window, the newest included
+ *             (one per row, since the layers of a step fold into the batch); a
+ *             value below 1 is flagged KVQ8_DEV_BAD_CTX_LEN and taken as 1
+ *   sinks     first tokens that stay visible, >= 0
+ * Other arguments and the workspace as kvq8_decode_attn.
+ *
+ * kvq8_decode_step_window -- the same as one decode step: appends k_new, v_new
+ * at position ctx_lens[b] - 1 as kvq8_decode_step does, then attends.
+ */
+kvq8_status kvq8_decode_attn_window(const float *q, int batch, int nqh, int nkv, int hd,
+                                    const int8_t *k_pool, const int8_t *v_pool,
+                                    const float *k_scale, const float *v_scale,
+                                    int num_blocks, const int32_t *block_table,
+                                    int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, const int32_t *windows, int sinks,
+                                    float sm_scale, float *out,
+                                    void *workspace, size_t workspace_bytes,
+                                    uint32_t *dev_status, void *stream);
+
+kvq8_status kvq8_decode_step_window(const float *q, const float *k_new, const float *v_new,
+                                    int batch, int nqh, int nkv, int hd,
+                                    int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                                    int num_blocks, const int32_t *block_table,
+                                    int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, const int32_t *windows, int sinks,
+                                    float sm_scale, float *out,
+                                    void *workspace, size_t workspace_bytes,
+                                    uint32_t *dev_status, void *stream);
+
+/* ------------------------------------- accumulated attention weights --- */
+
+/*
+ * kvq8_decode_attn_weights -- kvq8_decode_attn that also adds up what each
+ * cached token was weighted with: with p_{j,t} the softmax weight that query
+ * head j gave token t,
+ *   weight_sum[block of t][kv head h][slot of t] += sum of p_{j,t} over the
+ *   G query heads j of h, for every t < ctx_lens[b]
+ * in fp32.  `out` is kvq8_decode_attn's.  The sums say which tokens
+ * kvq8_evict keeps.  Every block listed below ctx_lens[b] must belong to that
+ * sequence alone: two rows that list one block race on its sums.
+ *
+ *   weight_sum  fp32 [num_blocks][nkv][256], 16-byte aligned; set to zero by
+ *               the caller for tokens that are appended
+ *               (kvq8_norm_rope_append does it itself)
+ *   workspace   at least kvq8_weights_workspace_bytes(...) bytes, otherwise as
+ *               kvq8_decode_attn
+ * Tokens whose block id is outside the pool are skipped and flagged, as there.
+ *
+ * kvq8_decode_step_weights -- the same as one decode step: appends k_new,
+ * v_new at position ctx_lens[b] - 1 as kvq8_decode_step does, then attends.
+ * The new token's sum starts with this step's weight, whatever its slot held.
+ */
+size_t kvq8_weights_workspace_bytes(int batch, int nqh, int nkv, int hd, int max_blocks,
+                                    int block_size);
+
+kvq8_status kvq8_decode_attn_weights(const float *q, int batch, int nqh, int nkv, int hd,
+                                     const int8_t *k_pool, const int8_t *v_pool,
+                                     const float *k_scale, const float *v_scale,
+                                     int num_blocks, const int32_t *block_table,
+                                     int max_blocks, int block_size,
+                                     const int32_t *ctx_lens, float sm_scale,
+                                     float *out, float *weight_sum,
+                                     void *workspace, size_t workspace_bytes,
+                                     uint32_t *dev_status, void *stream);
+
+kvq8_status kvq8_decode_step_weights(const float *q, const float *k_new, const float *v_new,
+                                     int batch, int nqh, int nkv, int hd,
+                                     int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                                     int num_blocks, const int32_t *block_table,
+                                     int max_blocks, int block_size,
+                                     const int32_t *ctx_lens, float sm_scale,
+                                     float *out, float *weight_sum,
+                                     void *workspace, size_t workspace_bytes,
+                                     uint32_t *dev_status, void *stream);
+
+/* -------------------------- eviction by accumulated attention weight --- */
+
+/*
+ * kvq8_evict -- keep at most `keep` tokens of every (sequence, kv head): the
+ * first n_first, the last n_recent, and of the others those of largest
+ * weight_sum (equal weights: the lower position first; a NaN is below every
+ * other value).  The kept tokens' codes, scales and weights are copied, in
+ * order of position, to tokens 0, 1, ... of the blocks of dst_table, so that
+ * dst_table and new_lens take the places of block_table and ctx_lens in the
+ * calls that follow.  Every kv head keeps its own tokens, all heads the same
+ * number.  The source blocks are left as they were, and so are the slots of
+ * the destination blocks behind the last kept token.
+ *
+ *   keep, n_first, n_recent   keep >= 1, n_first + n_recent <= keep
+ *   dst_table   int32 [batch][dst_max_blocks], dst_max_blocks * 256 >= keep:
+ *               blocks of the same pool.  They must not be listed in any row
+ *               of block_table, nor twice.
+ *   kept        int32 [batch][nkv][keep]: the positions of the kept tokens in
+ *               increasing order, -1 behind the last
+ *   new_lens    int32 [batch]: min(ctx_lens[b], keep)
+ * A ctx_lens[b] outside the table is flagged KVQ8_DEV_BAD_CTX_LEN and clamped.
+ * A sequence for which a needed id of either row lies outside the pool, or a
+ * needed destination is among its own sources or listed twice in its row, is
+ * flagged KVQ8_DEV_BAD_BLOCK_ID and left out: kept -1, new_lens 0, nothing is
+ * copied.
+ */
+kvq8_status kvq8_evict(int batch, int nkv, int hd,
+                       int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                       float *weight_sum, int num_blocks,
+                       const int32_t *block_table, int max_blocks, int block_size,
+                       const int32_t *ctx_lens, int keep, int n_first, int n_recent,
+                       const int32_t *dst_table, int dst_max_blocks,
+                       int32_t *kept, int32_t *new_lens,
+                       uint32_t *dev_status, void *stream);
+
+/* ----------------------- head norm, position rotation and append --- */
+
+#define KVQ8_DTYPE_F32 0
+#define KVQ8_DTYPE_BF16 1
+#define KVQ8_DTYPE_F16 2
+
+/* Rotate the pairs (2i, 2i + 1); otherwise the pairs (i, i + 64). */
+#define KVQ8_ROPE_PAIRS 0x1u
+
+/*
+ * kvq8_rope_table -- the rotation's table: row t (t < n_pos) holds
+ * cos(t * inv_freq[i]) for i < 64, then sin(t * inv_freq[i]), computed in 64
+ * bits and rounded once.
+ *   inv_freq  fp64 [hd/2]
+ *   table     fp32 [n_pos][hd], 16-byte aligned
+ */
+kvq8_status kvq8_rope_table(const double *inv_freq, int n_pos, int hd, float *table, void *stream);
+
+/*
+ * kvq8_norm_rope_append -- what lies between a layer's projections and its
+ * decode, in one pass over the rows: every query and key row x of 128 values
+ * is normed, weighted and rotated to its position; queries are written in
+ * fp32, keys and values are quantised into the cache.
+ *   r = 1 / sqrt(mean(x^2) + eps),  u = x * r * weight   (u = x without weights)
+ *   y_a = u_a cos_i - u_b sin_i,  y_b = u_b cos_i + u_a sin_i
+ *   for the pairs (a, b) = (i, i + 64), or (2i, 2i + 1) with KVQ8_ROPE_PAIRS.
+ * Keys: scale = max|y| * (1/127) and code = round_half_even(127 y / max|y|);
+ * the code is the one of the exactly computed y (0 where the scale is 0).
+ * Values: scale = max|v| * (1/127), code = round_half_even(v / scale) clamped
+ * to [-127, 127].  (1/127 rounded to fp32, as in the query's rule: the product
+ * saves a row the division of kvq8_quantize_append, from whose scale it is at
+ * most the last bit away.)  A key or value row that
+ * comes out with a NaN or an infinity is stored as a row of zeros and flagged
+ * KVQ8_DEV_NONFINITE; query rows are IEEE arithmetic, unflagged.
+ *
+ *   q, k, v    rows of `dtype` (KVQ8_DTYPE_*): the heads of a token lie side
+ *              by side ([nqh][hd], [nkv][hd]); token i of sequence b is row
+ *              b * n_new + i, rows q_stride (k_stride, v_stride) elements
+ *              apart, so that they may be parts of one packed projection.
+ *              Pointers 16-byte aligned, strides multiples of 16 bytes
+ *   q_weight, k_weight  fp32 [hd], or both NULL: no norm
+ *   eps        in [1e-20, 1] (ignored without weights)
+ *   rope_table fp32 [n_pos][hd] as kvq8_rope_table makes it
+ *   positions  int32 [batch][n_new] in [0, n_pos), or NULL: the position in
+ *              the cache.  (After kvq8_evict a sequence's positions run ahead
+ *              of its slots.)
+ *   n_tokens   int32 [batch], or NULL: tokens i >= n_tokens[b] are padding:
+ *              nothing is read or written for them
+ *   start_pos .. v_scale   as kvq8_quantize_append
+ *   weight_sum fp32 [num_blocks][nkv][256], or NULL: set to zero at the
+ *              appended tokens (kvq8_decode_attn_weights)
+ *   q_out      fp32 [batch][n_new][nqh][hd], not overlapping q, k or v
+ * A token whose rotation position is outside the table is flagged
+ * KVQ8_DEV_BAD_POSITION and skipped; one whose place in the cache is outside
+ * the block table or the pool is flagged (KVQ8_DEV_BAD_POSITION,
+ * KVQ8_DEV_BAD_BLOCK_ID) and not appended.  No two new tokens may share a place.
+ */
+kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, int dtype,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  int batch, int n_new, int nqh, int nkv, int hd,
+                                  const float *q_weight, const float *k_weight, float eps,
+                                  const float *rope_table, int n_pos, const int32_t *positions,
+                                  const int32_t *n_tokens, uint32_t flags,
+                                  const int32_t *start_pos, const int32_t *block_table,
+                                  int max_blocks, int block_size, int num_blocks,
+                                  int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                                  float *weight_sum, float *q_out,
+                                  uint32_t *dev_status, void *stream);
+
 /* -------------------------------------------- 4-bit cache (NEXT row) --- */
 
 /*

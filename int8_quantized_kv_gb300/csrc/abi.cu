@@ -78,6 +78,10 @@ kvq8_status fill_decode_params(const float *q, int batch, int nqh, int nkv,
     p->out = nullptr;
     p->first_q8_block = nullptr;
     p->cache_ready = 0;
+    p->windows = nullptr;
+    p->sinks = 0;
+    p->ws_scores = nullptr;
+    p->weight_sum = nullptr;
     p->ws_meta2 = nullptr;
     p->ws_ml2 = nullptr;
     p->ws_acc2 = nullptr;
@@ -367,6 +371,246 @@ kvq8_status kvq8_decode_step_ex(const float *q, const float *k_new, const float 
     if (st != KVQ8_OK || batch == 0) return st;
     p.cache_ready = (flags & KVQ8_STEP_CACHE_READY) ? 1 : 0;
     return launch_decode_step(p, plan, (cudaStream_t)stream);
+}
+
+// ------------------------------------------- window, weights, norm, evict --
+
+// Shared by the windowed entry points (k_new null: no append).
+static kvq8_status run_window(const float *q, const float *k_new, const float *v_new, bool step, int batch,
+                              int nqh, int nkv, int hd, const int8_t *k_pool, const int8_t *v_pool,
+                              const float *k_scale, const float *v_scale, int num_blocks,
+                              const int32_t *block_table, int max_blocks, int block_size,
+                              const int32_t *ctx_lens, const int32_t *windows, int sinks, float sm_scale,
+                              float *out, void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                              void *stream) {
+    kvq8_status st = check_decode_args(q, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale,
+                                       num_blocks, block_table, max_blocks, block_size, ctx_lens);
+    if (st != KVQ8_OK) return st;
+    if (sinks < 0) return KVQ8_ERR_INVALID_ARG;
+    if (batch == 0) return KVQ8_OK;
+    if (!out || !aligned(out, 16) || !isfinite(sm_scale)) return KVQ8_ERR_INVALID_ARG;
+    if (!windows || !aligned(windows, 4)) return KVQ8_ERR_INVALID_ARG;
+    if (step && (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))) return KVQ8_ERR_INVALID_ARG;
+    DecodeParams p;
+    DecodePlan plan;
+    st = fill_decode_params(q, batch, nqh, nkv, k_pool, v_pool, k_scale, v_scale, num_blocks, block_table,
+                            max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &p, &plan);
+    if (st != KVQ8_OK) return st;
+    p.out = out;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.windows = windows;
+    p.sinks = sinks;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (launch_decode_window_split(p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    if (launch_decode_combine(p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
+}
+
+kvq8_status kvq8_decode_attn_window(const float *q, int batch, int nqh, int nkv, int hd, const int8_t *k_pool,
+                                    const int8_t *v_pool, const float *k_scale, const float *v_scale,
+                                    int num_blocks, const int32_t *block_table, int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, const int32_t *windows, int sinks, float sm_scale,
+                                    float *out, void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                                    void *stream) {
+    return run_window(q, nullptr, nullptr, false, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale,
+                      num_blocks, block_table, max_blocks, block_size, ctx_lens, windows, sinks, sm_scale, out,
+                      workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq8_status kvq8_decode_step_window(const float *q, const float *k_new, const float *v_new, int batch, int nqh,
+                                    int nkv, int hd, int8_t *k_pool, int8_t *v_pool, float *k_scale,
+                                    float *v_scale, int num_blocks, const int32_t *block_table, int max_blocks,
+                                    int block_size, const int32_t *ctx_lens, const int32_t *windows, int sinks,
+                                    float sm_scale, float *out, void *workspace, size_t workspace_bytes,
+                                    uint32_t *dev_status, void *stream) {
+    return run_window(q, k_new, v_new, true, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale, num_blocks,
+                      block_table, max_blocks, block_size, ctx_lens, windows, sinks, sm_scale, out, workspace,
+                      workspace_bytes, dev_status, stream);
+}
+
+// Bytes of the scores plane of a weights call.
+static size_t scores_bytes(int batch, int nqh, int max_blocks) {
+    return (size_t)batch * nqh * max_blocks * kBS * sizeof(float);   // units * G = batch * nqh
+}
+
+size_t kvq8_weights_workspace_bytes(int batch, int nqh, int nkv, int hd, int max_blocks, int block_size) {
+    const size_t base = kvq8_decode_workspace_bytes(batch, nqh, nkv, hd, max_blocks, block_size);
+    return base ? base + scores_bytes(batch, nqh, max_blocks) : 0;
+}
+
+static kvq8_status run_weights(const float *q, const float *k_new, const float *v_new, bool step, int batch,
+                               int nqh, int nkv, int hd, const int8_t *k_pool, const int8_t *v_pool,
+                               const float *k_scale, const float *v_scale, int num_blocks,
+                               const int32_t *block_table, int max_blocks, int block_size,
+                               const int32_t *ctx_lens, float sm_scale, float *out, float *weight_sum,
+                               void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    kvq8_status st = check_decode_args(q, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale,
+                                       num_blocks, block_table, max_blocks, block_size, ctx_lens);
+    if (st != KVQ8_OK || batch == 0) return st;
+    if (!out || !aligned(out, 16) || !isfinite(sm_scale)) return KVQ8_ERR_INVALID_ARG;
+    if (!weight_sum || !aligned(weight_sum, 16)) return KVQ8_ERR_INVALID_ARG;
+    if (step && (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))) return KVQ8_ERR_INVALID_ARG;
+    if (weights_merge_blocks(batch, nqh, nkv, max_blocks) > 2147483647) return KVQ8_ERR_UNSUPPORTED;
+    DecodeParams p;
+    DecodePlan plan;
+    st = fill_decode_params(q, batch, nqh, nkv, k_pool, v_pool, k_scale, v_scale, num_blocks, block_table,
+                            max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &p, &plan);
+    if (st != KVQ8_OK) return st;
+    if (workspace_bytes < plan.bytes + scores_bytes(batch, nqh, max_blocks)) return KVQ8_ERR_WORKSPACE;
+    p.out = out;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.ws_scores = (float *)((char *)workspace + plan.bytes);
+    p.weight_sum = weight_sum;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (launch_decode_weights_split(p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    if (launch_weights_merge(p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
+}
+
+kvq8_status kvq8_decode_attn_weights(const float *q, int batch, int nqh, int nkv, int hd, const int8_t *k_pool,
+                                     const int8_t *v_pool, const float *k_scale, const float *v_scale,
+                                     int num_blocks, const int32_t *block_table, int max_blocks, int block_size,
+                                     const int32_t *ctx_lens, float sm_scale, float *out, float *weight_sum,
+                                     void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                                     void *stream) {
+    return run_weights(q, nullptr, nullptr, false, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale,
+                       num_blocks, block_table, max_blocks, block_size, ctx_lens, sm_scale, out, weight_sum,
+                       workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq8_status kvq8_decode_step_weights(const float *q, const float *k_new, const float *v_new, int batch, int nqh,
+                                     int nkv, int hd, int8_t *k_pool, int8_t *v_pool, float *k_scale,
+                                     float *v_scale, int num_blocks, const int32_t *block_table, int max_blocks,
+                                     int block_size, const int32_t *ctx_lens, float sm_scale, float *out,
+                                     float *weight_sum, void *workspace, size_t workspace_bytes,
+                                     uint32_t *dev_status, void *stream) {
+    return run_weights(q, k_new, v_new, true, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale, num_blocks,
+                       block_table, max_blocks, block_size, ctx_lens, sm_scale, out, weight_sum, workspace,
+                       workspace_bytes, dev_status, stream);
+}
+
+kvq8_status kvq8_rope_table(const double *inv_freq, int n_pos, int hd, float *table, void *stream) {
+    if (hd != kHD) return KVQ8_ERR_UNSUPPORTED;
+    if (n_pos < 0) return KVQ8_ERR_INVALID_ARG;
+    if (n_pos == 0) return KVQ8_OK;
+    if (!inv_freq || !table || !aligned(inv_freq, 8) || !aligned(table, 16)) return KVQ8_ERR_INVALID_ARG;
+    if (launch_rope_table(inv_freq, n_pos, table, (cudaStream_t)stream) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
+}
+
+kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, int batch, int n_new, int nqh, int nkv,
+                                  int hd, const float *q_weight, const float *k_weight, float eps,
+                                  const float *rope_table, int n_pos, const int32_t *positions,
+                                  const int32_t *n_tokens, uint32_t flags, const int32_t *start_pos,
+                                  const int32_t *block_table, int max_blocks, int block_size, int num_blocks,
+                                  int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                                  float *weight_sum, float *q_out, uint32_t *dev_status, void *stream) {
+    kvq8_status st = check_shape(hd, block_size);
+    if (st != KVQ8_OK) return st;
+    if ((st = check_heads(nqh, nkv)) != KVQ8_OK) return st;
+    if (batch < 0 || n_new < 0 || num_blocks <= 0 || max_blocks <= 0 || n_pos <= 0) return KVQ8_ERR_INVALID_ARG;
+    if (max_blocks > 2147483647 / kBS || batch > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
+    if (dtype != KVQ8_DTYPE_F32 && dtype != KVQ8_DTYPE_BF16 && dtype != KVQ8_DTYPE_F16) return KVQ8_ERR_UNSUPPORTED;
+    if (flags & ~(uint32_t)KVQ8_ROPE_PAIRS) return KVQ8_ERR_INVALID_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return KVQ8_ERR_INVALID_ARG;
+    if (q_weight && !(eps >= 1e-20f && eps <= 1.0f)) return KVQ8_ERR_INVALID_ARG;
+    if (batch == 0 || n_new == 0) return KVQ8_OK;
+    if (!q || !k || !v || !rope_table || !start_pos || !block_table || !k_pool || !v_pool || !k_scale ||
+        !v_scale || !q_out)
+        return KVQ8_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_weight, 16) ||
+        !aligned(k_weight, 16) || !aligned(rope_table, 16) || !aligned(positions, 4) || !aligned(n_tokens, 4) ||
+        !aligned(start_pos, 4) || !aligned(block_table, 4) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
+        !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(weight_sum, 16) || !aligned(q_out, 16))
+        return KVQ8_ERR_INVALID_ARG;
+    const int64_t unit = dtype == KVQ8_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes
+    if (q_stride < (int64_t)nqh * kHD || k_stride < (int64_t)nkv * kHD || v_stride < (int64_t)nkv * kHD ||
+        q_stride % unit || k_stride % unit || v_stride % unit)
+        return KVQ8_ERR_INVALID_ARG;
+    if ((int64_t)batch * n_new > 2147483647 / (nqh + 2 * (int64_t)nkv)) return KVQ8_ERR_UNSUPPORTED;
+    NormRopeParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.dtype = dtype;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.batch = batch;
+    p.n_new = n_new;
+    p.nqh = nqh;
+    p.nkv = nkv;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.eps = eps;
+    p.rope = rope_table;
+    p.n_pos = n_pos;
+    p.pairs = (flags & KVQ8_ROPE_PAIRS) ? 1 : 0;
+    p.positions = positions;
+    p.n_tokens = n_tokens;
+    p.start_pos = start_pos;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.num_blocks = num_blocks;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.weight_sum = weight_sum;
+    p.q_out = q_out;
+    p.dev_status = dev_status;
+    if (launch_norm_rope_append(p, (cudaStream_t)stream) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
+}
+
+kvq8_status kvq8_evict(int batch, int nkv, int hd, int8_t *k_pool, int8_t *v_pool, float *k_scale,
+                       float *v_scale, float *weight_sum, int num_blocks, const int32_t *block_table,
+                       int max_blocks, int block_size, const int32_t *ctx_lens, int keep, int n_first,
+                       int n_recent, const int32_t *dst_table, int dst_max_blocks, int32_t *kept,
+                       int32_t *new_lens, uint32_t *dev_status, void *stream) {
+    const kvq8_status st = check_shape(hd, block_size);
+    if (st != KVQ8_OK) return st;
+    if (batch < 0 || nkv <= 0 || num_blocks <= 0 || max_blocks <= 0 || dst_max_blocks <= 0)
+        return KVQ8_ERR_INVALID_ARG;
+    if (keep < 1 || n_first < 0 || n_recent < 0 || n_first > keep || n_recent > keep - n_first)
+        return KVQ8_ERR_INVALID_ARG;
+    if (max_blocks > 2147483647 / kBS || dst_max_blocks > 2147483647 / kBS) return KVQ8_ERR_UNSUPPORTED;
+    if (batch > kMaxGridYZ || nkv > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
+    if (keep > dst_max_blocks * kBS) return KVQ8_ERR_INVALID_ARG;
+    if (batch == 0) return KVQ8_OK;
+    if ((int64_t)batch * nkv * keep > 2147483647) return KVQ8_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool || !k_scale || !v_scale || !weight_sum || !block_table || !ctx_lens || !dst_table ||
+        !kept || !new_lens)
+        return KVQ8_ERR_INVALID_ARG;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+        !aligned(weight_sum, 16) || !aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(dst_table, 4) ||
+        !aligned(kept, 4) || !aligned(new_lens, 4))
+        return KVQ8_ERR_INVALID_ARG;
+    EvictParams p;
+    p.batch = batch;
+    p.nkv = nkv;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.weight_sum = weight_sum;
+    p.num_blocks = num_blocks;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.ctx_lens = ctx_lens;
+    p.keep = keep;
+    p.n_first = n_first;
+    p.n_recent = n_recent;
+    p.dst_table = dst_table;
+    p.dst_max_blocks = dst_max_blocks;
+    p.kept = kept;
+    p.new_lens = new_lens;
+    p.dev_status = dev_status;
+    if (launch_evict(p, (cudaStream_t)stream) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
 }
 
 kvq8_status kvq8_decode_step_host(const float *q_host, const float *k_new_host, const float *v_new_host,

@@ -116,16 +116,48 @@ struct Misc {
 
 __device__ __forceinline__ int clamp_len(int L, int cap) { return max(0, min(L, cap)); }
 
-// The tokens [x, y) of sequence b that this launch decodes: [0, L) normally;
-// [256 * first_q8_block[b], L) when the older blocks of the sequence are held
-// in the 4-bit cache (mixed precision by token age; kMixed).
-template <bool kMixed = true>
-__device__ __forceinline__ int2 seq_span(const DecodeParams &p, int b, int cap) {
+// What a split launch computes besides the partial records.
+enum SplitMode {
+    kWhole = 0,      // every token of the span
+    kWindowed = 1,   // tokens t < sinks or t >= L - windows[b]
+    kScored = 2      // every token, and its scores (base 2) are written to ws_scores
+};
+
+// The tokens of sequence b that this launch decodes: [x, y) in stages of 64
+// from x on, after `ns` stages from token 0 on (kWindowed: the first tokens).
+// x is a multiple of 64.  Tokens of these stages from min(sinks, lo) to lo are
+// masked (kWindowed; lo = 0 otherwise).
+struct SeqSpan {
+    int x, y, ns, lo;
+};
+
+// [0, L) normally; [256 * first_q8_block[b], L) when the older blocks of the
+// sequence are held in the 4-bit cache (mixed precision by token age; kMixed).
+// kWindowed: the stages that hold a token t < sinks, then those that hold a
+// token of [L - windows[b], L); one run of stages where the two meet, so that
+// no stage is decoded twice.  A window below 1 counts as 1.
+template <bool kMixed = true, int kMode = kWhole>
+__device__ __forceinline__ SeqSpan seq_span(const DecodeParams &p, int b, int cap) {
     const int L = clamp_len(p.ctx_lens[b], cap);
+    if (kMode == kWindowed) {
+        const int lo = max(0, L - max(1, p.windows[b]));
+        const int x = lo / kStageTok * kStageTok;
+        const int ns = p.sinks / kStageTok + (p.sinks % kStageTok ? 1 : 0);
+        if (ns >= x / kStageTok) return {0, L, 0, lo};
+        return {x, L, ns, lo};
+    }
     const int s = (kMixed && p.first_q8_block) ? min(L, max(0, min(p.first_q8_block[b], cap / kBS)) * kBS) : 0;
-    return make_int2(s, L);
+    return {s, L, 0, 0};
 }
-__device__ __forceinline__ int span_stages(int2 sp) { return (sp.y - sp.x + kStageTok - 1) / kStageTok; }
+__device__ __forceinline__ int span_stages(SeqSpan sp) {
+    return sp.ns + (sp.y - sp.x + kStageTok - 1) / kStageTok;
+}
+// First token of the span's stage j.
+template <int kMode>
+__device__ __forceinline__ int stage_token(const SeqSpan &sp, int j) {
+    if (kMode == kWindowed) return j < sp.ns ? j * kStageTok : sp.x + (j - sp.ns) * kStageTok;
+    return sp.x + j * kStageTok;
+}
 
 // int8 codes v of 4 consecutive tokens -> two fp16 pairs (tokens 0,1 and 2,3)
 // holding (v + 128) * 2^-24: the offset byte in the low bits of a half is the
@@ -141,6 +173,13 @@ __device__ __forceinline__ void codes_to_sub2(uint32_t w, uint32_t &lo, uint32_t
 // share of the accumulator for that stage.
 constexpr uint32_t kNegOffset = 0x80808080u;
 constexpr float kCodeUnit = 16777216.0f;   // 2^24: one code step of codes_to_sub2
+
+// The fp16 pair of codes_to_sub2 without the offset: v * 2^-24 each (exact).
+__device__ __forceinline__ uint32_t sub2_signed(uint32_t x) {
+    uint32_t y;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(kNegOffset));
+    return y;
+}
 
 __device__ __forceinline__ int4 lds128(const void *p) { return *reinterpret_cast<const int4 *>(p); }
 
@@ -216,7 +255,7 @@ __device__ __noinline__ void append_new_token(const DecodeParams &p, int b, int 
 template <int G, bool kMixed, int kCtas>
 using SplitLay = SplitLayout<G, kCtas == 2 ? kSmemLimit2 : (kMixed ? kSmemLimitMixed : kSmemLimit)>;
 
-template <int G, bool kMixed, int kCtas>
+template <int G, bool kMixed, int kCtas, int kMode = kWhole>
 __global__ void __launch_bounds__(kSplitThreads, kCtas)
 decode_split_kernel(DecodeParams p) {
     using Lay = SplitLay<G, kMixed, kCtas>;
@@ -263,7 +302,8 @@ decode_split_kernel(DecodeParams p) {
     for (int b = b_lo; b < b_hi; ++b) {
         const int L = b == b_lo ? L_first : p.ctx_lens[b];
         if (c == 0 && (L < 0 || L > cap)) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
-        mine += (long long)p.nkv * span_stages(seq_span<kMixed>(p, b, cap));
+        if (kMode == kWindowed && c == 0 && p.windows[b] < 1) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
+        mine += (long long)p.nkv * span_stages(seq_span<kMixed, kMode>(p, b, cap));
     }
     long long incl = mine;
 #pragma unroll
@@ -301,7 +341,7 @@ decode_split_kernel(DecodeParams p) {
     if (mine > 0 && excl <= lo && lo < excl + mine) {
         long long acc = excl;
         for (int b = b_lo; b < b_hi; ++b) {
-            const long long n = (long long)p.nkv * span_stages(seq_span<kMixed>(p, b, cap));
+            const long long n = (long long)p.nkv * span_stages(seq_span<kMixed, kMode>(p, b, cap));
             if (lo < acc + n) {
                 misc->b0 = b;
                 misc->base = acc;
@@ -315,7 +355,7 @@ decode_split_kernel(DecodeParams p) {
     int b = 0, h = 0, off = 0;
     if (hi > lo) {
         b = misc->b0;
-        const int nb = span_stages(seq_span<kMixed>(p, b, cap));
+        const int nb = span_stages(seq_span<kMixed, kMode>(p, b, cap));
         const long long rel = lo - misc->base;   // < nkv * nb
         if (rel <= 0x7fffffffLL) {
             h = (int)rel / nb;
@@ -333,7 +373,7 @@ decode_split_kernel(DecodeParams p) {
         long long remaining = hi - lo;
         int kbase = 0;
         while (remaining > 0 && b < p.batch) {
-            const int2 sp = seq_span<kMixed>(p, b, cap);
+            const SeqSpan sp = seq_span<kMixed, kMode>(p, b, cap);
             const int nb = span_stages(sp);
             if (nb == 0) { ++b; h = 0; off = 0; continue; }
             const int seg_n = (int)min((long long)(nb - off), remaining);
@@ -342,7 +382,7 @@ decode_split_kernel(DecodeParams p) {
             for (int j = 0; j < seg_n; ++j) {
                 const int k = kbase + j, slot = k % Lay::kStages;
                 const uint32_t par = ((k / Lay::kStages) & 1) ^ 1;
-                const int t0 = sp.x + (off + j) * kStageTok;
+                const int t0 = stage_token<kMode>(sp, off + j);
                 const int lb = t0 / kBS, quarter = (t0 / kStageTok) & 3;
                 if (tbl_base < 0 || lb >= tbl_base + 32) {
                     tbl_base = lb;
@@ -429,7 +469,7 @@ decode_split_kernel(DecodeParams p) {
             qh = hh;
         };
         while (remaining > 0 && b < p.batch) {
-            const int2 sp = seq_span<kMixed>(p, b, cap);
+            const SeqSpan sp = seq_span<kMixed, kMode>(p, b, cap);
             const int L = sp.y;
             const int nb = span_stages(sp);
             if (nb == 0) { ++b; h = 0; off = 0; continue; }
@@ -451,7 +491,7 @@ decode_split_kernel(DecodeParams p) {
             float4 nxk = make_float4(0.f, 0.f, 0.f, 0.f), nxv = nxk;
             int nphys = -1;
             if (kPreloadNew && app_pos >= sp.x) {
-                const int sj = (app_pos - sp.x) / kStageTok - off;
+                const int sj = sp.ns + (app_pos - sp.x) / kStageTok - off;
                 if (sj >= 0 && sj < seg_n && sj % kConsumerWarps == warp) {
                     const size_t src = ((size_t)b * p.nkv + h) * kHD;
                     nxk = reinterpret_cast<const float4 *>(p.k_new + src)[lane];
@@ -504,8 +544,9 @@ decode_split_kernel(DecodeParams p) {
                     const int8_t *vst = kst + kStageKBytes;
                     const float *ks_st = reinterpret_cast<const float *>(st + kStageKBytes + kStageVBytes);
                     const float *vs_st = ks_st + kStageTok;
-                    const int nvalid = min(kStageTok, L - (sp.x + (off + j) * kStageTok));
-                    const int tnew = app_pos - (sp.x + (off + j) * kStageTok);
+                    const int t0 = stage_token<kMode>(sp, off + j);
+                    const int nvalid = min(kStageTok, L - t0);
+                    const int tnew = app_pos - t0;
                     if (tnew >= 0 && tnew < kStageTok) {
                         if (!kPreloadNew) {
                             const size_t src = ((size_t)b * p.nkv + h) * kHD;
@@ -515,7 +556,11 @@ decode_split_kernel(DecodeParams p) {
                         append_new_token(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
                     }
                     const int ta = lane, tb = lane + 32;
-                    const bool va = ta < nvalid, vb = tb < nvalid;
+                    bool va = ta < nvalid, vb = tb < nvalid;
+                    if (kMode == kWindowed) {
+                        va &= t0 + ta < p.sinks || t0 + ta >= sp.lo;
+                        vb &= t0 + tb < p.sinks || t0 + tb >= sp.lo;
+                    }
 
                     // ---- segment 2a: int32 block dots, lane = token ----
                     int da[G][kNQB], db[G][kNQB];
@@ -566,6 +611,15 @@ decode_split_kernel(DecodeParams p) {
                         bb = fmaf((float)db[g][3], qs.w, bb);
                         sa[g] = va ? a * ksa * p.sm_scale_log2 : -INFINITY;
                         sb[g] = vb ? bb * ksb * p.sm_scale_log2 : -INFINITY;
+                    }
+                    if (kMode == kScored) {
+                        // plane g of unit u: [u][g][cap] (the slots past L are never read)
+                        float *sc = p.ws_scores + ((size_t)u * G) * cap + t0;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            if (va) sc[(size_t)g * cap + ta] = sa[g];
+                            if (vb) sc[(size_t)g * cap + tb] = sb[g];
+                        }
                     }
                     // The running maximum M is raised only when a score exceeds it by
                     // more than 2^kLazyLog2; below that the weights 2^(s-M) stay < 2^8
@@ -643,9 +697,16 @@ decode_split_kernel(DecodeParams p) {
                         for (int i = 0; i < 8; ++i) bl[i] = 0u;
                     }
                     // the stage's offset correction, one tile shared by all dims
+                    // (the windowed and scored splits take the offset off the
+                    // codes themselves instead, and add each stage's product to
+                    // the accumulator in fp32: the tensor cores cut off what an
+                    // accumulator cannot hold, which next to the offset's share
+                    // costs an output of 4096 tokens 1.3e-5 of itself, and over
+                    // the 60 stages of a long segment 4e-6)
+                    constexpr bool kSigned = kMode != kWhole;
                     float corr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < 4 && !kSigned; ++s) {
                         mma_f16_16816(corr, kNegOffset, kNegOffset, kNegOffset, kNegOffset, bh[2 * s], bh[2 * s + 1]);
                         if (!kPackPV)
                             mma_f16_16816(corr, kNegOffset, kNegOffset, kNegOffset, kNegOffset, bl[2 * s], bl[2 * s + 1]);
@@ -657,20 +718,30 @@ decode_split_kernel(DecodeParams p) {
                         const int4 v1 = lds128(vst + (d + 8) * kStageTok + t4 * 16);
                         const uint32_t w0[4] = {(uint32_t)v0.x, (uint32_t)v0.y, (uint32_t)v0.z, (uint32_t)v0.w};
                         const uint32_t w1[4] = {(uint32_t)v1.x, (uint32_t)v1.y, (uint32_t)v1.z, (uint32_t)v1.w};
+                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float (&sum)[4] = kSigned ? part : acc[mt];
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
                             uint32_t a0, a2, a1, a3;
                             codes_to_sub2(w0[s], a0, a2);
                             codes_to_sub2(w1[s], a1, a3);
-                            mma_f16_16816(acc[mt], a0, a1, a2, a3, bh[2 * s], bh[2 * s + 1]);
-                            if (!kPackPV) mma_f16_16816(acc[mt], a0, a1, a2, a3, bl[2 * s], bl[2 * s + 1]);
+                            if (kSigned) {
+                                a0 = sub2_signed(a0); a1 = sub2_signed(a1);
+                                a2 = sub2_signed(a2); a3 = sub2_signed(a3);
+                            }
+                            mma_f16_16816(sum, a0, a1, a2, a3, bh[2 * s], bh[2 * s + 1]);
+                            if (!kPackPV) mma_f16_16816(sum, a0, a1, a2, a3, bl[2 * s], bl[2 * s + 1]);
+                        }
+                        if (kSigned) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[mt][i] += part[i];
                         }
                     }
                     // remove the stage's offset now, so that the accumulator never
                     // carries more than one stage of it (its rounding stays at the
                     // scale of the result)
 #pragma unroll
-                    for (int mt = 0; mt < 8; ++mt)
+                    for (int mt = 0; mt < 8 && !kSigned; ++mt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[mt][i] += corr[i];
                 }
@@ -768,7 +839,7 @@ int device_sm_count() {
     return cached[dev];
 }
 
-template <int G, bool kMixed, int kCtas>
+template <int G, bool kMixed, int kCtas, int kMode = kWhole>
 cudaError_t launch_split_gm(const DecodeParams &p, cudaStream_t s) {
     using Lay = SplitLay<G, kMixed, kCtas>;
     static std::atomic<uint64_t> configured{0};
@@ -787,10 +858,10 @@ cudaError_t launch_split_gm(const DecodeParams &p, cudaStream_t s) {
     return launch_after_setting(
         configured,
         [] {
-            return cudaFuncSetAttribute(decode_split_kernel<G, kMixed, kCtas>,
+            return cudaFuncSetAttribute(decode_split_kernel<G, kMixed, kCtas, kMode>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
         },
-        [&] { return cudaLaunchKernelEx(&cfg, decode_split_kernel<G, kMixed, kCtas>, p); });
+        [&] { return cudaLaunchKernelEx(&cfg, decode_split_kernel<G, kMixed, kCtas, kMode>, p); });
 }
 
 }  // namespace

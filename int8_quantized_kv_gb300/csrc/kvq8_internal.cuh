@@ -114,6 +114,12 @@ struct DecodeParams {
     // prologue and copies run before it waits for that kernel (only q, k_new,
     // v_new and the workspace wait).  Zero: every thread waits first.
     int cache_ready;
+    // sliding window with first tokens (windowed split only)
+    const int32_t *windows;       // [batch]
+    int sinks;
+    // accumulated attention weights (scored split and its merge only)
+    float *ws_scores;             // [units][G][max_blocks * 256]: scores, base 2
+    float *weight_sum;            // [num_blocks][nkv][256]
 };
 cudaError_t launch_decode_split(const DecodeParams &p, int group, cudaStream_t s);
 cudaError_t launch_decode_combine(const DecodeParams &p, int group, cudaStream_t s);
@@ -121,6 +127,57 @@ cudaError_t launch_decode_combine(const DecodeParams &p, int group, cudaStream_t
 // int4_split_count(L, nsplit) splits j (nsplit <= 8), read without the record
 // directory.
 cudaError_t launch_decode_combine_fixed(const DecodeParams &p, int group, int nsplit, cudaStream_t s);
+
+// The split over a window and the first tokens (p.windows, p.sinks); merged by
+// launch_decode_combine.
+cudaError_t launch_decode_window_split(const DecodeParams &p, int group, cudaStream_t s);
+// The split that also writes its scores (p.ws_scores), and the merge that also
+// adds the tokens' weights to p.weight_sum; weights_merge_blocks: its grid.
+cudaError_t launch_decode_weights_split(const DecodeParams &p, int group, cudaStream_t s);
+cudaError_t launch_weights_merge(const DecodeParams &p, int group, cudaStream_t s);
+int64_t weights_merge_blocks(int batch, int nqh, int nkv, int max_blocks);
+
+// ------------------------------------- norm, rotation and quantise-append --
+struct NormRopeParams {
+    const void *q, *k, *v;        // rows of dtype; strides: elements from one token's row to the next
+    int dtype;                    // KVQ8_DTYPE_*
+    int64_t q_stride, k_stride, v_stride;
+    int batch, n_new, nqh, nkv;
+    const float *q_weight, *k_weight;   // [hd], or null: no norm
+    float eps;
+    const float *rope;            // [n_pos][cos 64 | sin 64]
+    int n_pos;
+    int pairs;                    // 1: pairs (2i, 2i + 1); 0: (i, i + 64)
+    const int32_t *positions;     // [batch][n_new], or null: the cache position
+    const int32_t *n_tokens;      // [batch], or null: n_new each
+    const int32_t *start_pos, *block_table;
+    int max_blocks, num_blocks;
+    int8_t *k_pool, *v_pool;
+    float *k_scale, *v_scale;
+    float *weight_sum;            // null, or [num_blocks][nkv][256]: zeroed at the appended slots
+    float *q_out;                 // [batch][n_new][nqh][hd]
+    uint32_t *dev_status;
+};
+cudaError_t launch_norm_rope_append(const NormRopeParams &p, cudaStream_t s);
+cudaError_t launch_rope_table(const double *inv_freq, int64_t n_pos, float *table, cudaStream_t s);
+
+// --------------------------------------------------------------- eviction --
+struct EvictParams {
+    int batch, nkv;
+    int8_t *k_pool, *v_pool;
+    float *k_scale, *v_scale, *weight_sum;
+    int num_blocks;
+    const int32_t *block_table;
+    int max_blocks;
+    const int32_t *ctx_lens;
+    int keep, n_first, n_recent;
+    const int32_t *dst_table;     // [batch][dst_max_blocks]
+    int dst_max_blocks;
+    int32_t *kept;                // [batch][nkv][keep]
+    int32_t *new_lens;            // [batch]
+    uint32_t *dev_status;
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
 
 // ------------------------------------------------------------ INT4 cache --
 // A unit of L tokens cut into nsplit splits of whole 32-token chunks (the

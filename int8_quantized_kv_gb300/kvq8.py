@@ -76,6 +76,20 @@ SIGNATURES = {
                                _P, _F, _P, _P, _SZ, _P, _P]),
     "kvq8_decode_attn_noalloc": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I,
                                       _P, _F, _P, _P, _P]),
+    "kvq8_decode_attn_window": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I,
+                                     _P, _P, _I, _F, _P, _P, _SZ, _P, _P]),
+    "kvq8_decode_step_window": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I,
+                                     _P, _P, _I, _F, _P, _P, _SZ, _P, _P]),
+    "kvq8_weights_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "kvq8_decode_attn_weights": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I,
+                                      _P, _F, _P, _P, _P, _SZ, _P, _P]),
+    "kvq8_decode_step_weights": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I,
+                                      _P, _F, _P, _P, _P, _SZ, _P, _P]),
+    "kvq8_evict": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P, _I, _I, _I,
+                        _P, _I, _P, _P, _P, _P]),
+    "kvq8_rope_table": (_I, [_P, _I, _I, _P, _P]),
+    "kvq8_norm_rope_append": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P,
+                                   _P, ctypes.c_uint32, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -458,6 +472,211 @@ def selftest_bounded_wait(timeout_ns: int, dev_status, waited_ns=None, stream=No
     _need_cuda(dev_status, waited_ns)
     _check("kvq8_selftest_bounded_wait",
            load().kvq8_selftest_bounded_wait(_ptr(dev_status), int(timeout_ns), _ptr(waited_ns), _stream(stream)))
+
+
+# ------------------------------- window, weights, eviction, norm and rotation ---
+ROPE_PAIRS = 0x1                          # KVQ8_ROPE_PAIRS
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2   # KVQ8_DTYPE_*
+
+
+def _need(what: str, t, dtype: str, shape):
+    """A contiguous device tensor of this type and shape, on the current device."""
+    torch = _torch()
+    if isinstance(t, HostMapped):
+        if dtype != "float32" or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: expected {dtype} {list(shape)}, got host memory of {list(t.shape)}")
+        return
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected a tensor on the current device, got one on {t.device}")
+    if t.dtype is not getattr(torch, dtype) or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _need_cache(cache: KVCache, weight_sum=None):
+    nb, nkv = cache.k_pool.shape[:2]
+    _need("k_pool", cache.k_pool, "int8", (nb, nkv, BLOCK_SIZE, HEAD_DIM))
+    _need("v_pool", cache.v_pool, "int8", (nb, nkv, BLOCK_SIZE // 64, HEAD_DIM, 64))
+    _need("k_scale", cache.k_scale, "float32", (nb, nkv, BLOCK_SIZE))
+    _need("v_scale", cache.v_scale, "float32", (nb, nkv, BLOCK_SIZE))
+    if weight_sum is not None:
+        _need("weight_sum", weight_sum, "float32", (nb, nkv, BLOCK_SIZE))
+    return nb, nkv
+
+
+def _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum=None):
+    """Checks what the window and weights decodes share; returns their leading arguments."""
+    nb, nkv = _need_cache(cache, weight_sum)
+    batch, nqh, hd = q.shape
+    max_blocks = block_table.shape[1]
+    _need("q", q, "float32", (batch, nqh, hd))
+    _need("out", out, "float32", (batch, nqh, hd))
+    _need("block_table", block_table, "int32", (batch, max_blocks))
+    _need("ctx_lens", ctx_lens, "int32", (batch,))
+    if k_new is not None:
+        _need("k_new", k_new, "float32", (batch, nkv, hd))
+        _need("v_new", v_new, "float32", (batch, nkv, hd))
+    if dev_status is not None:
+        _need("dev_status", dev_status, "int32", (1,))
+    _need_cuda(workspace)
+    new = () if k_new is None else (_ptr(k_new), _ptr(v_new))
+    return (_ptr(q), *new, batch, nqh, nkv, hd, _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale),
+            _ptr(cache.v_scale), nb, _ptr(block_table), max_blocks, BLOCK_SIZE, _ptr(ctx_lens))
+
+
+def _window(fn, q, k_new, v_new, cache, block_table, ctx_lens, windows, sinks, out, workspace, sm_scale,
+            dev_status, stream):
+    lead = _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status)
+    _need("windows", windows, "int32", (q.shape[0],))
+    sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
+    _check(fn, getattr(load(), fn)(*lead, _ptr(windows), int(sinks), sm, _ptr(out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                   _stream(stream)))
+
+
+def decode_attn_window(q, cache: KVCache, block_table, ctx_lens, windows, sinks: int, out, workspace,
+                       sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_attn over the tokens t < sinks or t >= ctx_lens - windows (int32
+    [batch]) of every row."""
+    _window("kvq8_decode_attn_window", q, None, None, cache, block_table, ctx_lens, windows, sinks, out, workspace,
+            sm_scale, dev_status, stream)
+
+
+def decode_step_window(q, k_new, v_new, cache: KVCache, block_table, ctx_lens, windows, sinks: int, out, workspace,
+                       sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_step (append k_new/v_new at ctx_lens-1, then attend) over the
+    tokens t < sinks or t >= ctx_lens - windows (int32 [batch]) of every row."""
+    _window("kvq8_decode_step_window", q, k_new, v_new, cache, block_table, ctx_lens, windows, sinks, out,
+            workspace, sm_scale, dev_status, stream)
+
+
+def alloc_weight_sum(num_blocks: int, nkv: int, device="cuda"):
+    """Accumulated attention weights of every cache slot, all zero."""
+    return _torch().zeros((num_blocks, nkv, BLOCK_SIZE), dtype=_torch().float32, device=device)
+
+
+def weights_workspace_bytes(batch: int, nqh: int, nkv: int, max_blocks: int) -> int:
+    return int(load().kvq8_weights_workspace_bytes(batch, nqh, nkv, HEAD_DIM, max_blocks, BLOCK_SIZE))
+
+
+def alloc_weights_workspace(batch: int, nqh: int, nkv: int, max_blocks: int, device="cuda"):
+    n = weights_workspace_bytes(batch, nqh, nkv, max_blocks)
+    if n == 0:
+        raise ValueError("unsupported decode sizes")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def _weights(fn, q, k_new, v_new, cache, block_table, ctx_lens, out, weight_sum, workspace, sm_scale, dev_status,
+             stream):
+    lead = _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum)
+    sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
+    _check(fn, getattr(load(), fn)(*lead, sm, _ptr(out), _ptr(weight_sum), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                   _stream(stream)))
+
+
+def decode_attn_weights(q, cache: KVCache, block_table, ctx_lens, out, weight_sum, workspace,
+                        sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_attn that adds each token's softmax weight, summed over the query
+    heads of its kv head, to weight_sum (fp32 [num_blocks][nkv][256], see
+    alloc_weight_sum); workspace from alloc_weights_workspace."""
+    _weights("kvq8_decode_attn_weights", q, None, None, cache, block_table, ctx_lens, out, weight_sum, workspace,
+             sm_scale, dev_status, stream)
+
+
+def decode_step_weights(q, k_new, v_new, cache: KVCache, block_table, ctx_lens, out, weight_sum, workspace,
+                        sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_step that adds up weights as decode_attn_weights does; the new
+    token's sum starts with this step's weight."""
+    _weights("kvq8_decode_step_weights", q, k_new, v_new, cache, block_table, ctx_lens, out, weight_sum, workspace,
+             sm_scale, dev_status, stream)
+
+
+def evict(cache: KVCache, weight_sum, block_table, ctx_lens, keep: int, dst_table, kept, new_lens, n_first: int = 0,
+          n_recent: int = 0, dev_status=None, stream=None):
+    """Keep at most `keep` tokens of every (sequence, kv head) - the first
+    n_first, the last n_recent, and the others of largest weight_sum - copied
+    in order into the blocks of dst_table (int32 [batch][dst_max_blocks], none
+    of them in block_table).  kept (int32 [batch][nkv][keep]) receives their
+    positions, -1 behind the last, and new_lens (int32 [batch]) their number."""
+    nb, nkv = _need_cache(cache, weight_sum)
+    batch, max_blocks = block_table.shape
+    _need("block_table", block_table, "int32", (batch, max_blocks))
+    _need("dst_table", dst_table, "int32", (batch, dst_table.shape[1]))
+    _need("ctx_lens", ctx_lens, "int32", (batch,))
+    _need("kept", kept, "int32", (batch, nkv, keep))
+    _need("new_lens", new_lens, "int32", (batch,))
+    if dev_status is not None:
+        _need("dev_status", dev_status, "int32", (1,))
+    _check("kvq8_evict", load().kvq8_evict(
+        batch, nkv, HEAD_DIM, _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale), _ptr(cache.v_scale),
+        _ptr(weight_sum), nb, _ptr(block_table), max_blocks, BLOCK_SIZE, _ptr(ctx_lens), int(keep), int(n_first),
+        int(n_recent), _ptr(dst_table), dst_table.shape[1], _ptr(kept), _ptr(new_lens), _ptr(dev_status),
+        _stream(stream)))
+
+
+def rope_table(inv_freq, n_pos: int, stream=None):
+    """The rotation's table, fp32 [n_pos][128]: cosines of position * inv_freq
+    (fp64 [64], device), then sines."""
+    _need("inv_freq", inv_freq, "float64", (HEAD_DIM // 2,))
+    table = _torch().empty((n_pos, HEAD_DIM), dtype=_torch().float32, device=inv_freq.device)
+    _check("kvq8_rope_table", load().kvq8_rope_table(_ptr(inv_freq), int(n_pos), HEAD_DIM, _ptr(table),
+                                                     _stream(stream)))
+    return table
+
+
+def _token_rows(what: str, t, dtype, batch: int, n_new: int, heads=None) -> int:
+    """Checks [batch][n_new][heads][128] rows (heads side by side, all tokens one
+    distance apart) and returns that distance in elements."""
+    if t.dim() != 4 or t.shape[:2] != (batch, n_new) or t.shape[3] != HEAD_DIM or heads not in (None, t.shape[2]):
+        raise ValueError(f"{what}: expected [{batch}][{n_new}][heads][{HEAD_DIM}] rows, got {list(t.shape)}")
+    if not t.is_cuda or t.device.index != _torch().cuda.current_device() or t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype} on the current device, got {t.dtype} on {t.device}")
+    sb, sn, sh, sd = t.stride()
+    n_heads = t.shape[2]
+    dense = n_heads * HEAD_DIM
+    stride = sn if n_new > 1 else sb if batch > 1 else dense
+    if sd != 1 or (n_heads > 1 and sh != HEAD_DIM) or (n_new > 1 and batch > 1 and sb != n_new * stride):
+        raise ValueError(f"{what}: the heads of a token must lie side by side and all tokens one distance apart")
+    return stride
+
+
+def norm_rope_append(q, k, v, q_weight, k_weight, eps: float, rope_table, start_pos, block_table, cache: KVCache,
+                     q_out, positions=None, n_tokens=None, interleaved: bool = False, weight_sum=None,
+                     dev_status=None, stream=None):
+    """Norm and rotate the query and key heads of new tokens and quantise-append
+    K and V, in one pass.  q [batch][n_new][nqh][128], k, v [..][nkv][128]:
+    fp32, bf16 or fp16, possibly parts of one packed projection; q_weight,
+    k_weight fp32 [128] or both None (no norm); rope_table as rope_table()
+    makes it; positions int32 [batch][n_new] (None: the cache position);
+    n_tokens int32 [batch] (None: no padding); interleaved: rotate pairs
+    (2i, 2i + 1) instead of (i, i + 64); weight_sum: zeroed at the appended
+    tokens.  q_out fp32 [batch][n_new][nqh][128]."""
+    torch = _torch()
+    nb, nkv = _need_cache(cache, weight_sum)
+    batch, n_new, nqh = q.shape[:3]
+    dtype = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(q.dtype)
+    if dtype is None:
+        raise ValueError(f"q: expected fp32, bf16 or fp16, got {q.dtype}")
+    strides = (_token_rows("q", q, q.dtype, batch, n_new), _token_rows("k", k, q.dtype, batch, n_new, nkv),
+               _token_rows("v", v, q.dtype, batch, n_new, nkv))
+    max_blocks = block_table.shape[1]
+    _need("q_out", q_out, "float32", (batch, n_new, nqh, HEAD_DIM))
+    _need("rope_table", rope_table, "float32", (rope_table.shape[0], HEAD_DIM))
+    _need("block_table", block_table, "int32", (batch, max_blocks))
+    _need("start_pos", start_pos, "int32", (batch,))
+    for what, t, kind, shape in (("q_weight", q_weight, "float32", (HEAD_DIM,)),
+                                 ("k_weight", k_weight, "float32", (HEAD_DIM,)),
+                                 ("positions", positions, "int32", (batch, n_new)),
+                                 ("n_tokens", n_tokens, "int32", (batch,)),
+                                 ("dev_status", dev_status, "int32", (1,))):
+        if t is not None:
+            _need(what, t, kind, shape)
+    _check("kvq8_norm_rope_append", load().kvq8_norm_rope_append(
+        _ptr(q), _ptr(k), _ptr(v), dtype, *strides, batch, n_new, nqh, nkv, HEAD_DIM, _ptr(q_weight),
+        _ptr(k_weight), eps, _ptr(rope_table), rope_table.shape[0], _ptr(positions), _ptr(n_tokens),
+        ROPE_PAIRS if interleaved else 0, _ptr(start_pos), _ptr(block_table), max_blocks, BLOCK_SIZE, nb,
+        _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(weight_sum),
+        _ptr(q_out), _ptr(dev_status), _stream(stream)))
 
 
 # ------------------------------------------------------------ 4-bit cache ---

@@ -1,0 +1,190 @@
+"""Decode with accumulated attention weights: the output is the plain decode's
+and the sums are those of the oracle's softmax weights.
+
+Tolerance of a sum, against weights p of the 64-bit softmax over the same
+codes: a score s (base 2) is a sum of four exact integers times scales, five
+roundings and two products: off by at most 8 * 2^-24 |s|; |s| <= 64 on these
+inputs, so 2^s is off by 64 * 8 * 2^-24 * ln 2 < 2.2e-5 of itself, the sum in
+the denominator by as much again, and the base-2 exponential, the division and
+the G additions add less than 2e-6: within 1e-4 of p.  Below that, values under
+2^-126 of the maximum are lost: 1e-30.  An addition to a sum that is there
+rounds once: 2^-24 of it."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from int8_quantized_kv_gb300 import kvq8
+from int8_quantized_kv_gb300 import workloads as wl
+from kvq8_harness import SM_SCALE, Case, StepCase, assert_close
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(case, wsum, step=False, table=None, ws=None):
+    cfg = case.cfg
+    out = torch.full_like(case.q_d, float("nan"))
+    if ws is None:
+        ws = kvq8.alloc_weights_workspace(cfg.batch, cfg.nqh, cfg.nkv, case.max_blocks)
+        ws.fill_(255)                                        # NaN patterns: nothing stale may count
+    args = (case.cache, case.table_d if table is None else table, case.lens_d, out, wsum, ws)
+    if step:
+        kvq8.decode_step_weights(case.q_d, case.k_new_d, case.v_new_d, *args, dev_status=case.status)
+    else:
+        kvq8.decode_attn_weights(case.q_d, *args, dev_status=case.status)
+    torch.cuda.synchronize()
+    return out.cpu().numpy()
+
+
+def _unit_weights(case, b, h, L):
+    cfg, G = case.cfg, case.cfg.group
+    k, v = wl.unit_kv(cfg, b, h, L)
+    kq, ks = oracle.kv_quantize_rows(k)
+    qi, qsc = oracle.q_quantize_blocks(case.q[b, h * G:(h + 1) * G])
+    p = np.zeros(L)
+    for g in range(G):
+        s = oracle.scores_q8(qi[g], qsc[g], kq, ks, SM_SCALE)
+        assert np.abs(s).max() / np.log(2) <= 64
+        w = np.exp(s - s.max())
+        p += w / w.sum()
+    return p
+
+
+def _check_sums(case, before, after, step=False, lens=None):
+    """Every slot of every block: the listed ones as the oracle says, the others untouched."""
+    cfg = case.cfg
+    want = before.astype(np.float64)
+    tol = np.zeros_like(want)
+    for b in range(cfg.batch):
+        L = int(case.lens[b]) if lens is None else lens[b]
+        if L == 0:
+            continue
+        t = np.arange(L)
+        phys, slot = case.table[b, t // 256], t % 256
+        for h in range(cfg.nkv):
+            p = _unit_weights(case, b, h, L)
+            if step:
+                want[phys[-1], h, slot[-1]] = 0.0
+            want[phys, h, slot] += p
+            tol[phys, h, slot] = 1e-4 * p + 1e-30 + 2.0**-24 * np.abs(want[phys, h, slot])
+    err = np.abs(after.astype(np.float64) - want)
+    assert np.all(err <= tol), f"worst {np.max(err - tol)} at {np.unravel_index(np.argmax(err - tol), err.shape)}"
+
+
+def _sums(case, seed=1):
+    x = np.random.default_rng(seed).random((case.num_blocks, case.cfg.nkv, 256), np.float32)
+    return x, torch.from_numpy(x).cuda()
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_output_and_sums(gpu_lib, G):
+    lens = [1, 3, 0, 64, 65, 511, 512, 513, 700, 1025, 1301]
+    cfg = wl.Workload("s", 800 + G, batch=len(lens), nqh=2 * G, nkv=2)
+    case = Case(cfg, lens=lens)
+    before, wsum = _sums(case)
+    plain = case.decode()
+    got = _run(case, wsum)
+    ref_b = 8
+    assert_close(got[ref_b, :G], case.oracle_unit(ref_b, 0), "out")
+    assert_close(got, plain, "against the plain decode")
+    _check_sums(case, before, wsum.cpu().numpy())
+    assert case.status_bits() == 0
+
+
+def test_sums_add_up_over_calls_and_to_the_group_size(gpu_lib):
+    cfg = wl.Workload("s", 820, batch=3, nqh=16, nkv=4)
+    case = Case(cfg, lens=[900, 17, 2000])
+    wsum = kvq8.alloc_weight_sum(case.num_blocks, 4)
+    for i in range(3):
+        _run(case, wsum)
+    # each call adds weights that sum to G per unit, each sum of 3 * 2^-24 relative roundings and
+    # weights within 1e-4 of themselves
+    w = wsum.cpu().numpy().astype(np.float64)
+    for b, L in enumerate([900, 17, 2000]):
+        t = np.arange(L)
+        for h in range(4):
+            assert abs(w[case.table[b, t // 256], h, t % 256].sum() - 3 * 4) <= 3 * 4 * 1.1e-4
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_step_starts_the_new_tokens_sum(gpu_lib, G):
+    lens = [1, 64, 65, 257, 512, 1301, 0]
+    cfg = wl.Workload("s", 830 + G, batch=len(lens), nqh=2 * G, nkv=2)
+    case = StepCase(cfg, lens=lens)
+    before, wsum = _sums(case, 2)
+    # whatever the new token's slot held, NaN included, is gone
+    for b, L in enumerate(lens):
+        if L:
+            wsum[int(case.table[b, (L - 1) // 256]), :, (L - 1) % 256] = float("nan")
+    got = _run(case, wsum, step=True)
+    _check_sums(case, before, wsum.cpu().numpy(), step=True)
+    full = Case(cfg, lens=lens)
+    pools, fpools = case.host_pools(), full.host_pools()
+    for b in range(cfg.batch):
+        for h in range(2):
+            for x, y in zip(case.gather_unit(pools, b, h), full.gather_unit(fpools, b, h)):
+                assert np.array_equal(x, y)
+    assert np.array_equal(got, _run(full, torch.zeros_like(wsum)))
+
+
+def test_steep_scores(gpu_lib):
+    # all weight on one late token: the others' sums grow by next to nothing
+    L, G = 700, 4
+    q, k, v = wl.steered_unit(3, L, G, "spike")
+    cache = kvq8.alloc_cache(3, 1)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    kvq8.quantize_append(torch.from_numpy(k)[None, :, None].contiguous().cuda(),
+                         torch.from_numpy(v)[None, :, None].contiguous().cuda(),
+                         torch.zeros(1, dtype=torch.int32, device="cuda"), table, cache)
+    wsum = kvq8.alloc_weight_sum(3, 1)
+    out = torch.empty((1, G, 128), device="cuda")
+    kvq8.decode_attn_weights(torch.from_numpy(q)[None].cuda(), cache, table,
+                             torch.tensor([L], dtype=torch.int32, device="cuda"), out, wsum,
+                             kvq8.alloc_weights_workspace(1, G, 1, 3))
+    t = np.arange(L)
+    w = wsum.cpu().numpy()[np.array([2, 0, 1])[t // 256], 0, t % 256]
+    top = 2 * L // 3
+    assert abs(w[top] - G) <= 1e-4 * G and np.all(np.delete(w, top) <= 1e-4)
+    ref, _ = oracle.decode_unit_q8(q, k, v, SM_SCALE)
+    assert_close(out.cpu().numpy()[0], ref)
+
+
+def test_bad_lengths_and_blocks(gpu_lib):
+    cfg = wl.Workload("s", 840, batch=3, nqh=4, nkv=2)
+    case = Case(cfg, lens=[600, 600, 600])
+    before, wsum = _sums(case, 3)
+    table = case.table.copy()
+    table[0, 1], table[1, 0], table[2, :] = -1, case.num_blocks, 10**9
+    got = _run(case, wsum, table=torch.from_numpy(table).cuda())
+    assert case.status_bits() == kvq8.DEV_BAD_BLOCK_ID and np.all(np.isfinite(got)) and not got[2].any()
+    after = wsum.cpu().numpy()
+    G = cfg.group
+    want = before.astype(np.float64)
+    for b, vis in ((0, np.r_[0:256, 512:600]), (1, np.arange(256, 600))):
+        for h in range(2):
+            k, v = wl.unit_kv(cfg, b, h, 600)
+            ref, qz = oracle.decode_unit_q8(case.q[b, h * G:(h + 1) * G], k[vis], v[vis], SM_SCALE)
+            assert_close(got[b, h * G:(h + 1) * G], ref)
+            for g in range(G):
+                s = oracle.scores_q8(qz["qi"][g], qz["qsc"][g], qz["kq"], qz["ks"], SM_SCALE)
+                w = np.exp(s - s.max())
+                want[case.table[b, vis // 256], h, vis % 256] += w / w.sum()
+    assert np.abs(after - want).max() <= 1e-4
+    untouched = np.ones(before.shape, bool)
+    for b, vis in ((0, np.r_[0:256, 512:600]), (1, np.arange(256, 600))):
+        untouched[case.table[b, vis // 256], :, vis % 256] = False
+    assert np.array_equal(after[untouched], before[untouched])
+    case.status.zero_()
+    case.lens_d.copy_(torch.tensor([-1, 100000, 5], dtype=torch.int32))    # beyond the table: clamped
+    got = _run(case, wsum)
+    assert case.status_bits() & kvq8.DEV_BAD_CTX_LEN and not got[0].any() and np.all(np.isfinite(got[2]))
+
+
+def test_long_context_offsets(gpu_lib):
+    # one unit's plane of scores past 2^31 bytes in the workspace would need 2 GB; the largest table
+    # that a test affords, with the sequence in the last row
+    cfg = wl.Workload("s", 850, batch=3, nqh=8, nkv=1)
+    case = Case(cfg, lens=[5, 2, 40000])
+    before, wsum = _sums(case, 4)
+    _run(case, wsum)
+    _check_sums(case, before, wsum.cpu().numpy())
