@@ -21,9 +21,89 @@
 namespace kvq8 {
 namespace {
 
-constexpr int kRowWarps = 8;   // warps per CTA, one row each
+constexpr int kTaskWarps = 4;             // warps per CTA, one task each
+constexpr int kRunTok = 16;               // tokens per key/value task
+constexpr int kGroupTok = 4;              // tokens of it loaded at once
+constexpr int kQUnroll = 4;               // query heads of a task loaded at once
+constexpr int kQueryTasks = 152 * 32;     // query tasks that fill the GPU
 
-// Largest |x| of a row held as a float4 per lane; a row with a NaN or an
+// A row x is held two ways.  Turned rows (queries, keys): lane l holds dims
+// 2l, 2l + 1 (x, y) and 64 + 2l, 65 + 2l (z, w), so that both kinds of pairs,
+// (i, i + 64) and (2i, 2i + 1), lie within a lane and turning needs no
+// exchange.  Value rows: dims 4l..4l+3, as the append holds them.
+__device__ __forceinline__ float2 load2(const float *p) { return __ldcs(reinterpret_cast<const float2 *>(p)); }
+__device__ __forceinline__ float2 load2(const __half *p) {
+    const uint32_t v = __ldcs(reinterpret_cast<const unsigned int *>(p));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t v = __ldcs(reinterpret_cast<const unsigned int *>(p));   // a bf16 is the high half of an fp32
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 load4(const __half *p) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ float4 load_turned(const T *row, int lane) {
+    const float2 lo = load2(row + 2 * lane), hi = load2(row + kHD / 2 + 2 * lane);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+// The weights of a lane's dims (1 without a norm).
+__device__ __forceinline__ float4 load_weight(const float *w, int lane) {
+    if (!w) return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    const float2 lo = reinterpret_cast<const float2 *>(w)[lane], hi = reinterpret_cast<const float2 *>(w + kHD / 2)[lane];
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+// Cosine and sine of a lane's two pairs from a table row [cos 64 | sin 64]:
+// (c.x, s.x) turns the first pair, (c.y, s.y) the second.
+struct Turn {
+    float2 c, s;
+};
+template <bool kPairs>
+__device__ __forceinline__ Turn load_turn(const float *row, int lane) {
+    if (kPairs) return {make_float2(row[lane], row[32 + lane]), make_float2(row[64 + lane], row[96 + lane])};
+    return {reinterpret_cast<const float2 *>(row)[lane], reinterpret_cast<const float2 *>(row + kHD / 2)[lane]};
+}
+template <bool kPairs>
+__device__ __forceinline__ float4 turned(float4 u, const Turn &t) {
+    if (kPairs)
+        return make_float4(u.x * t.c.x - u.y * t.s.x, u.y * t.c.x + u.x * t.s.x,
+                           u.z * t.c.y - u.w * t.s.y, u.w * t.c.y + u.z * t.s.y);
+    return make_float4(u.x * t.c.x - u.z * t.s.x, u.y * t.c.y - u.w * t.s.y,
+                       u.z * t.c.x + u.x * t.s.x, u.w * t.c.y + u.y * t.s.y);
+}
+
+__device__ __forceinline__ float4 scaled(float4 x, float f) {
+    return make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+}
+__device__ __forceinline__ float sum_squares(float4 x) {
+    return warp_sum(fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w))));
+}
+
+// x * r * w for the row's r = 1 / sqrt(mean(x^2) + eps).  Squares that
+// overflow (|x| above about 2^60) are taken of x * 2^-64 instead.
+__device__ __forceinline__ float4 normed(float4 x, float4 w, float eps) {
+    float f = 1.0f;
+    float ss = sum_squares(x);
+    if (ss > 0x1p120f) {   // warp-uniform
+        f = 0x1p-64f;
+        x = scaled(x, f);
+        ss = sum_squares(x);
+    }
+    x = scaled(x, rsqrtf(fmaf(ss, 1.0f / kHD, eps * f * f)));
+    return make_float4(x.x * w.x, x.y * w.y, x.z * w.z, x.w * w.w);
+}
+
+// Largest |x| of a row held as four values per lane; a row with a NaN or an
 // infinity is cleared and flagged, and its maximum is 0.
 __device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
     const uint32_t a = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
@@ -37,172 +117,247 @@ __device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
     return __uint_as_float(m);
 }
 
-// Four consecutive values of a row.
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __half *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);   // a bf16 is the high half of an fp32
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
-}
-
-__device__ __forceinline__ float4 scaled(float4 x, float f) {
-    return make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-}
-__device__ __forceinline__ float4 times(float4 x, float4 w) {
-    return make_float4(x.x * w.x, x.y * w.y, x.z * w.z, x.w * w.w);
-}
-
-// x * r for the row's r = 1 / sqrt(mean(x^2) + eps).  Squares that overflow
-// (|x| above about 2^60) are taken of x * 2^-64 instead.
-__device__ __forceinline__ float4 normed(float4 x, float eps) {
-    float f = 1.0f;
-    float ss = warp_sum(fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w))));
-    if (ss > 0x1p120f) {   // warp-uniform
-        f = 0x1p-64f;
-        x = scaled(x, f);
-        ss = warp_sum(fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w))));
-    }
-    return scaled(x, rsqrtf(fmaf(ss, 1.0f / kHD, eps * f * f)));
-}
-
-// The rotation of a row held as dims 4l..4l+3 in lane l.  Halves: lane l and
-// lane l ^ 16 hold the two ends of the same pairs; pairs: both ends are in the
-// lane.  cs, sn: cosines and sines of the lane's values (see load_turn).
+// The codes of a key row from its inputs in 64 bits, for the values of `mask`
+// (bit k: the lane's value k); x * w is exact there.
 template <bool kPairs>
-__device__ __forceinline__ float4 rotated(float4 u, float4 cs, float4 sn, int lane) {
-    if (kPairs)
-        return make_float4(u.x * cs.x - u.y * sn.x, u.y * cs.x + u.x * sn.x,
-                           u.z * cs.y - u.w * sn.y, u.w * cs.y + u.z * sn.y);
-    float4 o;
-    o.x = __shfl_xor_sync(0xffffffffu, u.x, 16);
-    o.y = __shfl_xor_sync(0xffffffffu, u.y, 16);
-    o.z = __shfl_xor_sync(0xffffffffu, u.z, 16);
-    o.w = __shfl_xor_sync(0xffffffffu, u.w, 16);
-    const float f = lane < 16 ? -1.0f : 1.0f;
-    return make_float4(u.x * cs.x + o.x * (f * sn.x), u.y * cs.y + o.y * (f * sn.y),
-                       u.z * cs.z + o.z * (f * sn.z), u.w * cs.w + o.w * (f * sn.w));
-}
-
-// The same in 64 bits, of x * w.
-template <bool kPairs>
-__device__ __forceinline__ void rotated64(float4 x, float4 w, float4 cs, float4 sn, int lane, double (&z)[4]) {
-    double u[4] = {(double)x.x * w.x, (double)x.y * w.y, (double)x.z * w.z, (double)x.w * w.w};
+__device__ __noinline__ uint4 exact_codes(float4 x, float4 w, Turn t, uint4 codes, int mask) {
+    const double ux = (double)x.x * w.x, uy = (double)x.y * w.y, uz = (double)x.z * w.z, uw = (double)x.w * w.w;
+    double z[4];
     if (kPairs) {
-        z[0] = u[0] * cs.x - u[1] * sn.x;
-        z[1] = u[1] * cs.x + u[0] * sn.x;
-        z[2] = u[2] * cs.y - u[3] * sn.y;
-        z[3] = u[3] * cs.y + u[2] * sn.y;
-        return;
-    }
-    const double f = lane < 16 ? -1.0 : 1.0;
-    const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const double o = __shfl_xor_sync(0xffffffffu, u[i], 16);
-        z[i] = u[i] * c[i] + o * (f * s[i]);
-    }
-}
-
-// Cosines and sines of the lane's values from a table row [cos 64 | sin 64].
-template <bool kPairs>
-__device__ __forceinline__ void load_turn(const float *row, int lane, float4 &cs, float4 &sn) {
-    if (kPairs) {
-        const float2 c = reinterpret_cast<const float2 *>(row)[lane];
-        const float2 s = reinterpret_cast<const float2 *>(row + kHD / 2)[lane];
-        cs = make_float4(c.x, c.y, 0.0f, 0.0f);
-        sn = make_float4(s.x, s.y, 0.0f, 0.0f);
+        z[0] = ux * t.c.x - uy * t.s.x;
+        z[1] = uy * t.c.x + ux * t.s.x;
+        z[2] = uz * t.c.y - uw * t.s.y;
+        z[3] = uw * t.c.y + uz * t.s.y;
     } else {
-        cs = reinterpret_cast<const float4 *>(row)[lane & 15];
-        sn = reinterpret_cast<const float4 *>(row + kHD / 2)[lane & 15];
+        z[0] = ux * t.c.x - uz * t.s.x;
+        z[1] = uy * t.c.y - uw * t.s.y;
+        z[2] = uz * t.c.x + ux * t.s.x;
+        z[3] = uw * t.c.y + uy * t.s.y;
     }
+    double top = fmax(fmax(fabs(z[0]), fabs(z[1])), fmax(fabs(z[2]), fabs(z[3])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (mask >> k & 1) c[k] = (uint32_t)__double2int_rn(127.0 * z[k] / top);
+    return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// One warp per (new token, head): query heads, then key heads, then value heads.
-template <typename T, bool kPairs>
-__global__ void __launch_bounds__(kRowWarps * 32)
-norm_rope_append_kernel(NormRopeParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int heads = p.nqh + 2 * p.nkv;
-    const int64_t task = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    if (task >= (int64_t)p.batch * p.n_new * heads) return;
-    const int64_t row = task / heads;
-    int head = (int)(task % heads);
-    const int b = (int)(row / p.n_new), i = (int)(row % p.n_new);
-    if (p.n_tokens && i >= p.n_tokens[b]) return;   // padding
-    const int64_t slot_pos = (int64_t)p.start_pos[b] + i;
-    const int64_t pos = p.positions ? p.positions[row] : slot_pos;
-    if (pos < 0 || pos >= p.n_pos) {
-        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-        return;
+// Codes (low bytes) of a key row y = turned x * r * w with maximum m > 0 and
+// scale s: round_half_even(127 y* / max|y*|) of the exact values y*, whose
+// common factor r cancels.  In units of eps = 2^-24 and Z = max|y*|: u = x r w
+// carries two roundings (r's own cancels), the turn one of a product and one of
+// the sum, and |u_a c| + |u_b s| <= |(u_a, u_b)| |(c, s)| <= sqrt(2) Z, so that
+// y is within (3 sqrt(2) + 1) eps Z of y* and so is m of Z; 127 * rcp(m) adds 3
+// eps.  127 y / m is then within 127 * 13.5 eps < 2^-13.2 of 127 y* / Z, and
+// where its distance to the rounded value is at most 1/2 - 2^-13 that value is
+// the code (t = fl(y * inv + 1.5 * 2^23) holds it in its low mantissa bits, as
+// in kv_code_bytes4).  The others, 2^-12 of values and a value in 3 % of rows,
+// are decided in 64 bits, as are rows whose range leaves the products' errors
+// unbounded.
+template <bool kPairs>
+__device__ __forceinline__ uint4 key_codes(float4 y, float m, float s, float4 x, float4 w, const Turn &t) {
+    if (s == 0.0f) return make_uint4(0u, 0u, 0u, 0u);   // warp-uniform
+    constexpr float kShift = 0x1.8p23f;
+    constexpr float kLim = 0.5f - 0x1p-13f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(m));
+    inv *= 127.0f;
+    const float t0 = __fmaf_rn(y.x, inv, kShift), t1 = __fmaf_rn(y.y, inv, kShift);
+    const float t2 = __fmaf_rn(y.z, inv, kShift), t3 = __fmaf_rn(y.w, inv, kShift);
+    const float e0 = __fmaf_rn(y.x, inv, -__fsub_rn(t0, kShift)), e1 = __fmaf_rn(y.y, inv, -__fsub_rn(t1, kShift));
+    const float e2 = __fmaf_rn(y.z, inv, -__fsub_rn(t2, kShift)), e3 = __fmaf_rn(y.w, inv, -__fsub_rn(t3, kShift));
+    uint4 c = make_uint4(__float_as_uint(t0), __float_as_uint(t1), __float_as_uint(t2), __float_as_uint(t3));
+    const bool wide = !(m >= 0x1p-100f && m <= 0x1p120f);
+    const bool near = !((fabsf(e0) <= kLim) & (fabsf(e1) <= kLim) & (fabsf(e2) <= kLim) & (fabsf(e3) <= kLim));
+    if (__any_sync(0xffffffffu, wide | near)) {
+        const int mask = wide ? 15 : !(fabsf(e0) <= kLim) | !(fabsf(e1) <= kLim) << 1 | !(fabsf(e2) <= kLim) << 2 |
+                                         !(fabsf(e3) <= kLim) << 3;
+        c = exact_codes<kPairs>(x, w, t, c, mask);
     }
-    const bool is_q = head < p.nqh, is_k = !is_q && head < p.nqh + p.nkv;
-    const T *src = reinterpret_cast<const T *>(is_q ? p.q : is_k ? p.k : p.v) +
-                   row * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride);
-    if (!is_q) head -= is_k ? p.nqh : p.nqh + p.nkv;
-    float4 x = load4(src + (size_t)head * kHD + 4 * lane);
+    return c;
+}
 
-    float4 y, w = make_float4(1.0f, 1.0f, 1.0f, 1.0f), cs, sn;
-    if (is_q || is_k) {
-        const float *weight = is_q ? p.q_weight : p.k_weight;
-        load_turn<kPairs>(p.rope + (size_t)pos * kHD, lane, cs, sn);
-        y = x;
-        if (weight) {
-            w = load4(weight + 4 * lane);
-            y = times(normed(x, p.eps), w);
-        }
-        y = rotated<kPairs>(y, cs, sn, lane);
-        if (is_q) {
-            *reinterpret_cast<float4 *>(p.q_out + (row * p.nqh + head) * kHD + 4 * lane) = y;
-            return;
-        }
-    }
-    if (slot_pos < 0 || slot_pos >= (int64_t)p.max_blocks * kBS) {
+// Writes a key row's codes, held as a turned row, to the row at dst of a slot.
+__device__ __forceinline__ void store_key_codes(unsigned char *dst, int slot, int lane, uint4 c) {
+    const int j = lane >> 3, at = 2 * (lane & 7);
+    *reinterpret_cast<uint16_t *>(dst + ((j ^ (slot & 7)) << 4) + at) = (uint16_t)__byte_perm(c.x, c.y, 0x0040);
+    *reinterpret_cast<uint16_t *>(dst + (((4 + j) ^ (slot & 7)) << 4) + at) = (uint16_t)__byte_perm(c.z, c.w, 0x0040);
+}
+
+// New tokens of sequence b (the rest of its n_new rows is padding).
+__device__ __forceinline__ int token_count(const NormRopeParams &p, int b) {
+    return p.n_tokens ? min(p.n_new, p.n_tokens[b]) : p.n_new;
+}
+
+// Key/value task w = (b * runs + x) * nkv + h: the new tokens of sequence b in
+// run x of 16 cache slots, counted from the run of the first, of kv head h.
+template <typename T, bool kPairs>
+__device__ __forceinline__ void append_run(const NormRopeParams &p, int64_t w, int runs, int lane) {
+    const int h = (int)(w % p.nkv);
+    w /= p.nkv;
+    const int b = (int)(w / runs);
+    const int64_t cap = (int64_t)p.max_blocks * kBS;
+    const int64_t start = p.start_pos[b];
+    const int nt = token_count(p, b);
+    // slots [r0, r0 + 16), of which tokens with positions in [lo, hi) are written
+    const int64_t r0 = (start >= 0 ? start / kRunTok : -((-start + kRunTok - 1) / kRunTok)) * kRunTok +
+                       (w % runs) * kRunTok;
+    int64_t lo = max(start, r0), hi = min(start + nt, r0 + kRunTok);
+    if (lo >= hi) return;
+    if (lo < 0 || hi > cap) {
         if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-        return;
+        lo = max(lo, (int64_t)0);
+        hi = min(hi, cap);
+        if (lo >= hi) return;
     }
-    const int phys = p.block_table[(size_t)b * p.max_blocks + slot_pos / kBS];
+    const int phys = p.block_table[(size_t)b * p.max_blocks + r0 / kBS];
+    // lane r: the rotation position of the token in slot r0 + r
+    const int64_t row0 = (int64_t)b * p.n_new + (r0 - start);   // row of the token in slot r0 (may precede the tensor)
+    const bool mine = lane < kRunTok && r0 + lane >= lo && r0 + lane < hi;
+    int64_t pos = 0;
+    if (mine) pos = p.positions ? p.positions[row0 + lane] : r0 + lane;
+    const bool good = mine && pos >= 0 && pos < p.n_pos;
+    if (mine && !good) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
     if (phys < 0 || phys >= p.num_blocks) {
         if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
         return;
     }
-    const int slot = (int)(slot_pos % kBS);
-    const size_t tile = (size_t)phys * p.nkv + head;
-    if (is_k) {
-        const float s = __fmul_rn(row_max_checked(y, p.dev_status), KVQ8_INV127);
-        int code[4] = {0, 0, 0, 0};
-        if (s > 0.0f) {   // warp-uniform
-            double z[4];
-            rotated64<kPairs>(x, w, cs, sn, lane, z);
-            double top = fmax(fmax(fabs(z[0]), fabs(z[1])), fmax(fabs(z[2]), fabs(z[3])));
+    const unsigned todo = __ballot_sync(0xffffffffu, good);
+    const size_t tile = (size_t)phys * p.nkv + h;
+    const int slot0 = (int)(r0 % kBS);
+    unsigned char *krow = reinterpret_cast<unsigned char *>(p.k_pool) + (tile * kBS + slot0) * kHD;
+    int8_t *vrun = p.v_pool + tile * kHD * kBS + (size_t)(slot0 / kStageTok) * kTileVQuarter + slot0 % kStageTok;
+    const T *ksrc = reinterpret_cast<const T *>(p.k) + (size_t)h * kHD;
+    const T *vsrc = reinterpret_cast<const T *>(p.v) + (size_t)h * kHD + 4 * lane;
+    const float4 weight = load_weight(p.k_weight, lane);
+    const bool norm = p.k_weight != nullptr;
+
+    if (todo == 0xffffu) {
+        // the whole run, four tokens at a time
+        uint32_t vw[4][kRunTok / 4];   // after group g, vw[i][3]: the codes of its tokens of dim 4 * lane + i
+        float sc_keep = 0.0f;          // lane r < 16: K scale of row r; lane 16 + r: V scale
+#pragma unroll 1
+        for (int g = 0; g < kRunTok / kGroupTok; ++g) {
+            float4 xk[kGroupTok], xv[kGroupTok];
+            Turn tn[kGroupTok];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int u = 0; u < kGroupTok; ++u) {
+                const int r = kGroupTok * g + u;
+                xk[u] = load_turned(ksrc + (row0 + r) * p.k_stride, lane);
+                xv[u] = load4(vsrc + (row0 + r) * p.v_stride);
+                tn[u] = load_turn<kPairs>(p.rope + (size_t)__shfl_sync(0xffffffffu, (int)pos, r) * kHD, lane);
+            }
+            uint32_t wg[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) code[k] = __double2int_rn(127.0 * z[k] / top);
+            for (int u = 0; u < kGroupTok; ++u) {
+                const int r = kGroupTok * g + u;
+                float4 y = turned<kPairs>(norm ? normed(xk[u], weight, p.eps) : xk[u], tn[u]);
+                const float mk = row_max_checked(y, p.dev_status), sk = __fmul_rn(mk, KVQ8_INV127);
+                store_key_codes(krow + r * kHD, r, lane, key_codes<kPairs>(y, mk, sk, xk[u], weight, tn[u]));
+                const float sv = __fmul_rn(row_max_checked(xv[u], p.dev_status), KVQ8_INV127);
+                const uint4 cv = kv_code_bytes4(xv[u], sv);
+                if (lane == r) sc_keep = sk;
+                if (lane == 16 + r) sc_keep = sv;
+                constexpr uint32_t kIns[4] = {0x3210, 0x3240, 0x3410, 0x4210};
+                if (u == 0) {
+                    wg[0] = cv.x; wg[1] = cv.y; wg[2] = cv.z; wg[3] = cv.w;
+                } else {
+                    wg[0] = __byte_perm(wg[0], cv.x, kIns[u]);
+                    wg[1] = __byte_perm(wg[1], cv.y, kIns[u]);
+                    wg[2] = __byte_perm(wg[2], cv.z, kIns[u]);
+                    wg[3] = __byte_perm(wg[3], cv.w, kIns[u]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                vw[i][0] = vw[i][1];
+                vw[i][1] = vw[i][2];
+                vw[i][2] = vw[i][3];
+                vw[i][3] = wg[i];
+            }
         }
-        unsigned char *dst = reinterpret_cast<unsigned char *>(p.k_pool) + (tile * kBS + slot) * kHD;
-        reinterpret_cast<uint32_t *>(dst + (((lane >> 2) ^ (slot & 7)) << 4))[lane & 3] =
-            low_bytes4(make_uint4(code[0], code[1], code[2], code[3]));
+        (lane < 16 ? p.k_scale : p.v_scale)[tile * kBS + slot0 + (lane & 15)] = sc_keep;
+        if (p.weight_sum && lane < 16) p.weight_sum[tile * kBS + slot0 + lane] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(vrun + (size_t)(4 * lane + i) * kStageTok) =
+                make_uint4(vw[i][0], vw[i][1], vw[i][2], vw[i][3]);
+        return;
+    }
+    // part of a run: row by row
+    for (unsigned left = todo; left; left &= left - 1) {
+        const int r = __ffs(left) - 1;
+        const float4 xk = load_turned(ksrc + (row0 + r) * p.k_stride, lane);
+        float4 xv = load4(vsrc + (row0 + r) * p.v_stride);
+        const Turn tn = load_turn<kPairs>(p.rope + (size_t)__shfl_sync(0xffffffffu, (int)pos, r) * kHD, lane);
+        float4 y = turned<kPairs>(norm ? normed(xk, weight, p.eps) : xk, tn);
+        const float mk = row_max_checked(y, p.dev_status), sk = __fmul_rn(mk, KVQ8_INV127);
+        store_key_codes(krow + r * kHD, r, lane, key_codes<kPairs>(y, mk, sk, xk, weight, tn));
+        const float sv = __fmul_rn(row_max_checked(xv, p.dev_status), KVQ8_INV127);
+        const uint4 c = kv_code_bytes4(xv, sv);
+        vrun[(size_t)(4 * lane + 0) * kStageTok + r] = (int8_t)c.x;
+        vrun[(size_t)(4 * lane + 1) * kStageTok + r] = (int8_t)c.y;
+        vrun[(size_t)(4 * lane + 2) * kStageTok + r] = (int8_t)c.z;
+        vrun[(size_t)(4 * lane + 3) * kStageTok + r] = (int8_t)c.w;
         if (lane == 0) {
-            p.k_scale[tile * kBS + slot] = s;
-            if (p.weight_sum) p.weight_sum[tile * kBS + slot] = 0.0f;
+            p.k_scale[tile * kBS + slot0 + r] = sk;
+            p.v_scale[tile * kBS + slot0 + r] = sv;
+            if (p.weight_sum) p.weight_sum[tile * kBS + slot0 + r] = 0.0f;
         }
-    } else {
-        const float s = __fmul_rn(row_max_checked(x, p.dev_status), KVQ8_INV127);
-        const uint4 c = kv_code_bytes4(x, s);
-        int8_t *vg = p.v_pool + tile * kHD * kBS + (size_t)(slot / kStageTok) * kTileVQuarter + slot % kStageTok;
-        vg[(size_t)(4 * lane + 0) * kStageTok] = (int8_t)c.x;
-        vg[(size_t)(4 * lane + 1) * kStageTok] = (int8_t)c.y;
-        vg[(size_t)(4 * lane + 2) * kStageTok] = (int8_t)c.z;
-        vg[(size_t)(4 * lane + 3) * kStageTok] = (int8_t)c.w;
-        if (lane == 0) p.v_scale[tile * kBS + slot] = s;
+    }
+}
+
+// Query task w = row * parts + c: heads [c * hp, (c + 1) * hp) of a token.
+template <typename T, bool kPairs>
+__device__ __forceinline__ void turn_queries(const NormRopeParams &p, int64_t w, int hp, int lane) {
+    const int parts = (p.nqh + hp - 1) / hp;
+    const int64_t row = w / parts;
+    const int h0 = (int)(w % parts) * hp, h1 = min(p.nqh, h0 + hp);
+    const int b = (int)(row / p.n_new), i = (int)(row % p.n_new);
+    if (p.n_tokens && i >= p.n_tokens[b]) return;   // padding
+    const int64_t pos = p.positions ? p.positions[row] : (int64_t)p.start_pos[b] + i;
+    if (pos < 0 || pos >= p.n_pos) {
+        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+        return;
+    }
+    const T *src = reinterpret_cast<const T *>(p.q) + row * p.q_stride;
+    float *dst = p.q_out + row * p.nqh * kHD;
+    const float4 weight = load_weight(p.q_weight, lane);
+    const bool norm = p.q_weight != nullptr;
+    const Turn tn = load_turn<kPairs>(p.rope + (size_t)pos * kHD, lane);
+    for (int h = h0; h < h1; h += kQUnroll) {
+        float4 x[kQUnroll];
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u)
+            if (h + u < h1) x[u] = load_turned(src + (size_t)(h + u) * kHD, lane);
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u) {
+            if (h + u < h1) {
+                const float4 y = turned<kPairs>(norm ? normed(x[u], weight, p.eps) : x[u], tn);
+                float *d = dst + (size_t)(h + u) * kHD + 2 * lane;
+                *reinterpret_cast<float2 *>(d) = make_float2(y.x, y.y);
+                *reinterpret_cast<float2 *>(d + kHD / 2) = make_float2(y.z, y.w);
+            }
+        }
+    }
+}
+
+// One task per warp: first the key/value tasks, which are longer, then the
+// query tasks.
+template <typename T, bool kPairs>
+__global__ void __launch_bounds__(kTaskWarps * 32)
+norm_rope_append_kernel(NormRopeParams p, int runs, int hp) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t task = (int64_t)blockIdx.x * kTaskWarps + (threadIdx.x >> 5);
+    const int64_t kv = (int64_t)p.batch * runs * p.nkv;
+    if (task < kv) {
+        append_run<T, kPairs>(p, task, runs, lane);
+    } else if (task - kv < (int64_t)p.batch * p.n_new * ((p.nqh + hp - 1) / hp)) {
+        turn_queries<T, kPairs>(p, task - kv, hp, lane);
     }
 }
 
@@ -223,12 +378,19 @@ rope_table_kernel(const double *inv_freq, int64_t n, float *table) {
 
 template <typename T, bool kPairs>
 cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
-    const int64_t tasks = (int64_t)p.batch * p.n_new * (p.nqh + 2 * p.nkv);
-    const int64_t blocks = (tasks + kRowWarps - 1) / kRowWarps;
+    // runs of 16 slots that n_new consecutive positions touch, at most
+    const int runs = (int)(((int64_t)p.n_new + kRunTok - 2) / kRunTok + 1);
+    const int64_t rows = (int64_t)p.batch * p.n_new;
+    // A query task takes one head while that leaves the GPU short of warps, and
+    // up to 8 (which then share one turn and weight) when there are many.
+    int hp = 1;
+    while (hp < 8 && rows * p.nqh >= (int64_t)hp * 2 * kQueryTasks) hp *= 2;
+    const int64_t tasks = (int64_t)p.batch * runs * p.nkv + rows * ((p.nqh + hp - 1) / hp);
+    const int64_t blocks = (tasks + kTaskWarps - 1) / kTaskWarps;
     if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.blockDim = dim3(kTaskWarps * 32);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -236,7 +398,7 @@ cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, kPairs>, p);
+    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, kPairs>, p, runs, hp);
 }
 
 template <typename T>
