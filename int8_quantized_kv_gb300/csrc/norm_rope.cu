@@ -5,12 +5,23 @@
 //   r = 1 / sqrt(mean(x^2) + eps), u = x * r * w (u = x without a weight),
 //   y_a = u_a cos - u_b sin, y_b = u_b cos + u_a sin
 // for the pairs (a, b) = (i, i + 64) or (2i, 2i + 1).  A query row is written
-// in fp32; a key row goes to the int8 cache with scale = max|y| * (1/127) and code
-// = round_half_even(127 y / max|y|).  The code is that of the exact values: r
-// is common to the row and cancels, and where fp32 cannot tell on which side
-// of a border 127 y / max|y| lies, 64 bits decide.  A value row is quantised
-// by the append's own rule, but that both scales are the product with the
-// rounded 1/127 (as the query blocks'), not a division.
+// in fp32; a key row goes to the int8 cache with scale = max|y| * (1/127) and
+// code = round_half_even(127 y / max|y|).  The code is that of the exact
+// values: r is common to the row and cancels, and where fp32 cannot tell on
+// which side of a border 127 y / max|y| lies, 64 bits decide.  A value row is
+// quantised by the append's own rule, but that both scales are the product
+// with the rounded 1/127 (as the query blocks'), not a division.
+//
+// Two kinds of warp tasks, mixed evenly over the grid so that the loads of the
+// one overlap the arithmetic of the other:
+//  * turn tasks: up to four heads at a time of one token, eight lanes to a
+//    row.  With 16 values a lane, a row's sum and maximum take three exchanges
+//    instead of five, shared by four rows, and the table row is loaded once
+//    for all heads of the task.
+//  * value tasks: the new tokens of a run of 16 (or 4) cache slots of one kv
+//    head, a warp to a row, since V is stored with 64 tokens of a dim side by
+//    side: lane l gathers the codes of its 4 dims over the run and writes them
+//    as one 16-byte (4-byte) piece each.
 #include "kvq8_device.cuh"
 #include "kvq8_internal.cuh"
 #include "kvq8_ptx.cuh"
@@ -22,88 +33,440 @@ namespace kvq8 {
 namespace {
 
 constexpr int kTaskWarps = 4;             // warps per CTA, one task each
-constexpr int kRunTok = 16;               // tokens per key/value task
-constexpr int kGroupTok = 4;              // tokens of it loaded at once
-constexpr int kQUnroll = 4;               // query heads of a task loaded at once
-constexpr int kQueryTasks = 152 * 32;     // query tasks that fill the GPU
+constexpr int kMinCtas = 5;               // CTAs per SM
+constexpr int kFullTasks = 152 * 32;      // tasks that fill the GPU
+constexpr int kMostGroups = 6;            // groups of four heads per turn task
+constexpr int kLongRuns = kFullTasks / 2; // value tasks of 16 slots from which on they are used
 
-// A row x is held two ways.  Turned rows (queries, keys): lane l holds dims
-// 2l, 2l + 1 (x, y) and 64 + 2l, 65 + 2l (z, w), so that both kinds of pairs,
-// (i, i + 64) and (2i, 2i + 1), lie within a lane and turning needs no
-// exchange.  Value rows: dims 4l..4l+3, as the append holds them.
-__device__ __forceinline__ float2 load2(const float *p) { return __ldcs(reinterpret_cast<const float2 *>(p)); }
-__device__ __forceinline__ float2 load2(const __half *p) {
-    const uint32_t v = __ldcs(reinterpret_cast<const unsigned int *>(p));
+// ------------------------------------------------------------- conversion --
+__device__ __forceinline__ float2 pair_of(uint32_t v, __half) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
-    const uint32_t v = __ldcs(reinterpret_cast<const unsigned int *>(p));   // a bf16 is the high half of an fp32
+__device__ __forceinline__ float2 pair_of(uint32_t v, __nv_bfloat16) {   // a bf16 is the high half of an fp32
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+template <typename T>
+__device__ __forceinline__ float2 load2(const T *p) { return pair_of(*reinterpret_cast<const uint32_t *>(p), T()); }
 __device__ __forceinline__ float4 load4(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ float4 load4(const __half *p) {
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
     const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+    const float2 a = pair_of(v.x, T()), b = pair_of(v.y, T());
     return make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+// Eight consecutive values.
+__device__ __forceinline__ void load8(const float *p, float *x) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 template <typename T>
-__device__ __forceinline__ float4 load_turned(const T *row, int lane) {
-    const float2 lo = load2(row + 2 * lane), hi = load2(row + kHD / 2 + 2 * lane);
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-// The weights of a lane's dims (1 without a norm).
-__device__ __forceinline__ float4 load_weight(const float *w, int lane) {
-    if (!w) return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    const float2 lo = reinterpret_cast<const float2 *>(w)[lane], hi = reinterpret_cast<const float2 *>(w + kHD / 2)[lane];
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-// Cosine and sine of a lane's two pairs from a table row [cos 64 | sin 64]:
-// (c.x, s.x) turns the first pair, (c.y, s.y) the second.
-struct Turn {
-    float2 c, s;
-};
-template <bool kPairs>
-__device__ __forceinline__ Turn load_turn(const float *row, int lane) {
-    if (kPairs) return {make_float2(row[lane], row[32 + lane]), make_float2(row[64 + lane], row[96 + lane])};
-    return {reinterpret_cast<const float2 *>(row)[lane], reinterpret_cast<const float2 *>(row + kHD / 2)[lane]};
-}
-template <bool kPairs>
-__device__ __forceinline__ float4 turned(float4 u, const Turn &t) {
-    if (kPairs)
-        return make_float4(u.x * t.c.x - u.y * t.s.x, u.y * t.c.x + u.x * t.s.x,
-                           u.z * t.c.y - u.w * t.s.y, u.w * t.c.y + u.z * t.s.y);
-    return make_float4(u.x * t.c.x - u.z * t.s.x, u.y * t.c.y - u.w * t.s.y,
-                       u.z * t.c.x + u.x * t.s.x, u.w * t.c.y + u.y * t.s.y);
-}
-
-__device__ __forceinline__ float4 scaled(float4 x, float f) {
-    return make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-}
-__device__ __forceinline__ float sum_squares(float4 x) {
-    return warp_sum(fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w))));
-}
-
-// x * r * w for the row's r = 1 / sqrt(mean(x^2) + eps).  Squares that
-// overflow (|x| above about 2^60) are taken of x * 2^-64 instead.
-__device__ __forceinline__ float4 normed(float4 x, float4 w, float eps) {
-    float f = 1.0f;
-    float ss = sum_squares(x);
-    if (ss > 0x1p120f) {   // warp-uniform
-        f = 0x1p-64f;
-        x = scaled(x, f);
-        ss = sum_squares(x);
+__device__ __forceinline__ void load8(const T *p, float *x) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = pair_of(w[i], T());
+        x[2 * i] = a.x;
+        x[2 * i + 1] = a.y;
     }
-    x = scaled(x, rsqrtf(fmaf(ss, 1.0f / kHD, eps * f * f)));
-    return make_float4(x.x * w.x, x.y * w.y, x.z * w.z, x.w * w.w);
 }
 
-// Largest |x| of a row held as four values per lane; a row with a NaN or an
+// ------------------------------------------------------------- turn tasks --
+// Eight lanes to a row: lane j (of 8) holds dims 8j..8j+7 in x[0..7] and
+// 64+8j..64+8j+7 in x[8..15], so that both kinds of pairs lie within a lane.
+template <typename T>
+__device__ __forceinline__ void load_row(const T *row, int j, float (&x)[16]) {
+    load8(row + 8 * j, x);
+    load8(row + kHD / 2 + 8 * j, x + 8);
+}
+// Cosines and sines of the lane's eight pairs from a table row [cos 64 | sin
+// 64]: pairs (x[e], x[8+e]), or (x[2e], x[2e+1]) for e < 8.
+template <bool kPairs>
+__device__ __forceinline__ void load_turn(const float *row, int j, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int at = kPairs ? 32 * half + 4 * j : 8 * j + 4 * half;
+        const float4 a = *reinterpret_cast<const float4 *>(row + at);
+        const float4 b = *reinterpret_cast<const float4 *>(row + kHD / 2 + at);
+        c[4 * half] = a.x; c[4 * half + 1] = a.y; c[4 * half + 2] = a.z; c[4 * half + 3] = a.w;
+        s[4 * half] = b.x; s[4 * half + 1] = b.y; s[4 * half + 2] = b.z; s[4 * half + 3] = b.w;
+    }
+}
+template <bool kPairs>
+__device__ __forceinline__ void turn(float (&u)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float &a = u[kPairs ? 2 * e : e], &b = u[kPairs ? 2 * e + 1 : 8 + e];
+        const float ya = fmaf(a, c[e], -(b * s[e])), yb = fmaf(b, c[e], a * s[e]);
+        a = ya;
+        b = yb;
+    }
+}
+__device__ __forceinline__ void weighted(float (&x)[16], const float *w, int j) {
+#pragma unroll
+    for (int half = 0; half < 4; ++half) {
+        const float4 v = *reinterpret_cast<const float4 *>(w + (half / 2) * (kHD / 2) + 8 * j + 4 * (half % 2));
+        x[4 * half] *= v.x;
+        x[4 * half + 1] *= v.y;
+        x[4 * half + 2] *= v.z;
+        x[4 * half + 3] *= v.w;
+    }
+}
+// Over the eight lanes of a row.
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float row_squares(const float (&x)[16]) {
+    float a = x[0] * x[0], b = x[1] * x[1];
+#pragma unroll
+    for (int e = 2; e < 16; e += 2) {
+        a = fmaf(x[e], x[e], a);
+        b = fmaf(x[e + 1], x[e + 1], b);
+    }
+    return row_sum(a + b);
+}
+constexpr float kMostSquares = 0x1p120f;
+
+// Where a token's keys go: the tile of kv head 0 and the slot; tile < 0: nowhere.
+struct KeyPlace {
+    int64_t tile;
+    int slot;
+};
+__device__ __forceinline__ KeyPlace key_place(const NormRopeParams &p, int b, int64_t at, int lane) {
+    KeyPlace k = {-1, 0};
+    if (at < 0 || at >= (int64_t)p.max_blocks * kBS) {
+        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+        return k;
+    }
+    const int phys = p.block_table[(size_t)b * p.max_blocks + at / kBS];
+    if (phys < 0 || phys >= p.num_blocks) {
+        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
+        return k;
+    }
+    k.tile = (int64_t)phys * p.nkv;
+    k.slot = (int)(at % kBS);
+    return k;
+}
+
+// round_half_even(127 z / top) for |z| <= top without a division: the nearest
+// integer by fp32, which is at most one off, moved by the exact remainder.
+__device__ __forceinline__ uint32_t exact_code(double z, double top, float inv) {
+    const double v = 127.0 * z;
+    int k = __float2int_rn((float)v * inv);
+    const double d = fma(-(double)k, top, v), half = 0.5 * top;
+    if (d > half || (d == half && (k & 1))) ++k;
+    else if (d < -half || (d == -half && (k & 1))) --k;
+    return (uint32_t)k;
+}
+
+// A key row of kv head h by the whole warp in 64 bits (x * w is exact there),
+// lane l holding dims 2l, 2l + 1, 64 + 2l, 65 + 2l.  sc: the row's scale, or
+// negative: the scale is found here too, for rows that fp32 cannot hold
+// (squares or products beyond its range, a NaN or an infinity: stored as zeros
+// and flagged).
+template <typename T, bool kPairs>
+__device__ __noinline__ void exact_key_row(const NormRopeParams &p, int64_t row, int64_t pos, int h, KeyPlace at,
+                                           float sc, int lane) {
+    const T *src = reinterpret_cast<const T *>(p.k) + row * p.k_stride + (size_t)h * kHD;
+    const float2 x0 = load2(src + 2 * lane), x1 = load2(src + kHD / 2 + 2 * lane);
+    const double x[4] = {x0.x, x0.y, x1.x, x1.y};
+    double u[4] = {x[0], x[1], x[2], x[3]};
+    if (p.k_weight) {
+        const float2 w0 = load2(p.k_weight + 2 * lane), w1 = load2(p.k_weight + kHD / 2 + 2 * lane);
+        u[0] *= w0.x;
+        u[1] *= w0.y;
+        u[2] *= w1.x;
+        u[3] *= w1.y;
+    }
+    const float *t = p.rope + (size_t)pos * kHD;
+    double z[4];
+    if (kPairs) {
+        const double c0 = t[lane], c1 = t[32 + lane], s0 = t[64 + lane], s1 = t[96 + lane];
+        z[0] = u[0] * c0 - u[1] * s0;
+        z[1] = u[1] * c0 + u[0] * s0;
+        z[2] = u[2] * c1 - u[3] * s1;
+        z[3] = u[3] * c1 + u[2] * s1;
+    } else {
+        const float2 c = load2(t + 2 * lane), s = load2(t + kHD / 2 + 2 * lane);
+        z[0] = u[0] * c.x - u[2] * s.x;
+        z[1] = u[1] * c.y - u[3] * s.y;
+        z[2] = u[2] * c.x + u[0] * s.x;
+        z[3] = u[3] * c.y + u[1] * s.y;
+    }
+    double top = fmax(fmax(fabs(z[0]), fabs(z[1])), fmax(fabs(z[2]), fabs(z[3])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (sc < 0.0f) {   // warp-uniform
+        double r = 1.0;
+        if (p.k_weight) {
+            double ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            r = 1.0 / sqrt(ss / kHD + (double)p.eps);
+        }
+        sc = __fmul_rn((float)(top * r), KVQ8_INV127);
+    }
+    // a NaN or an infinity among the inputs, or a value beyond fp32
+    bool bad = !(sc < INFINITY);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= !isfinite(z[k]);
+    if (__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_NONFINITE);
+        sc = 0.0f;
+    }
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    if (sc > 0.0f) {
+        // z and top brought near 1 by a power of two (top's exponent), which fp32 needs for its candidate
+        const double f = __hiloint2double((2046 << 20) - (__double2hiint(top) & 0x7ff00000), 0);
+        const float inv = 1.0f / (float)(top * f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = exact_code(z[k] * f, top * f, inv);
+    }
+    const size_t place = (size_t)(at.tile + h) * kBS + at.slot;
+    unsigned char *dst = reinterpret_cast<unsigned char *>(p.k_pool) + place * kHD;
+    const int chunk = lane >> 3, byte = 2 * (lane & 7);
+    *reinterpret_cast<uint16_t *>(dst + ((chunk ^ (at.slot & 7)) << 4) + byte) = (uint16_t)__byte_perm(c[0], c[1], 0x0040);
+    *reinterpret_cast<uint16_t *>(dst + (((4 + chunk) ^ (at.slot & 7)) << 4) + byte) =
+        (uint16_t)__byte_perm(c[2], c[3], 0x0040);
+    if (lane == 0) {
+        p.k_scale[place] = sc;
+        if (p.weight_sum) p.weight_sum[place] = 0.0f;
+    }
+}
+
+// Stores the codes t[16] (low bytes) and the scale of a lane's part of a key row.
+__device__ __forceinline__ void store_codes(const NormRopeParams &p, const uint32_t (&t)[16], float sc, int h,
+                                            KeyPlace at, int j) {
+    const size_t place = (size_t)(at.tile + h) * kBS + at.slot;
+    unsigned char *dst = reinterpret_cast<unsigned char *>(p.k_pool) + place * kHD + 8 * (j & 1);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t lo = low_bytes4(make_uint4(t[8 * half], t[8 * half + 1], t[8 * half + 2], t[8 * half + 3]));
+        const uint32_t hi = low_bytes4(make_uint4(t[8 * half + 4], t[8 * half + 5], t[8 * half + 6], t[8 * half + 7]));
+        *reinterpret_cast<uint2 *>(dst + (((4 * half + (j >> 1)) ^ (at.slot & 7)) << 4)) = make_uint2(lo, hi);
+    }
+    if (j == 0) {
+        p.k_scale[place] = sc;
+        if (p.weight_sum) p.weight_sum[place] = 0.0f;
+    }
+}
+
+// a + b = sum + err exactly.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+    const float t = __fadd_rn(a, b), v = __fsub_rn(t, a);
+    return make_float2(t, __fadd_rn(__fsub_rn(a, __fsub_rn(t, v)), __fsub_rn(b, v)));
+}
+
+// Key rows with a value next to a border, again with every value held as a
+// pair of fp32 (hi + lo, products split by fma): z within 12 * 2^-48 of the
+// row's maximum, which decides all but values within 2^-36 of a border.  mask:
+// the lanes that found such a value; their rows (eight lanes each) are stored.
+// Returns the lanes that find a value within 2^-34 of a border (or a NaN):
+// those rows are left to exact_key_row.  (64-bit arithmetic has a hundredth of
+// the rate: with it here a call of 64 tokens takes 8.6 us, not 5.)
+template <typename T, bool kPairs>
+__device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t row, int64_t pos, int h0, KeyPlace at,
+                                               float sc, unsigned mask, int lane) {
+    const int j = lane & 7, h = min(h0 + (lane >> 3), p.nkv - 1);
+    float x[16], w[16], c[8], s[8], zl[16];
+    load_row(reinterpret_cast<const T *>(p.k) + row * p.k_stride + (size_t)h * kHD, j, x);
+    load_turn<kPairs>(p.rope + (size_t)pos * kHD, j, c, s);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 1.0f;
+    if (p.k_weight) load_row(p.k_weight, j, w);
+    float mh = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int ia = kPairs ? 2 * e : e, ib = kPairs ? 2 * e + 1 : 8 + e;
+        const float ah = __fmul_rn(x[ia], w[ia]), al = __fmaf_rn(x[ia], w[ia], -ah);
+        const float bh = __fmul_rn(x[ib], w[ib]), bl = __fmaf_rn(x[ib], w[ib], -bh);
+        // (fh + fl) * g as a pair
+        auto prod = [](float fh, float fl, float g) {
+            const float h2 = __fmul_rn(fh, g);
+            return make_float2(h2, __fmaf_rn(fl, g, __fmaf_rn(fh, g, -h2)));
+        };
+        auto add = [](float2 a, float2 b) {
+            const float2 t = two_sum(a.x, b.x);
+            return two_sum(t.x, __fadd_rn(t.y, __fadd_rn(a.y, b.y)));
+        };
+        const float2 za = add(prod(ah, al, c[e]), prod(-bh, -bl, s[e]));
+        const float2 zb = add(prod(bh, bl, c[e]), prod(ah, al, s[e]));
+        x[ia] = za.x;
+        zl[ia] = za.y;
+        x[ib] = zb.x;
+        zl[ib] = zb.y;
+        mh = fmaxf(mh, fmaxf(fabsf(za.x), fabsf(zb.x)));
+    }
+    mh = row_max(mh);
+    float ml = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (fabsf(x[e]) == mh) ml = fmaxf(ml, x[e] < 0.0f ? -zl[e] : zl[e]);
+    ml = row_max(ml);
+    const float inv = __fdividef(127.0f, mh);
+    bool open = false;
+    uint32_t t[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        // k = the nearest integer or next to it; d = 127 z - k m as a pair
+        float k = rintf(__fmul_rn(x[e], inv));
+        const float p1 = __fmul_rn(127.0f, x[e]), e1 = __fmaf_rn(127.0f, x[e], -p1);
+        const float p2 = __fmul_rn(k, mh), e2 = __fmaf_rn(k, mh, -p2);
+        const float2 d = two_sum(p1, -p2);
+        const float dl = __fadd_rn(__fadd_rn(d.y, __fsub_rn(e1, e2)), __fsub_rn(__fmul_rn(127.0f, zl[e]), __fmul_rn(k, ml)));
+        // its distances above m/2 and above -m/2
+        const float up = __fadd_rn(__fsub_rn(d.x, 0.5f * mh), __fsub_rn(dl, 0.5f * ml));
+        const float dn = __fadd_rn(__fadd_rn(d.x, 0.5f * mh), __fadd_rn(dl, 0.5f * ml));
+        if (up > 0.0f) k += 1.0f;
+        else if (dn < 0.0f) k -= 1.0f;
+        open |= !(fminf(fabsf(up), fabsf(dn)) >= 0x1p-34f * mh);
+        t[e] = (uint32_t)__float2int_rn(k);
+    }
+    const bool mine = (mask >> (lane & 24)) & 0xffu;
+    const unsigned rest = __ballot_sync(0xffffffffu, open && mine);
+    if (mine && !((rest >> (lane & 24)) & 0xffu)) store_codes(p, t, sc, h, at, j);
+    return rest;
+}
+
+// Keys of kv heads h0 .. h0 + 3 (below nkv) of a token; x: the rows, one per
+// eight lanes.
+//
+// Codes in fp32: z = turned x * w (r left out).  In units of eps = 2^-24 and Z
+// = max|z*| of the exact values: x * w carries one rounding, the turn one of a
+// product and one of the sum, and |u_a c| + |u_b s| <= |(u_a, u_b)| |(c, s)|
+// <= sqrt(2) Z, so that z is within (2 sqrt(2) + 1) eps Z of z*, and so is m =
+// max|z| of Z; 127 * rcp(m) adds 3 eps.  127 z / m is then within 127 * 10.7
+// eps < 2^-13.5 of 127 z* / Z, and where its distance to the rounded value is
+// at most 1/2 - 2^-13 that value is the code (t = fl(z * inv + 1.5 * 2^23)
+// holds it in its low mantissa bits, as in kv_code_bytes4).  Rows with another
+// (2^-12 of values, one in 3 % of rows) go to near_key_rows; rows out of the
+// range in which these errors are relative ones to exact_key_row.
+template <typename T, bool kPairs>
+__device__ __forceinline__ void store_keys(const NormRopeParams &p, float (&x)[16], const float (&c)[8],
+                                           const float (&s)[8], int64_t row, int64_t pos, int h0, KeyPlace at,
+                                           int lane) {
+    constexpr float kShift = 0x1.8p23f;
+    constexpr float kLim = 0.5f - 0x1p-13f;
+    const int j = lane & 7, h = h0 + (lane >> 3);
+    const float ss = row_squares(x);
+    if (p.k_weight) weighted(x, p.k_weight, j);
+    turn<kPairs>(x, c, s);
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+    m = row_max(m);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(m));
+    inv *= 127.0f;
+    const float r = p.k_weight ? rsqrtf(fmaf(ss, 1.0f / kHD, p.eps)) : 1.0f;
+    const float sc = __fmul_rn(m * r, KVQ8_INV127);
+    const bool wide = !(m >= 0x1p-60f && m <= 0x1p60f && ss < kMostSquares && sc >= 0x1p-100f);   // the whole row
+    bool odd = wide;
+    uint32_t t[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float f = __fmaf_rn(x[e], inv, kShift);
+        odd |= !(fabsf(__fmaf_rn(x[e], inv, -__fsub_rn(f, kShift))) <= kLim);
+        t[e] = __float_as_uint(f);
+    }
+    const bool live = h < p.nkv;
+    const unsigned who = __ballot_sync(0xffffffffu, odd && live);
+    if (live && !((who >> (lane & 24)) & 0xffu)) store_codes(p, t, sc, h, at, j);
+    if (who) {   // warp-uniform
+        const unsigned whole = __ballot_sync(0xffffffffu, wide && live);
+        unsigned left = whole;
+        if (who & ~whole) left |= near_key_rows<T, kPairs>(p, row, pos, h0, at, sc, who & ~whole, lane);
+        while (left) {
+            const int g = (__ffs(left) - 1) >> 3;
+            left &= ~(0xffu << (8 * g));
+            // (a negative scale asks for it to be found too)
+            exact_key_row<T, kPairs>(p, row, pos, h0 + g, at, __shfl_sync(0xffffffffu, wide ? -1.0f : sc, 8 * g), lane);
+        }
+    }
+}
+
+// Queries of heads h0 .. h0 + 3 (below nqh) of a token.  Squares that overflow
+// (|x| above about 2^60) are taken of x * 2^-64.
+template <bool kPairs>
+__device__ __forceinline__ void store_queries(const NormRopeParams &p, float (&x)[16], const float (&c)[8],
+                                              const float (&s)[8], int64_t row, int h0, int lane) {
+    const int j = lane & 7, h = h0 + (lane >> 3);
+    if (p.q_weight) {
+        float ss = row_squares(x), f = 1.0f;
+        if (__any_sync(0xffffffffu, ss > kMostSquares)) {
+            if (ss > kMostSquares) {
+                f = 0x1p-64f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] *= f;
+            }
+            ss = row_squares(x);
+        }
+        const float r = rsqrtf(fmaf(ss, 1.0f / kHD, p.eps * f * f));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= r;
+        weighted(x, p.q_weight, j);
+    }
+    turn<kPairs>(x, c, s);
+    if (h < p.nqh) {
+        float *d = p.q_out + (row * p.nqh + h) * kHD + 8 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(d + (i / 2) * (kHD / 2) + 4 * (i % 2)) =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    }
+}
+
+// Turn task w = row * parts + c: groups [c * gp, (c + 1) * gp) of four heads
+// of a token, the query heads' groups before the kv heads'.
+template <typename T, bool kPairs>
+__device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int parts, int gp, int lane) {
+    const int row = w / parts;
+    const int b = row / p.n_new, i = row - b * p.n_new;
+    if (p.n_tokens && i >= p.n_tokens[b]) return;   // padding
+    const int64_t at = (int64_t)p.start_pos[b] + i;
+    const int64_t pos = p.positions ? p.positions[row] : at;
+    const int j = lane & 7, g = lane >> 3;
+    const int qg = (p.nqh + 3) / 4, groups = qg + (p.nkv + 3) / 4;
+    const int g0 = (w - row * parts) * gp, g1 = min(groups, g0 + gp);
+    // a lane whose head is beyond the last loads the last
+    auto fetch = [&](int gi, float (&x)[16]) {
+        const bool is_q = gi < qg;
+        const int h = min((is_q ? gi : gi - qg) * 4 + g, (is_q ? p.nqh : p.nkv) - 1);
+        load_row(reinterpret_cast<const T *>(is_q ? p.q : p.k) + (int64_t)row * (is_q ? p.q_stride : p.k_stride) +
+                     (size_t)h * kHD, j, x);
+    };
+    float x[16];
+    fetch(g0, x);
+    if (pos < 0 || pos >= p.n_pos) {
+        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+        return;
+    }
+    float c[8], s[8];
+    load_turn<kPairs>(p.rope + (size_t)pos * kHD, j, c, s);
+    KeyPlace place = {-1, 0};
+    if (g1 > qg) place = key_place(p, b, at, lane);
+#pragma unroll 1
+    for (int gi = g0; gi < g1; ++gi) {
+        float nx[16];
+        if (gi + 1 < g1) fetch(gi + 1, nx);
+        if (gi < qg) store_queries<kPairs>(p, x, c, s, row, 4 * gi, lane);
+        else if (place.tile >= 0) store_keys<T, kPairs>(p, x, c, s, row, pos, 4 * (gi - qg), place, lane);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = nx[e];
+    }
+}
+
+// ------------------------------------------------------------ value tasks --
+// Largest |x| of a row held as a float4 per lane; a row with a NaN or an
 // infinity is cleared and flagged, and its maximum is 0.
 __device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
     const uint32_t a = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
@@ -117,247 +480,110 @@ __device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
     return __uint_as_float(m);
 }
 
-// The codes of a key row from its inputs in 64 bits, for the values of `mask`
-// (bit k: the lane's value k); x * w is exact there.
-template <bool kPairs>
-__device__ __noinline__ uint4 exact_codes(float4 x, float4 w, Turn t, uint4 codes, int mask) {
-    const double ux = (double)x.x * w.x, uy = (double)x.y * w.y, uz = (double)x.z * w.z, uw = (double)x.w * w.w;
-    double z[4];
-    if (kPairs) {
-        z[0] = ux * t.c.x - uy * t.s.x;
-        z[1] = uy * t.c.x + ux * t.s.x;
-        z[2] = uz * t.c.y - uw * t.s.y;
-        z[3] = uw * t.c.y + uz * t.s.y;
-    } else {
-        z[0] = ux * t.c.x - uz * t.s.x;
-        z[1] = uy * t.c.y - uw * t.s.y;
-        z[2] = uz * t.c.x + ux * t.s.x;
-        z[3] = uw * t.c.y + uy * t.s.y;
-    }
-    double top = fmax(fmax(fabs(z[0]), fabs(z[1])), fmax(fabs(z[2]), fabs(z[3])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-    uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (mask >> k & 1) c[k] = (uint32_t)__double2int_rn(127.0 * z[k] / top);
-    return make_uint4(c[0], c[1], c[2], c[3]);
-}
-
-// Codes (low bytes) of a key row y = turned x * r * w with maximum m > 0 and
-// scale s: round_half_even(127 y* / max|y*|) of the exact values y*, whose
-// common factor r cancels.  In units of eps = 2^-24 and Z = max|y*|: u = x r w
-// carries two roundings (r's own cancels), the turn one of a product and one of
-// the sum, and |u_a c| + |u_b s| <= |(u_a, u_b)| |(c, s)| <= sqrt(2) Z, so that
-// y is within (3 sqrt(2) + 1) eps Z of y* and so is m of Z; 127 * rcp(m) adds 3
-// eps.  127 y / m is then within 127 * 13.5 eps < 2^-13.2 of 127 y* / Z, and
-// where its distance to the rounded value is at most 1/2 - 2^-13 that value is
-// the code (t = fl(y * inv + 1.5 * 2^23) holds it in its low mantissa bits, as
-// in kv_code_bytes4).  The others, 2^-12 of values and a value in 3 % of rows,
-// are decided in 64 bits, as are rows whose range leaves the products' errors
-// unbounded.
-template <bool kPairs>
-__device__ __forceinline__ uint4 key_codes(float4 y, float m, float s, float4 x, float4 w, const Turn &t) {
-    if (s == 0.0f) return make_uint4(0u, 0u, 0u, 0u);   // warp-uniform
-    constexpr float kShift = 0x1.8p23f;
-    constexpr float kLim = 0.5f - 0x1p-13f;
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(m));
-    inv *= 127.0f;
-    const float t0 = __fmaf_rn(y.x, inv, kShift), t1 = __fmaf_rn(y.y, inv, kShift);
-    const float t2 = __fmaf_rn(y.z, inv, kShift), t3 = __fmaf_rn(y.w, inv, kShift);
-    const float e0 = __fmaf_rn(y.x, inv, -__fsub_rn(t0, kShift)), e1 = __fmaf_rn(y.y, inv, -__fsub_rn(t1, kShift));
-    const float e2 = __fmaf_rn(y.z, inv, -__fsub_rn(t2, kShift)), e3 = __fmaf_rn(y.w, inv, -__fsub_rn(t3, kShift));
-    uint4 c = make_uint4(__float_as_uint(t0), __float_as_uint(t1), __float_as_uint(t2), __float_as_uint(t3));
-    const bool wide = !(m >= 0x1p-100f && m <= 0x1p120f);
-    const bool near = !((fabsf(e0) <= kLim) & (fabsf(e1) <= kLim) & (fabsf(e2) <= kLim) & (fabsf(e3) <= kLim));
-    if (__any_sync(0xffffffffu, wide | near)) {
-        const int mask = wide ? 15 : !(fabsf(e0) <= kLim) | !(fabsf(e1) <= kLim) << 1 | !(fabsf(e2) <= kLim) << 2 |
-                                         !(fabsf(e3) <= kLim) << 3;
-        c = exact_codes<kPairs>(x, w, t, c, mask);
-    }
-    return c;
-}
-
-// Writes a key row's codes, held as a turned row, to the row at dst of a slot.
-__device__ __forceinline__ void store_key_codes(unsigned char *dst, int slot, int lane, uint4 c) {
-    const int j = lane >> 3, at = 2 * (lane & 7);
-    *reinterpret_cast<uint16_t *>(dst + ((j ^ (slot & 7)) << 4) + at) = (uint16_t)__byte_perm(c.x, c.y, 0x0040);
-    *reinterpret_cast<uint16_t *>(dst + (((4 + j) ^ (slot & 7)) << 4) + at) = (uint16_t)__byte_perm(c.z, c.w, 0x0040);
-}
-
-// New tokens of sequence b (the rest of its n_new rows is padding).
-__device__ __forceinline__ int token_count(const NormRopeParams &p, int b) {
-    return p.n_tokens ? min(p.n_new, p.n_tokens[b]) : p.n_new;
-}
-
-// Key/value task w = (b * runs + x) * nkv + h: the new tokens of sequence b in
-// run x of 16 cache slots, counted from the run of the first, of kv head h.
-template <typename T, bool kPairs>
-__device__ __forceinline__ void append_run(const NormRopeParams &p, int64_t w, int runs, int lane) {
-    const int h = (int)(w % p.nkv);
-    w /= p.nkv;
-    const int b = (int)(w / runs);
+// Value task w = (b * runs + x) * nkv + h: the new tokens of sequence b in run
+// x of kRun cache slots, counted from the run of the first, of kv head h.
+// Places outside the table or the pool are flagged by the turn tasks.
+template <typename T, int kRun>
+__device__ __forceinline__ void append_values(const NormRopeParams &p, int w, int runs, int lane) {
+    const int bx = w / p.nkv, h = w - bx * p.nkv;
+    const int b = bx / runs;
     const int64_t cap = (int64_t)p.max_blocks * kBS;
     const int64_t start = p.start_pos[b];
-    const int nt = token_count(p, b);
-    // slots [r0, r0 + 16), of which tokens with positions in [lo, hi) are written
-    const int64_t r0 = (start >= 0 ? start / kRunTok : -((-start + kRunTok - 1) / kRunTok)) * kRunTok +
-                       (w % runs) * kRunTok;
-    int64_t lo = max(start, r0), hi = min(start + nt, r0 + kRunTok);
+    const int nt = p.n_tokens ? min(p.n_new, p.n_tokens[b]) : p.n_new;   // the rest is padding
+    // slots [r0, r0 + kRun), of which tokens with positions in [lo, hi) are written
+    const int64_t r0 = (start >= 0 ? start / kRun : -((-start + kRun - 1) / kRun)) * kRun +
+                       (int64_t)(bx - b * runs) * kRun;
+    const int64_t lo = max(max(start, r0), (int64_t)0), hi = min(min(start + nt, r0 + kRun), cap);
     if (lo >= hi) return;
-    if (lo < 0 || hi > cap) {
-        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-        lo = max(lo, (int64_t)0);
-        hi = min(hi, cap);
-        if (lo >= hi) return;
-    }
     const int phys = p.block_table[(size_t)b * p.max_blocks + r0 / kBS];
-    // lane r: the rotation position of the token in slot r0 + r
+    // lane r: whether the token in slot r0 + r is appended
     const int64_t row0 = (int64_t)b * p.n_new + (r0 - start);   // row of the token in slot r0 (may precede the tensor)
-    const bool mine = lane < kRunTok && r0 + lane >= lo && r0 + lane < hi;
-    int64_t pos = 0;
-    if (mine) pos = p.positions ? p.positions[row0 + lane] : r0 + lane;
-    const bool good = mine && pos >= 0 && pos < p.n_pos;
-    if (mine && !good) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-    if (phys < 0 || phys >= p.num_blocks) {
-        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
-        return;
+    bool good = lane < kRun && r0 + lane >= lo && r0 + lane < hi;
+    if (good) {
+        const int64_t pos = p.positions ? p.positions[row0 + lane] : r0 + lane;
+        good = pos >= 0 && pos < p.n_pos;
     }
+    if (phys < 0 || phys >= p.num_blocks) return;
     const unsigned todo = __ballot_sync(0xffffffffu, good);
     const size_t tile = (size_t)phys * p.nkv + h;
     const int slot0 = (int)(r0 % kBS);
-    unsigned char *krow = reinterpret_cast<unsigned char *>(p.k_pool) + (tile * kBS + slot0) * kHD;
     int8_t *vrun = p.v_pool + tile * kHD * kBS + (size_t)(slot0 / kStageTok) * kTileVQuarter + slot0 % kStageTok;
-    const T *ksrc = reinterpret_cast<const T *>(p.k) + (size_t)h * kHD;
-    const T *vsrc = reinterpret_cast<const T *>(p.v) + (size_t)h * kHD + 4 * lane;
-    const float4 weight = load_weight(p.k_weight, lane);
-    const bool norm = p.k_weight != nullptr;
+    const T *src = reinterpret_cast<const T *>(p.v) + (size_t)h * kHD + 4 * lane;
 
-    if (todo == 0xffffu) {
-        // the whole run, four tokens at a time
-        uint32_t vw[4][kRunTok / 4];   // after group g, vw[i][3]: the codes of its tokens of dim 4 * lane + i
-        float sc_keep = 0.0f;          // lane r < 16: K scale of row r; lane 16 + r: V scale
-#pragma unroll 1
-        for (int g = 0; g < kRunTok / kGroupTok; ++g) {
-            float4 xk[kGroupTok], xv[kGroupTok];
-            Turn tn[kGroupTok];
+    if (todo == (1u << kRun) - 1) {
+        // the whole run, four tokens at a time, the next four being loaded
+        float4 v[4], nv[4];
 #pragma unroll
-            for (int u = 0; u < kGroupTok; ++u) {
-                const int r = kGroupTok * g + u;
-                xk[u] = load_turned(ksrc + (row0 + r) * p.k_stride, lane);
-                xv[u] = load4(vsrc + (row0 + r) * p.v_stride);
-                tn[u] = load_turn<kPairs>(p.rope + (size_t)__shfl_sync(0xffffffffu, (int)pos, r) * kHD, lane);
-            }
-            uint32_t wg[4];
+        for (int u = 0; u < 4; ++u) v[u] = load4(src + (row0 + u) * p.v_stride);
+        uint32_t vw[4][kRun / 4] = {};   // codes so far of dim 4 * lane + i, the last four tokens on top
+        float sc_keep = 0.0f;            // lane r: scale of row r
 #pragma unroll
-            for (int u = 0; u < kGroupTok; ++u) {
-                const int r = kGroupTok * g + u;
-                float4 y = turned<kPairs>(norm ? normed(xk[u], weight, p.eps) : xk[u], tn[u]);
-                const float mk = row_max_checked(y, p.dev_status), sk = __fmul_rn(mk, KVQ8_INV127);
-                store_key_codes(krow + r * kHD, r, lane, key_codes<kPairs>(y, mk, sk, xk[u], weight, tn[u]));
-                const float sv = __fmul_rn(row_max_checked(xv[u], p.dev_status), KVQ8_INV127);
-                const uint4 cv = kv_code_bytes4(xv[u], sv);
-                if (lane == r) sc_keep = sk;
-                if (lane == 16 + r) sc_keep = sv;
-                constexpr uint32_t kIns[4] = {0x3210, 0x3240, 0x3410, 0x4210};
-                if (u == 0) {
-                    wg[0] = cv.x; wg[1] = cv.y; wg[2] = cv.z; wg[3] = cv.w;
-                } else {
-                    wg[0] = __byte_perm(wg[0], cv.x, kIns[u]);
-                    wg[1] = __byte_perm(wg[1], cv.y, kIns[u]);
-                    wg[2] = __byte_perm(wg[2], cv.z, kIns[u]);
-                    wg[3] = __byte_perm(wg[3], cv.w, kIns[u]);
-                }
-            }
+        for (int g = 0; g < kRun / 4; ++g) {
+            if (g + 1 < kRun / 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                vw[i][0] = vw[i][1];
-                vw[i][1] = vw[i][2];
-                vw[i][2] = vw[i][3];
-                vw[i][3] = wg[i];
+                for (int u = 0; u < 4; ++u) nv[u] = load4(src + (row0 + 4 * g + 4 + u) * p.v_stride);
             }
+            uint4 cv[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float sc = __fmul_rn(row_max_checked(v[u], p.dev_status), KVQ8_INV127);
+                cv[u] = kv_code_bytes4(v[u], sc);
+                if (lane == 4 * g + u) sc_keep = sc;
+            }
+            vw[0][g] = low_bytes4(make_uint4(cv[0].x, cv[1].x, cv[2].x, cv[3].x));
+            vw[1][g] = low_bytes4(make_uint4(cv[0].y, cv[1].y, cv[2].y, cv[3].y));
+            vw[2][g] = low_bytes4(make_uint4(cv[0].z, cv[1].z, cv[2].z, cv[3].z));
+            vw[3][g] = low_bytes4(make_uint4(cv[0].w, cv[1].w, cv[2].w, cv[3].w));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = nv[u];
         }
-        (lane < 16 ? p.k_scale : p.v_scale)[tile * kBS + slot0 + (lane & 15)] = sc_keep;
-        if (p.weight_sum && lane < 16) p.weight_sum[tile * kBS + slot0 + lane] = 0.0f;
+        if (lane < kRun) p.v_scale[tile * kBS + slot0 + lane] = sc_keep;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(vrun + (size_t)(4 * lane + i) * kStageTok) =
-                make_uint4(vw[i][0], vw[i][1], vw[i][2], vw[i][3]);
+        for (int i = 0; i < 4; ++i) {
+            int8_t *d = vrun + (size_t)(4 * lane + i) * kStageTok;
+            if constexpr (kRun == 16)
+                *reinterpret_cast<uint4 *>(d) = make_uint4(vw[i][0], vw[i][1], vw[i][2], vw[i][3]);
+            else
+                *reinterpret_cast<uint32_t *>(d) = vw[i][0];
+        }
         return;
     }
     // part of a run: row by row
     for (unsigned left = todo; left; left &= left - 1) {
         const int r = __ffs(left) - 1;
-        const float4 xk = load_turned(ksrc + (row0 + r) * p.k_stride, lane);
-        float4 xv = load4(vsrc + (row0 + r) * p.v_stride);
-        const Turn tn = load_turn<kPairs>(p.rope + (size_t)__shfl_sync(0xffffffffu, (int)pos, r) * kHD, lane);
-        float4 y = turned<kPairs>(norm ? normed(xk, weight, p.eps) : xk, tn);
-        const float mk = row_max_checked(y, p.dev_status), sk = __fmul_rn(mk, KVQ8_INV127);
-        store_key_codes(krow + r * kHD, r, lane, key_codes<kPairs>(y, mk, sk, xk, weight, tn));
-        const float sv = __fmul_rn(row_max_checked(xv, p.dev_status), KVQ8_INV127);
-        const uint4 c = kv_code_bytes4(xv, sv);
+        float4 v = load4(src + (row0 + r) * p.v_stride);
+        const float sc = __fmul_rn(row_max_checked(v, p.dev_status), KVQ8_INV127);
+        const uint4 c = kv_code_bytes4(v, sc);
         vrun[(size_t)(4 * lane + 0) * kStageTok + r] = (int8_t)c.x;
         vrun[(size_t)(4 * lane + 1) * kStageTok + r] = (int8_t)c.y;
         vrun[(size_t)(4 * lane + 2) * kStageTok + r] = (int8_t)c.z;
         vrun[(size_t)(4 * lane + 3) * kStageTok + r] = (int8_t)c.w;
-        if (lane == 0) {
-            p.k_scale[tile * kBS + slot0 + r] = sk;
-            p.v_scale[tile * kBS + slot0 + r] = sv;
-            if (p.weight_sum) p.weight_sum[tile * kBS + slot0 + r] = 0.0f;
-        }
+        if (lane == 0) p.v_scale[tile * kBS + slot0 + r] = sc;
     }
 }
 
-// Query task w = row * parts + c: heads [c * hp, (c + 1) * hp) of a token.
-template <typename T, bool kPairs>
-__device__ __forceinline__ void turn_queries(const NormRopeParams &p, int64_t w, int hp, int lane) {
-    const int parts = (p.nqh + hp - 1) / hp;
-    const int64_t row = w / parts;
-    const int h0 = (int)(w % parts) * hp, h1 = min(p.nqh, h0 + hp);
-    const int b = (int)(row / p.n_new), i = (int)(row % p.n_new);
-    if (p.n_tokens && i >= p.n_tokens[b]) return;   // padding
-    const int64_t pos = p.positions ? p.positions[row] : (int64_t)p.start_pos[b] + i;
-    if (pos < 0 || pos >= p.n_pos) {
-        if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-        return;
-    }
-    const T *src = reinterpret_cast<const T *>(p.q) + row * p.q_stride;
-    float *dst = p.q_out + row * p.nqh * kHD;
-    const float4 weight = load_weight(p.q_weight, lane);
-    const bool norm = p.q_weight != nullptr;
-    const Turn tn = load_turn<kPairs>(p.rope + (size_t)pos * kHD, lane);
-    for (int h = h0; h < h1; h += kQUnroll) {
-        float4 x[kQUnroll];
-#pragma unroll
-        for (int u = 0; u < kQUnroll; ++u)
-            if (h + u < h1) x[u] = load_turned(src + (size_t)(h + u) * kHD, lane);
-#pragma unroll
-        for (int u = 0; u < kQUnroll; ++u) {
-            if (h + u < h1) {
-                const float4 y = turned<kPairs>(norm ? normed(x[u], weight, p.eps) : x[u], tn);
-                float *d = dst + (size_t)(h + u) * kHD + 2 * lane;
-                *reinterpret_cast<float2 *>(d) = make_float2(y.x, y.y);
-                *reinterpret_cast<float2 *>(d + kHD / 2) = make_float2(y.z, y.w);
-            }
-        }
-    }
-}
+// How the two kinds of tasks are laid out over the grid.
+struct TaskPlan {
+    int turn_tasks, parts, gp;    // groups of four heads per turn task, such parts per token
+    int value_tasks, runs;
+    uint32_t ratio;               // value CTAs per CTA, in 2^-32 (rounded up)
+};
 
-// One task per warp: first the key/value tasks, which are longer, then the
-// query tasks.
-template <typename T, bool kPairs>
-__global__ void __launch_bounds__(kTaskWarps * 32)
-norm_rope_append_kernel(NormRopeParams p, int runs, int hp) {
+template <typename T, bool kPairs, int kRun>
+__global__ void __launch_bounds__(kTaskWarps * 32, kMinCtas)
+norm_rope_append_kernel(NormRopeParams p, TaskPlan plan) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t task = (int64_t)blockIdx.x * kTaskWarps + (threadIdx.x >> 5);
-    const int64_t kv = (int64_t)p.batch * runs * p.nkv;
-    if (task < kv) {
-        append_run<T, kPairs>(p, task, runs, lane);
-    } else if (task - kv < (int64_t)p.batch * p.n_new * ((p.nqh + hp - 1) / hp)) {
-        turn_queries<T, kPairs>(p, task - kv, hp, lane);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // CTAs 0 .. i - 1 hold v0 = ceil-ratio * i value CTAs: CTA i is one when the next count is larger
+    const uint32_t i = blockIdx.x;
+    const uint32_t v0 = __umulhi(i, plan.ratio), v1 = __umulhi(i + 1, plan.ratio);
+    if (v1 > v0) {
+        const int64_t w = (int64_t)v0 * kTaskWarps + warp;
+        if (w < plan.value_tasks) append_values<T, kRun>(p, (int)w, plan.runs, lane);
+    } else {
+        const int64_t w = (int64_t)(i - v0) * kTaskWarps + warp;
+        if (w < plan.turn_tasks) turn_heads<T, kPairs>(p, (int)w, plan.parts, plan.gp, lane);
     }
 }
 
@@ -376,20 +602,25 @@ rope_table_kernel(const double *inv_freq, int64_t n, float *table) {
     table[t * kHD + kHD / 2 + f] = (float)s;
 }
 
-template <typename T, bool kPairs>
-cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
-    // runs of 16 slots that n_new consecutive positions touch, at most
-    const int runs = (int)(((int64_t)p.n_new + kRunTok - 2) / kRunTok + 1);
+template <typename T, bool kPairs, int kRun>
+cudaError_t launch_runs(const NormRopeParams &p, cudaStream_t s) {
+    TaskPlan plan;
+    // runs of kRun slots that n_new consecutive positions touch, at most
+    plan.runs = (int)(((int64_t)p.n_new + kRun - 2) / kRun + 1);
     const int64_t rows = (int64_t)p.batch * p.n_new;
-    // A query task takes one head while that leaves the GPU short of warps, and
-    // up to 8 (which then share one turn and weight) when there are many.
-    int hp = 1;
-    while (hp < 8 && rows * p.nqh >= (int64_t)hp * 2 * kQueryTasks) hp *= 2;
-    const int64_t tasks = (int64_t)p.batch * runs * p.nkv + rows * ((p.nqh + hp - 1) / hp);
-    const int64_t blocks = (tasks + kTaskWarps - 1) / kTaskWarps;
-    if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
+    // A turn task takes one group of four heads while that leaves the GPU short
+    // of warps, and several (which share one turn) when there are many.
+    const int groups = (p.nqh + 3) / 4 + (p.nkv + 3) / 4;
+    plan.gp = (int)max((int64_t)1, min((int64_t)kMostGroups, rows * groups / kFullTasks));
+    plan.parts = (groups + plan.gp - 1) / plan.gp;
+    const int64_t values = (int64_t)p.batch * plan.runs * p.nkv, turns = rows * plan.parts;
+    const int64_t vb = (values + kTaskWarps - 1) / kTaskWarps, tb = (turns + kTaskWarps - 1) / kTaskWarps;
+    if (values > 2147483647 || turns > 2147483647 || vb + tb > 2147483647) return cudaErrorInvalidConfiguration;
+    plan.value_tasks = (int)values;
+    plan.turn_tasks = (int)turns;
+    plan.ratio = (uint32_t)((((uint64_t)vb << 32) + (uint64_t)(vb + tb) - 1) / (uint64_t)(vb + tb));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(vb + tb));
     cfg.blockDim = dim3(kTaskWarps * 32);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = s;
@@ -398,7 +629,15 @@ cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, kPairs>, p, runs, hp);
+    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, kPairs, kRun>, p, plan);
+}
+
+// A value task takes 16 slots (its V pieces are then 16 bytes) when there are
+// enough of them, else 4 (a quarter of the latency).
+template <typename T, bool kPairs>
+cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
+    if ((int64_t)p.batch * p.nkv * ((p.n_new + 15) / 16) >= kLongRuns) return launch_runs<T, kPairs, 16>(p, s);
+    return launch_runs<T, kPairs, 4>(p, s);
 }
 
 template <typename T>
