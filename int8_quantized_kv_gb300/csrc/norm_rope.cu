@@ -48,6 +48,9 @@ __device__ __forceinline__ float2 pair_of(uint32_t v, __nv_bfloat16) {   // a bf
 __device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 template <typename T>
 __device__ __forceinline__ float2 load2(const T *p) { return pair_of(*reinterpret_cast<const uint32_t *>(p), T()); }
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const __half *p) { return __half2float(*p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float4 load4(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p) {
@@ -55,43 +58,42 @@ __device__ __forceinline__ float4 load4(const T *p) {
     const float2 a = pair_of(v.x, T()), b = pair_of(v.y, T());
     return make_float4(a.x, a.y, b.x, b.y);
 }
-// Eight consecutive values.
-__device__ __forceinline__ void load8(const float *p, float *x) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *x) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = pair_of(w[i], T());
-        x[2 * i] = a.x;
-        x[2 * i + 1] = a.y;
-    }
-}
-
 // ------------------------------------------------------------- turn tasks --
-// Eight lanes to a row: lane j (of 8) holds dims 8j..8j+7 in x[0..7] and
-// 64+8j..64+8j+7 in x[8..15], so that both kinds of pairs lie within a lane.
+// Eight lanes to a row: lane j (of 8) holds dims 32c + 4j + i in x[4c + i] (i <
+// 4, c < 4).  Both kinds of pairs lie within a lane, and the eight lanes read
+// or write a whole 128-byte (64-byte) line of the row at a time.  (With 8
+// consecutive values a lane, every access touches half a sector.)
 template <typename T>
 __device__ __forceinline__ void load_row(const T *row, int j, float (&x)[16]) {
-    load8(row + 8 * j, x);
-    load8(row + kHD / 2 + 8 * j, x + 8);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float4 v = load4(row + 32 * c + 4 * j);
+        x[4 * c] = v.x;
+        x[4 * c + 1] = v.y;
+        x[4 * c + 2] = v.z;
+        x[4 * c + 3] = v.w;
+    }
 }
 // Cosines and sines of the lane's eight pairs from a table row [cos 64 | sin
 // 64]: pairs (x[e], x[8+e]), or (x[2e], x[2e+1]) for e < 8.
 template <bool kPairs>
 __device__ __forceinline__ void load_turn(const float *row, int j, float (&c)[8], float (&s)[8]) {
+    if (kPairs) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int at = kPairs ? 32 * half + 4 * j : 8 * j + 4 * half;
-        const float4 a = *reinterpret_cast<const float4 *>(row + at);
-        const float4 b = *reinterpret_cast<const float4 *>(row + kHD / 2 + at);
-        c[4 * half] = a.x; c[4 * half + 1] = a.y; c[4 * half + 2] = a.z; c[4 * half + 3] = a.w;
-        s[4 * half] = b.x; s[4 * half + 1] = b.y; s[4 * half + 2] = b.z; s[4 * half + 3] = b.w;
+        for (int q = 0; q < 4; ++q) {
+            const float2 a = *reinterpret_cast<const float2 *>(row + 16 * q + 2 * j);
+            const float2 b = *reinterpret_cast<const float2 *>(row + kHD / 2 + 16 * q + 2 * j);
+            c[2 * q] = a.x; c[2 * q + 1] = a.y;
+            s[2 * q] = b.x; s[2 * q + 1] = b.y;
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + 32 * q + 4 * j);
+        const float4 b = *reinterpret_cast<const float4 *>(row + kHD / 2 + 32 * q + 4 * j);
+        c[4 * q] = a.x; c[4 * q + 1] = a.y; c[4 * q + 2] = a.z; c[4 * q + 3] = a.w;
+        s[4 * q] = b.x; s[4 * q + 1] = b.y; s[4 * q + 2] = b.z; s[4 * q + 3] = b.w;
     }
 }
 template <bool kPairs>
@@ -106,12 +108,12 @@ __device__ __forceinline__ void turn(float (&u)[16], const float (&c)[8], const 
 }
 __device__ __forceinline__ void weighted(float (&x)[16], const float *w, int j) {
 #pragma unroll
-    for (int half = 0; half < 4; ++half) {
-        const float4 v = *reinterpret_cast<const float4 *>(w + (half / 2) * (kHD / 2) + 8 * j + 4 * (half % 2));
-        x[4 * half] *= v.x;
-        x[4 * half + 1] *= v.y;
-        x[4 * half + 2] *= v.z;
-        x[4 * half + 3] *= v.w;
+    for (int c = 0; c < 4; ++c) {
+        const float4 v = *reinterpret_cast<const float4 *>(w + 32 * c + 4 * j);
+        x[4 * c] *= v.x;
+        x[4 * c + 1] *= v.y;
+        x[4 * c + 2] *= v.z;
+        x[4 * c + 3] *= v.w;
     }
 }
 // Over the eight lanes of a row.
@@ -247,13 +249,11 @@ __device__ __noinline__ void exact_key_row(const NormRopeParams &p, int64_t row,
 __device__ __forceinline__ void store_codes(const NormRopeParams &p, const uint32_t (&t)[16], float sc, int h,
                                             KeyPlace at, int j) {
     const size_t place = (size_t)(at.tile + h) * kBS + at.slot;
-    unsigned char *dst = reinterpret_cast<unsigned char *>(p.k_pool) + place * kHD + 8 * (j & 1);
+    unsigned char *dst = reinterpret_cast<unsigned char *>(p.k_pool) + place * kHD + 4 * (j & 3);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint32_t lo = low_bytes4(make_uint4(t[8 * half], t[8 * half + 1], t[8 * half + 2], t[8 * half + 3]));
-        const uint32_t hi = low_bytes4(make_uint4(t[8 * half + 4], t[8 * half + 5], t[8 * half + 6], t[8 * half + 7]));
-        *reinterpret_cast<uint2 *>(dst + (((4 * half + (j >> 1)) ^ (at.slot & 7)) << 4)) = make_uint2(lo, hi);
-    }
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint32_t *>(dst + (((2 * c + (j >> 2)) ^ (at.slot & 7)) << 4)) =
+            low_bytes4(make_uint4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]));
     if (j == 0) {
         p.k_scale[place] = sc;
         if (p.weight_sum) p.weight_sum[place] = 0.0f;
@@ -266,13 +266,78 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
     return make_float2(t, __fadd_rn(__fsub_rn(a, __fsub_rn(t, v)), __fsub_rn(b, v)));
 }
 
-// Key rows with a value next to a border, again with every value held as a
-// pair of fp32 (hi + lo, products split by fma): z within 12 * 2^-48 of the
-// row's maximum, which decides all but values within 2^-36 of a border.  mask:
-// the lanes that found such a value; their rows (eight lanes each) are stored.
-// Returns the lanes that find a value within 2^-34 of a border (or a NaN):
-// those rows are left to exact_key_row.  (64-bit arithmetic has a hundredth of
-// the rate: with it here a call of 64 tokens takes 8.6 us, not 5.)
+// (h + l) * g, and a + b, as pairs hi + lo of fp32.
+__device__ __forceinline__ float2 pair_times(float h, float l, float g) {
+    const float t = __fmul_rn(h, g);
+    return make_float2(t, __fmaf_rn(l, g, __fmaf_rn(h, g, -t)));
+}
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+    const float2 t = two_sum(a.x, b.x);
+    return two_sum(t.x, __fadd_rn(t.y, __fadd_rn(a.y, b.y)));
+}
+
+// round_half_even(127 z / m) of pairs z = zh + zl and m = mh + ml >= |z|, inv
+// near 127 / m; `open` is set where 127 z / m is within 2^-34 of a border.
+// With z and m within 12 * 2^-48 m of the exact values the others are theirs.
+__device__ __forceinline__ uint32_t pair_code(float zh, float zl, float mh, float ml, float inv, bool &open) {
+    // k = the nearest integer or next to it; d = 127 z - k m
+    float k = rintf(__fmul_rn(zh, inv));
+    const float p1 = __fmul_rn(127.0f, zh), e1 = __fmaf_rn(127.0f, zh, -p1);
+    const float p2 = __fmul_rn(k, mh), e2 = __fmaf_rn(k, mh, -p2);
+    const float2 d = two_sum(p1, -p2);
+    const float dl = __fadd_rn(__fadd_rn(d.y, __fsub_rn(e1, e2)), __fsub_rn(__fmul_rn(127.0f, zl), __fmul_rn(k, ml)));
+    // its distances above m/2 and above -m/2
+    const float up = __fadd_rn(__fsub_rn(d.x, 0.5f * mh), __fsub_rn(dl, 0.5f * ml));
+    const float dn = __fadd_rn(__fadd_rn(d.x, 0.5f * mh), __fadd_rn(dl, 0.5f * ml));
+    if (up > 0.0f) k += 1.0f;
+    else if (dn < 0.0f) k -= 1.0f;
+    open |= !(fminf(fabsf(up), fabsf(dn)) >= 0x1p-34f * mh);
+    return (uint32_t)__float2int_rn(k);
+}
+
+// One value (dim `dim`) of turned x * w as a pair, from memory.
+template <typename T, bool kPairs>
+__device__ __forceinline__ float2 pair_value(const NormRopeParams &p, const T *x, const float *turn, int dim) {
+    const int other = kPairs ? dim ^ 1 : dim ^ (kHD / 2), i = kPairs ? dim >> 1 : dim & (kHD / 2 - 1);
+    const bool second = kPairs ? dim & 1 : dim >= kHD / 2;
+    const float c = turn[i], s = turn[kHD / 2 + i];
+    const float xa = load1(x + dim), xb = load1(x + other);
+    float wa = 1.0f, wb = 1.0f;
+    if (p.k_weight) {
+        wa = p.k_weight[dim];
+        wb = second ? p.k_weight[other] : -p.k_weight[other];
+    } else if (!second) {
+        wb = -1.0f;
+    }
+    const float ah = __fmul_rn(xa, wa), al = __fmaf_rn(xa, wa, -ah);
+    const float bh = __fmul_rn(xb, wb), bl = __fmaf_rn(xb, wb, -bh);
+    return pair_add(pair_times(ah, al, c), pair_times(bh, bl, s));
+}
+
+// Key rows with one value next to a border (dim `near` in one or more of the
+// row's lanes, -1 in the others) and one that can be the maximum (dim `peak`
+// in one lane): only these are computed as pairs.  Returns the code at `near`;
+// `open` as pair_code.
+template <typename T, bool kPairs>
+__device__ __noinline__ uint32_t near_code(const NormRopeParams &p, int64_t row, int64_t pos, int h, int near, int peak,
+                                           float inv, bool &open, int lane) {
+    const T *x = reinterpret_cast<const T *>(p.k) + row * p.k_stride + (size_t)h * kHD;
+    const float *turn = p.rope + (size_t)pos * kHD;
+    float2 top = make_float2(0.0f, 0.0f), z = top;
+    if (near >= 0) z = pair_value<T, kPairs>(p, x, turn, near);
+    if (peak >= 0) top = pair_value<T, kPairs>(p, x, turn, peak);
+    if (top.x < 0.0f) top = make_float2(-top.x, -top.y);
+    const int src = (lane & 24) + __ffs((__ballot_sync(0xffffffffu, peak >= 0) >> (lane & 24)) & 0xffu) - 1;
+    top.x = __shfl_sync(0xffffffffu, top.x, src & 31);
+    top.y = __shfl_sync(0xffffffffu, top.y, src & 31);
+    open = false;
+    return pair_code(z.x, z.y, top.x, top.y, inv, open);
+}
+
+// Key rows of which more than one value is next to a border, every value held
+// as a pair of fp32.  mask: the lanes of these rows (eight to a row); the rows
+// are stored.  Returns the lanes that find a value undecided (or a NaN): their
+// rows are left to exact_key_row.
 template <typename T, bool kPairs>
 __device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t row, int64_t pos, int h0, KeyPlace at,
                                                float sc, unsigned mask, int lane) {
@@ -289,17 +354,8 @@ __device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t 
         const int ia = kPairs ? 2 * e : e, ib = kPairs ? 2 * e + 1 : 8 + e;
         const float ah = __fmul_rn(x[ia], w[ia]), al = __fmaf_rn(x[ia], w[ia], -ah);
         const float bh = __fmul_rn(x[ib], w[ib]), bl = __fmaf_rn(x[ib], w[ib], -bh);
-        // (fh + fl) * g as a pair
-        auto prod = [](float fh, float fl, float g) {
-            const float h2 = __fmul_rn(fh, g);
-            return make_float2(h2, __fmaf_rn(fl, g, __fmaf_rn(fh, g, -h2)));
-        };
-        auto add = [](float2 a, float2 b) {
-            const float2 t = two_sum(a.x, b.x);
-            return two_sum(t.x, __fadd_rn(t.y, __fadd_rn(a.y, b.y)));
-        };
-        const float2 za = add(prod(ah, al, c[e]), prod(-bh, -bl, s[e]));
-        const float2 zb = add(prod(bh, bl, c[e]), prod(ah, al, s[e]));
+        const float2 za = pair_add(pair_times(ah, al, c[e]), pair_times(-bh, -bl, s[e]));
+        const float2 zb = pair_add(pair_times(bh, bl, c[e]), pair_times(ah, al, s[e]));
         x[ia] = za.x;
         zl[ia] = za.y;
         x[ib] = zb.x;
@@ -317,19 +373,7 @@ __device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t 
     uint32_t t[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        // k = the nearest integer or next to it; d = 127 z - k m as a pair
-        float k = rintf(__fmul_rn(x[e], inv));
-        const float p1 = __fmul_rn(127.0f, x[e]), e1 = __fmaf_rn(127.0f, x[e], -p1);
-        const float p2 = __fmul_rn(k, mh), e2 = __fmaf_rn(k, mh, -p2);
-        const float2 d = two_sum(p1, -p2);
-        const float dl = __fadd_rn(__fadd_rn(d.y, __fsub_rn(e1, e2)), __fsub_rn(__fmul_rn(127.0f, zl[e]), __fmul_rn(k, ml)));
-        // its distances above m/2 and above -m/2
-        const float up = __fadd_rn(__fsub_rn(d.x, 0.5f * mh), __fsub_rn(dl, 0.5f * ml));
-        const float dn = __fadd_rn(__fadd_rn(d.x, 0.5f * mh), __fadd_rn(dl, 0.5f * ml));
-        if (up > 0.0f) k += 1.0f;
-        else if (dn < 0.0f) k -= 1.0f;
-        open |= !(fminf(fabsf(up), fabsf(dn)) >= 0x1p-34f * mh);
-        t[e] = (uint32_t)__float2int_rn(k);
+        t[e] = pair_code(x[e], zl[e], mh, ml, inv, open);
     }
     const bool mine = (mask >> (lane & 24)) & 0xffu;
     const unsigned rest = __ballot_sync(0xffffffffu, open && mine);
@@ -345,17 +389,21 @@ __device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t 
 // product and one of the sum, and |u_a c| + |u_b s| <= |(u_a, u_b)| |(c, s)|
 // <= sqrt(2) Z, so that z is within (2 sqrt(2) + 1) eps Z of z*, and so is m =
 // max|z| of Z; 127 * rcp(m) adds 3 eps.  127 z / m is then within 127 * 10.7
-// eps < 2^-13.5 of 127 z* / Z, and where its distance to the rounded value is
-// at most 1/2 - 2^-13 that value is the code (t = fl(z * inv + 1.5 * 2^23)
-// holds it in its low mantissa bits, as in kv_code_bytes4).  Rows with another
-// (2^-12 of values, one in 3 % of rows) go to near_key_rows; rows out of the
-// range in which these errors are relative ones to exact_key_row.
+// eps of 127 z* / Z, and where its distance to the rounded value is at most 1/2
+// - 1408 eps that value is the code (t = fl(z * inv + 1.5 * 2^23) holds it in
+// its low mantissa bits, as in kv_code_bytes4).  Of the others (1.7e-4 of
+// values, one in 2 % of rows) and of the row's largest, z is computed again as a
+// pair of fp32 (near_code); a row with several of either goes to
+// near_key_rows, one out of the range in which these errors are relative ones,
+// or within 2^-34 of a border, to exact_key_row.  (64-bit arithmetic has a
+// hundredth of fp32's rate: with it for all of these a call of 64 tokens takes
+// 8.6 us instead of 5.4.)
 template <typename T, bool kPairs>
 __device__ __forceinline__ void store_keys(const NormRopeParams &p, float (&x)[16], const float (&c)[8],
                                            const float (&s)[8], int64_t row, int64_t pos, int h0, KeyPlace at,
                                            int lane) {
     constexpr float kShift = 0x1.8p23f;
-    constexpr float kLim = 0.5f - 0x1p-13f;
+    constexpr float kLim = 0.5f - 1408.0f * 0x1p-24f;
     const int j = lane & 7, h = h0 + (lane >> 3);
     const float ss = row_squares(x);
     if (p.k_weight) weighted(x, p.k_weight, j);
@@ -380,11 +428,38 @@ __device__ __forceinline__ void store_keys(const NormRopeParams &p, float (&x)[1
     }
     const bool live = h < p.nkv;
     const unsigned who = __ballot_sync(0xffffffffu, odd && live);
-    if (live && !((who >> (lane & 24)) & 0xffu)) store_codes(p, t, sc, h, at, j);
+    const bool mine = (who >> (lane & 24)) & 0xffu;   // this row has such a value
+    if (live && !mine) store_codes(p, t, sc, h, at, j);
     if (who) {   // warp-uniform
-        const unsigned whole = __ballot_sync(0xffffffffu, wide && live);
-        unsigned left = whole;
-        if (who & ~whole) left |= near_key_rows<T, kPairs>(p, row, pos, h0, at, sc, who & ~whole, lane);
+        int near = -1, peak = -1, several = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int dim = 32 * (e / 4) + 4 * j + e % 4;
+            const float f = __uint_as_float(t[e]);
+            if (!(fabsf(__fmaf_rn(x[e], inv, -__fsub_rn(f, kShift))) <= kLim)) {
+                several |= near >= 0;
+                near = dim;
+            }
+            if (fabsf(x[e]) >= m * (1.0f - 0x1p-21f)) {   // z's error is below 2^-22 m
+                several |= peak >= 0;
+                peak = dim;
+            }
+        }
+        const unsigned peaks = __ballot_sync(0xffffffffu, peak >= 0) >> (lane & 24) & 0xffu;
+        several |= (peaks & (peaks - 1)) != 0 || peaks == 0 || wide;
+        unsigned hard = __ballot_sync(0xffffffffu, mine && several);   // by lanes, then by rows
+        bool open;
+        const uint32_t code = near_code<T, kPairs>(p, row, pos, min(h, p.nkv - 1), near, peak, inv, open, lane);
+        hard |= __ballot_sync(0xffffffffu, mine && near >= 0 && open);
+        if (live && mine && !((hard >> (lane & 24)) & 0xffu)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (near == 32 * (e / 4) + 4 * j + e % 4) t[e] = code;
+            store_codes(p, t, sc, h, at, j);
+        }
+        unsigned left = __ballot_sync(0xffffffffu, wide && live);
+        const unsigned pairs = __ballot_sync(0xffffffffu, live && mine && !wide && ((hard >> (lane & 24)) & 0xffu));
+        if (pairs) left |= near_key_rows<T, kPairs>(p, row, pos, h0, at, sc, pairs, lane);
         while (left) {
             const int g = (__ffs(left) - 1) >> 3;
             left &= ~(0xffu << (8 * g));
@@ -417,11 +492,10 @@ __device__ __forceinline__ void store_queries(const NormRopeParams &p, float (&x
     }
     turn<kPairs>(x, c, s);
     if (h < p.nqh) {
-        float *d = p.q_out + (row * p.nqh + h) * kHD + 8 * j;
+        float *d = p.q_out + (row * p.nqh + h) * kHD + 4 * j;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4 *>(d + (i / 2) * (kHD / 2) + 4 * (i % 2)) =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            *reinterpret_cast<float4 *>(d + 32 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     }
 }
 
@@ -450,14 +524,16 @@ __device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int p
         if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
         return;
     }
-    float c[8], s[8];
-    load_turn<kPairs>(p.rope + (size_t)pos * kHD, j, c, s);
     KeyPlace place = {-1, 0};
     if (g1 > qg) place = key_place(p, b, at, lane);
 #pragma unroll 1
     for (int gi = g0; gi < g1; ++gi) {
         float nx[16];
         if (gi + 1 < g1) fetch(gi + 1, nx);
+        // the table row comes from L1 again for each group: kept, its 16
+        // registers push others out (166 us against 155 at 8 x 4096 tokens)
+        float c[8], s[8];
+        load_turn<kPairs>(p.rope + (size_t)pos * kHD, j, c, s);
         if (gi < qg) store_queries<kPairs>(p, x, c, s, row, 4 * gi, lane);
         else if (place.tile >= 0) store_keys<T, kPairs>(p, x, c, s, row, pos, 4 * (gi - qg), place, lane);
 #pragma unroll
