@@ -16,7 +16,9 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kCopyWarps = 8;
+constexpr int kDigitBits = 11;                  // three digits of 11, 11 and 10 bits
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kMostCached = 40 * 1024;          // tokens whose keys stay in shared memory (160 KiB)
 
 // Order of a weight as an unsigned number: larger weights above smaller ones,
 // -0 equal to 0, a NaN below everything.  Nothing maps to 0xffffffff, which
@@ -28,19 +30,43 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (x >> 31) ? ~x : (x | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t token_key(const EvictParams &p, const int32_t *row, int h, int t, int L) {
-    if (t < p.n_first || t >= L - p.n_recent) return 0xffffffffu;
-    return weight_key(p.weight_sum[((size_t)row[t / kBS] * p.nkv + h) * kBS + t % kBS]);
+// A unit's tokens in the order that decides what is kept.  The keys of the
+// first n_cached tokens are kept in shared memory, the others' made again.
+struct Keys {
+    const int32_t *row;
+    const float *weight_sum;
+    int nkv, h, L, first, recent0;   // tokens below first and from recent0 on are kept
+    uint32_t *cache;
+    int n_cached;
+    __device__ __forceinline__ uint32_t key(int t, float w) const {
+        return t < first || t >= recent0 ? 0xffffffffu : weight_key(w);
+    }
+    __device__ __forceinline__ const float *at(int t) const {
+        return weight_sum + ((size_t)row[t / kBS] * nkv + h) * kBS + t % kBS;
+    }
+    __device__ __forceinline__ uint32_t get(int t) const { return t < n_cached ? cache[t] : key(t, *at(t)); }
+};
+
+// Inclusive sum over the warp's lanes from lane on to the last.
+__device__ __forceinline__ int warp_suffix(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, v, o);
+        if (lane + o < 32) v += x;
+    }
+    return v;
 }
 
-// One CTA per unit.
+// One CTA per unit: a radix selection over the keys, then the list of kept
+// tokens in order of position.
 __global__ void __launch_bounds__(kSelectThreads)
-evict_select_kernel(EvictParams p) {
+evict_select_kernel(EvictParams p, int cache_tokens) {
+    extern __shared__ __align__(16) uint32_t sm_keys[];
+    __shared__ int hist[kBins];
+    __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
+    __shared__ int sh_digit, sh_need, sh_bad;
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ int hist[256];
-    __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
-    __shared__ int sh_digit, sh_need, sh_bad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int u = blockIdx.x, b = u / p.nkv, h = u % p.nkv;
     const int cap = p.max_blocks * kBS;
@@ -54,6 +80,7 @@ evict_select_kernel(EvictParams p) {
         sh_bad = 0;
         if (Lraw != L && h == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
     }
+    hist[tid] = hist[tid + kSelectThreads] = 0;
     __syncthreads();
 
     // every block id must lie in the pool, and a destination must be neither a
@@ -61,11 +88,11 @@ evict_select_kernel(EvictParams p) {
     const int n_src = (L + kBS - 1) / kBS, n_dst = (m + kBS - 1) / kBS;
     bool bad = false;
     for (int i = tid; i < n_src; i += kSelectThreads) bad |= row[i] < 0 || row[i] >= p.num_blocks;
-    for (int64_t i = tid; i < (int64_t)n_dst * (n_src + n_dst); i += kSelectThreads) {
-        const int d = (int)(i / (n_src + n_dst)), j = (int)(i % (n_src + n_dst));
+    for (int d = warp; d < n_dst; d += kSelectWarps) {
         const int id = dst[d];
-        if (j < n_src) bad |= id == row[j];
-        else bad |= j - n_src == d ? (id < 0 || id >= p.num_blocks) : id == dst[j - n_src];
+        bad |= id < 0 || id >= p.num_blocks;
+        for (int j = lane; j < n_src; j += 32) bad |= row[j] == id;
+        for (int j = lane; j < d; j += 32) bad |= dst[j] == id;
     }
     if (bad) sh_bad = 1;
     __syncthreads();
@@ -78,114 +105,264 @@ evict_select_kernel(EvictParams p) {
         return;
     }
     if (tid == 0 && h == 0) p.new_lens[b] = m;
+    for (int j = m + tid; j < p.keep; j += kSelectThreads) kept[j] = -1;
+    if (m == L) {   // everything is kept
+        for (int t = tid; t < L; t += kSelectThreads) kept[t] = t;
+        return;
+    }
 
+    Keys keys = {row, p.weight_sum, p.nkv, h, L, p.n_first, L - p.n_recent, sm_keys, min(L, cache_tokens)};
     // the m-th largest key, digit by digit from the top: `prefix` holds the
-    // digits found, `need` how many tokens with exactly this prefix are kept
+    // digits found, `need` how many tokens with exactly this prefix are kept.
+    // The first digit is counted as the weights are loaded, four at a time.
+    for (int t = 4 * tid; t < L; t += 4 * kSelectThreads) {
+        const float4 w = *reinterpret_cast<const float4 *>(keys.at(t));   // (within the block: t % 4 == 0)
+        const uint4 k = make_uint4(keys.key(t, w.x), keys.key(t + 1, w.y), keys.key(t + 2, w.z), keys.key(t + 3, w.w));
+        if (t < keys.n_cached) *reinterpret_cast<uint4 *>(sm_keys + t) = k;   // (room for whole fours)
+        atomicAdd(&hist[k.x >> 21], 1);
+        if (t + 1 < L) atomicAdd(&hist[k.y >> 21], 1);
+        if (t + 2 < L) atomicAdd(&hist[k.z >> 21], 1);
+        if (t + 3 < L) atomicAdd(&hist[k.w >> 21], 1);
+    }
     uint32_t prefix = 0;
     int need = m;
-    for (int shift = 24; shift >= 0 && m < L; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int t = tid; t < L; t += kSelectThreads) {
-            const uint32_t k = token_key(p, row, h, t, L);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(k >> shift) & 255], 1);
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        if (pass > 0) {
+            const int above = pass == 1 ? 21 : 10;
+            for (int t = tid; t < L; t += kSelectThreads) {
+                const uint32_t k = keys.get(t);
+                if ((k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & (pass == 1 ? kBins - 1 : 1023)], 1);
+            }
         }
         __syncthreads();
-        if (tid == 0) {
-            int left = need, d = 255;
-            while (d > 0 && hist[d] < left) left -= hist[d--];
-            sh_digit = d;
-            sh_need = left;
+        // thread i: bins 2i and 2i + 1; the bin in which the need-th token from the top lies
+        const int lo = hist[2 * tid], hi = hist[2 * tid + 1];
+        const int suffix = warp_suffix(lo + hi, lane);
+        if (lane == 0) warp_a[warp] = suffix;
+        __syncthreads();
+        hist[2 * tid] = hist[2 * tid + 1] = 0;
+        const int later = warp_suffix(lane > warp ? warp_a[lane] : 0, lane);
+        const int above_hi = __shfl_sync(0xffffffffu, later, 0) + suffix - lo - hi;   // tokens in bins above 2i + 1
+        if (above_hi < need && need <= above_hi + lo + hi) {
+            const bool upper = need <= above_hi + hi;
+            sh_digit = 2 * tid + (upper ? 1 : 0);
+            sh_need = need - above_hi - (upper ? 0 : hi);
         }
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
         need = sh_need;
-        __syncthreads();
+        // (the next pass's first barrier keeps these reads before the next writes)
     }
 
-    // tokens above the m-th largest are kept, and the first `need` equal to it
-    int base_gt = 0, base_eq = 0;
-    for (int t0 = 0; t0 < L; t0 += kSelectThreads) {
-        const int t = t0 + tid;
-        const uint32_t k = t < L ? (m < L ? token_key(p, row, h, t, L) : 1u) : 0u;
-        const bool gt = t < L && k > prefix, eq = t < L && k == prefix;
-        const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            warp_gt[warp] = __popc(bg);
-            warp_eq[warp] = __popc(be);
-        }
-        __syncthreads();
-        int g = base_gt, e = base_eq;
-        for (int w = 0; w < kSelectWarps; ++w) {
-            if (w == warp) {
-                const unsigned below = (1u << lane) - 1;
-                const int ng = g + __popc(bg & below), ne = e + __popc(be & below);
-                if (gt) kept[ng + min(ne, need)] = t;
-                else if (eq && ne < need) kept[ng + ne] = t;
-            }
-            g += warp_gt[w];
-            e += warp_eq[w];
-        }
-        base_gt = g;
-        base_eq = e;
-        __syncthreads();
+    // tokens above the m-th largest are kept, and the first `need` equal to it:
+    // each warp counts both in its share of the tokens, and writes them behind
+    // those of the warps before it
+    const int share = ((L + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int t_lo = min(L, warp * share), t_hi = min(L, t_lo + share);
+    int gt = 0, eq = 0;
+    for (int t = t_lo; t < t_hi; t += 32) {
+        const uint32_t k = t + lane < t_hi ? keys.get(t + lane) : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, t + lane < t_hi && k > prefix));
+        eq += __popc(__ballot_sync(0xffffffffu, t + lane < t_hi && k == prefix));
     }
-    for (int j = m + tid; j < p.keep; j += kSelectThreads) kept[j] = -1;
+    if (lane == 0) {
+        warp_a[warp] = gt;
+        warp_b[warp] = eq;
+    }
+    __syncthreads();
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
+    for (int t = t_lo; t < t_hi; t += 32) {
+        const uint32_t k = t + lane < t_hi ? keys.get(t + lane) : 0u;
+        const bool is_gt = t + lane < t_hi && k > prefix, is_eq = t + lane < t_hi && k == prefix;
+        const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+        const unsigned below = (1u << lane) - 1;
+        const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
+        if (is_gt) kept[ng + min(ne, need)] = t + lane;
+        else if (is_eq && ne < need) kept[ng + ne] = t + lane;
+        gt += __popc(bg);
+        eq += __popc(be);
+    }
 }
 
-// One warp per kept token of a unit.
-__global__ void __launch_bounds__(kCopyWarps * 32)
-evict_copy_kernel(EvictParams p) {
+// One CTA per 64 kept tokens of a unit (a quarter of a destination tile).  K
+// rows are copied 16 bytes at a time into their new chunk order.  V is stored
+// with the 64 tokens of a quarter side by side per dim, so a token is a byte
+// of every 64-byte row: the source quarters that hold one of the tokens pass
+// through shared memory, kSrcQuarters at a time, only the 32-byte halves of
+// their rows that hold one, and each thread collects the 16 bytes of (dim, 16
+// tokens) from there.
+constexpr int kCopyThreads = 128;
+constexpr int kSrcQuarters = 4;
+constexpr int kVRow = 68;   // bytes of a staged V row: 64, and 4 that spread the rows over the banks
+
+__global__ void __launch_bounds__(kCopyThreads)
+evict_copy_kernel(EvictParams p, int quarters) {
+    __shared__ __align__(16) unsigned char stage[kSrcQuarters * kHD * kVRow];
+    __shared__ int src_tok[kStageTok];          // source position of each token, -1 behind the last
+    __shared__ int16_t src_list[kStageTok];     // which of the distinct source quarters a token is in
+    __shared__ int list_q[kStageTok];           // the distinct source quarters, and which halves of them
+    __shared__ unsigned list_half[kStageTok];
+    __shared__ int n_list;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t task = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
-    if (task >= (int64_t)p.batch * p.nkv * p.keep) return;
-    const int u = (int)(task / p.keep), j = (int)(task % p.keep);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int u = blockIdx.x / quarters, qd = blockIdx.x % quarters;
     const int b = u / p.nkv, h = u % p.nkv;
-    const int t = p.kept[task];
-    if (t < 0) return;
-    const size_t src = (size_t)p.block_table[(size_t)b * p.max_blocks + t / kBS] * p.nkv + h;
-    const size_t dst = (size_t)p.dst_table[(size_t)b * p.dst_max_blocks + j / kBS] * p.nkv + h;
-    const int s = t % kBS, d = j % kBS;
-    const int c = lane >> 2, w = lane & 3;
-    const uint32_t *ks = reinterpret_cast<const uint32_t *>(p.k_pool + (src * kBS + s) * kHD);
-    uint32_t *kd = reinterpret_cast<uint32_t *>(p.k_pool + (dst * kBS + d) * kHD);
-    kd[((c ^ (d & 7)) << 2) + w] = ks[((c ^ (s & 7)) << 2) + w];
-    const int8_t *vs = p.v_pool + src * kBS * kHD + (size_t)(s / kStageTok) * kTileVQuarter + s % kStageTok;
-    int8_t *vd = p.v_pool + dst * kBS * kHD + (size_t)(d / kStageTok) * kTileVQuarter + d % kStageTok;
+    const int32_t *kept = p.kept + (size_t)u * p.keep + qd * kStageTok;
+    const int most = min(kStageTok, p.keep - qd * kStageTok);
+    if (kept[0] < 0) return;
+    if (tid < kStageTok) {
+        src_tok[tid] = tid < most ? kept[tid] : -1;
+        list_half[tid] = 0u;
+    }
+    __syncthreads();
+    const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
+    const size_t dst = (size_t)p.dst_table[(size_t)b * p.dst_max_blocks + qd / 4] * p.nkv + h;
+    const int slot0 = (qd % 4) * kStageTok;     // slot of the first token
+
+    // warp 0: the distinct source quarters, in order (the positions increase)
+    if (warp == 0) {
+        int before = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vd[(size_t)(lane + 32 * i) * kStageTok] = vs[(size_t)(lane + 32 * i) * kStageTok];
-    if (lane == 0) p.k_scale[dst * kBS + d] = p.k_scale[src * kBS + s];
-    if (lane == 1) p.v_scale[dst * kBS + d] = p.v_scale[src * kBS + s];
-    if (lane == 2) p.weight_sum[dst * kBS + d] = p.weight_sum[src * kBS + s];
+        for (int i = 0; i < 2; ++i) {
+            const int j = lane + 32 * i, t = src_tok[j];
+            const bool fresh = t >= 0 && (j == 0 || src_tok[j - 1] / kStageTok != t / kStageTok);
+            const unsigned f = __ballot_sync(0xffffffffu, fresh);
+            const int at = before + __popc(f & ((2u << lane) - 1)) - 1;
+            if (fresh) list_q[at] = t / kStageTok;
+            src_list[j] = (int16_t)at;
+            if (t >= 0) atomicOr(&list_half[at], 1u << ((t % kStageTok) / 32));
+            before += __popc(f);
+        }
+        if (lane == 0) n_list = before;
+    }
+    // the other warps meanwhile: scales and weights
+    for (int i = tid - 32; i >= 0 && i < 3 * kStageTok; i += kCopyThreads - 32) {
+        const int j = i % kStageTok, t = src_tok[j];
+        float *x = i < kStageTok ? p.k_scale : i < 2 * kStageTok ? p.v_scale : p.weight_sum;
+        if (t >= 0) x[dst * kBS + slot0 + j] = x[((size_t)row[t / kBS] * p.nkv + h) * kBS + t % kBS];
+    }
+    // K: eight threads to a row
+    {
+        uint4 v[4];
+        const int c = tid & 7;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = src_tok[(tid >> 3) + 16 * i];
+            if (t >= 0) {
+                const size_t tile = (size_t)row[t / kBS] * p.nkv + h;
+                v[i] = reinterpret_cast<const uint4 *>(p.k_pool + (tile * kBS + t % kBS) * kHD)[c ^ (t & 7)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = (tid >> 3) + 16 * i;
+            if (src_tok[j] >= 0)
+                reinterpret_cast<uint4 *>(p.k_pool + (dst * kBS + slot0 + j) * kHD)[c ^ (j & 7)] = v[i];
+        }
+    }
+    __syncthreads();
+    const int n = n_list;
+    // V: thread (r, g): the 16 tokens 16g.. of dims r, r + 32, r + 64, r + 96
+    const int g = tid & 3, r = tid >> 2;
+    uint32_t out[4][4] = {};
+    for (int q0 = 0; q0 < n; q0 += kSrcQuarters) {
+        // 512 pieces of 16 bytes per source quarter
+        uint4 v[kSrcQuarters];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int piece = tid + kCopyThreads * i;
+#pragma unroll
+            for (int k = 0; k < kSrcQuarters; ++k) {
+                if (q0 + k < n && (list_half[q0 + k] >> ((piece & 3) >> 1) & 1)) {
+                    const int q = list_q[q0 + k];
+                    const size_t tile = (size_t)row[q / 4] * p.nkv + h;
+                    v[k] = reinterpret_cast<const uint4 *>(p.v_pool + tile * kBS * kHD + (size_t)(q % 4) * kTileVQuarter)[piece];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kSrcQuarters; ++k) {
+                if (q0 + k < n && (list_half[q0 + k] >> ((piece & 3) >> 1) & 1)) {
+                    uint32_t *d = reinterpret_cast<uint32_t *>(stage + (k * kHD + (piece >> 2)) * kVRow + (piece & 3) * 16);
+                    d[0] = v[k].x;
+                    d[1] = v[k].y;
+                    d[2] = v[k].z;
+                    d[3] = v[k].w;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 16 * g + 4 * w + k;
+                const int from = src_list[j] - q0;
+                if (src_tok[j] >= 0 && from >= 0 && from < kSrcQuarters) {
+                    const unsigned char *s = stage + (from * kHD + r) * kVRow + src_tok[j] % kStageTok;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out[i][w] |= (uint32_t)s[32 * i * kVRow] << (8 * k);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // 16 tokens of a dim are 16 contiguous bytes; behind the last token nothing is written
+    const int live = min(16, max(0, __popc(__ballot_sync(0xffffffffu, src_tok[lane] >= 0)) +
+                                       __popc(__ballot_sync(0xffffffffu, src_tok[32 + lane] >= 0)) - 16 * g));
+    int8_t *vd = p.v_pool + dst * kBS * kHD + (size_t)(qd % 4) * kTileVQuarter + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int8_t *d = vd + (r + 32 * i) * kStageTok;
+        if (live == 16) {
+            *reinterpret_cast<uint4 *>(d) = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (k < live) d[k] = (int8_t)(out[i][k / 4] >> (8 * (k % 4)));
+        }
+    }
 }
 
-cudaError_t launch_pdl(void (*kernel)(EvictParams), unsigned grid, unsigned block, const EvictParams &p,
-                       cudaStream_t s) {
+cudaError_t launch_pdl(void (*kernel)(EvictParams, int), unsigned grid, unsigned block, size_t smem,
+                       const EvictParams &p, int arg, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, arg);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
-    const int64_t tokens = (int64_t)p.batch * p.nkv * p.keep;
-    const int64_t blocks = (tokens + kCopyWarps - 1) / kCopyWarps;
+    static std::atomic<uint64_t> configured{0};
+    const int quarters = (p.keep + kStageTok - 1) / kStageTok;
+    const int64_t blocks = (int64_t)p.batch * p.nkv * quarters;
     if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(evict_select_kernel, (unsigned)(p.batch * p.nkv), kSelectThreads, p, s);
+    // keys of as many tokens as the table can hold, up to kMostCached
+    const int cached = (int)min((int64_t)p.max_blocks * kBS, (int64_t)kMostCached);
+    const cudaError_t e = launch_after_setting(
+        configured,
+        [] {
+            return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kMostCached * (int)sizeof(uint32_t));
+        },
+        [&] {
+            return launch_pdl(evict_select_kernel, (unsigned)(p.batch * p.nkv), kSelectThreads,
+                              cached * sizeof(uint32_t), p, cached, s);
+        });
     if (e != cudaSuccess) return e;
-    return launch_pdl(evict_copy_kernel, (unsigned)blocks, kCopyWarps * 32, p, s);
+    return launch_pdl(evict_copy_kernel, (unsigned)blocks, kCopyThreads, 0, p, quarters, s);
 }
 
 }  // namespace kvq8
