@@ -14,10 +14,13 @@
 namespace kvq8 {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+// Two CTAs of 512 threads fit an SM (64 registers each); with 1024 one does,
+// and 224 units took two rounds: 21 us against @@.
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;                  // three digits of 11, 11 and 10 bits
 constexpr int kBins = 1 << kDigitBits;
+constexpr int kThreadBins = kBins / kSelectThreads;
 constexpr int kMostCached = 40 * 1024;          // tokens whose keys stay in shared memory (160 KiB)
 
 // Order of a weight as an unsigned number: larger weights above smaller ones,
@@ -59,10 +62,10 @@ __device__ __forceinline__ int warp_suffix(int v, int lane) {
 
 // One CTA per unit: a radix selection over the keys, then the list of kept
 // tokens in order of position.
-__global__ void __launch_bounds__(kSelectThreads)
+__global__ void __launch_bounds__(kSelectThreads, 2)
 evict_select_kernel(EvictParams p, int cache_tokens) {
     extern __shared__ __align__(16) uint32_t sm_keys[];
-    __shared__ int hist[kBins];
+    __shared__ __align__(16) int hist[kBins];
     __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
     __shared__ int sh_digit, sh_need, sh_bad;
     pdl_launch_dependents();
@@ -80,7 +83,7 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         sh_bad = 0;
         if (Lraw != L && h == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
     }
-    hist[tid] = hist[tid + kSelectThreads] = 0;
+    for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
     __syncthreads();
 
     // every block id must lie in the pool, and a destination must be neither a
@@ -137,18 +140,25 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
             }
         }
         __syncthreads();
-        // thread i: bins 2i and 2i + 1; the bin in which the need-th token from the top lies
-        const int lo = hist[2 * tid], hi = hist[2 * tid + 1];
-        const int suffix = warp_suffix(lo + hi, lane);
+        // thread i: bins 4i .. 4i + 3; the bin in which the need-th token from the top lies
+        static_assert(kThreadBins == 4, "one int4 of bins per thread");
+        const int4 bin = reinterpret_cast<const int4 *>(hist)[tid];
+        const int sum = bin.x + bin.y + bin.z + bin.w;
+        const int suffix = warp_suffix(sum, lane);
         if (lane == 0) warp_a[warp] = suffix;
         __syncthreads();
-        hist[2 * tid] = hist[2 * tid + 1] = 0;
-        const int later = warp_suffix(lane > warp ? warp_a[lane] : 0, lane);
-        const int above_hi = __shfl_sync(0xffffffffu, later, 0) + suffix - lo - hi;   // tokens in bins above 2i + 1
-        if (above_hi < need && need <= above_hi + lo + hi) {
-            const bool upper = need <= above_hi + hi;
-            sh_digit = 2 * tid + (upper ? 1 : 0);
-            sh_need = need - above_hi - (upper ? 0 : hi);
+        reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
+        int above = __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelectWarps ? warp_a[lane] : 0) + suffix - sum;
+        if (above < need && need <= above + sum) {   // (tokens above this thread's bins)
+            const int c[4] = {bin.x, bin.y, bin.z, bin.w};
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                if (above < need && need <= above + c[i]) {
+                    sh_digit = 4 * tid + i;
+                    sh_need = need - above;
+                }
+                above += c[i];
+            }
         }
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
@@ -172,7 +182,7 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         warp_b[warp] = eq;
     }
     __syncthreads();
-    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);   // (warp < kSelectWarps <= 32)
     eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
     for (int t = t_lo; t < t_hi; t += 32) {
         const uint32_t k = t + lane < t_hi ? keys.get(t + lane) : 0u;
@@ -190,21 +200,23 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
 // One CTA per 64 kept tokens of a unit (a quarter of a destination tile).  K
 // rows are copied 16 bytes at a time into their new chunk order.  V is stored
 // with the 64 tokens of a quarter side by side per dim, so a token is a byte
-// of every 64-byte row: the source quarters that hold one of the tokens pass
-// through shared memory, kSrcQuarters at a time, only the 32-byte halves of
-// their rows that hold one, and each thread collects the 16 bytes of (dim, 16
-// tokens) from there.
+// of every 64-byte row: the source quarters that hold one of the tokens are
+// copied into shared memory, kSrcQuarters at a time, only the 32-byte halves
+// of their rows that hold one, and each thread collects the 16 bytes of (dim,
+// 16 tokens) from there.
 constexpr int kCopyThreads = 128;
-constexpr int kSrcQuarters = 4;
-constexpr int kVRow = 68;   // bytes of a staged V row: 64, and 4 that spread the rows over the banks
+constexpr int kSrcQuarters = 3;   // half of the tokens kept: two or three source quarters
+constexpr int kVRow = 80;         // bytes of a staged V row: 64, and 16 that spread the rows over the banks
+constexpr int kVStage = kHD * kVRow;
 
-__global__ void __launch_bounds__(kCopyThreads)
+__global__ void __launch_bounds__(kCopyThreads, 7)
 evict_copy_kernel(EvictParams p, int quarters) {
-    __shared__ __align__(16) unsigned char stage[kSrcQuarters * kHD * kVRow];
+    __shared__ __align__(16) unsigned char stage[kSrcQuarters * kVStage];
     __shared__ int src_tok[kStageTok];          // source position of each token, -1 behind the last
-    __shared__ int16_t src_list[kStageTok];     // which of the distinct source quarters a token is in
-    __shared__ int list_q[kStageTok];           // the distinct source quarters, and which halves of them
-    __shared__ unsigned list_half[kStageTok];
+    __shared__ int src_tile[kStageTok];         // its (block, kv head) tile
+    __shared__ __align__(16) int src_off[kStageTok];          // its byte in the staged rows of all its source quarters
+    __shared__ int list_q[kStageTok];           // the distinct source quarters: tile * 4 + quarter
+    __shared__ unsigned list_half[kStageTok];   // which halves of them
     __shared__ int n_list;
     pdl_launch_dependents();
     pdl_wait();
@@ -213,14 +225,16 @@ evict_copy_kernel(EvictParams p, int quarters) {
     const int b = u / p.nkv, h = u % p.nkv;
     const int32_t *kept = p.kept + (size_t)u * p.keep + qd * kStageTok;
     const int most = min(kStageTok, p.keep - qd * kStageTok);
-    if (kept[0] < 0) return;
+    const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
+    const size_t dst = (size_t)p.dst_table[(size_t)b * p.dst_max_blocks + qd / 4] * p.nkv + h;
     if (tid < kStageTok) {
-        src_tok[tid] = tid < most ? kept[tid] : -1;
+        const int t = tid < most ? kept[tid] : -1;
+        src_tok[tid] = t;
+        src_tile[tid] = t >= 0 ? row[t / kBS] * p.nkv + h : 0;
         list_half[tid] = 0u;
     }
     __syncthreads();
-    const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
-    const size_t dst = (size_t)p.dst_table[(size_t)b * p.dst_max_blocks + qd / 4] * p.nkv + h;
+    if (src_tok[0] < 0) return;
     const int slot0 = (qd % 4) * kStageTok;     // slot of the first token
 
     // warp 0: the distinct source quarters, in order (the positions increase)
@@ -232,87 +246,93 @@ evict_copy_kernel(EvictParams p, int quarters) {
             const bool fresh = t >= 0 && (j == 0 || src_tok[j - 1] / kStageTok != t / kStageTok);
             const unsigned f = __ballot_sync(0xffffffffu, fresh);
             const int at = before + __popc(f & ((2u << lane) - 1)) - 1;
-            if (fresh) list_q[at] = t / kStageTok;
-            src_list[j] = (int16_t)at;
+            if (fresh) list_q[at] = src_tile[j] * 4 + (t / kStageTok) % 4;
+            src_off[j] = t >= 0 ? at * kVStage + t % kStageTok : -1;
             if (t >= 0) atomicOr(&list_half[at], 1u << ((t % kStageTok) / 32));
             before += __popc(f);
         }
         if (lane == 0) n_list = before;
     }
-    // the other warps meanwhile: scales and weights
-    for (int i = tid - 32; i >= 0 && i < 3 * kStageTok; i += kCopyThreads - 32) {
-        const int j = i % kStageTok, t = src_tok[j];
-        float *x = i < kStageTok ? p.k_scale : i < 2 * kStageTok ? p.v_scale : p.weight_sum;
-        if (t >= 0) x[dst * kBS + slot0 + j] = x[((size_t)row[t / kBS] * p.nkv + h) * kBS + t % kBS];
-    }
     // K: eight threads to a row
-    {
-        uint4 v[4];
-        const int c = tid & 7;
+    uint4 k[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = src_tok[(tid >> 3) + 16 * i];
-            if (t >= 0) {
-                const size_t tile = (size_t)row[t / kBS] * p.nkv + h;
-                v[i] = reinterpret_cast<const uint4 *>(p.k_pool + (tile * kBS + t % kBS) * kHD)[c ^ (t & 7)];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = (tid >> 3) + 16 * i;
-            if (src_tok[j] >= 0)
-                reinterpret_cast<uint4 *>(p.k_pool + (dst * kBS + slot0 + j) * kHD)[c ^ (j & 7)] = v[i];
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int j = (tid >> 3) + 16 * i, t = src_tok[j];
+        if (t >= 0)
+            k[i] = reinterpret_cast<const uint4 *>(p.k_pool + ((size_t)src_tile[j] * kBS + t % kBS) * kHD)[(tid & 7) ^ (t & 7)];
     }
     __syncthreads();
+    // copies of the source quarters q0 .. q0 + kSrcQuarters - 1 into the stage
     const int n = n_list;
+    auto fetch = [&](int q0) {
+#pragma unroll
+        for (int q = 0; q < kSrcQuarters; ++q) {
+            if (q0 + q < n) {
+                const unsigned half = list_half[q0 + q];
+                const int at = list_q[q0 + q];
+                const int8_t *src = p.v_pool + (size_t)(at >> 2) * kBS * kHD + (size_t)(at & 3) * kTileVQuarter;
+                if (half >> ((tid & 3) >> 1) & 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // thread: piece tid & 3 of rows tid >> 2, + 32, + 64, + 96
+                        const int d = (tid >> 2) + 32 * i;
+                        cp_async16_cg(stage + q * kVStage + d * kVRow + (tid & 3) * 16, src + d * kStageTok + (tid & 3) * 16);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    fetch(0);
+    // scales and weights meanwhile, and K's rows
+    float sw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = tid + kCopyThreads * i, j = x % kStageTok, t = src_tok[j];
+        const float *a = x < kStageTok ? p.k_scale : x < 2 * kStageTok ? p.v_scale : p.weight_sum;
+        if (x < 3 * kStageTok && t >= 0) sw[i] = a[(size_t)src_tile[j] * kBS + t % kBS];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = (tid >> 3) + 16 * i;
+        if (src_tok[j] >= 0)
+            reinterpret_cast<uint4 *>(p.k_pool + (dst * kBS + slot0 + j) * kHD)[(tid & 7) ^ (j & 7)] = k[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = tid + kCopyThreads * i, j = x % kStageTok;
+        float *a = x < kStageTok ? p.k_scale : x < 2 * kStageTok ? p.v_scale : p.weight_sum;
+        if (x < 3 * kStageTok && src_tok[j] >= 0) a[dst * kBS + slot0 + j] = sw[i];
+    }
     // V: thread (r, g): the 16 tokens 16g.. of dims r, r + 32, r + 64, r + 96
     const int g = tid & 3, r = tid >> 2;
     uint32_t out[4][4] = {};
     for (int q0 = 0; q0 < n; q0 += kSrcQuarters) {
-        // 512 pieces of 16 bytes per source quarter
-        uint4 v[kSrcQuarters];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int piece = tid + kCopyThreads * i;
-#pragma unroll
-            for (int k = 0; k < kSrcQuarters; ++k) {
-                if (q0 + k < n && (list_half[q0 + k] >> ((piece & 3) >> 1) & 1)) {
-                    const int q = list_q[q0 + k];
-                    const size_t tile = (size_t)row[q / 4] * p.nkv + h;
-                    v[k] = reinterpret_cast<const uint4 *>(p.v_pool + tile * kBS * kHD + (size_t)(q % 4) * kTileVQuarter)[piece];
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kSrcQuarters; ++k) {
-                if (q0 + k < n && (list_half[q0 + k] >> ((piece & 3) >> 1) & 1)) {
-                    uint32_t *d = reinterpret_cast<uint32_t *>(stage + (k * kHD + (piece >> 2)) * kVRow + (piece & 3) * 16);
-                    d[0] = v[k].x;
-                    d[1] = v[k].y;
-                    d[2] = v[k].z;
-                    d[3] = v[k].w;
-                }
-            }
-        }
+        cp_async_wait<0>();
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
+            const int4 off = *reinterpret_cast<const int4 *>(src_off + 16 * g + 4 * w);
+            const int o[4] = {off.x, off.y, off.z, off.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = 16 * g + 4 * w + k;
-                const int from = src_list[j] - q0;
-                if (src_tok[j] >= 0 && from >= 0 && from < kSrcQuarters) {
-                    const unsigned char *s = stage + (from * kHD + r) * kVRow + src_tok[j] % kStageTok;
+            for (int c = 0; c < 4; ++c) {
+                const int from = o[c] - q0 * kVStage;
+                if (o[c] >= 0 && from >= 0 && from < kSrcQuarters * kVStage) {
+                    const unsigned char *x = stage + from + r * kVRow;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) out[i][w] |= (uint32_t)s[32 * i * kVRow] << (8 * k);
+                    for (int i = 0; i < 4; ++i) out[i][w] |= (uint32_t)x[32 * i * kVRow] << (8 * c);
                 }
             }
         }
-        __syncthreads();
+        if (q0 + kSrcQuarters < n) {
+            __syncthreads();
+            fetch(q0 + kSrcQuarters);
+        }
     }
     // 16 tokens of a dim are 16 contiguous bytes; behind the last token nothing is written
-    const int live = min(16, max(0, __popc(__ballot_sync(0xffffffffu, src_tok[lane] >= 0)) +
-                                       __popc(__ballot_sync(0xffffffffu, src_tok[32 + lane] >= 0)) - 16 * g));
+    int live = 16;
+    if (src_tok[kStageTok - 1] < 0)
+        live = min(16, max(0, __popc(__ballot_sync(0xffffffffu, src_tok[lane] >= 0)) +
+                                  __popc(__ballot_sync(0xffffffffu, src_tok[32 + lane] >= 0)) - 16 * g));
     int8_t *vd = p.v_pool + dst * kBS * kHD + (size_t)(qd % 4) * kTileVQuarter + 16 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -321,8 +341,8 @@ evict_copy_kernel(EvictParams p, int quarters) {
             *reinterpret_cast<uint4 *>(d) = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (k < live) d[k] = (int8_t)(out[i][k / 4] >> (8 * (k % 4)));
+            for (int c = 0; c < 16; ++c)
+                if (c < live) d[c] = (int8_t)(out[i][c / 4] >> (8 * (c % 4)));
         }
     }
 }
