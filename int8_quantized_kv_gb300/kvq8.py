@@ -143,7 +143,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream, device=None) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = _torch()
+        if device is None:   # the current stream's handle without a Stream object (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
@@ -355,6 +357,9 @@ class HostMapped:
     def is_contiguous(self) -> bool:
         return True
 
+    def get_device(self) -> int:
+        return _torch().cuda.current_device()
+
     def numel(self) -> int:
         return self._t.numel()
 
@@ -479,64 +484,67 @@ ROPE_PAIRS = 0x1                          # KVQ8_ROPE_PAIRS
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2   # KVQ8_DTYPE_*
 
 
-def _need(what: str, t, dtype: str, shape):
-    """A contiguous device tensor of this type and shape, on the current device."""
+def _need(*wanted):
+    """Each (name, tensor, dtype, shape): a contiguous tensor of this type and
+    shape on the current device.  (One call for all of an entry point's
+    tensors: these checks are most of a small call's time on the host.)"""
+    dev = _torch().cuda.current_device()
+    for what, t, dtype, shape in wanted:
+        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)} on the current device (cuda:{dev}), "
+                             f"got {t.dtype} {list(t.shape)} on device {t.get_device()}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _cache_wants(cache: KVCache, weight_sum=None):
+    """(blocks, kv heads, what _need is to check) of a cache and its weight sums."""
     torch = _torch()
-    if isinstance(t, HostMapped):
-        if dtype != "float32" or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{what}: expected {dtype} {list(shape)}, got host memory of {list(t.shape)}")
-        return
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: expected a tensor on the current device, got one on {t.device}")
-    if t.dtype is not getattr(torch, dtype) or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-def _need_cache(cache: KVCache, weight_sum=None):
-    nb, nkv = cache.k_pool.shape[:2]
-    _need("k_pool", cache.k_pool, "int8", (nb, nkv, BLOCK_SIZE, HEAD_DIM))
-    _need("v_pool", cache.v_pool, "int8", (nb, nkv, BLOCK_SIZE // 64, HEAD_DIM, 64))
-    _need("k_scale", cache.k_scale, "float32", (nb, nkv, BLOCK_SIZE))
-    _need("v_scale", cache.v_scale, "float32", (nb, nkv, BLOCK_SIZE))
+    k_pool, v_pool, k_scale, v_scale = cache
+    nb, nkv = k_pool.shape[:2]
+    i8, f32, scales = torch.int8, torch.float32, (nb, nkv, BLOCK_SIZE)
+    wants = [("k_pool", k_pool, i8, (nb, nkv, BLOCK_SIZE, HEAD_DIM)),
+             ("v_pool", v_pool, i8, (nb, nkv, BLOCK_SIZE // 64, HEAD_DIM, 64)),
+             ("k_scale", k_scale, f32, scales), ("v_scale", v_scale, f32, scales)]
     if weight_sum is not None:
-        _need("weight_sum", weight_sum, "float32", (nb, nkv, BLOCK_SIZE))
-    return nb, nkv
+        wants.append(("weight_sum", weight_sum, f32, scales))
+    return nb, nkv, wants
 
 
-def _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum=None):
-    """Checks what the window and weights decodes share; returns their leading arguments."""
-    nb, nkv = _need_cache(cache, weight_sum)
+def _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum, windows):
+    """Checks the tensors of the window and weights decodes; returns their leading arguments."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    nb, nkv, wants = _cache_wants(cache, weight_sum)
     batch, nqh, hd = q.shape
     max_blocks = block_table.shape[1]
-    _need("q", q, "float32", (batch, nqh, hd))
-    _need("out", out, "float32", (batch, nqh, hd))
-    _need("block_table", block_table, "int32", (batch, max_blocks))
-    _need("ctx_lens", ctx_lens, "int32", (batch,))
+    wants += [("q", q, f32, (batch, nqh, hd)), ("out", out, f32, (batch, nqh, hd)),
+              ("block_table", block_table, i32, (batch, max_blocks)), ("ctx_lens", ctx_lens, i32, (batch,)),
+              ("workspace", workspace, torch.uint8, (workspace.shape[0],))]
+    new = ()
     if k_new is not None:
-        _need("k_new", k_new, "float32", (batch, nkv, hd))
-        _need("v_new", v_new, "float32", (batch, nkv, hd))
+        wants += [("k_new", k_new, f32, (batch, nkv, hd)), ("v_new", v_new, f32, (batch, nkv, hd))]
+        new = (k_new.data_ptr(), v_new.data_ptr())
+    if windows is not None:
+        wants.append(("windows", windows, i32, (batch,)))
     if dev_status is not None:
-        _need("dev_status", dev_status, "int32", (1,))
-    _need_cuda(workspace)
-    new = () if k_new is None else (_ptr(k_new), _ptr(v_new))
-    return (_ptr(q), *new, batch, nqh, nkv, hd, _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale),
-            _ptr(cache.v_scale), nb, _ptr(block_table), max_blocks, BLOCK_SIZE, _ptr(ctx_lens))
+        wants.append(("dev_status", dev_status, i32, (1,)))
+    _need(*wants)
+    return (q.data_ptr(), *new, batch, nqh, nkv, hd, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+            cache[3].data_ptr(), nb, block_table.data_ptr(), max_blocks, BLOCK_SIZE, ctx_lens.data_ptr())
 
 
 def _window(fn, q, k_new, v_new, cache, block_table, ctx_lens, windows, sinks, out, workspace, sm_scale,
             dev_status, stream):
-    lead = _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status)
-    _need("windows", windows, "int32", (q.shape[0],))
+    lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, None, windows)
     sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
-    _check(fn, getattr(load(), fn)(*lead, _ptr(windows), int(sinks), sm, _ptr(out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                   _stream(stream)))
+    _check(fn, getattr(load(), fn)(*lead, windows.data_ptr(), int(sinks), sm, out.data_ptr(), workspace.data_ptr(),
+                                   workspace.shape[0], _ptr(dev_status), _stream(stream)))
 
 
 def decode_attn_window(q, cache: KVCache, block_table, ctx_lens, windows, sinks: int, out, workspace,
                        sm_scale: Optional[float] = None, dev_status=None, stream=None):
     """decode_attn over the tokens t < sinks or t >= ctx_lens - windows (int32
-    [batch]) of every row."""
+    [batch]) of every row; workspace from alloc_workspace."""
     _window("kvq8_decode_attn_window", q, None, None, cache, block_table, ctx_lens, windows, sinks, out, workspace,
             sm_scale, dev_status, stream)
 
@@ -567,11 +575,10 @@ def alloc_weights_workspace(batch: int, nqh: int, nkv: int, max_blocks: int, dev
 
 def _weights(fn, q, k_new, v_new, cache, block_table, ctx_lens, out, weight_sum, workspace, sm_scale, dev_status,
              stream):
-    lead = _need_decode(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum)
+    lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum, None)
     sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
-    _check(fn, getattr(load(), fn)(*lead, sm, _ptr(out), _ptr(weight_sum), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                   _stream(stream)))
+    _check(fn, getattr(load(), fn)(*lead, sm, out.data_ptr(), weight_sum.data_ptr(), workspace.data_ptr(),
+                                   workspace.shape[0], _ptr(dev_status), _stream(stream)))
 
 
 def decode_attn_weights(q, cache: KVCache, block_table, ctx_lens, out, weight_sum, workspace,
@@ -598,44 +605,40 @@ def evict(cache: KVCache, weight_sum, block_table, ctx_lens, keep: int, dst_tabl
     in order into the blocks of dst_table (int32 [batch][dst_max_blocks], none
     of them in block_table).  kept (int32 [batch][nkv][keep]) receives their
     positions, -1 behind the last, and new_lens (int32 [batch]) their number."""
-    nb, nkv = _need_cache(cache, weight_sum)
+    i32 = _torch().int32
+    nb, nkv, wants = _cache_wants(cache, weight_sum)
     batch, max_blocks = block_table.shape
-    _need("block_table", block_table, "int32", (batch, max_blocks))
-    _need("dst_table", dst_table, "int32", (batch, dst_table.shape[1]))
-    _need("ctx_lens", ctx_lens, "int32", (batch,))
-    _need("kept", kept, "int32", (batch, nkv, keep))
-    _need("new_lens", new_lens, "int32", (batch,))
+    dst_blocks = dst_table.shape[1]
+    wants += [("block_table", block_table, i32, (batch, max_blocks)), ("dst_table", dst_table, i32, (batch, dst_blocks)),
+              ("ctx_lens", ctx_lens, i32, (batch,)), ("kept", kept, i32, (batch, nkv, keep)),
+              ("new_lens", new_lens, i32, (batch,))]
     if dev_status is not None:
-        _need("dev_status", dev_status, "int32", (1,))
+        wants.append(("dev_status", dev_status, i32, (1,)))
+    _need(*wants)
     _check("kvq8_evict", load().kvq8_evict(
-        batch, nkv, HEAD_DIM, _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale), _ptr(cache.v_scale),
-        _ptr(weight_sum), nb, _ptr(block_table), max_blocks, BLOCK_SIZE, _ptr(ctx_lens), int(keep), int(n_first),
-        int(n_recent), _ptr(dst_table), dst_table.shape[1], _ptr(kept), _ptr(new_lens), _ptr(dev_status),
-        _stream(stream)))
+        batch, nkv, HEAD_DIM, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
+        weight_sum.data_ptr(), nb, block_table.data_ptr(), max_blocks, BLOCK_SIZE, ctx_lens.data_ptr(), int(keep),
+        int(n_first), int(n_recent), dst_table.data_ptr(), dst_blocks, kept.data_ptr(), new_lens.data_ptr(),
+        _ptr(dev_status), _stream(stream)))
 
 
 def rope_table(inv_freq, n_pos: int, stream=None):
     """The rotation's table, fp32 [n_pos][128]: cosines of position * inv_freq
     (fp64 [64], device), then sines."""
-    _need("inv_freq", inv_freq, "float64", (HEAD_DIM // 2,))
-    table = _torch().empty((n_pos, HEAD_DIM), dtype=_torch().float32, device=inv_freq.device)
+    torch = _torch()
+    _need(("inv_freq", inv_freq, torch.float64, (HEAD_DIM // 2,)))
+    table = torch.empty((n_pos, HEAD_DIM), dtype=torch.float32, device=inv_freq.device)
     _check("kvq8_rope_table", load().kvq8_rope_table(_ptr(inv_freq), int(n_pos), HEAD_DIM, _ptr(table),
                                                      _stream(stream)))
     return table
 
 
-def _token_rows(what: str, t, dtype, batch: int, n_new: int, heads=None) -> int:
-    """Checks [batch][n_new][heads][128] rows (heads side by side, all tokens one
-    distance apart) and returns that distance in elements."""
-    if t.dim() != 4 or t.shape[:2] != (batch, n_new) or t.shape[3] != HEAD_DIM or heads not in (None, t.shape[2]):
-        raise ValueError(f"{what}: expected [{batch}][{n_new}][heads][{HEAD_DIM}] rows, got {list(t.shape)}")
-    if not t.is_cuda or t.device.index != _torch().cuda.current_device() or t.dtype is not dtype:
-        raise ValueError(f"{what}: expected {dtype} on the current device, got {t.dtype} on {t.device}")
+def _token_stride(what: str, t, batch: int, n_new: int, heads: int) -> int:
+    """Elements between the rows of a tensor's [batch][n_new] tokens, whose heads
+    [heads][128] must lie side by side."""
     sb, sn, sh, sd = t.stride()
-    n_heads = t.shape[2]
-    dense = n_heads * HEAD_DIM
-    stride = sn if n_new > 1 else sb if batch > 1 else dense
-    if sd != 1 or (n_heads > 1 and sh != HEAD_DIM) or (n_new > 1 and batch > 1 and sb != n_new * stride):
+    stride = sn if n_new > 1 else sb if batch > 1 else heads * HEAD_DIM
+    if sd != 1 or (heads > 1 and sh != HEAD_DIM) or (n_new > 1 and batch > 1 and sb != n_new * stride):
         raise ValueError(f"{what}: the heads of a token must lie side by side and all tokens one distance apart")
     return stride
 
@@ -652,31 +655,40 @@ def norm_rope_append(q, k, v, q_weight, k_weight, eps: float, rope_table, start_
     (2i, 2i + 1) instead of (i, i + 64); weight_sum: zeroed at the appended
     tokens.  q_out fp32 [batch][n_new][nqh][128]."""
     torch = _torch()
-    nb, nkv = _need_cache(cache, weight_sum)
-    batch, n_new, nqh = q.shape[:3]
-    dtype = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(q.dtype)
-    if dtype is None:
-        raise ValueError(f"q: expected fp32, bf16 or fp16, got {q.dtype}")
-    strides = (_token_rows("q", q, q.dtype, batch, n_new), _token_rows("k", k, q.dtype, batch, n_new, nkv),
-               _token_rows("v", v, q.dtype, batch, n_new, nkv))
-    max_blocks = block_table.shape[1]
-    _need("q_out", q_out, "float32", (batch, n_new, nqh, HEAD_DIM))
-    _need("rope_table", rope_table, "float32", (rope_table.shape[0], HEAD_DIM))
-    _need("block_table", block_table, "int32", (batch, max_blocks))
-    _need("start_pos", start_pos, "int32", (batch,))
-    for what, t, kind, shape in (("q_weight", q_weight, "float32", (HEAD_DIM,)),
-                                 ("k_weight", k_weight, "float32", (HEAD_DIM,)),
-                                 ("positions", positions, "int32", (batch, n_new)),
-                                 ("n_tokens", n_tokens, "int32", (batch,)),
-                                 ("dev_status", dev_status, "int32", (1,))):
-        if t is not None:
-            _need(what, t, kind, shape)
+    f32, i32 = torch.float32, torch.int32
+    nb, nkv, wants = _cache_wants(cache, weight_sum)
+    batch, n_new, nqh, _ = shape = q.shape
+    kind = q.dtype
+    dtype = DTYPE_BF16 if kind is torch.bfloat16 else DTYPE_F32 if kind is f32 else DTYPE_F16
+    dev = torch.cuda.current_device()
+    for what, t, want in (("q", q, (batch, n_new, nqh, HEAD_DIM)), ("k", k, (batch, n_new, nkv, HEAD_DIM)),
+                          ("v", v, (batch, n_new, nkv, HEAD_DIM))):
+        if t.shape != want or t.dtype is not kind or t.get_device() != dev:
+            raise ValueError(f"{what}: expected {kind} {list(want)} on the current device (cuda:{dev}), got {t.dtype} "
+                             f"{list(t.shape)} on device {t.get_device()}")
+    if dtype == DTYPE_F16 and kind is not torch.float16:
+        raise ValueError(f"q: expected fp32, bf16 or fp16, got {kind}")
+    max_blocks, n_pos = block_table.shape[1], rope_table.shape[0]
+    wants += [("q_out", q_out, f32, shape), ("rope_table", rope_table, f32, (n_pos, HEAD_DIM)),
+              ("block_table", block_table, i32, (batch, max_blocks)), ("start_pos", start_pos, i32, (batch,))]
+    if q_weight is not None:
+        wants.append(("q_weight", q_weight, f32, (HEAD_DIM,)))
+    if k_weight is not None:
+        wants.append(("k_weight", k_weight, f32, (HEAD_DIM,)))
+    if positions is not None:
+        wants.append(("positions", positions, i32, (batch, n_new)))
+    if n_tokens is not None:
+        wants.append(("n_tokens", n_tokens, i32, (batch,)))
+    if dev_status is not None:
+        wants.append(("dev_status", dev_status, i32, (1,)))
+    _need(*wants)
     _check("kvq8_norm_rope_append", load().kvq8_norm_rope_append(
-        _ptr(q), _ptr(k), _ptr(v), dtype, *strides, batch, n_new, nqh, nkv, HEAD_DIM, _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(rope_table), rope_table.shape[0], _ptr(positions), _ptr(n_tokens),
-        ROPE_PAIRS if interleaved else 0, _ptr(start_pos), _ptr(block_table), max_blocks, BLOCK_SIZE, nb,
-        _ptr(cache.k_pool), _ptr(cache.v_pool), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(weight_sum),
-        _ptr(q_out), _ptr(dev_status), _stream(stream)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, _token_stride("q", q, batch, n_new, nqh),
+        _token_stride("k", k, batch, n_new, nkv), _token_stride("v", v, batch, n_new, nkv), batch, n_new, nqh, nkv,
+        HEAD_DIM, _ptr(q_weight), _ptr(k_weight), eps, rope_table.data_ptr(), n_pos, _ptr(positions),
+        _ptr(n_tokens), ROPE_PAIRS if interleaved else 0, start_pos.data_ptr(), block_table.data_ptr(), max_blocks,
+        BLOCK_SIZE, nb, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
+        _ptr(weight_sum), q_out.data_ptr(), _ptr(dev_status), _stream(stream)))
 
 
 # ------------------------------------------------------------ 4-bit cache ---

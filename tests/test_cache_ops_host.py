@@ -144,37 +144,33 @@ def test_norm_rope_refusals(lib):
 
 
 def test_binding_refuses_host_tensors_and_strides():
-    t = torch.zeros(2, 128)
-    with pytest.raises(ValueError, match="current device"):
-        kvq8._need("t", t, "float32", (2, 128))
+    class Dev:   # a device tensor's face, for the checks alone
+        def __init__(self, t, device=0):
+            self.t, self.dtype, self.shape, self.device = t, t.dtype, t.shape, device
 
-    class Dev:   # a device tensor's face, for the shape checks alone
-        is_cuda, device = True, torch.device("cuda", 0)
-
-        def __init__(self, t):
-            self.t, self.dtype, self.shape = t, t.dtype, t.shape
+        def get_device(self):
+            return self.device
 
         def __getattr__(self, name):
             return getattr(self.t, name)
 
+    t, f32 = torch.zeros(2, 128), torch.float32
     cur, torch.cuda.current_device = torch.cuda.current_device, lambda: 0
     try:
-        kvq8._need("t", Dev(t), "float32", (2, 128))
-        for bad in (t.half(), t.T, torch.zeros(2, 129), torch.zeros(2, 256)[:, ::2]):
-            with pytest.raises(ValueError, match="expected contiguous"):
-                kvq8._need("t", Dev(bad), "float32", (2, 128))
-        packed = torch.zeros(3, 5, 12 * 128)
-        rows = packed[..., 256:1280].unflatten(-1, (8, 128))
-        assert kvq8._token_rows("q", Dev(rows), torch.float32, 3, 5) == 12 * 128
-        assert kvq8._token_rows("q", Dev(rows[:1]), torch.float32, 1, 5) == 12 * 128
-        assert kvq8._token_rows("q", Dev(rows[:, :1]), torch.float32, 3, 1) == 5 * 12 * 128
-        assert kvq8._token_rows("q", Dev(rows[:1, :1]), torch.float32, 1, 1) == 8 * 128
-        for bad in (rows.transpose(1, 2), rows[:, :4], rows[..., :64], rows.transpose(0, 1), rows[:, :, ::2]):
-            with pytest.raises(ValueError):
-                kvq8._token_rows("q", Dev(bad), torch.float32, 3, 5)
-        with pytest.raises(ValueError):
-            kvq8._token_rows("q", Dev(rows[:, :4]), torch.float32, 3, 4)     # tokens not one distance apart
-        with pytest.raises(ValueError):
-            kvq8._token_rows("k", Dev(rows), torch.float32, 3, 5, 4)
+        kvq8._need(("t", Dev(t), f32, (2, 128)), ("u", Dev(t[0]), f32, (128,)))
+        for bad in (t, Dev(t, 1), Dev(t.half()), Dev(t.T), Dev(torch.zeros(2, 129)), Dev(torch.zeros(2, 256)[:, ::2])):
+            with pytest.raises(ValueError, match="t: expected contiguous"):
+                kvq8._need(("u", Dev(t[0]), f32, (128,)), ("t", bad, f32, (2, 128)))
     finally:
         torch.cuda.current_device = cur
+    packed = torch.zeros(3, 5, 12 * 128)
+    rows = packed[..., 256:1280].unflatten(-1, (8, 128))
+    assert kvq8._token_stride("q", rows, 3, 5, 8) == 12 * 128
+    assert kvq8._token_stride("q", rows[:1], 1, 5, 8) == 12 * 128
+    assert kvq8._token_stride("q", rows[:, :1], 3, 1, 8) == 5 * 12 * 128
+    assert kvq8._token_stride("q", rows[:1, :1], 1, 1, 8) == 8 * 128
+    wide = torch.zeros(3, 5, 8, 256)
+    for bad in (rows.transpose(1, 2).contiguous().transpose(1, 2), rows.transpose(0, 1)[:3], wide[..., ::2],
+                wide[..., :128], torch.zeros(3, 6, 8, 128)[:, :5]):
+        with pytest.raises(ValueError, match="side by side"):
+            kvq8._token_stride("q", bad, *bad.shape[:3])
