@@ -864,5 +864,15 @@ cudaError_t launch_split_gm(const DecodeParams &p, cudaStream_t s) {
         [&] { return cudaLaunchKernelEx(&cfg, decode_split_kernel<G, kMixed, kCtas, kMode>, p); });
 }
 
+// A G = 2 call: two CTAs per SM when it is large enough (see kSmemLimit2).
+template <int kMode>
+cudaError_t launch_split_two(const DecodeParams &p, cudaStream_t s) {
+    const int64_t units = (int64_t)p.batch * p.nkv;
+    const int64_t stages_max = units * p.max_blocks * (kBS / kStageTok);
+    if (units >= kTwoPerSmMinUnits && stages_max >= (int64_t)kTwoPerSmMinStages * 2 * device_sm_count())
+        return launch_split_gm<2, false, 2, kMode>(p, s);
+    return launch_split_gm<2, false, 1, kMode>(p, s);
+}
+
 }  // namespace
 }  // namespace kvq8

@@ -12,21 +12,13 @@
 #include "decode_split.cuh"
 
 namespace kvq8 {
-namespace {
-
-template <int G>
-cudaError_t launch_window_g(const DecodeParams &p, cudaStream_t s) {
-    return launch_split_gm<G, false, 1, kWindowed>(p, s);
-}
-
-}  // namespace
 
 cudaError_t launch_decode_window_split(const DecodeParams &p, int group, cudaStream_t s) {
     switch (group) {
-        case 1: return launch_window_g<1>(p, s);
-        case 2: return launch_window_g<2>(p, s);
-        case 4: return launch_window_g<4>(p, s);
-        case 8: return launch_window_g<8>(p, s);
+        case 1: return launch_split_gm<1, false, 1, kWindowed>(p, s);
+        case 2: return launch_split_two<kWindowed>(p, s);
+        case 4: return launch_split_gm<4, false, 1, kWindowed>(p, s);
+        case 8: return launch_split_gm<8, false, 1, kWindowed>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }
