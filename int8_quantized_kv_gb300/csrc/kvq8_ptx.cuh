@@ -85,6 +85,12 @@ __device__ __forceinline__ void cp_async16_cg(void *dst, const void *src) {
                  : "memory");
 }
 
+// 8 bytes (dst, src 8-byte aligned), through L1.
+__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Waits until at most N of this thread's copy groups are pending.

@@ -33,10 +33,11 @@ namespace kvq8 {
 namespace {
 
 constexpr int kTaskWarps = 4;             // warps per CTA, one task each
-constexpr int kMinCtas = 5;               // CTAs per SM
+constexpr int kMinCtas = 6;               // CTAs per SM
+constexpr int kDepth = 3;                 // stages of a warp's ring
 constexpr int kFullTasks = 152 * 32;      // tasks that fill the GPU
-constexpr int kMostGroups = 6;            // groups of four heads per turn task
-constexpr int kLongRuns = kFullTasks / 2; // value tasks of 16 slots from which on they are used
+constexpr int kMostGroups = 8;            // groups of four heads per turn task
+constexpr int kLongRuns = kFullTasks;     // value tasks of 16 slots from which on they are used
 
 // ------------------------------------------------------------- conversion --
 __device__ __forceinline__ float2 pair_of(uint32_t v, __half) {
@@ -51,23 +52,54 @@ __device__ __forceinline__ float2 load2(const T *p) { return pair_of(*reinterpre
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 __device__ __forceinline__ float load1(const __half *p) { return __half2float(*p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float4 load4(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
     const float2 a = pair_of(v.x, T()), b = pair_of(v.y, T());
     return make_float4(a.x, a.y, b.x, b.y);
 }
 // ------------------------------------------------------------- turn tasks --
 // Eight lanes to a row: lane j (of 8) holds dims 32c + 4j + i in x[4c + i] (i <
 // 4, c < 4).  Both kinds of pairs lie within a lane, and the eight lanes read
-// or write a whole 128-byte (64-byte) line of the row at a time.  (With 8
-// consecutive values a lane, every access touches half a sector.)
+// or write whole sectors of the row at a time.  (With 8 consecutive values a
+// lane every access touches half a sector, and the ring below made 8 x 4096
+// tokens slower, 165 -> 190 us, where it now takes 155 to 137.)
 template <typename T>
 __device__ __forceinline__ void load_row(const T *row, int j, float (&x)[16]) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const float4 v = load4(row + 32 * c + 4 * j);
+        x[4 * c] = v.x;
+        x[4 * c + 1] = v.y;
+        x[4 * c + 2] = v.z;
+        x[4 * c + 3] = v.w;
+    }
+}
+// The rows of a turn task (four at a time, one stage) and of a value task (four
+// rows, one stage) pass through a ring of kDepth stages in shared memory, of
+// which kDepth - 1 are in flight: what bounds the turn tasks is how many bytes
+// 24 warps keep in flight (2 KiB a warp: 79 % of the copy peak; 4 KiB: 96 %).
+// A lane copies the pieces that it reads back itself, [piece][lane], so that
+// its own copy groups order everything and the warp needs no barrier.
+template <typename T>
+__host__ __device__ constexpr int stage_bytes() {
+    return 4 * kHD * (int)sizeof(T);
+}
+__device__ __forceinline__ void copy4(void *dst, const float *src) { cp_async16_cg(dst, src); }
+template <typename T>
+__device__ __forceinline__ void copy4(void *dst, const T *src) { cp_async8(dst, src); }
+template <typename T>
+__device__ __forceinline__ void fetch_row(unsigned char *stage, const T *row, int j, int lane) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        copy4(stage + (c * 32 + lane) * 4 * (int)sizeof(T), row + 32 * c + 4 * j);
+}
+template <typename T>
+__device__ __forceinline__ void read_row(const unsigned char *stage, int lane, float (&x)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float4 v = load4(reinterpret_cast<const T *>(stage) + (c * 32 + lane) * 4);
         x[4 * c] = v.x;
         x[4 * c + 1] = v.y;
         x[4 * c + 2] = v.z;
@@ -502,7 +534,8 @@ __device__ __forceinline__ void store_queries(const NormRopeParams &p, float (&x
 // Turn task w = row * parts + c: groups [c * gp, (c + 1) * gp) of four heads
 // of a token, the query heads' groups before the kv heads'.
 template <typename T, bool kPairs>
-__device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int parts, int gp, int lane) {
+__device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int parts, int gp, int lane,
+                                           unsigned char *ring) {
     const int row = w / parts;
     const int b = row / p.n_new, i = row - b * p.n_new;
     if (p.n_tokens && i >= p.n_tokens[b]) return;   // padding
@@ -512,32 +545,37 @@ __device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int p
     const int qg = (p.nqh + 3) / 4, groups = qg + (p.nkv + 3) / 4;
     const int g0 = (w - row * parts) * gp, g1 = min(groups, g0 + gp);
     // a lane whose head is beyond the last loads the last
-    auto fetch = [&](int gi, float (&x)[16]) {
-        const bool is_q = gi < qg;
-        const int h = min((is_q ? gi : gi - qg) * 4 + g, (is_q ? p.nqh : p.nkv) - 1);
-        load_row(reinterpret_cast<const T *>(is_q ? p.q : p.k) + (int64_t)row * (is_q ? p.q_stride : p.k_stride) +
-                     (size_t)h * kHD, j, x);
+    auto fetch = [&](int gi) {
+        if (gi < g1) {
+            const bool is_q = gi < qg;
+            const int h = min((is_q ? gi : gi - qg) * 4 + g, (is_q ? p.nqh : p.nkv) - 1);
+            fetch_row(ring + (gi - g0) % kDepth * stage_bytes<T>(),
+                      reinterpret_cast<const T *>(is_q ? p.q : p.k) + (int64_t)row * (is_q ? p.q_stride : p.k_stride) +
+                          (size_t)h * kHD, j, lane);
+        }
+        cp_async_commit();   // possibly empty: one group per stage
     };
-    float x[16];
-    fetch(g0, x);
+#pragma unroll
+    for (int d = 0; d < kDepth - 1; ++d) fetch(g0 + d);
     if (pos < 0 || pos >= p.n_pos) {
         if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+        cp_async_wait<0>();
         return;
     }
     KeyPlace place = {-1, 0};
     if (g1 > qg) place = key_place(p, b, at, lane);
 #pragma unroll 1
     for (int gi = g0; gi < g1; ++gi) {
-        float nx[16];
-        if (gi + 1 < g1) fetch(gi + 1, nx);
+        cp_async_wait<kDepth - 2>();
+        float x[16];
+        read_row<T>(ring + (gi - g0) % kDepth * stage_bytes<T>(), lane, x);
+        fetch(gi + kDepth - 1);   // into the stage read before this one
         // the table row comes from L1 again for each group: kept, its 16
-        // registers push others out (166 us against 155 at 8 x 4096 tokens)
+        // registers push others out
         float c[8], s[8];
         load_turn<kPairs>(p.rope + (size_t)pos * kHD, j, c, s);
         if (gi < qg) store_queries<kPairs>(p, x, c, s, row, 4 * gi, lane);
         else if (place.tile >= 0) store_keys<T, kPairs>(p, x, c, s, row, pos, 4 * (gi - qg), place, lane);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = nx[e];
     }
 }
 
@@ -560,7 +598,8 @@ __device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
 // x of kRun cache slots, counted from the run of the first, of kv head h.
 // Places outside the table or the pool are flagged by the turn tasks.
 template <typename T, int kRun>
-__device__ __forceinline__ void append_values(const NormRopeParams &p, int w, int runs, int lane) {
+__device__ __forceinline__ void append_values(const NormRopeParams &p, int w, int runs, int lane,
+                                              unsigned char *ring) {
     const int bx = w / p.nkv, h = w - bx * p.nkv;
     const int b = bx / runs;
     const int64_t cap = (int64_t)p.max_blocks * kBS;
@@ -587,18 +626,28 @@ __device__ __forceinline__ void append_values(const NormRopeParams &p, int w, in
     const T *src = reinterpret_cast<const T *>(p.v) + (size_t)h * kHD + 4 * lane;
 
     if (todo == (1u << kRun) - 1) {
-        // the whole run, four tokens at a time, the next four being loaded
-        float4 v[4], nv[4];
+        // the whole run, four tokens at a time through the ring (a lane reads what it copied)
+        auto fetch = [&](int g) {
+            if (g < kRun / 4) {
+                unsigned char *st = ring + g % kDepth * stage_bytes<T>();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = load4(src + (row0 + u) * p.v_stride);
-        uint32_t vw[4][kRun / 4] = {};   // codes so far of dim 4 * lane + i, the last four tokens on top
+                for (int u = 0; u < 4; ++u)
+                    copy4(st + (u * 32 + lane) * 4 * (int)sizeof(T), src + (row0 + 4 * g + u) * p.v_stride);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int g = 0; g < kDepth - 1; ++g) fetch(g);
+        uint32_t vw[4][kRun / 4];        // codes of dim 4 * lane + i
         float sc_keep = 0.0f;            // lane r: scale of row r
 #pragma unroll
         for (int g = 0; g < kRun / 4; ++g) {
-            if (g + 1 < kRun / 4) {
+            cp_async_wait<kDepth - 2>();
+            float4 v[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) nv[u] = load4(src + (row0 + 4 * g + 4 + u) * p.v_stride);
-            }
+            for (int u = 0; u < 4; ++u)
+                v[u] = load4(reinterpret_cast<const T *>(ring + g % kDepth * stage_bytes<T>()) + (u * 32 + lane) * 4);
+            fetch(g + kDepth - 1);
             uint4 cv[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -610,8 +659,6 @@ __device__ __forceinline__ void append_values(const NormRopeParams &p, int w, in
             vw[1][g] = low_bytes4(make_uint4(cv[0].y, cv[1].y, cv[2].y, cv[3].y));
             vw[2][g] = low_bytes4(make_uint4(cv[0].z, cv[1].z, cv[2].z, cv[3].z));
             vw[3][g] = low_bytes4(make_uint4(cv[0].w, cv[1].w, cv[2].w, cv[3].w));
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = nv[u];
         }
         if (lane < kRun) p.v_scale[tile * kBS + slot0 + lane] = sc_keep;
 #pragma unroll
@@ -648,6 +695,7 @@ struct TaskPlan {
 template <typename T, bool kPairs, int kRun>
 __global__ void __launch_bounds__(kTaskWarps * 32, kMinCtas)
 norm_rope_append_kernel(NormRopeParams p, TaskPlan plan) {
+    __shared__ __align__(16) unsigned char rings[kTaskWarps][kDepth * stage_bytes<T>()];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -656,10 +704,10 @@ norm_rope_append_kernel(NormRopeParams p, TaskPlan plan) {
     const uint32_t v0 = __umulhi(i, plan.ratio), v1 = __umulhi(i + 1, plan.ratio);
     if (v1 > v0) {
         const int64_t w = (int64_t)v0 * kTaskWarps + warp;
-        if (w < plan.value_tasks) append_values<T, kRun>(p, (int)w, plan.runs, lane);
+        if (w < plan.value_tasks) append_values<T, kRun>(p, (int)w, plan.runs, lane, rings[warp]);
     } else {
         const int64_t w = (int64_t)(i - v0) * kTaskWarps + warp;
-        if (w < plan.turn_tasks) turn_heads<T, kPairs>(p, (int)w, plan.parts, plan.gp, lane);
+        if (w < plan.turn_tasks) turn_heads<T, kPairs>(p, (int)w, plan.parts, plan.gp, lane, rings[warp]);
     }
 }
 
