@@ -15,7 +15,7 @@ namespace kvq8 {
 namespace {
 
 // Two CTAs of 512 threads fit an SM (64 registers each); with 1024 one does,
-// and 224 units took two rounds: 21 us against @@.
+// and 224 units of 8192 tokens took two rounds.
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;                  // three digits of 11, 11 and 10 bits
@@ -40,14 +40,21 @@ struct Keys {
     const float *weight_sum;
     int nkv, h, L, first, recent0;   // tokens below first and from recent0 on are kept
     uint32_t *cache;
-    int n_cached;
+    int n_cached;                    // a multiple of 4
     __device__ __forceinline__ uint32_t key(int t, float w) const {
         return t < first || t >= recent0 ? 0xffffffffu : weight_key(w);
     }
     __device__ __forceinline__ const float *at(int t) const {
         return weight_sum + ((size_t)row[t / kBS] * nkv + h) * kBS + t % kBS;
     }
-    __device__ __forceinline__ uint32_t get(int t) const { return t < n_cached ? cache[t] : key(t, *at(t)); }
+    // Keys of the four tokens from t on, a multiple of 4 (w: their weights).
+    __device__ __forceinline__ uint4 four(int t, float4 w) const {
+        return make_uint4(key(t, w.x), key(t + 1, w.y), key(t + 2, w.z), key(t + 3, w.w));
+    }
+    __device__ __forceinline__ uint4 get4(int t) const {
+        if (t < n_cached) return *reinterpret_cast<const uint4 *>(cache + t);
+        return four(t, *reinterpret_cast<const float4 *>(at(t)));
+    }
 };
 
 // Inclusive sum over the warp's lanes from lane on to the last.
@@ -114,18 +121,30 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         return;
     }
 
-    Keys keys = {row, p.weight_sum, p.nkv, h, L, p.n_first, L - p.n_recent, sm_keys, min(L, cache_tokens)};
+    Keys keys = {row, p.weight_sum, p.nkv, h, L, p.n_first, L - p.n_recent, sm_keys, min((L + 3) / 4 * 4, cache_tokens)};
     // the m-th largest key, digit by digit from the top: `prefix` holds the
     // digits found, `need` how many tokens with exactly this prefix are kept.
     // The first digit is counted as the weights are loaded, four at a time.
-    for (int t = 4 * tid; t < L; t += 4 * kSelectThreads) {
-        const float4 w = *reinterpret_cast<const float4 *>(keys.at(t));   // (within the block: t % 4 == 0)
-        const uint4 k = make_uint4(keys.key(t, w.x), keys.key(t + 1, w.y), keys.key(t + 2, w.z), keys.key(t + 3, w.w));
-        if (t < keys.n_cached) *reinterpret_cast<uint4 *>(sm_keys + t) = k;   // (room for whole fours)
-        atomicAdd(&hist[k.x >> 21], 1);
-        if (t + 1 < L) atomicAdd(&hist[k.y >> 21], 1);
-        if (t + 2 < L) atomicAdd(&hist[k.z >> 21], 1);
-        if (t + 3 < L) atomicAdd(&hist[k.w >> 21], 1);
+    constexpr int kAhead = 4;   // weights loaded at once, in fours per thread
+    for (int t0 = 4 * tid; t0 < L; t0 += kAhead * 4 * kSelectThreads) {
+        float4 w[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = t0 + i * 4 * kSelectThreads;
+            if (t < L) w[i] = *reinterpret_cast<const float4 *>(keys.at(t));   // (t % 4 == 0: within the block)
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = t0 + i * 4 * kSelectThreads;
+            if (t < L) {
+                const uint4 k = keys.four(t, w[i]);
+                if (t < keys.n_cached) *reinterpret_cast<uint4 *>(sm_keys + t) = k;
+                atomicAdd(&hist[k.x >> 21], 1);
+                if (t + 1 < L) atomicAdd(&hist[k.y >> 21], 1);
+                if (t + 2 < L) atomicAdd(&hist[k.z >> 21], 1);
+                if (t + 3 < L) atomicAdd(&hist[k.w >> 21], 1);
+            }
+        }
     }
     uint32_t prefix = 0;
     int need = m;
@@ -134,9 +153,13 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         if (pass > 0) {
             const int above = pass == 1 ? 21 : 10;
-            for (int t = tid; t < L; t += kSelectThreads) {
-                const uint32_t k = keys.get(t);
-                if ((k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & (pass == 1 ? kBins - 1 : 1023)], 1);
+            for (int t = 4 * tid; t < L; t += 4 * kSelectThreads) {
+                const uint4 k4 = keys.get4(t);
+                const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t + i < L && (k[i] >> above) == (prefix >> above))
+                        atomicAdd(&hist[(k[i] >> shift) & (pass == 1 ? kBins - 1 : 1023)], 1);
             }
         }
         __syncthreads();
@@ -169,14 +192,30 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
     // tokens above the m-th largest are kept, and the first `need` equal to it:
     // each warp counts both in its share of the tokens, and writes them behind
     // those of the warps before it
-    const int share = ((L + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int share = ((L + kSelectWarps - 1) / kSelectWarps + 127) / 128 * 128;
     const int t_lo = min(L, warp * share), t_hi = min(L, t_lo + share);
+    // (tokens above, tokens equal) of the four tokens from t on
+    auto count4 = [&](uint4 k4, int t, bool (&gt)[4], bool (&eq)[4]) {
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        int n_gt = 0, n_eq = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            gt[i] = t + i < t_hi && k[i] > prefix;
+            eq[i] = t + i < t_hi && k[i] == prefix;
+            n_gt += gt[i];
+            n_eq += eq[i];
+        }
+        return make_int2(n_gt, n_eq);
+    };
+    bool is_gt[4], is_eq[4];
     int gt = 0, eq = 0;
-    for (int t = t_lo; t < t_hi; t += 32) {
-        const uint32_t k = t + lane < t_hi ? keys.get(t + lane) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, t + lane < t_hi && k > prefix));
-        eq += __popc(__ballot_sync(0xffffffffu, t + lane < t_hi && k == prefix));
+    for (int t = t_lo + 4 * lane; t < t_hi; t += 128) {
+        const int2 c = count4(keys.get4(t), t, is_gt, is_eq);
+        gt += c.x;
+        eq += c.y;
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
         warp_a[warp] = gt;
         warp_b[warp] = eq;
@@ -184,16 +223,26 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
     __syncthreads();
     gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);   // (warp < kSelectWarps <= 32)
     eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
-    for (int t = t_lo; t < t_hi; t += 32) {
-        const uint32_t k = t + lane < t_hi ? keys.get(t + lane) : 0u;
-        const bool is_gt = t + lane < t_hi && k > prefix, is_eq = t + lane < t_hi && k == prefix;
-        const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-        const unsigned below = (1u << lane) - 1;
-        const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
-        if (is_gt) kept[ng + min(ne, need)] = t + lane;
-        else if (is_eq && ne < need) kept[ng + ne] = t + lane;
-        gt += __popc(bg);
-        eq += __popc(be);
+    for (int t0 = t_lo; t0 < t_hi; t0 += 128) {
+        const int t = t0 + 4 * lane;
+        const int2 c = count4(t < t_hi ? keys.get4(t) : make_uint4(0u, 0u, 0u, 0u), t, is_gt, is_eq);
+        int run = c.x | c.y << 16, incl = run;   // both at most 128
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
+        run = incl - run;
+        int ng = gt + (run & 0xffff), ne = eq + (run >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (is_gt[i] || (is_eq[i] && ne < need)) kept[ng + min(ne, need)] = t + i;
+            ng += is_gt[i];
+            ne += is_eq[i];
+        }
+        gt += all & 0xffff;
+        eq += all >> 16;
     }
 }
 
