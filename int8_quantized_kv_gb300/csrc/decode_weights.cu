@@ -13,8 +13,12 @@
 namespace kvq8 {
 namespace {
 
-constexpr int kTokThread = 4;                    // tokens per thread of a weights block
-constexpr int kChunkTok = kTokThread * kHD;      // tokens per weights block
+constexpr int kRowTok = 4 * kHD;                 // tokens that a block takes at once, four per thread
+// Times that a weights block does so: twice, so that half as many blocks look
+// for the softmax's maximum and sum (28 layers at 8K: 87.6 -> 86.2 us; 4 x
+// 128K, G = 4: 195.9 -> 193.7 us; four times spills).  G = 8 has no registers
+// for it.
+constexpr int block_rows(int G) { return G >= 8 ? 1 : 2; }
 
 // The output of one (sequence, query head), thread = dim: the merge rule of
 // decode_combine_kernel with the records' (M, S) spread over the lanes, so that
@@ -55,7 +59,7 @@ __device__ __forceinline__ void combine_row_lanes(const DecodeParams &p, int G, 
 }
 
 // Blocks [0, batch * nqh): the output row of one (sequence, query head).  The
-// others: kChunkTok tokens of one unit, whose scores and sums are loaded
+// others: block_rows(G) * kRowTok tokens of one unit, whose scores and sums are loaded
 // before the softmax's maximum and sum are known.
 template <int G>
 __global__ void __launch_bounds__(kHD, 8)
@@ -72,23 +76,27 @@ weights_merge_kernel(DecodeParams p, int chunks) {
     const int w = blockIdx.x - rows;
     const int u = w / chunks, b = u / p.nkv, h = u % p.nkv;
     const int cap = p.max_blocks * kBS;
-    const int t = (w % chunks) * kChunkTok + kTokThread * tid;
+    constexpr int kRows = block_rows(G);
+    const int t_lo = (w % chunks) * (kRows * kRowTok) + 4 * tid;
     const int Lraw = p.ctx_lens[b];
     const int2 meta = p.ws_meta[u];
     const int L = clamp_len(Lraw, cap);
-    if (t - kTokThread * tid >= L) return;
-    int phys = -1;
-    float4 sc[G], old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float *dst = p.weight_sum;
-    if (t < L) {
-        phys = p.block_table[(size_t)b * p.max_blocks + t / kBS];
-        const float *src = p.ws_scores + (size_t)u * G * cap + t;
+    if (t_lo - 4 * tid >= L) return;
+    float4 sc[kRows][G], old[kRows];
+    float *dst[kRows];
 #pragma unroll
-        for (int g = 0; g < G; ++g) sc[g] = __ldcs(reinterpret_cast<const float4 *>(src + (size_t)g * cap));
-        if (phys >= p.num_blocks) phys = -1;   // (flagged by the split)
-        if (phys >= 0) {
-            dst += ((size_t)phys * p.nkv + h) * kBS + t % kBS;
-            old = *reinterpret_cast<const float4 *>(dst);
+    for (int r = 0; r < kRows; ++r) {
+        const int t = t_lo + r * kRowTok;
+        dst[r] = nullptr;
+        if (t < L) {
+            const int phys = p.block_table[(size_t)b * p.max_blocks + t / kBS];
+            const float *src = p.ws_scores + (size_t)u * G * cap + t;
+#pragma unroll
+            for (int g = 0; g < G; ++g) sc[r][g] = __ldcs(reinterpret_cast<const float4 *>(src + (size_t)g * cap));
+            if (phys >= 0 && phys < p.num_blocks) {   // (else flagged by the split)
+                dst[r] = p.weight_sum + ((size_t)phys * p.nkv + h) * kBS + t % kBS;
+                old[r] = *reinterpret_cast<const float4 *>(dst[r]);
+            }
         }
     }
     // the softmax's maximum and sum over the unit's records
@@ -109,30 +117,34 @@ weights_merge_kernel(DecodeParams p, int chunks) {
         }
     }
     __syncthreads();
-    if (phys < 0) return;
-    float4 w4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const float m = sm_m[g], inv = sm_inv[g];
-        if (inv > 0.0f) {
-            w4.x = fmaf(ex2_approx(sc[g].x - m), inv, w4.x);
-            w4.y = fmaf(ex2_approx(sc[g].y - m), inv, w4.y);
-            w4.z = fmaf(ex2_approx(sc[g].z - m), inv, w4.z);
-            w4.w = fmaf(ex2_approx(sc[g].w - m), inv, w4.w);
-        }
-    }
     // a step's new token starts its sum here (none for a length beyond the table)
     const int fresh = p.k_new && Lraw == L ? L - 1 : -1;
-    const float v[4] = {w4.x, w4.y, w4.z, w4.w};
-    const float o[4] = {old.x, old.y, old.z, old.w};
-    if (t + kTokThread <= L) {
-        *reinterpret_cast<float4 *>(dst) =
-            make_float4(t == fresh ? v[0] : o[0] + v[0], t + 1 == fresh ? v[1] : o[1] + v[1],
-                        t + 2 == fresh ? v[2] : o[2] + v[2], t + 3 == fresh ? v[3] : o[3] + v[3]);
-    } else {
 #pragma unroll
-        for (int i = 0; i < kTokThread; ++i)
-            if (t + i < L) dst[i] = t + i == fresh ? v[i] : o[i] + v[i];
+    for (int r = 0; r < kRows; ++r) {
+        if (!dst[r]) continue;
+        const int t = t_lo + r * kRowTok;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float m = sm_m[g], inv = sm_inv[g];
+            if (inv > 0.0f) {
+                v[0] = fmaf(ex2_approx(sc[r][g].x - m), inv, v[0]);
+                v[1] = fmaf(ex2_approx(sc[r][g].y - m), inv, v[1]);
+                v[2] = fmaf(ex2_approx(sc[r][g].z - m), inv, v[2]);
+                v[3] = fmaf(ex2_approx(sc[r][g].w - m), inv, v[3]);
+            }
+        }
+        const float o[4] = {old[r].x, old[r].y, old[r].z, old[r].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t + i != fresh) v[i] += o[i];
+        if (t + 4 <= L) {
+            *reinterpret_cast<float4 *>(dst[r]) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + i < L) dst[r][i] = v[i];
+        }
     }
 }
 
@@ -151,14 +163,15 @@ cudaError_t launch_merge_g(const DecodeParams &p, int chunks, unsigned grid, cud
     return cudaLaunchKernelEx(&cfg, weights_merge_kernel<G>, p, chunks);
 }
 
-int weights_chunks(int max_blocks) {
-    return (int)(((int64_t)max_blocks * kBS + kChunkTok - 1) / kChunkTok);
+int weights_chunks(int max_blocks, int group) {
+    const int64_t tokens = block_rows(group) * kRowTok;
+    return (int)(((int64_t)max_blocks * kBS + tokens - 1) / tokens);
 }
 
 }  // namespace
 
 int64_t weights_merge_blocks(int batch, int nqh, int nkv, int max_blocks) {
-    return (int64_t)batch * nqh + (int64_t)batch * nkv * weights_chunks(max_blocks);
+    return (int64_t)batch * nqh + (int64_t)batch * nkv * weights_chunks(max_blocks, nqh / nkv);
 }
 
 cudaError_t launch_decode_weights_split(const DecodeParams &p, int group, cudaStream_t s) {
@@ -172,7 +185,7 @@ cudaError_t launch_decode_weights_split(const DecodeParams &p, int group, cudaSt
 }
 
 cudaError_t launch_weights_merge(const DecodeParams &p, int group, cudaStream_t s) {
-    const int chunks = weights_chunks(p.max_blocks);
+    const int chunks = weights_chunks(p.max_blocks, group);
     const int64_t blocks = weights_merge_blocks(p.batch, p.nqh, p.nkv, p.max_blocks);
     if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
     switch (group) {
