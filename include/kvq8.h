@@ -365,6 +365,16 @@ kvq8_status kvq8_selftest_bounded_wait(uint32_t *dev_status, uint64_t timeout_ns
 /* --------------------------- sliding window with first tokens (sinks) --- */
 
 /*
+ * Rounding in the operators from here to kvq8_norm_rope_append: where
+ * kvq8_quantize_append, kvq8_quantize_q and kvq8_decode_step divide, these
+ * multiply by rounded reciprocals (cheaper, and as near to the exact quotient
+ * to half a step): a row's scale is max|v| * (1/127), a query block's factor
+ * 127 * (1/qm), 1/127 and 1/qm rounded to fp32.  A scale may differ from the
+ * other rule's in its last bit, and a code by one where its value lies within
+ * a few 2^-24 of a border; everything else is as there.
+ */
+
+/*
  * kvq8_decode_attn_window -- kvq8_decode_attn over a sliding window and the
  * first tokens: of a sequence of L = ctx_lens[b] tokens, token t is attended
  * when t < sinks or t >= L - windows[b].  Only the 64-token stages that hold
@@ -511,9 +521,7 @@ kvq8_status kvq8_rope_table(const double *inv_freq, int n_pos, int hd, float *ta
  * Keys: scale = max|y| * (1/127) and code = round_half_even(127 y / max|y|);
  * the code is the one of the exactly computed y (0 where the scale is 0).
  * Values: scale = max|v| * (1/127), code = round_half_even(v / scale) clamped
- * to [-127, 127].  (1/127 rounded to fp32, as in the query's rule: the product
- * saves a row the division of kvq8_quantize_append, from whose scale it is at
- * most the last bit away.)  A key or value row that
+ * to [-127, 127].  A key or value row that
  * comes out with a NaN or an infinity is stored as a row of zeros and flagged
  * KVQ8_DEV_NONFINITE; query rows are IEEE arithmetic, unflagged.
  *

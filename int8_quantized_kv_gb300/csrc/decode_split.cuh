@@ -215,11 +215,13 @@ __device__ __forceinline__ bool slot_turn_bounded(volatile int *done, int round,
 // kernels), written over the row the copy brought in (K row with its chunk
 // order, V column of the dim-major quarter, both scales) and into the pools
 // and scale arrays.  Only this CTA reads that position in this launch.  The
-// block id is valid: the stage was copied.
+// block id is valid: the stage was copied.  kRecip: the scale's rule of
+// kv_row_scale_checked.
+template <bool kRecip>
 __device__ __noinline__ void append_new_token(const DecodeParams &p, int b, int h, int pos, int t,
                                                  int lane, unsigned char *st, float4 xk, float4 xv, int phys) {
     if (phys < 0) phys = p.block_table[(size_t)b * p.max_blocks + pos / kBS];
-    const float sk = kv_row_scale_checked(xk, p.dev_status), sv = kv_row_scale_checked(xv, p.dev_status);
+    const float sk = kv_row_scale_checked<kRecip>(xk, p.dev_status), sv = kv_row_scale_checked<kRecip>(xv, p.dev_status);
     const uint32_t wk = low_bytes4(kv_code_bytes4(xk, sk));
     const uint4 cv = kv_code_bytes4(xv, sv);
     const int slot = pos % kBS;   // slot & 7 == t & 7: stages start at multiples of 64
@@ -506,7 +508,7 @@ decode_split_kernel(DecodeParams p) {
 #pragma unroll
             for (int i = 0; i < kQRows; ++i) {
                 const int g = warp + i * kConsumerWarps;
-                if (g < G) quantize_q_vals_warp(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
+                if (g < G) quantize_q_vals_warp<kMode != kWhole>(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
             }
             named_barrier_sync(1, kConsumerWarps * 32);
             if (remaining > seg_n) {   // the next segment's unit follows this one
@@ -553,7 +555,7 @@ decode_split_kernel(DecodeParams p) {
                             nxk = reinterpret_cast<const float4 *>(p.k_new + src)[lane];
                             nxv = reinterpret_cast<const float4 *>(p.v_new + src)[lane];
                         }
-                        append_new_token(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
+                        append_new_token<kMode != kWhole>(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
                     }
                     const int ta = lane, tb = lane + 32;
                     bool va = ta < nvalid, vb = tb < nvalid;

@@ -97,6 +97,8 @@ __device__ __forceinline__ bool nonfinite(float v) {
 // pattern: non-negative floats order like their bit patterns, infinity above
 // every finite value and NaN above infinity, so one unsigned warp reduction
 // gives both the row maximum and the test.
+// kRecip: the scale is the product with the rounded 1/127.
+template <bool kRecip = false>
 __device__ __forceinline__ float kv_row_scale_checked(float4 &x, uint32_t *status) {
     const uint32_t a = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
                            max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
@@ -106,7 +108,7 @@ __device__ __forceinline__ float kv_row_scale_checked(float4 &x, uint32_t *statu
         if ((threadIdx.x & 31) == 0) flag_status(status, KVQ8_DEV_NONFINITE);
         return 0.0f;
     }
-    return kv_row_scale(__uint_as_float(m));
+    return kRecip ? __fmul_rn(__uint_as_float(m), KVQ8_INV127) : kv_row_scale(__uint_as_float(m));
 }
 
 // 32-block query rule ([Day 9-2] §2 segment 1) for one row of 128 values,
@@ -118,6 +120,9 @@ __device__ __forceinline__ float kv_row_scale_checked(float4 &x, uint32_t *statu
 // four block maxima are four independent unsigned warp reductions of |x| as
 // bit patterns (the order of kv_row_scale_checked), which also detect the
 // non-finite blocks.
+// kRecip: the factor 127/qm is the product of the rounded 1/qm with 127 (the
+// windowed and scored decodes).
+template <bool kRecip = false>
 __device__ __forceinline__ void quantize_q_vals_warp(const float (&xs)[4], int lane, int8_t *codes,
                                                      float *scales, uint32_t *status) {
     uint32_t mb[4];
@@ -135,7 +140,7 @@ __device__ __forceinline__ void quantize_q_vals_warp(const float (&xs)[4], int l
             qm = __uint_as_float(mb[k]);
             if (qm < 1e-6f) qm = 1.0f;
         }
-        const float iq = __fdiv_rn(127.0f, qm);
+        const float iq = kRecip ? __fmul_rn(__frcp_rn(qm), 127.0f) : __fdiv_rn(127.0f, qm);
         int c = __float2int_rn(__fmul_rn(x, iq));
         c = max(-128, min(127, c));
         codes[32 * k + lane] = (int8_t)c;

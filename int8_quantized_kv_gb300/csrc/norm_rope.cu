@@ -580,20 +580,6 @@ __device__ __forceinline__ void turn_heads(const NormRopeParams &p, int w, int p
 }
 
 // ------------------------------------------------------------ value tasks --
-// Largest |x| of a row held as a float4 per lane; a row with a NaN or an
-// infinity is cleared and flagged, and its maximum is 0.
-__device__ __forceinline__ float row_max_checked(float4 &x, uint32_t *status) {
-    const uint32_t a = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
-                           max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
-    const uint32_t m = __reduce_max_sync(0xffffffffu, a);
-    if (m >= 0x7f800000u) {   // warp-uniform
-        x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if ((threadIdx.x & 31) == 0) flag_status(status, KVQ8_DEV_NONFINITE);
-        return 0.0f;
-    }
-    return __uint_as_float(m);
-}
-
 // Value task w = (b * runs + x) * nkv + h: the new tokens of sequence b in run
 // x of kRun cache slots, counted from the run of the first, of kv head h.
 // Places outside the table or the pool are flagged by the turn tasks.
@@ -651,7 +637,7 @@ __device__ __forceinline__ void append_values(const NormRopeParams &p, int w, in
             uint4 cv[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float sc = __fmul_rn(row_max_checked(v[u], p.dev_status), KVQ8_INV127);
+                const float sc = kv_row_scale_checked<true>(v[u], p.dev_status);
                 cv[u] = kv_code_bytes4(v[u], sc);
                 if (lane == 4 * g + u) sc_keep = sc;
             }
@@ -675,7 +661,7 @@ __device__ __forceinline__ void append_values(const NormRopeParams &p, int w, in
     for (unsigned left = todo; left; left &= left - 1) {
         const int r = __ffs(left) - 1;
         float4 v = load4(src + (row0 + r) * p.v_stride);
-        const float sc = __fmul_rn(row_max_checked(v, p.dev_status), KVQ8_INV127);
+        const float sc = kv_row_scale_checked<true>(v, p.dev_status);
         const uint4 c = kv_code_bytes4(v, sc);
         vrun[(size_t)(4 * lane + 0) * kStageTok + r] = (int8_t)c.x;
         vrun[(size_t)(4 * lane + 1) * kStageTok + r] = (int8_t)c.y;

@@ -4,9 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-import oracle
+import cache_ops_ref as ref
 from int8_quantized_kv_gb300 import kvq8
-from kvq8_harness import SM_SCALE, assert_close, k_rows_logical, v_rows_logical
+from kvq8_harness import assert_close, k_rows_logical, v_rows_logical
 
 pytestmark = pytest.mark.gpu
 HD = 128
@@ -63,9 +63,8 @@ class Loop:
             for h in range(self.nkv):
                 kq, ks, vq, vs = self.unit(table, b, h, lens[b])
                 vis = np.arange(lens[b]) if seen is None else seen[b]
-                qi, qsc = oracle.q_quantize_blocks(q[b, h * 4:(h + 1) * 4].cpu().numpy())
-                ref = oracle.decode_quantized_unit(qi, qsc, kq[vis], ks[vis], vq[vis], vs[vis], SM_SCALE)
-                assert_close(out[b, h * 4:(h + 1) * 4].cpu().numpy(), ref, f"b={b} h={h}")
+                want = ref.decode(q[b, h * 4:(h + 1) * 4].cpu().numpy(), kq[vis], ks[vis], vq[vis], vs[vis])
+                assert_close(out[b, h * 4:(h + 1) * 4].cpu().numpy(), want, f"b={b} h={h}")
 
 
 def test_prompt_decode_evict_decode(gpu_lib):
@@ -85,11 +84,7 @@ def test_prompt_decode_evict_decode(gpu_lib):
         for b in range(2):
             for h in range(s.nkv):
                 kq, ks, vq, vs = s.unit(s.table, b, h, lens[b])
-                qi, qsc = oracle.q_quantize_blocks(q[b, h * 4:(h + 1) * 4].cpu().numpy())
-                for g in range(4):
-                    w = oracle.scores_q8(qi[g], qsc[g], kq, ks, SM_SCALE)
-                    w = np.exp(w - w.max())
-                    sums[b, h, :lens[b]] += w / w.sum()
+                sums[b, h, :lens[b]] += ref.weights(q[b, h * 4:(h + 1) * 4].cpu().numpy(), kq, ks)[0]
     t = np.arange(1024)
     got = s.wsum.cpu().numpy()
     for b in range(2):

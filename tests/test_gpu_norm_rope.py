@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+from cache_ops_ref import row_codes
 from int8_quantized_kv_gb300 import kvq8
 from kvq8_harness import k_rows_logical, v_rows_logical
 
@@ -40,15 +41,6 @@ def _turned(x, w, eps, cs, pairs):
     else:
         y[..., :64], y[..., 64:], n[..., :64], n[..., 64:] = ya, yb, r, r
     return y, n
-
-
-def _v_rule(v):
-    """V rows by the documented fp32 rule (non-finite rows as zeros)."""
-    v = np.where(np.isfinite(v).all(-1, keepdims=True), v, np.float32(0))
-    s = np.abs(v).max(-1) * (np.float32(1) / np.float32(127))
-    with np.errstate(all="ignore"):
-        c = np.where(s[..., None] == 0, np.float32(0), np.rint(v / s[..., None]))
-    return np.clip(c, -127, 127).astype(np.int8), s
 
 
 def _k_codes(y):
@@ -139,7 +131,7 @@ class Case:
             # the exact codes are meant: a case whose values sit on a border to within fp64 would say nothing
             assert border[~bad].min(initial=1) > 1e-10 or not self._generic
             phys, slot = self.table[b, (self.start[b] + rows) // 256], (self.start[b] + rows) % 256
-            vc, vsc = _v_rule(self.x[b, rows][:, nqh + nkv:])
+            vc, vsc = row_codes(self.x[b, rows][:, nqh + nkv:])
             for h in range(nkv):
                 got = k_rows_logical(kp, phys, h, slot)
                 assert np.array_equal(got, codes[:, h]), (b, h, np.argwhere(got != codes[:, h])[:5])

@@ -13,10 +13,10 @@ import numpy as np
 import pytest
 import torch
 
-import oracle
+import cache_ops_ref as ref
 from int8_quantized_kv_gb300 import kvq8
 from int8_quantized_kv_gb300 import workloads as wl
-from kvq8_harness import SM_SCALE, Case, StepCase, assert_close
+from kvq8_harness import Case, StepCase, assert_close
 
 pytestmark = pytest.mark.gpu
 
@@ -36,17 +36,11 @@ def _run(case, wsum, step=False, table=None, ws=None):
     return out.cpu().numpy()
 
 
-def _unit_weights(case, b, h, L):
-    cfg, G = case.cfg, case.cfg.group
-    k, v = wl.unit_kv(cfg, b, h, L)
-    kq, ks = oracle.kv_quantize_rows(k)
-    qi, qsc = oracle.q_quantize_blocks(case.q[b, h * G:(h + 1) * G])
-    p = np.zeros(L)
-    for g in range(G):
-        s = oracle.scores_q8(qi[g], qsc[g], kq, ks, SM_SCALE)
-        assert np.abs(s).max() / np.log(2) <= 64
-        w = np.exp(s - s.max())
-        p += w / w.sum()
+def _unit_weights(case, b, h, L, step):
+    G = case.cfg.group
+    kq, ks, _, _ = ref.unit_rows(*wl.unit_kv(case.cfg, b, h, L), step)
+    p, most = ref.weights(case.q[b, h * G:(h + 1) * G], kq, ks)
+    assert most <= 64
     return p
 
 
@@ -62,7 +56,7 @@ def _check_sums(case, before, after, step=False, lens=None):
         t = np.arange(L)
         phys, slot = case.table[b, t // 256], t % 256
         for h in range(cfg.nkv):
-            p = _unit_weights(case, b, h, L)
+            p = _unit_weights(case, b, h, L, step)
             if step:
                 want[phys[-1], h, slot[-1]] = 0.0
             want[phys, h, slot] += p
@@ -84,8 +78,7 @@ def test_output_and_sums(gpu_lib, G):
     before, wsum = _sums(case)
     plain = case.decode()
     got = _run(case, wsum)
-    ref_b = 8
-    assert_close(got[ref_b, :G], case.oracle_unit(ref_b, 0), "out")
+    assert_close(got[8, :G], ref.decode(case.q[8, :G], *ref.unit_rows(*wl.unit_kv(cfg, 8, 0, lens[8]))), "out")
     assert_close(got, plain, "against the plain decode")
     _check_sums(case, before, wsum.cpu().numpy())
     assert case.status_bits() == 0
@@ -118,13 +111,14 @@ def test_step_starts_the_new_tokens_sum(gpu_lib, G):
             wsum[int(case.table[b, (L - 1) // 256]), :, (L - 1) % 256] = float("nan")
     got = _run(case, wsum, step=True)
     _check_sums(case, before, wsum.cpu().numpy(), step=True)
-    full = Case(cfg, lens=lens)
-    pools, fpools = case.host_pools(), full.host_pools()
+    pools = case.host_pools()
     for b in range(cfg.batch):
         for h in range(2):
-            for x, y in zip(case.gather_unit(pools, b, h), full.gather_unit(fpools, b, h)):
-                assert np.array_equal(x, y)
-    assert np.array_equal(got, _run(full, torch.zeros_like(wsum)))
+            if lens[b]:
+                for x, y in zip(case.gather_unit(pools, b, h), ref.unit_rows(*wl.unit_kv(cfg, b, h, lens[b]), True)):
+                    assert np.array_equal(x, y)
+    # the token is in the cache now: the same decode without the append
+    assert np.array_equal(got, _run(case, torch.zeros_like(wsum)))
 
 
 def test_steep_scores(gpu_lib):
@@ -145,8 +139,7 @@ def test_steep_scores(gpu_lib):
     w = wsum.cpu().numpy()[np.array([2, 0, 1])[t // 256], 0, t % 256]
     top = 2 * L // 3
     assert abs(w[top] - G) <= 1e-4 * G and np.all(np.delete(w, top) <= 1e-4)
-    ref, _ = oracle.decode_unit_q8(q, k, v, SM_SCALE)
-    assert_close(out.cpu().numpy()[0], ref)
+    assert_close(out.cpu().numpy()[0], ref.decode(q, *ref.unit_rows(k, v)))
 
 
 def test_bad_lengths_and_blocks(gpu_lib):
@@ -163,12 +156,9 @@ def test_bad_lengths_and_blocks(gpu_lib):
     for b, vis in ((0, np.r_[0:256, 512:600]), (1, np.arange(256, 600))):
         for h in range(2):
             k, v = wl.unit_kv(cfg, b, h, 600)
-            ref, qz = oracle.decode_unit_q8(case.q[b, h * G:(h + 1) * G], k[vis], v[vis], SM_SCALE)
-            assert_close(got[b, h * G:(h + 1) * G], ref)
-            for g in range(G):
-                s = oracle.scores_q8(qz["qi"][g], qz["qsc"][g], qz["kq"], qz["ks"], SM_SCALE)
-                w = np.exp(s - s.max())
-                want[case.table[b, vis // 256], h, vis % 256] += w / w.sum()
+            rows = ref.unit_rows(k[vis], v[vis])
+            assert_close(got[b, h * G:(h + 1) * G], ref.decode(case.q[b, h * G:(h + 1) * G], *rows))
+            want[case.table[b, vis // 256], h, vis % 256] += ref.weights(case.q[b, h * G:(h + 1) * G], *rows[:2])[0]
     assert np.abs(after - want).max() <= 1e-4
     untouched = np.ones(before.shape, bool)
     for b, vis in ((0, np.r_[0:256, 512:600]), (1, np.arange(256, 600))):
