@@ -577,7 +577,8 @@ kvq8_status kvq8_evict(int batch, int nkv, int hd, int8_t *k_pool, int8_t *v_poo
         return KVQ8_ERR_INVALID_ARG;
     if (keep < 1 || n_first < 0 || n_recent < 0 || n_first > keep || n_recent > keep - n_first)
         return KVQ8_ERR_INVALID_ARG;
-    if (max_blocks > 2147483647 / kBS || dst_max_blocks > 2147483647 / kBS) return KVQ8_ERR_UNSUPPORTED;
+    // (the selection steps through positions 8192 at a time in 32 bits)
+    if (max_blocks > (1 << 30) / kBS || dst_max_blocks > (1 << 30) / kBS) return KVQ8_ERR_UNSUPPORTED;
     if (batch > kMaxGridYZ || nkv > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
     if (keep > dst_max_blocks * kBS) return KVQ8_ERR_INVALID_ARG;
     if (batch == 0) return KVQ8_OK;

@@ -21,7 +21,9 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;                  // three digits of 11, 11 and 10 bits
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kThreadBins = kBins / kSelectThreads;
-constexpr int kMostCached = 40 * 1024;          // tokens whose keys stay in shared memory (160 KiB)
+// Tokens whose keys stay in shared memory: 96 KiB, so that two CTAs share an SM
+// even where the table is wide (the keys of the others are made again from L2).
+constexpr int kMostCached = 24 * 1024;
 
 // Order of a weight as an unsigned number: larger weights above smaller ones,
 // -0 equal to 0, a NaN below everything.  Nothing maps to 0xffffffff, which

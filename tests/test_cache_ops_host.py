@@ -95,6 +95,8 @@ def test_evict_refusals(lib):
     assert _evict(lib, hd=96) == kvq8.ERR_UNSUPPORTED
     assert _evict(lib, bs=64) == kvq8.ERR_UNSUPPORTED
     assert _evict(lib, batch=65536) == kvq8.ERR_UNSUPPORTED
+    assert _evict(lib, max_blocks=2**22 + 1) == kvq8.ERR_UNSUPPORTED       # more than 2^30 positions
+    assert _evict(lib, dst_blocks=2**22 + 1) == kvq8.ERR_UNSUPPORTED
     assert _evict(lib, batch=60000, nkv=60000, keep=2, first=0, recent=0) == kvq8.ERR_UNSUPPORTED   # more kept rows than 2^31
     for bad in (dict(keep=0, first=0, recent=0), dict(keep=-5), dict(first=-1), dict(recent=-1),
                 dict(keep=35), dict(keep=300, first=301, recent=0), dict(first=2**31 - 1, recent=2**31 - 1),

@@ -257,3 +257,75 @@ def test_binding_refuses_wrong_tensors(gpu_lib):
         kvq8.norm_rope_append(st["q"][:, None], st["k"][:, None], st["v"][:, None],
                               torch.ones(HD, device="cuda"), None, 1e-6, st["rope"], st["start"], st["table"],
                               st["cache"], o[:, None])
+
+
+def test_streams_at_once(gpu_lib):
+    want = []
+    for i in range(4):
+        st = _state(10 + i)
+        for _ in range(10):
+            _all(st)
+        want.append(_result(st))
+    states, streams = [_state(10 + i) for i in range(4)], [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(10):         # the calls of the four streams overlap
+        for st, s in zip(states, streams):
+            _all(st, stream=s)
+    for st, ref_ in zip(states, want):
+        assert all(np.array_equal(x, y) for x, y in zip(_result(st), ref_))
+
+
+def test_page_locked_host_buffers(gpu_lib):
+    # q, the new rows and out in host memory, read and written by the kernels
+    a, b = _state(20), _state(20)
+    kw = dict(dev_status=a["status"])
+    o = torch.zeros_like(a["q"])
+    kvq8.decode_step_window(a["q"], a["k"], a["v"], a["cache"], a["table"], a["lens"], a["windows"], 4, o, a["ws"], **kw)
+    w = torch.zeros_like(a["q"])
+    kvq8.decode_step_weights(a["q"], a["k"], a["v"], a["cache"], a["table"], a["lens"], w, a["wsum"], a["ws"], **kw)
+    host = {n: b[n].cpu().pin_memory() for n in ("q", "k", "v")}
+    oh, wh = torch.zeros_like(host["q"]).pin_memory(), torch.zeros_like(host["q"]).pin_memory()
+    q, k, v = (kvq8.HostMapped(host[n]) for n in ("q", "k", "v"))
+    kvq8.decode_step_window(q, k, v, b["cache"], b["table"], b["lens"], b["windows"], 4, kvq8.HostMapped(oh), b["ws"])
+    kvq8.decode_step_weights(q, k, v, b["cache"], b["table"], b["lens"], kvq8.HostMapped(wh), b["wsum"], b["ws"])
+    torch.cuda.synchronize()
+    assert torch.equal(o.cpu(), oh) and torch.equal(w.cpu(), wh) and torch.equal(a["wsum"], b["wsum"])
+    with pytest.raises(ValueError):
+        kvq8.decode_step_window(q, k, v, b["cache"], b["table"], b["lens"], b["windows"], 4, o[:1], b["ws"])
+
+
+def test_pools_past_32_bits(gpu_lib):
+    # block ids whose tiles lie beyond 2^32 bytes (and 2^31 tokens' worth of codes) of the pools
+    nb, nkv, nqh = 20000, 8, 16
+    cache, wsum = kvq8.alloc_cache(nb, nkv), torch.empty((nb, nkv, 256), device="cuda")
+    assert cache.k_pool.numel() > 2**32
+    small, small_sum = kvq8.alloc_cache(8, nkv), torch.empty((8, nkv, 256), device="cuda")
+    high = np.array([[19999, 19990, 19001], [18003, 17777, 16500]], np.int32)     # the last: destinations
+    low = np.array([[0, 1, 2], [3, 4, 5]], np.int32)
+    rng = np.random.default_rng(21)
+    L = 700
+    x = torch.from_numpy(rng.standard_normal((1, L, nqh + 2 * nkv, HD), np.float32)).cuda()
+    rope = kvq8.rope_table(_dev(1e4 ** (-np.arange(64) / 64.0)), 1024)
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    got = []
+    for c, w, t in ((cache, wsum, high), (small, small_sum, low)):
+        table, dst = _dev(t[:1]), _dev(t[1:])
+        out = torch.empty((1, L, nqh, HD), device="cuda")
+        kvq8.norm_rope_append(x[:, :, :nqh], x[:, :, nqh:nqh + nkv], x[:, :, nqh + nkv:], None, None, 0.0, rope,
+                              torch.zeros(1, dtype=torch.int32, device="cuda"), table, c, out, weight_sum=w)
+        q = out[:, -1].contiguous()
+        o1, o2 = torch.empty_like(q), torch.empty_like(q)
+        ws = kvq8.alloc_weights_workspace(1, nqh, nkv, 3)
+        kvq8.decode_attn_window(q, c, table, lens, torch.tensor([90], dtype=torch.int32, device="cuda"), 4, o1, ws)
+        kvq8.decode_attn_weights(q, c, table, lens, o2, w, ws)
+        kept = torch.empty((1, nkv, 600), dtype=torch.int32, device="cuda")
+        new = torch.empty((1,), dtype=torch.int32, device="cuda")
+        kvq8.evict(c, w, table, lens, 600, dst, kept, new, n_recent=10)
+        ids = torch.from_numpy(t.reshape(-1).astype(np.int64)).cuda()
+        live = torch.arange(768, device="cuda").reshape(3, 256)
+        mask = torch.cat([live < L, live < 600])[:, None]                          # [6][1][256]
+        pools = [torch.where(mask, p[ids], 0) for p in (c.k_scale, c.v_scale, w)]
+        pools.append(torch.where(mask[..., None], c.k_pool[ids], 0))
+        pools.append(torch.where(mask.reshape(6, 1, 4, 1, 64), c.v_pool[ids], 0))
+        got.append([y.cpu() for y in (out, o1, o2, kept, new, *pools)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -170,9 +170,22 @@ def test_bad_lengths_and_blocks(gpu_lib):
     assert case.status_bits() & kvq8.DEV_BAD_CTX_LEN and not got[0].any() and np.all(np.isfinite(got[2]))
 
 
-def test_long_context_offsets(gpu_lib):
-    # one unit's plane of scores past 2^31 bytes in the workspace would need 2 GB; the largest table
-    # that a test affords, with the sequence in the last row
+def test_many_units_of_two_heads(gpu_lib):
+    # enough units and table for two CTAs per SM
+    rng = np.random.default_rng(6)
+    lens = rng.integers(1, 3000, 40).tolist()
+    lens[3] = 0
+    cfg = wl.Workload("s", 845, batch=40, nqh=8, nkv=4)
+    for step in (False, True):
+        case = (StepCase if step else Case)(cfg, lens=lens)
+        assert cfg.batch * cfg.nkv * case.max_blocks * 4 >= 16 * 2 * 152
+        before, wsum = _sums(case, 7)
+        _run(case, wsum, step=step)
+        _check_sums(case, before, wsum.cpu().numpy(), step=step)
+
+
+def test_wide_table(gpu_lib):
+    # lengths far below the table's width, and one near it in the last row
     cfg = wl.Workload("s", 850, batch=3, nqh=8, nkv=1)
     case = Case(cfg, lens=[5, 2, 40000])
     before, wsum = _sums(case, 4)
