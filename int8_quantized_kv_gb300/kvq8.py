@@ -162,9 +162,15 @@ def _need_host(*tensors):
             raise ValueError("host buffers are fp32")
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:   # (imported with the first call, not with this module)
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _need_cuda(*tensors):
@@ -481,19 +487,27 @@ def selftest_bounded_wait(timeout_ns: int, dev_status, waited_ns=None, stream=No
 
 # ------------------------------- window, weights, eviction, norm and rotation ---
 ROPE_PAIRS = 0x1                          # KVQ8_ROPE_PAIRS
+SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)      # the softmax scale when none is given
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2   # KVQ8_DTYPE_*
 
 
 def _need(*wanted):
     """Each (name, tensor, dtype, shape): a contiguous tensor of this type and
-    shape on the current device.  (One call for all of an entry point's
-    tensors: these checks are most of a small call's time on the host.)"""
-    dev = _torch().cuda.current_device()
+    shape on the current device, whose index is returned.  (One call for all of
+    an entry point's tensors: these checks are most of a small call's time on
+    the host.)"""
+    dev = _torch_module.cuda.current_device()
     for what, t, dtype, shape in wanted:
         if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)} on the current device (cuda:{dev}), "
                              f"got {t.dtype} {list(t.shape)} on device {t.get_device()}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return dev
+
+
+def _stream_on(stream, dev: int):
+    """_stream, for the current device's index where it is known already."""
+    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _cache_wants(cache: KVCache, weight_sum=None):
@@ -528,17 +542,19 @@ def _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, 
         wants.append(("windows", windows, i32, (batch,)))
     if dev_status is not None:
         wants.append(("dev_status", dev_status, i32, (1,)))
-    _need(*wants)
-    return (q.data_ptr(), *new, batch, nqh, nkv, hd, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+    dev = _need(*wants)
+    return dev, (q.data_ptr(), *new, batch, nqh, nkv, hd, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
             cache[3].data_ptr(), nb, block_table.data_ptr(), max_blocks, BLOCK_SIZE, ctx_lens.data_ptr())
 
 
 def _window(fn, q, k_new, v_new, cache, block_table, ctx_lens, windows, sinks, out, workspace, sm_scale,
             dev_status, stream):
-    lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, None, windows)
-    sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
-    _check(fn, getattr(load(), fn)(*lead, windows.data_ptr(), int(sinks), sm, out.data_ptr(), workspace.data_ptr(),
-                                   workspace.shape[0], _ptr(dev_status), _stream(stream)))
+    dev, lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, None, windows)
+    st = getattr(load(), fn)(*lead, windows.data_ptr(), sinks, SM_SCALE if sm_scale is None else sm_scale,
+                             out.data_ptr(), workspace.data_ptr(), workspace.shape[0],
+                             None if dev_status is None else dev_status.data_ptr(), _stream_on(stream, dev))
+    if st != OK:
+        raise Kvq8Error(fn, st)
 
 
 def decode_attn_window(q, cache: KVCache, block_table, ctx_lens, windows, sinks: int, out, workspace,
@@ -575,10 +591,13 @@ def alloc_weights_workspace(batch: int, nqh: int, nkv: int, max_blocks: int, dev
 
 def _weights(fn, q, k_new, v_new, cache, block_table, ctx_lens, out, weight_sum, workspace, sm_scale, dev_status,
              stream):
-    lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum, None)
-    sm = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
-    _check(fn, getattr(load(), fn)(*lead, sm, out.data_ptr(), weight_sum.data_ptr(), workspace.data_ptr(),
-                                   workspace.shape[0], _ptr(dev_status), _stream(stream)))
+    dev, lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, weight_sum,
+                             None)
+    st = getattr(load(), fn)(*lead, SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(),
+                             weight_sum.data_ptr(), workspace.data_ptr(), workspace.shape[0],
+                             None if dev_status is None else dev_status.data_ptr(), _stream_on(stream, dev))
+    if st != OK:
+        raise Kvq8Error(fn, st)
 
 
 def decode_attn_weights(q, cache: KVCache, block_table, ctx_lens, out, weight_sum, workspace,
@@ -614,12 +633,12 @@ def evict(cache: KVCache, weight_sum, block_table, ctx_lens, keep: int, dst_tabl
               ("new_lens", new_lens, i32, (batch,))]
     if dev_status is not None:
         wants.append(("dev_status", dev_status, i32, (1,)))
-    _need(*wants)
+    dev = _need(*wants)
     _check("kvq8_evict", load().kvq8_evict(
         batch, nkv, HEAD_DIM, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
         weight_sum.data_ptr(), nb, block_table.data_ptr(), max_blocks, BLOCK_SIZE, ctx_lens.data_ptr(), int(keep),
         int(n_first), int(n_recent), dst_table.data_ptr(), dst_blocks, kept.data_ptr(), new_lens.data_ptr(),
-        _ptr(dev_status), _stream(stream)))
+        _ptr(dev_status), _stream_on(stream, dev)))
 
 
 def rope_table(inv_freq, n_pos: int, stream=None):
@@ -660,7 +679,8 @@ def norm_rope_append(q, k, v, q_weight, k_weight, eps: float, rope_table, start_
     batch, n_new, nqh, _ = shape = q.shape
     kind = q.dtype
     dtype = DTYPE_BF16 if kind is torch.bfloat16 else DTYPE_F32 if kind is f32 else DTYPE_F16
-    dev = torch.cuda.current_device()
+    dev = _need(*wants)
+    wants = []
     for what, t, want in (("q", q, (batch, n_new, nqh, HEAD_DIM)), ("k", k, (batch, n_new, nkv, HEAD_DIM)),
                           ("v", v, (batch, n_new, nkv, HEAD_DIM))):
         if t.shape != want or t.dtype is not kind or t.get_device() != dev:
@@ -688,7 +708,7 @@ def norm_rope_append(q, k, v, q_weight, k_weight, eps: float, rope_table, start_
         HEAD_DIM, _ptr(q_weight), _ptr(k_weight), eps, rope_table.data_ptr(), n_pos, _ptr(positions),
         _ptr(n_tokens), ROPE_PAIRS if interleaved else 0, start_pos.data_ptr(), block_table.data_ptr(), max_blocks,
         BLOCK_SIZE, nb, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
-        _ptr(weight_sum), q_out.data_ptr(), _ptr(dev_status), _stream(stream)))
+        _ptr(weight_sum), q_out.data_ptr(), _ptr(dev_status), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------ 4-bit cache ---

@@ -156,6 +156,7 @@ def test_binding_refuses_host_tensors_and_strides():
         def __getattr__(self, name):
             return getattr(self.t, name)
 
+    kvq8._torch()
     t, f32 = torch.zeros(2, 128), torch.float32
     cur, torch.cuda.current_device = torch.cuda.current_device, lambda: 0
     try:
