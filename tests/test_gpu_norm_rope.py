@@ -193,6 +193,24 @@ def test_many_values(gpu_lib):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_long_runs(gpu_lib, dtype, pairs):
+    # enough new tokens for value tasks of 16 slots, with and without padding
+    c = Case(4, 900, 8, 8, dtype, start=[3, 16, 255, 31], pairs=pairs, seed=23)
+    c._generic = False
+    c.call()
+    c.check()
+    c = Case(8, 1300, 8, 8, dtype, start=[5, 0, 8, 77, 1, 2, 300, 15], pairs=pairs, seed=24,
+             n_tokens=[1300, 0, 1, 16, 900, 33, 1299, 640])
+    c._generic = False
+    for b, n in enumerate(c.n_tokens):
+        c.v[b, n:] = float("nan")
+    c.call()
+    c.check()
+    assert int(c.status.item()) == 0
+
+
 @pytest.mark.parametrize("n_new", [1, 40])
 def test_positions_ahead_of_the_slots_and_far(gpu_lib, n_new):
     pos = np.array([[100000], [7], [131071 - n_new + 1]]) + np.arange(n_new)
