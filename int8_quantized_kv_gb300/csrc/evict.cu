@@ -254,18 +254,24 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
 // of every 64-byte row: the source quarters that hold one of the tokens are
 // copied into shared memory, kSrcQuarters at a time, only the 32-byte halves
 // of their rows that hold one, and each thread collects the 16 bytes of (dim,
-// 16 tokens) from there.
+// 16 tokens) from there.  Which bytes these are is the same for every dim: four
+// tokens' bytes come from at most four aligned words of the row, and a byte
+// permutation per word, made once per CTA, puts them in place.
 constexpr int kCopyThreads = 128;
 constexpr int kSrcQuarters = 3;   // half of the tokens kept: two or three source quarters
-constexpr int kVRow = 80;         // bytes of a staged V row: 64, and 16 that spread the rows over the banks
-constexpr int kVStage = kHD * kVRow;
+constexpr int kVStage = kTileVQuarter;
 
-__global__ void __launch_bounds__(kCopyThreads, 7)
+// Where byte s (0..63) of dim d's row is in a staged quarter: its 16-byte
+// pieces are permuted so that eight rows' same word lies in different banks.
+__device__ __forceinline__ int staged_byte(int d, int s) { return d * kStageTok + (s ^ (((d >> 1) & 3) << 4)); }
+
+__global__ void __launch_bounds__(kCopyThreads, 9)
 evict_copy_kernel(EvictParams p, int quarters) {
     __shared__ __align__(16) unsigned char stage[kSrcQuarters * kVStage];
     __shared__ int src_tok[kStageTok];          // source position of each token, -1 behind the last
     __shared__ int src_tile[kStageTok];         // its (block, kv head) tile
-    __shared__ __align__(16) int src_off[kStageTok];          // its byte in the staged rows of all its source quarters
+    __shared__ int src_off[kStageTok];          // its byte in the staged rows: quarter's place in the list * kVStage + slot
+    __shared__ int2 moves[kStageTok / 4][4];    // per four tokens: (aligned word of the staged row, permutation), or -1
     __shared__ int list_q[kStageTok];           // the distinct source quarters: tile * 4 + quarter
     __shared__ unsigned list_half[kStageTok];   // which halves of them
     __shared__ int n_list;
@@ -303,6 +309,24 @@ evict_copy_kernel(EvictParams p, int quarters) {
             before += __popc(f);
         }
         if (lane == 0) n_list = before;
+        __syncwarp();
+        if (lane < kStageTok / 4) {
+            int word = -1, count = 0;
+            unsigned sel = 0x3210u;   // keep the four bytes as they are
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int off = src_off[4 * lane + i];
+                if (off < 0) break;
+                if (word >= 0 && (off & ~3) != word) {
+                    moves[lane][count++] = make_int2(word, (int)sel);
+                    sel = 0x3210u;
+                }
+                word = off & ~3;
+                sel = (sel & ~(0xfu << (4 * i))) | ((4u + (off & 3)) << (4 * i));   // byte i: byte off % 4 of the word
+            }
+            if (word >= 0) moves[lane][count++] = make_int2(word, (int)sel);
+            for (; count < 4; ++count) moves[lane][count] = make_int2(-1, 0);
+        }
     }
     // K: eight threads to a row
     uint4 k[4];
@@ -326,7 +350,7 @@ evict_copy_kernel(EvictParams p, int quarters) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {   // thread: piece tid & 3 of rows tid >> 2, + 32, + 64, + 96
                         const int d = (tid >> 2) + 32 * i;
-                        cp_async16_cg(stage + q * kVStage + d * kVRow + (tid & 3) * 16, src + d * kStageTok + (tid & 3) * 16);
+                        cp_async16_cg(stage + q * kVStage + staged_byte(d, (tid & 3) * 16), src + d * kStageTok + (tid & 3) * 16);
                     }
                 }
             }
@@ -362,15 +386,16 @@ evict_copy_kernel(EvictParams p, int quarters) {
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int4 off = *reinterpret_cast<const int4 *>(src_off + 16 * g + 4 * w);
-            const int o[4] = {off.x, off.y, off.z, off.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int from = o[c] - q0 * kVStage;
-                if (o[c] >= 0 && from >= 0 && from < kSrcQuarters * kVStage) {
-                    const unsigned char *x = stage + from + r * kVRow;
+            for (int e = 0; e < 4; ++e) {
+                const int2 mv = moves[4 * g + w][e];
+                const int from = mv.x - q0 * kVStage;
+                if (mv.x >= 0 && from >= 0 && from < kSrcQuarters * kVStage) {
+                    // (rows r, r + 32, ... have their pieces permuted alike)
+                    const unsigned char *x = stage + (from & ~(kStageTok - 1)) + staged_byte(r, from & (kStageTok - 1));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) out[i][w] |= (uint32_t)x[32 * i * kVRow] << (8 * c);
+                    for (int i = 0; i < 4; ++i)
+                        out[i][w] = __byte_perm(out[i][w], *reinterpret_cast<const uint32_t *>(x + 32 * i * kStageTok), mv.y);
                 }
             }
         }
