@@ -655,6 +655,8 @@ def rope_table(inv_freq, n_pos: int, stream=None):
 def _token_stride(what: str, t, batch: int, n_new: int, heads: int) -> int:
     """Elements between the rows of a tensor's [batch][n_new] tokens, whose heads
     [heads][128] must lie side by side."""
+    if isinstance(t, HostMapped):
+        raise ValueError(f"{what}: expected device memory")
     sb, sn, sh, sd = t.stride()
     stride = sn if n_new > 1 else sb if batch > 1 else heads * HEAD_DIM
     if sd != 1 or (heads > 1 and sh != HEAD_DIM) or (n_new > 1 and batch > 1 and sb != n_new * stride):

@@ -304,6 +304,46 @@ def test_nonfinite_rows(gpu_lib, n_new, dtype):
         assert int(c.status.item()) == kvq8.DEV_NONFINITE
 
 
+@pytest.mark.parametrize("n_new", [1, 30])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nonfinite_weight_and_table(gpu_lib, n_new, value):
+    # one weight: every key row comes out with it; one table entry: the rows at that position
+    c = Case(2, n_new, 4, 2, "bf16", start=3, seed=31)
+    c.kw[70] = value
+    c.dev["kw"] = torch.from_numpy(c.kw).cuda()
+    c.call()
+    c.check()
+    assert int(c.status.item()) == kvq8.DEV_NONFINITE and not c.cache.k_scale[c.table[0, 0], :, 3:3 + n_new].any()
+    c = Case(2, n_new, 4, 2, "fp32", start=3, seed=32)
+    c.rope[3 + n_new // 2, 64 + 17] = value
+    c.dev["rope"] = torch.from_numpy(c.rope).cuda()
+    c.call()
+    c.check(nonfinite=True)
+    assert int(c.status.item()) == kvq8.DEV_NONFINITE
+
+
+def test_borders_and_several_maxima(gpu_lib):
+    # rows with many values on and next to borders and the maximum taken several times, with either sign
+    rng = np.random.default_rng(33)
+    x = np.zeros((1, 96, 12, HD), np.float32)
+    for i in range(96):
+        for h in range(4, 8):
+            m = np.float32(2.0 ** rng.integers(-20, 20)) * np.float32(127 if i % 2 else rng.integers(1, 2**20))
+            r = rng.integers(-127, 127, HD) + (0.5 if i % 3 else rng.choice([0.0, 0.5], HD))
+            y = (r * np.float64(m) / 127.0).astype(np.float32)
+            step = rng.integers(-1, 2, HD)
+            y = np.where(step == 0, y, np.nextafter(y, np.float32(1e38) * step.astype(np.float32)))
+            y = np.clip(y, -m, m)
+            y[rng.choice(HD, 1 + i % 5, replace=False)] = m * rng.choice([-1, 1]).astype(np.float32)
+            x[0, i, h] = y
+    for norm, pos in ((False, np.zeros((1, 96), int)), (True, np.zeros((1, 96), int)), (False, None), (True, None)):
+        for pairs in (False, True):
+            c = Case(1, 96, 4, 4, "fp32", start=7, positions=pos, norm=norm, pairs=pairs, x=x, seed=34)
+            c._generic = False
+            c.call()
+            c.check()
+
+
 @pytest.mark.parametrize("n_new", [1, 20])
 def test_bad_positions_and_blocks(gpu_lib, n_new):
     last = n_new - 1
