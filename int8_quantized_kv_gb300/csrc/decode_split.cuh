@@ -829,18 +829,6 @@ decode_split_kernel(DecodeParams p) {
     __syncthreads();
 }
 
-int device_sm_count() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cached[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
 template <int G, bool kMixed, int kCtas, int kMode = kWhole>
 cudaError_t launch_split_gm(const DecodeParams &p, cudaStream_t s) {
     using Lay = SplitLay<G, kMixed, kCtas>;

@@ -14,16 +14,13 @@
 namespace kvq8 {
 namespace {
 
-// Two CTAs of 512 threads fit an SM (64 registers each); with 1024 one does,
-// and 224 units of 8192 tokens took two rounds.
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;                  // three digits of 11, 11 and 10 bits
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kThreadBins = kBins / kSelectThreads;
-// Tokens whose keys stay in shared memory: 96 KiB, so that two CTAs share an SM
-// even where the table is wide (the keys of the others are made again from L2).
-constexpr int kMostCached = 24 * 1024;
+// Tokens whose keys a CTA keeps in shared memory: 80 KiB, so that two CTAs share
+// an SM even where the table is wide (the keys of the others are made again
+// from L2).
+constexpr int kMostCached = 20 * 1024;
+constexpr int kMostCtas = 8;                    // of a unit's cluster
 
 // Order of a weight as an unsigned number: larger weights above smaller ones,
 // -0 equal to 0, a NaN below everything.  Nothing maps to 0xffffffff, which
@@ -35,14 +32,16 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (x >> 31) ? ~x : (x | 0x80000000u);
 }
 
-// A unit's tokens in the order that decides what is kept.  The keys of the
-// first n_cached tokens are kept in shared memory, the others' made again.
+// A CTA's share [lo, hi) of a unit's tokens, in the order that decides what is
+// kept.  The keys of its first n_cached tokens are kept in shared memory, the
+// others' made again.
 struct Keys {
     const int32_t *row;
     const float *weight_sum;
-    int nkv, h, L, first, recent0;   // tokens below first and from recent0 on are kept
+    int nkv, h, lo, hi;
+    int first, recent0;              // tokens below first and from recent0 on are kept
     uint32_t *cache;
-    int n_cached;                    // a multiple of 4
+    int n_cached;                    // a multiple of 4, as lo
     __device__ __forceinline__ uint32_t key(int t, float w) const {
         return t < first || t >= recent0 ? 0xffffffffu : weight_key(w);
     }
@@ -54,7 +53,7 @@ struct Keys {
         return make_uint4(key(t, w.x), key(t + 1, w.y), key(t + 2, w.z), key(t + 3, w.w));
     }
     __device__ __forceinline__ uint4 get4(int t) const {
-        if (t < n_cached) return *reinterpret_cast<const uint4 *>(cache + t);
+        if (t - lo < n_cached) return *reinterpret_cast<const uint4 *>(cache + (t - lo));
         return four(t, *reinterpret_cast<const float4 *>(at(t)));
     }
 };
@@ -69,82 +68,103 @@ __device__ __forceinline__ int warp_suffix(int v, int lane) {
     return v;
 }
 
-// One CTA per unit: a radix selection over the keys, then the list of kept
-// tokens in order of position.
-__global__ void __launch_bounds__(kSelectThreads, 2)
-evict_select_kernel(EvictParams p, int cache_tokens) {
+// One CTA per unit, or a cluster of n_ctas (kCluster): each CTA takes a share of
+// the unit's tokens, the digits' counts are added up through distributed shared
+// memory, and every CTA finds the same digit.  A radix selection over the keys,
+// then the list of kept tokens in order of position.  What the CTAs of a
+// cluster branch on is read from one of them or from all of them, so that all
+// take the same barriers.
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
+evict_select_kernel(EvictParams p, int cache_tokens, int n_ctas) {
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kThreadBins = kBins / kThreads;   // consecutive bins of a thread
     extern __shared__ __align__(16) uint32_t sm_keys[];
-    __shared__ __align__(16) int hist[kBins];
-    __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
-    __shared__ int sh_digit, sh_need, sh_bad;
+    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ int warp_a[kWarps], warp_b[kWarps];
+    __shared__ int sh_digit, sh_need, sh_bad, sh_len;
+    __shared__ __align__(8) int2 sh_total;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int u = blockIdx.x, b = u / p.nkv, h = u % p.nkv;
+    const int rank = kCluster ? cluster_rank() : 0;
+    if (!kCluster) n_ctas = 1;
+    auto sync_all = [&] {
+        if (kCluster) cluster_sync();
+        else __syncthreads();
+    };
+    const int u = blockIdx.x / n_ctas, b = u / p.nkv, h = u % p.nkv;
     const int cap = p.max_blocks * kBS;
-    const int Lraw = p.ctx_lens[b];
-    const int L = max(0, min(Lraw, cap));
-    const int m = min(L, p.keep);
     int32_t *kept = p.kept + (size_t)u * p.keep;
     const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
     const int32_t *dst = p.dst_table + (size_t)b * p.dst_max_blocks;
     if (tid == 0) {
         sh_bad = 0;
-        if (Lraw != L && h == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
+        if (rank == 0) {
+            const int Lraw = p.ctx_lens[b];
+            sh_len = max(0, min(Lraw, cap));
+            if (Lraw != sh_len && h == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
+        }
     }
-    for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
-    __syncthreads();
+    for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+    sync_all();
+    const int L = kCluster ? load_cluster_int(&sh_len, 0) : sh_len;
+    const int m = min(L, p.keep);
 
     // every block id must lie in the pool, and a destination must be neither a
     // source of the sequence nor listed twice
     const int n_src = (L + kBS - 1) / kBS, n_dst = (m + kBS - 1) / kBS;
     bool bad = false;
-    for (int i = tid; i < n_src; i += kSelectThreads) bad |= row[i] < 0 || row[i] >= p.num_blocks;
-    for (int d = warp; d < n_dst; d += kSelectWarps) {
+    for (int i = rank * kThreads + tid; i < n_src; i += n_ctas * kThreads) bad |= row[i] < 0 || row[i] >= p.num_blocks;
+    for (int d = rank * kWarps + warp; d < n_dst; d += n_ctas * kWarps) {
         const int id = dst[d];
         bad |= id < 0 || id >= p.num_blocks;
         for (int j = lane; j < n_src; j += 32) bad |= row[j] == id;
         for (int j = lane; j < d; j += 32) bad |= dst[j] == id;
     }
     if (bad) sh_bad = 1;
-    __syncthreads();
-    if (sh_bad) {   // the sequence is left out
-        for (int j = tid; j < p.keep; j += kSelectThreads) kept[j] = -1;
-        if (tid == 0) {
-            flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
-            if (h == 0) p.new_lens[b] = 0;
-        }
-        return;
+    sync_all();
+    int any_bad = sh_bad;
+    if (kCluster) any_bad = __any_sync(0xffffffffu, lane < n_ctas && load_cluster_int(&sh_bad, lane) != 0);
+    if (rank == 0 && tid == 0) {
+        if (any_bad) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
+        if (h == 0) p.new_lens[b] = any_bad ? 0 : m;
     }
-    if (tid == 0 && h == 0) p.new_lens[b] = m;
-    for (int j = m + tid; j < p.keep; j += kSelectThreads) kept[j] = -1;
-    if (m == L) {   // everything is kept
-        for (int t = tid; t < L; t += kSelectThreads) kept[t] = t;
+    // a sequence with a bad id is left out; behind the last kept token -1; all tokens kept: no selection
+    for (int j = (any_bad ? 0 : m) + rank * kThreads + tid; j < p.keep; j += n_ctas * kThreads) kept[j] = -1;
+    if (any_bad || m == L) {
+        if (!any_bad)
+            for (int t = rank * kThreads + tid; t < L; t += n_ctas * kThreads) kept[t] = t;
+        if (kCluster) cluster_sync();   // (no CTA leaves while another reads its shared memory)
         return;
     }
 
-    Keys keys = {row, p.weight_sum, p.nkv, h, L, p.n_first, L - p.n_recent, sm_keys, min((L + 3) / 4 * 4, cache_tokens)};
+    // this CTA's share of the tokens
+    const int cta_share = ((L + n_ctas - 1) / n_ctas + 127) / 128 * 128;
+    const int c_lo = min(L, rank * cta_share), c_hi = min(L, c_lo + cta_share);
+    const Keys keys = {row, p.weight_sum, p.nkv, h, c_lo, c_hi, p.n_first, L - p.n_recent, sm_keys,
+                       min((c_hi - c_lo + 3) / 4 * 4, cache_tokens)};
     // the m-th largest key, digit by digit from the top: `prefix` holds the
     // digits found, `need` how many tokens with exactly this prefix are kept.
-    // The first digit is counted as the weights are loaded, four at a time.
+    // The first digit is counted as the weights are loaded.
     constexpr int kAhead = 4;   // weights loaded at once, in fours per thread
-    for (int t0 = 4 * tid; t0 < L; t0 += kAhead * 4 * kSelectThreads) {
+    for (int t0 = c_lo + 4 * tid; t0 < c_hi; t0 += kAhead * 4 * kThreads) {
         float4 w[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int t = t0 + i * 4 * kSelectThreads;
-            if (t < L) w[i] = *reinterpret_cast<const float4 *>(keys.at(t));   // (t % 4 == 0: within the block)
+            const int t = t0 + i * 4 * kThreads;
+            if (t < c_hi) w[i] = *reinterpret_cast<const float4 *>(keys.at(t));   // (t % 4 == 0: within the block)
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int t = t0 + i * 4 * kSelectThreads;
-            if (t < L) {
+            const int t = t0 + i * 4 * kThreads;
+            if (t < c_hi) {
                 const uint4 k = keys.four(t, w[i]);
-                if (t < keys.n_cached) *reinterpret_cast<uint4 *>(sm_keys + t) = k;
-                atomicAdd(&hist[k.x >> 21], 1);
-                if (t + 1 < L) atomicAdd(&hist[k.y >> 21], 1);
-                if (t + 2 < L) atomicAdd(&hist[k.z >> 21], 1);
-                if (t + 3 < L) atomicAdd(&hist[k.w >> 21], 1);
+                if (t - c_lo < keys.n_cached) *reinterpret_cast<uint4 *>(sm_keys + (t - c_lo)) = k;
+                atomicAdd(&hist[0][k.x >> 21], 1);
+                if (t + 1 < c_hi) atomicAdd(&hist[0][k.y >> 21], 1);
+                if (t + 2 < c_hi) atomicAdd(&hist[0][k.z >> 21], 1);
+                if (t + 3 < c_hi) atomicAdd(&hist[0][k.w >> 21], 1);
             }
         }
     }
@@ -155,34 +175,49 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         if (pass > 0) {
             const int above = pass == 1 ? 21 : 10;
-            for (int t = 4 * tid; t < L; t += 4 * kSelectThreads) {
+            for (int t = c_lo + 4 * tid; t < c_hi; t += 4 * kThreads) {
                 const uint4 k4 = keys.get4(t);
                 const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (t + i < L && (k[i] >> above) == (prefix >> above))
-                        atomicAdd(&hist[(k[i] >> shift) & (pass == 1 ? kBins - 1 : 1023)], 1);
+                    if (t + i < c_hi && (k[i] >> above) == (prefix >> above))
+                        atomicAdd(&hist[pass][(k[i] >> shift) & (pass == 1 ? kBins - 1 : 1023)], 1);
             }
         }
-        __syncthreads();
-        // thread i: bins 4i .. 4i + 3; the bin in which the need-th token from the top lies
-        static_assert(kThreadBins == 4, "one int4 of bins per thread");
-        const int4 bin = reinterpret_cast<const int4 *>(hist)[tid];
-        const int sum = bin.x + bin.y + bin.z + bin.w;
+        sync_all();
+        // thread i: bins kThreadBins * i and on; the bin in which the need-th token from the top lies
+        int bin[kThreadBins], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kThreadBins / 4; ++i) {
+            const int4 *mine = reinterpret_cast<const int4 *>(hist[pass]) + tid * (kThreadBins / 4) + i;
+            int4 c = make_int4(0, 0, 0, 0);
+            if (kCluster) {
+                int4 x[kMostCtas];   // (all loads in flight at once)
+#pragma unroll
+                for (int r = 0; r < kMostCtas; ++r)
+                    x[r] = r < n_ctas ? load_cluster_int4(mine, r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < kMostCtas; ++r) {
+                    c.x += x[r].x; c.y += x[r].y; c.z += x[r].z; c.w += x[r].w;
+                }
+            } else {
+                c = *mine;
+            }
+            bin[4 * i] = c.x; bin[4 * i + 1] = c.y; bin[4 * i + 2] = c.z; bin[4 * i + 3] = c.w;
+            sum += c.x + c.y + c.z + c.w;
+        }
         const int suffix = warp_suffix(sum, lane);
         if (lane == 0) warp_a[warp] = suffix;
         __syncthreads();
-        reinterpret_cast<int4 *>(hist)[tid] = make_int4(0, 0, 0, 0);
-        int above = __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelectWarps ? warp_a[lane] : 0) + suffix - sum;
+        int above = __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? warp_a[lane] : 0) + suffix - sum;
         if (above < need && need <= above + sum) {   // (tokens above this thread's bins)
-            const int c[4] = {bin.x, bin.y, bin.z, bin.w};
 #pragma unroll
-            for (int i = 3; i >= 0; --i) {
-                if (above < need && need <= above + c[i]) {
-                    sh_digit = 4 * tid + i;
+            for (int i = kThreadBins - 1; i >= 0; --i) {
+                if (above < need && need <= above + bin[i]) {
+                    sh_digit = kThreadBins * tid + i;
                     sh_need = need - above;
                 }
-                above += c[i];
+                above += bin[i];
             }
         }
         __syncthreads();
@@ -193,9 +228,9 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
 
     // tokens above the m-th largest are kept, and the first `need` equal to it:
     // each warp counts both in its share of the tokens, and writes them behind
-    // those of the warps before it
-    const int share = ((L + kSelectWarps - 1) / kSelectWarps + 127) / 128 * 128;
-    const int t_lo = min(L, warp * share), t_hi = min(L, t_lo + share);
+    // those of the warps and CTAs before it
+    const int share = ((c_hi - c_lo + kWarps - 1) / kWarps + 127) / 128 * 128;
+    const int t_lo = min(c_hi, c_lo + warp * share), t_hi = min(c_hi, t_lo + share);
     // (tokens above, tokens equal) of the four tokens from t on
     auto count4 = [&](uint4 k4, int t, bool (&gt)[4], bool (&eq)[4]) {
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -223,8 +258,22 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         warp_b[warp] = eq;
     }
     __syncthreads();
-    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);   // (warp < kSelectWarps <= 32)
-    eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
+    if (kCluster) {
+        if (warp == 0) {
+            const int a = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_a[lane] : 0);
+            const int c = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_b[lane] : 0);
+            if (lane == 0) sh_total = make_int2(a, c);
+        }
+        cluster_sync();
+    }
+    gt = lane < warp ? warp_a[lane] : 0;   // (warp < kWarps <= 32)
+    eq = lane < warp ? warp_b[lane] : 0;
+    if (kCluster && lane < rank) {
+        gt += load_cluster_int(&sh_total.x, lane);
+        eq += load_cluster_int(&sh_total.y, lane);
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     for (int t0 = t_lo; t0 < t_hi; t0 += 128) {
         const int t = t0 + 4 * lane;
         const int2 c = count4(t < t_hi ? keys.get4(t) : make_uint4(0u, 0u, 0u, 0u), t, is_gt, is_eq);
@@ -246,6 +295,7 @@ evict_select_kernel(EvictParams p, int cache_tokens) {
         gt += all & 0xffff;
         eq += all >> 16;
     }
+    if (kCluster) cluster_sync();   // (as above)
 }
 
 // One CTA per 64 kept tokens of a unit (a quarter of a destination tile).  K
@@ -417,48 +467,86 @@ evict_copy_kernel(EvictParams p, int quarters) {
             *reinterpret_cast<uint4 *>(d) = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
         } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                if (c < live) d[c] = (int8_t)(out[i][c / 4] >> (8 * (c % 4)));
+            for (int w = 0; w < 4; ++w) {
+                if (4 * w + 4 <= live) {
+                    reinterpret_cast<uint32_t *>(d)[w] = out[i][w];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        if (4 * w + c < live) d[4 * w + c] = (int8_t)(out[i][w] >> (8 * c));
+                }
+            }
         }
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(EvictParams, int), unsigned grid, unsigned block, size_t smem,
-                       const EvictParams &p, int arg, cudaStream_t s) {
+cudaError_t launch_copy(const EvictParams &p, int quarters, unsigned blocks, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.dynamicSmemBytes = 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, arg);
+    return cudaLaunchKernelEx(&cfg, evict_copy_kernel, p, quarters);
+}
+
+template <int kThreads, bool kCluster>
+cudaError_t launch_select(const EvictParams &p, int n_ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> configured{0};
+    // keys of as many tokens as a CTA's share of the table, up to kMostCached
+    const int64_t share = ((int64_t)p.max_blocks * kBS + n_ctas - 1) / n_ctas;
+    const int cached = (int)min((share + 127) / 128 * 128, (int64_t)kMostCached);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.batch * p.nkv * n_ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = cached * sizeof(uint32_t);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = n_ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster ? 2 : 1;
+    return launch_after_setting(
+        configured,
+        [] {
+            return cudaFuncSetAttribute(evict_select_kernel<kThreads, kCluster>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCached * (int)sizeof(uint32_t));
+        },
+        [&] { return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads, kCluster>, p, cached, n_ctas); });
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
-    static std::atomic<uint64_t> configured{0};
     const int quarters = (p.keep + kStageTok - 1) / kStageTok;
-    const int64_t blocks = (int64_t)p.batch * p.nkv * quarters;
-    if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
-    // keys of as many tokens as the table can hold, up to kMostCached
-    const int cached = (int)min((int64_t)p.max_blocks * kBS, (int64_t)kMostCached);
-    const cudaError_t e = launch_after_setting(
-        configured,
-        [] {
-            return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kMostCached * (int)sizeof(uint32_t));
-        },
-        [&] {
-            return launch_pdl(evict_select_kernel, (unsigned)(p.batch * p.nkv), kSelectThreads,
-                              cached * sizeof(uint32_t), p, cached, s);
-        });
+    const int64_t units = (int64_t)p.batch * p.nkv, blocks = units * quarters;
+    const int64_t tokens = (int64_t)p.max_blocks * kBS;   // most tokens of a unit
+    if (blocks > 2147483647 || units > 2147483647 / 8) return cudaErrorInvalidConfiguration;
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // Small tables: CTAs of 128 threads, eight to an SM.  Else 512 threads, two
+    // to an SM (1024 leave room for one: 224 units of 8192 tokens then took two
+    // rounds), and where that leaves SMs idle, clusters of up to eight CTAs per
+    // unit with at least 8192 tokens each.  (Whole calls: 32 units of 131072
+    // tokens 363 -> 202 us, 32 of 32768 91 -> 66, 18 of 24000 53 -> 45; with
+    // 2048 tokens per CTA the cluster's barriers cost more than they save: 64
+    // units of 8192 44 -> 49, 32 of 32768 76.)
+    int n_ctas = 1;
+    while (n_ctas < kMostCtas && units * n_ctas <= sms && tokens / (2 * n_ctas) >= 8192) n_ctas *= 2;
+    cudaError_t e;
+    if (tokens <= 2048) e = launch_select<128, false>(p, 1, s);
+    else if (n_ctas > 1) e = launch_select<512, true>(p, n_ctas, s);
+    else e = launch_select<512, false>(p, 1, s);
     if (e != cudaSuccess) return e;
-    return launch_pdl(evict_copy_kernel, (unsigned)blocks, kCopyThreads, 0, p, quarters, s);
+    return launch_copy(p, quarters, (unsigned)blocks, s);
 }
 
 }  // namespace kvq8

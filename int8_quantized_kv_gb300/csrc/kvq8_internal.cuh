@@ -36,6 +36,19 @@ cudaError_t launch_after_setting(std::atomic<uint64_t> &configured, SetFn set, L
     return launch();
 }
 
+// Multiprocessors of the current device (0 when it cannot be read).
+inline int device_sm_count() {
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cached[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
 constexpr int kHD = 128;           // head dimension
 constexpr int kBS = 256;           // tokens per cache block
 constexpr int kQB = 32;            // query quantisation block

@@ -161,3 +161,27 @@ def test_lengths_outside_the_table(gpu_lib):
     assert np.array_equal(new_lens, [0, 300]) and np.all(kept[0] == -1)
     p.lens[1] = 768
     assert np.array_equal(kept[1, 0], p.want(1, 0, 0, 0))
+
+
+@pytest.mark.parametrize("longest", [16384, 40001, 131067])
+def test_clusters(gpu_lib, longest):
+    # tables of at least 16384 tokens: 2, 4 and 8 CTAs per unit, with short and empty sequences beside the long one,
+    # keys beyond a CTA's shared memory, everything kept, and ties over the CTAs' borders
+    lens = [longest, 0, 5, 3000, longest - 4097, 8193]
+    Pool(lens, 3000, 1, seed=longest).check(4, 100)
+    Pool(lens[:3], 9000, 2, seed=longest + 1, weights=_ties).check(0, 0)
+    Pool(lens[::4], 1, 1, seed=longest + 2, weights=_all_equal).check(0, 0)
+    p = Pool([longest, longest, 700], 500, 1, seed=longest + 3)
+    table, dst = p.table.copy(), p.dst.copy()
+    table[0, (longest - 1) // 256] = p.nb
+    dst[2, 1] = table[2, 0]
+    kept, new_lens = p.run(4, 10, table=table, dst=dst)
+    assert int(p.status.item()) == kvq8.DEV_BAD_BLOCK_ID
+    assert np.array_equal(new_lens, [0, 500, 0]) and np.all(kept[[0, 2]] == -1)
+    assert np.array_equal(kept[1, 0], p.want(1, 0, 4, 10))
+
+
+def test_wide_table_short_sequences(gpu_lib):
+    # more units than SMs with a wide table: keys beyond a CTA's shared memory in one of them
+    lens = [300] * 159 + [25000]
+    Pool(lens, 200, 1, seed=5).check(0, 20)
