@@ -43,7 +43,8 @@ __device__ __forceinline__ int kv_code(float v, float scale) {
     return max(-127, min(127, c));
 }
 
-// kv_code of four values of one row whose scale is sc = fl(max|row| / 127),
+// kv_code of four values of one row whose scale is sc = fl(max|row| / 127) (or
+// the product with fl(1/127), for which the bounds below hold as well),
 // each in the low byte of a word, with one reciprocal per row in place of a
 // division per value.  inv approximates 1 / sc (the hardware reciprocal, which
 // the PTX ISA bounds by one ulp; the argument below allows three).  t =

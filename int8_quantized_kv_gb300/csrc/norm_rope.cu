@@ -64,6 +64,7 @@ __device__ __forceinline__ float4 load4(const T *p) {
     const float2 a = pair_of(v.x, T()), b = pair_of(v.y, T());
     return make_float4(a.x, a.y, b.x, b.y);
 }
+
 // ------------------------------------------------------------- turn tasks --
 // Eight lanes to a row: lane j (of 8) holds dims 32c + 4j + i in x[4c + i] (i <
 // 4, c < 4).  Both kinds of pairs lie within a lane, and the eight lanes read
@@ -244,7 +245,9 @@ __device__ __noinline__ void exact_key_row(const NormRopeParams &p, int64_t row,
     double top = fmax(fmax(fabs(z[0]), fabs(z[1])), fmax(fabs(z[2]), fabs(z[3])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (sc < 0.0f) {   // warp-uniform
+    if (sc < 0.0f && top == 0.0) {   // warp-uniform: a row of zeros (or of NaN, see below)
+        sc = 0.0f;
+    } else if (sc < 0.0f) {
         double r = 1.0;
         if (p.k_weight) {
             double ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
@@ -434,7 +437,7 @@ __device__ __noinline__ unsigned near_key_rows(const NormRopeParams &p, int64_t 
 // near_key_rows, one out of the range in which these errors are relative ones,
 // or within 2^-34 of a border, to exact_key_row.  (64-bit arithmetic has a
 // hundredth of fp32's rate: with it for all of these a call of 64 tokens takes
-// 8.6 us instead of 5.4.)
+// 8.6 us instead of 5.1.)
 template <typename T, bool kPairs>
 __device__ __forceinline__ void store_keys(const NormRopeParams &p, float (&x)[16], const float (&c)[8],
                                            const float (&s)[8], int64_t row, int64_t pos, int h0, KeyPlace at,
@@ -749,7 +752,8 @@ cudaError_t launch_runs(const NormRopeParams &p, cudaStream_t s) {
 // enough of them, else 4 (a quarter of the latency).
 template <typename T, bool kPairs>
 cudaError_t launch_rows(const NormRopeParams &p, cudaStream_t s) {
-    if ((int64_t)p.batch * p.nkv * ((p.n_new + 15) / 16) >= (p.n_tokens ? kLongRunsPadded : kLongRuns)) return launch_runs<T, kPairs, 16>(p, s);
+    const int64_t runs = (int64_t)p.batch * p.nkv * ((p.n_new + 15) / 16);
+    if (runs >= (p.n_tokens ? kLongRunsPadded : kLongRuns)) return launch_runs<T, kPairs, 16>(p, s);
     return launch_runs<T, kPairs, 4>(p, s);
 }
 
