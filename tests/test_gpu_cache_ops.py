@@ -329,3 +329,38 @@ def test_pools_past_32_bits(gpu_lib):
         pools.append(torch.where(mask.reshape(6, 1, 4, 1, 64), c.v_pool[ids], 0))
         got.append([y.cpu() for y in (out, o1, o2, kept, new, *pools)])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_largest_batch(gpu_lib):
+    # 65535 sequences of one token: each output row is its value row as the cache holds it
+    B = 65535
+    g = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn((B, 1, 3, HD), generator=g, device="cuda")
+    ids = torch.randperm(2 * B, generator=g, device="cuda").to(torch.int32)
+    table, dst = ids[:B, None].contiguous(), ids[B:, None].contiguous()
+    cache, wsum = kvq8.alloc_cache(2 * B, 1), torch.full((2 * B, 1, 256), 9.0, device="cuda")
+    rope = kvq8.rope_table(_dev(1e4 ** (-np.arange(64) / 64.0)), 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.empty((B, 1, 1, HD), device="cuda")
+    kvq8.norm_rope_append(x[:, :, :1], x[:, :, 1:2], x[:, :, 2:], None, None, 0.0, rope,
+                          torch.zeros(B, dtype=torch.int32, device="cuda"), table, cache, q, weight_sum=wsum,
+                          dev_status=status)
+    assert torch.equal(q, x[:, :, :1])                       # position 0 turns nothing
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    scale = cache.v_scale[table[:, 0].long(), 0, 0]
+    want = cache.v_pool[table[:, 0].long(), 0, 0, :, 0].float() * scale[:, None]
+    assert (want - x[:, 0, 2]).abs().max().item() <= 0.51 * scale.max().item()
+    ws = kvq8.alloc_weights_workspace(B, 1, 1, 1)
+    q = q[:, 0]
+    for out in (torch.zeros_like(q), torch.zeros_like(q)):
+        kvq8.decode_attn_window(q, cache, table, lens, lens, 0, out, ws, dev_status=status)
+        assert (out[:, 0] - want).abs().max().item() <= 1e-5
+        out.zero_()
+        kvq8.decode_attn_weights(q, cache, table, lens, out, wsum, ws, dev_status=status)
+        assert (out[:, 0] - want).abs().max().item() <= 1e-5
+    assert (wsum[table[:, 0].long(), 0, 0] - 2.0).abs().max().item() <= 1e-5
+    kept, new = torch.empty((B, 1, 1), dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    kvq8.evict(cache, wsum, table, lens, 1, dst, kept, new, dev_status=status)
+    assert not kept.any() and torch.equal(new, lens) and int(status.item()) == 0
+    kvq8.decode_attn_window(q, cache, dst, new, lens, 0, out, ws)
+    assert (out[:, 0] - want).abs().max().item() <= 1e-5
