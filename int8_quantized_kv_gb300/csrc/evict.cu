@@ -84,8 +84,11 @@ evict_select_kernel(EvictParams p, int cache_tokens, int n_ctas) {
     __shared__ int warp_a[kWarps], warp_b[kWarps];
     __shared__ int sh_digit, sh_need, sh_bad, sh_len;
     __shared__ __align__(8) int2 sh_total;
-    pdl_launch_dependents();
+    // (in this order in every kernel that is not a split's merge: the next one then
+    // starts only when those before this one are done, as a step with the cache
+    // declared ready needs it)
     pdl_wait();
+    pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = kCluster ? cluster_rank() : 0;
     if (!kCluster) n_ctas = 1;
@@ -325,8 +328,8 @@ evict_copy_kernel(EvictParams p, int quarters) {
     __shared__ int list_q[kStageTok];           // the distinct source quarters: tile * 4 + quarter
     __shared__ unsigned list_half[kStageTok];   // which halves of them
     __shared__ int n_list;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int u = blockIdx.x / quarters, qd = blockIdx.x % quarters;
     const int b = u / p.nkv, h = u % p.nkv;

@@ -691,8 +691,10 @@ template <typename T, bool kPairs, int kRun>
 __global__ void __launch_bounds__(kTaskWarps * 32, kMinCtas)
 norm_rope_append_kernel(NormRopeParams p, TaskPlan plan) {
     __shared__ __align__(16) unsigned char rings[kTaskWarps][kDepth * stage_bytes<T>()];
-    pdl_launch_dependents();
+    // (the next kernel starts only when those before this one are done: a step
+    // with the cache declared ready reads what they wrote without waiting)
     pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= plan.turn_ctas) {
         const int64_t w = (int64_t)(blockIdx.x - plan.turn_ctas) * kTaskWarps + warp;

@@ -645,7 +645,10 @@ def rope_table(inv_freq, n_pos: int, stream=None):
     """The rotation's table, fp32 [n_pos][128]: cosines of position * inv_freq
     (fp64 [64], device), then sines."""
     torch = _torch()
-    _need(("inv_freq", inv_freq, torch.float64, (HEAD_DIM // 2,)))
+    dev = _need(("inv_freq", inv_freq, torch.float64, (HEAD_DIM // 2,)))
+    if stream is not None and _stream(stream) != _stream_on(None, dev):   # memory of the stream that writes it
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream))):
+            return rope_table(inv_freq, n_pos)
     table = torch.empty((n_pos, HEAD_DIM), dtype=torch.float32, device=inv_freq.device)
     _check("kvq8_rope_table", load().kvq8_rope_table(_ptr(inv_freq), int(n_pos), HEAD_DIM, _ptr(table),
                                                      _stream(stream)))

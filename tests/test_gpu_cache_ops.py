@@ -364,3 +364,64 @@ def test_largest_batch(gpu_lib):
     assert not kept.any() and torch.equal(new, lens) and int(status.item()) == 0
     kvq8.decode_attn_window(q, cache, dst, new, lens, 0, out, ws)
     assert (out[:, 0] - want).abs().max().item() <= 1e-5
+
+
+@pytest.mark.parametrize("batch, nkv, keep", [(1, 2, 1024), (2, 1, 1500), (28, 8, 1024)])
+def test_step_with_the_cache_ready_two_calls_behind(gpu_lib, batch, nkv, keep):
+    # a step that may read the cache before the call ahead of it ends still sees
+    # what the eviction before that call wrote
+    rng = np.random.default_rng(40)
+    nqh, n_dst = 2 * nkv, keep // 256 + 1
+    nb = batch * (8 + n_dst)
+    ids = rng.permutation(nb).astype(np.int32)
+    table, dst = _dev(ids[:8 * batch].reshape(batch, 8)), _dev(ids[8 * batch:].reshape(batch, n_dst))
+    cache, wsum = kvq8.alloc_cache(nb, nkv), torch.rand((nb, nkv, 256), device="cuda")
+    rows = torch.randn((batch, 2048, nkv, HD), device="cuda")
+    kvq8.quantize_append(rows, rows, torch.zeros(batch, dtype=torch.int32, device="cuda"), table, cache)
+    lens, after = (torch.full((batch,), n, dtype=torch.int32, device="cuda") for n in (2048, keep + 1))
+    kept = torch.empty((batch, nkv, keep), dtype=torch.int32, device="cuda")
+    new_lens = torch.empty_like(lens)
+    q, k, v = (torch.randn((batch, n, HD), device="cuda") for n in (nqh, nkv, nkv))
+    ws, status = kvq8.alloc_workspace(batch, nqh, nkv, 8), torch.zeros(1, dtype=torch.int32, device="cuda")
+    other, rope = kvq8.alloc_cache(1, 1), kvq8.rope_table(_dev(1e4 ** (-np.arange(64) / 64.0)), 16)
+    x = torch.randn((1, 1, 1, HD), device="cuda")
+    zero, q_out = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.empty((1, 1, 1, HD), device="cuda")
+    o = torch.empty_like(q)
+
+    def calls(ready):
+        kvq8.evict(cache, wsum, table, lens, keep, dst, kept, new_lens, 4, 64, dev_status=status)
+        kvq8.norm_rope_append(x, x, x, None, None, 1e-6, rope, zero[0], zero, other, q_out, dev_status=status)
+        kvq8.decode_step(q, k, v, cache, dst, after, o, ws, dev_status=status, cache_ready=ready)
+
+    calls(False)
+    torch.cuda.synchronize()
+    want = o.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(True)
+    for _ in range(20):
+        for c in cache:
+            c[dst.flatten().long()] = 0
+        o.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_rope_table_on_another_stream(gpu_lib, raw):
+    # the table's memory must not be one that the current stream still writes
+    inv = _dev(1e4 ** (-np.arange(64) / 64.0))
+    want = kvq8.rope_table(inv, 1000).cpu()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(1000)          # (its first launch may wait for the device)
+    x = torch.full((1000, HD), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    x.fill_(7.0)
+    del x
+    table = kvq8.rope_table(inv, 1000, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert torch.equal(table.cpu(), want)
