@@ -77,10 +77,12 @@ quantize_append_kernel(AppendParams p, int quarters, long long tasks) {
     __shared__ __align__(16) float4 ring[kBulkWarps][kRing][2][32];   // [warp][slot][K, V][lane]
 
     // a programmatic dependent of the kernel before it, whose outputs it may
-    // read: it waits for it first; the next kernel of the stream may be
-    // scheduled now (it waits for this grid before it reads what it writes)
-    pdl_launch_dependents();
+    // read: it waits for it first; the next kernel of the stream may then be
+    // scheduled (it waits for this grid before it reads what it writes; not
+    // earlier: a step with the cache declared ready reads what the kernels
+    // before this one wrote without waiting)
     pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long task = (long long)blockIdx.x * kBulkWarps + (threadIdx.x >> 5);
     if (task >= tasks) return;

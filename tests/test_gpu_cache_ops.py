@@ -366,8 +366,9 @@ def test_largest_batch(gpu_lib):
     assert (out[:, 0] - want).abs().max().item() <= 1e-5
 
 
+@pytest.mark.parametrize("between", ["turn", "rows"])
 @pytest.mark.parametrize("batch, nkv, keep", [(1, 2, 1024), (2, 1, 1500), (28, 8, 1024)])
-def test_step_with_the_cache_ready_two_calls_behind(gpu_lib, batch, nkv, keep):
+def test_step_with_the_cache_ready_two_calls_behind(gpu_lib, batch, nkv, keep, between):
     # a step that may read the cache before the call ahead of it ends still sees
     # what the eviction before that call wrote
     rng = np.random.default_rng(40)
@@ -386,11 +387,14 @@ def test_step_with_the_cache_ready_two_calls_behind(gpu_lib, batch, nkv, keep):
     other, rope = kvq8.alloc_cache(1, 1), kvq8.rope_table(_dev(1e4 ** (-np.arange(64) / 64.0)), 16)
     x = torch.randn((1, 1, 1, HD), device="cuda")
     zero, q_out = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.empty((1, 1, 1, HD), device="cuda")
-    o = torch.empty_like(q)
+    many, o = torch.randn((1, 40, 1, HD), device="cuda"), torch.empty_like(q)
 
     def calls(ready):
         kvq8.evict(cache, wsum, table, lens, keep, dst, kept, new_lens, 4, 64, dev_status=status)
-        kvq8.norm_rope_append(x, x, x, None, None, 1e-6, rope, zero[0], zero, other, q_out, dev_status=status)
+        if between == "rows":
+            kvq8.quantize_append(many, many, zero[0], zero, other, dev_status=status)
+        else:
+            kvq8.norm_rope_append(x, x, x, None, None, 1e-6, rope, zero[0], zero, other, q_out, dev_status=status)
         kvq8.decode_step(q, k, v, cache, dst, after, o, ws, dev_status=status, cache_ready=ready)
 
     calls(False)
