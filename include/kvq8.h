@@ -476,7 +476,7 @@ kvq8_status kvq8_decode_step_weights(const float *q, const float *k_new, const f
  *               of block_table, nor twice.
  *   kept        int32 [batch][nkv][keep]: the positions of the kept tokens in
  *               increasing order, -1 behind the last
- *   new_lens    int32 [batch]: min(ctx_lens[b], keep)
+ *   new_lens    int32 [batch]: min(ctx_lens[b], keep); may be ctx_lens itself
  * Tables of more than 2^30 tokens return KVQ8_ERR_UNSUPPORTED.
  * A ctx_lens[b] outside the table is flagged KVQ8_DEV_BAD_CTX_LEN and clamped.
  * A sequence for which a needed id of either row lies outside the pool, or a

@@ -129,10 +129,7 @@ evict_select_kernel(EvictParams p, int cache_tokens, int n_ctas) {
     sync_all();
     int any_bad = sh_bad;
     if (kCluster) any_bad = __any_sync(0xffffffffu, lane < n_ctas && load_cluster_int(&sh_bad, lane) != 0);
-    if (rank == 0 && tid == 0) {
-        if (any_bad) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
-        if (h == 0) p.new_lens[b] = any_bad ? 0 : m;
-    }
+    if (any_bad && rank == 0 && tid == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
     // a sequence with a bad id is left out; behind the last kept token -1; all tokens kept: no selection
     for (int j = (any_bad ? 0 : m) + rank * kThreads + tid; j < p.keep; j += n_ctas * kThreads) kept[j] = -1;
     if (any_bad || m == L) {
@@ -337,6 +334,9 @@ evict_copy_kernel(EvictParams p, int quarters) {
     const int most = min(kStageTok, p.keep - qd * kStageTok);
     const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
     const size_t dst = (size_t)p.dst_table[(size_t)b * p.dst_max_blocks + qd / 4] * p.nkv + h;
+    // the CTA of the sequence's last kept token knows how many there are (written
+    // here and not in the selection, so that new_lens may be ctx_lens itself)
+    const bool more = h == 0 && tid == 0 && p.keep - qd * kStageTok > kStageTok && kept[kStageTok] >= 0;
     if (tid < kStageTok) {
         const int t = tid < most ? kept[tid] : -1;
         src_tok[tid] = t;
@@ -344,6 +344,11 @@ evict_copy_kernel(EvictParams p, int quarters) {
         list_half[tid] = 0u;
     }
     __syncthreads();
+    if (warp == 0 && h == 0) {
+        const int count = __popc(__ballot_sync(0xffffffffu, src_tok[lane] >= 0)) +
+                          __popc(__ballot_sync(0xffffffffu, src_tok[32 + lane] >= 0));
+        if (lane == 0 && !more && (count > 0 || qd == 0)) p.new_lens[b] = qd * kStageTok + count;
+    }
     if (src_tok[0] < 0) return;
     const int slot0 = (qd % 4) * kStageTok;     // slot of the first token
 

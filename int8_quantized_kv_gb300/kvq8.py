@@ -623,7 +623,8 @@ def evict(cache: KVCache, weight_sum, block_table, ctx_lens, keep: int, dst_tabl
     n_first, the last n_recent, and the others of largest weight_sum - copied
     in order into the blocks of dst_table (int32 [batch][dst_max_blocks], none
     of them in block_table).  kept (int32 [batch][nkv][keep]) receives their
-    positions, -1 behind the last, and new_lens (int32 [batch]) their number."""
+    positions, -1 behind the last, and new_lens (int32 [batch], which may be
+    ctx_lens itself) their number."""
     i32 = _torch().int32
     nb, nkv, wants = _cache_wants(cache, weight_sum)
     batch, max_blocks = block_table.shape

@@ -185,3 +185,18 @@ def test_wide_table_short_sequences(gpu_lib):
     # more units than SMs with a wide table: keys beyond a CTA's shared memory in one of them
     lens = [300] * 159 + [25000]
     Pool(lens, 200, 1, seed=5).check(0, 20)
+
+
+@pytest.mark.parametrize("keep", [64, 500])
+def test_lengths_in_place(gpu_lib, keep):
+    # new_lens written over ctx_lens while other heads of the sequences may still wait for their selection
+    p = Pool([3000, 64, 0, 501] * 15, keep, 7, seed=keep)
+    kept, new_lens = p.run(4, 20)
+    q = Pool([3000, 64, 0, 501] * 15, keep, 7, seed=keep)
+    d = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    cache, wsum, table, dst = kvq8.KVCache(*(d(x) for x in (q.kp, q.vp, q.ks, q.vs))), d(q.w), d(q.table), d(q.dst)
+    for _ in range(5):
+        lens, again = d(np.array(q.lens, np.int32)), torch.empty_like(p.kept)
+        kvq8.evict(cache, wsum, table, lens, keep, dst, again, lens, n_first=4, n_recent=20, dev_status=q.status)
+        assert np.array_equal(lens.cpu().numpy(), new_lens) and np.array_equal(again.cpu().numpy(), kept)
+    assert all(torch.equal(a, b) for a, b in zip(cache, p.cache)) and int(q.status.item()) == 0
