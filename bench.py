@@ -246,10 +246,10 @@ def hbm_peak():
 # includes); a DRAM-traffic record is used only while their hash matches.
 _HEADERS = ("kvq8_device.cuh", "kvq8_internal.cuh", "kvq8_ptx.cuh", "../../include/kvq8.h")
 KERNEL_SOURCES = {
-    "decode_split_kernel": ("decode.cu",) + _HEADERS,
+    "decode_split_kernel": ("decode.cu", "decode_split.cuh") + _HEADERS,
     "quantize_append_kernel": ("append.cu",) + _HEADERS,
-    "kvq4_decode_attn": ("int4.cu", "decode.cu") + _HEADERS,
-    "kvmix_decode_attn": ("int4.cu", "decode.cu") + _HEADERS,
+    "kvq4_decode_attn": ("int4.cu", "decode.cu", "decode_split.cuh") + _HEADERS,
+    "kvmix_decode_attn": ("int4.cu", "decode.cu", "decode_split.cuh") + _HEADERS,
 }
 
 
