@@ -174,6 +174,16 @@ __device__ __forceinline__ float row_squares(const float (&x)[16]) {
     }
     return row_sum(a + b);
 }
+// The same of x * f.
+__device__ __forceinline__ float row_squares(const float (&x)[16], float f) {
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        a = fmaf(x[e] * f, x[e] * f, a);
+        b = fmaf(x[e + 1] * f, x[e + 1] * f, b);
+    }
+    return row_sum(a + b);
+}
 constexpr float kMostSquares = 0x1p120f;
 
 // Where a token's keys go: the tile of kv head 0 and the slot; tile < 0: nowhere.
@@ -509,25 +519,28 @@ __device__ __forceinline__ void store_keys(const NormRopeParams &p, float (&x)[1
     }
 }
 
-// Queries of heads h0 .. h0 + 3 (below nqh) of a token.  Squares that overflow
-// (|x| above about 2^60) are taken of x * 2^-64.
+// Queries of heads h0 .. h0 + 3 (below nqh) of a token.  Where the squares' sum
+// is beyond 2^120 it is taken again of x * 2^-68, of which 128 squares stay
+// below 2^7 (2^128 2^-68)^2 = 2^127 whatever the row; x itself is multiplied by
+// the scaled row's root, at most 2^12 there, and then by 2^-68 (exact).
 template <bool kPairs>
 __device__ __forceinline__ void store_queries(const NormRopeParams &p, float (&x)[16], const float (&c)[8],
                                               const float (&s)[8], int64_t row, int h0, int lane) {
     const int j = lane & 7, h = h0 + (lane >> 3);
     if (p.q_weight) {
         float ss = row_squares(x), f = 1.0f;
-        if (__any_sync(0xffffffffu, ss > kMostSquares)) {
-            if (ss > kMostSquares) {
-                f = 0x1p-64f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] *= f;
-            }
-            ss = row_squares(x);
+        const bool wide = __any_sync(0xffffffffu, ss > kMostSquares);
+        if (wide) {
+            if (ss > kMostSquares) f = 0x1p-68f;
+            ss = row_squares(x, f);
         }
         const float r = rsqrtf(fmaf(ss, 1.0f / kHD, p.eps * f * f));
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] *= r;
+        if (wide) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] *= f;
+        }
         weighted(x, p.q_weight, j);
     }
     turn<kPairs>(x, c, s);

@@ -290,6 +290,28 @@ def test_large_small_and_zero_rows(gpu_lib, n_new):
     c.check()
 
 
+@pytest.mark.parametrize("n_new", [1, 20])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_normed_rows_up_to_the_largest_value(gpu_lib, n_new, dtype, pairs):
+    # squares whose sum passes 2^128 even of much smaller rows: equal values of 1e38, the type's largest ones,
+    # spread rows, one such value beside small ones, and an ordinary row in the same task
+    rng = np.random.default_rng(35)
+    most = float(torch.finfo(TYPES[dtype]).max)
+    x = rng.standard_normal((1, n_new, 24, HD))
+    for h, row in enumerate([np.full(HD, 1e38), np.full(HD, most), most * rng.choice([-1, 1], HD),
+                             3e37 * np.clip(rng.standard_normal(HD), -3, 3), 1e18 * rng.standard_normal(HD), None,
+                             np.where(np.arange(HD) == 77, most, 1.0), most * rng.uniform(-1, 1, HD)]):
+        for first in (0, 8, 16):              # queries, keys, values
+            if row is not None:
+                x[:, :, first + h] = row
+    c = Case(1, n_new, 8, 8, dtype, start=11, pairs=pairs, x=x, seed=36)
+    c._generic = False
+    c.call()
+    c.check()
+    assert int(c.status.item()) == 0
+
+
 @pytest.mark.parametrize("n_new", [1, 50])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_nonfinite_rows(gpu_lib, n_new, dtype):
