@@ -64,8 +64,8 @@ __device__ __forceinline__ void combine_row_lanes(const DecodeParams &p, int G, 
 template <int G>
 __global__ void __launch_bounds__(kHD, 8)
 weights_merge_kernel(DecodeParams p, int chunks) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();   // (released before the wait: the same times)
     const int rows = p.batch * p.nqh;
     if (blockIdx.x < rows) {
         combine_row_lanes(p, G, blockIdx.x % p.nqh, blockIdx.x / p.nqh, threadIdx.x);
