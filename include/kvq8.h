@@ -282,12 +282,16 @@ kvq8_status kvq8_decode_step(const float *q, const float *k_new, const float *v_
  *
  * KVQ8_STEP_CACHE_READY: the caller vouches that the cache blocks this call
  * reads (apart from its new tokens' slots, which it writes itself),
- * block_table and ctx_lens held their final values before the kernel that
- * precedes this call in the stream began (they are not written by that
- * kernel, nor by anything it does not wait for).  The split kernel then runs
- * its prologue and starts copying the cache into shared memory without
- * waiting for that kernel; only the reads of q, k_new and v_new and the
- * writes of the workspace, the pools' new-token slots and out wait for it.
+ * block_table and ctx_lens held their final values before the call (or the
+ * caller's kernel) that precedes this one in the stream began: it writes none
+ * of them, except that it may be a decode step that appended the token at
+ * ctx_lens[b] - 2.  Its kernels may still run when this call reads the cache;
+ * everything ahead of it is done then (a caller's own kernel must not release
+ * its dependents before it has waited itself).  The split kernel runs its
+ * prologue and starts copying the cache into shared memory without waiting;
+ * only the copy of the 64 tokens that hold ctx_lens[b] - 2, the reads of q,
+ * k_new and v_new and the writes of the workspace, the pools' new-token slots
+ * and out wait for the preceding call.
  * A decode that runs one layer per call after the layer's own projections
  * (which write q, k_new and v_new only) meets this; so does a chain of steps
  * that differ only in those inputs.  Results are identical with and without

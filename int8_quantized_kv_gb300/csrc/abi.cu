@@ -78,6 +78,7 @@ kvq8_status fill_decode_params(const float *q, int batch, int nqh, int nkv,
     p->out = nullptr;
     p->first_q8_block = nullptr;
     p->cache_ready = 0;
+    p->release_early = 1;
     p->windows = nullptr;
     p->sinks = 0;
     p->ws_scores = nullptr;
@@ -280,6 +281,7 @@ kvq8_status kvq8_decode_combine(int batch, int nqh, int nkv, int hd, int max_blo
                             nullptr, &p, &plan);
     if (st != KVQ8_OK) return st;
     p.out = out;
+    p.release_early = 0;
     if (launch_decode_combine(p, plan.group, (cudaStream_t)stream) != cudaSuccess)
         return KVQ8_ERR_CUDA;
     return KVQ8_OK;

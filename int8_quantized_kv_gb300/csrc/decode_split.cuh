@@ -39,11 +39,11 @@
 // CTA unwinds without leaving copies in flight.  The kernel is launched as a
 // programmatic dependent of the previous kernel in its stream, so that its
 // launch overlaps that kernel; every thread waits for that kernel's results
-// first.  The combine releases the next kernel of the stream as soon as the
-// split's records are visible to it.  In a decode step the split kernel also
-// appends the step's new token: the consumer that decodes the stage holding
-// position ctx_lens[b] - 1 quantises the token into that staged stage and
-// into the pools (no separate append launch).
+// first.  The combine releases the next kernel of the stream when it starts.
+// In a decode step the split kernel also appends the step's new token: the
+// consumer that decodes the stage holding position ctx_lens[b] - 1 quantises
+// the token into that staged stage and into the pools (no separate append
+// launch).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -269,9 +269,13 @@ decode_split_kernel(DecodeParams p) {
     // (its launch overlaps that kernel's end), whose outputs may be this
     // kernel's inputs: every thread waits for it here first -- unless the
     // caller vouches that the cache, the block table and the context lengths
-    // were final before that kernel began (cache_ready): then the prologue and
-    // the producer's copies go ahead, and only the consumers wait (they read
-    // the query and the new token and write the workspace).
+    // were final before the call ahead of this one began (cache_ready): then
+    // the prologue and the producer's copies go ahead; the consumers wait (they
+    // read the query and the new token and write the workspace), and the
+    // producer before the stage of token L - 2, which that call may append.
+    // What lies ahead of that call is done when this kernel starts, since every
+    // thread waits before its CTA releases the next kernel: a merge, which
+    // releases at once, starts behind all that its split waited for.
     // In a mixed-precision decode (kMixed) the kernel before is the 4-bit split
     // of the same call, which writes nothing this kernel reads (it released
     // this one right after its own wait): no wait here; this kernel waits for
@@ -381,51 +385,63 @@ decode_split_kernel(DecodeParams p) {
             const int seg_n = (int)min((long long)(nb - off), remaining);
             const int32_t *row = p.block_table + (size_t)b * p.max_blocks;
             int tbl_base = -1, tbl_reg = -1;
-            for (int j = 0; j < seg_n; ++j) {
-                const int k = kbase + j, slot = k % Lay::kStages;
-                const uint32_t par = ((k / Lay::kStages) & 1) ^ 1;
-                const int t0 = stage_token<kMode>(sp, off + j);
-                const int lb = t0 / kBS, quarter = (t0 / kStageTok) & 3;
-                if (tbl_base < 0 || lb >= tbl_base + 32) {
-                    tbl_base = lb;
-                    tbl_reg = (lb + lane < p.max_blocks) ? row[lb + lane] : -1;
-                }
-                const int phys = __shfl_sync(0xffffffffu, tbl_reg, lb - tbl_base);
-                if (lane == 0) {
-                    const uint32_t fb = full0 + 8 * slot;
-                    if (!aborted && !mbar_wait_bounded(empty0 + 8 * slot, par, kWaitTimeoutNs)) {
-                        aborted = true;
-                        flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
+            // the stages that go ahead, then those from token L - 2 on (a loop of its
+            // own: a test per stage costs 0.1 us a call)
+            int j = 0, end = kMode == kWhole && !kMixed && p.cache_ready
+                                 ? max(0, min(seg_n, (sp.y - 2) / kStageTok - off)) : seg_n;
+            for (;;) {
+                for (; j < end; ++j) {
+                    const int k = kbase + j, slot = k % Lay::kStages;
+                    const uint32_t par = ((k / Lay::kStages) & 1) ^ 1;
+                    const int t0 = stage_token<kMode>(sp, off + j);
+                    const int lb = t0 / kBS, quarter = (t0 / kStageTok) & 3;
+                    if (tbl_base < 0 || lb >= tbl_base + 32) {
+                        tbl_base = lb;
+                        tbl_reg = (lb + lane < p.max_blocks) ? row[lb + lane] : -1;
                     }
-                    if (aborted) {
-                        // leave the slot unfilled; its consumer times out and unwinds
-                    } else if (phys >= 0 && phys < p.num_blocks) {
-                        skip[slot] = 0;
-                        const size_t tile = (size_t)phys * p.nkv + h;
-                        unsigned char *st = smem + Lay::oRing + (size_t)slot * kStageBytes;
-                        mbar_arrive_expect_tx(fb, kStageBytes);
-                        bulk_copy_g2s(smem_addr(st), p.k_pool + (tile * kBS + quarter * kStageTok) * kHD,
-                                      kStageKBytes, fb, pol);
-                        bulk_copy_g2s(smem_addr(st + kStageKBytes),
-                                      p.v_pool + tile * kHD * kBS + quarter * kTileVQuarter,
-                                      kStageVBytes, fb, pol);
-                        bulk_copy_g2s(smem_addr(st + kStageKBytes + kStageVBytes),
-                                      p.k_scale + tile * kBS + quarter * kStageTok, kStageSBytes, fb, pol);
-                        bulk_copy_g2s(smem_addr(st + kStageKBytes + kStageVBytes + kStageSBytes),
-                                      p.v_scale + tile * kBS + quarter * kStageTok, kStageSBytes, fb, pol);
-                    } else {
-                        skip[slot] = 1;
-                        flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
-                        mbar_arrive(fb);
+                    const int phys = __shfl_sync(0xffffffffu, tbl_reg, lb - tbl_base);
+                    if (lane == 0) {
+                        const uint32_t fb = full0 + 8 * slot;
+                        if (!aborted && !mbar_wait_bounded(empty0 + 8 * slot, par, kWaitTimeoutNs)) {
+                            aborted = true;
+                            flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
+                        }
+                        if (aborted) {
+                            // leave the slot unfilled; its consumer times out and unwinds
+                        } else if (phys >= 0 && phys < p.num_blocks) {
+                            skip[slot] = 0;
+                            const size_t tile = (size_t)phys * p.nkv + h;
+                            unsigned char *st = smem + Lay::oRing + (size_t)slot * kStageBytes;
+                            mbar_arrive_expect_tx(fb, kStageBytes);
+                            bulk_copy_g2s(smem_addr(st), p.k_pool + (tile * kBS + quarter * kStageTok) * kHD,
+                                          kStageKBytes, fb, pol);
+                            bulk_copy_g2s(smem_addr(st + kStageKBytes),
+                                          p.v_pool + tile * kHD * kBS + quarter * kTileVQuarter,
+                                          kStageVBytes, fb, pol);
+                            bulk_copy_g2s(smem_addr(st + kStageKBytes + kStageVBytes),
+                                          p.k_scale + tile * kBS + quarter * kStageTok, kStageSBytes, fb, pol);
+                            bulk_copy_g2s(smem_addr(st + kStageKBytes + kStageVBytes + kStageSBytes),
+                                          p.v_scale + tile * kBS + quarter * kStageTok, kStageSBytes, fb, pol);
+                        } else {
+                            skip[slot] = 1;
+                            flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
+                            mbar_arrive(fb);
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (end == seg_n) break;
+                pdl_wait();
+                end = seg_n;
             }
             remaining -= seg_n;
             kbase += seg_n;
             off = 0;
             if (++h == p.nkv) { h = 0; ++b; }
         }
+        // the release below counts for the CTA with its first thread: not before
+        // the kernel ahead of this one is done
+        if (kMode == kWhole && !kMixed && p.cache_ready) pdl_wait();
         // no copy may still be in flight when the CTA exits
         if (lane == 0) {
             for (int k = max(0, kbase - Lay::kStages); k < kbase; ++k)

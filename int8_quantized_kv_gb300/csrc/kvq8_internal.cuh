@@ -122,11 +122,15 @@ struct DecodeParams {
     const int32_t *first_q8_block;
     const int2 *ws_meta2;
     const float *ws_ml2, *ws_acc2;
-    // Nonzero: the cache, block_table and ctx_lens were final before the
-    // kernel preceding this call in the stream began, so the split kernel's
-    // prologue and copies run before it waits for that kernel (only q, k_new,
-    // v_new and the workspace wait).  Zero: every thread waits first.
+    // Nonzero: the cache, block_table and ctx_lens were final before the call
+    // preceding this one in the stream began (but for the token before the
+    // new one), so the split kernel's prologue and copies run before it waits
+    // for that call (q, k_new, v_new, the workspace and that token's stage
+    // wait).  Zero: every thread waits first.
     int cache_ready;
+    // merge: 1 when it follows its own split in the stream (it releases the next
+    // kernel before its wait), 0 when other kernels may lie between
+    int release_early;
     // sliding window with first tokens (windowed split only)
     const int32_t *windows;       // [batch]
     int sinks;

@@ -77,7 +77,7 @@ def _replays(calls, reset, outs, times=10):
             assert torch.equal(o, w)
 
 
-@pytest.mark.parametrize("ahead", ["weights"])
+@pytest.mark.parametrize("ahead", ["plain", "ready", "window", "weights"])
 @pytest.mark.parametrize("batch, nkv, group, L0", [(1, 1, 1, 1), (1, 2, 1, 61), (1, 8, 2, 190), (3, 1, 8, 253),
                                                    (4, 8, 4, 1021), (28, 8, 2, 1533), (1, 8, 2, 8190)])
 def test_token_of_the_step_ahead(gpu_lib, batch, nkv, group, L0, ahead):
@@ -97,7 +97,7 @@ def test_token_of_the_step_ahead(gpu_lib, batch, nkv, group, L0, ahead):
     assert int(s.status.item()) == 0
 
 
-@pytest.mark.parametrize("between", ["weights"])
+@pytest.mark.parametrize("between", ["step", "ready", "window", "weights", "attn", "int4", "combine"])
 @pytest.mark.parametrize("batch, nkv", [(1, 2), (28, 8)])
 def test_rows_of_the_call_before_the_one_ahead(gpu_lib, batch, nkv, between):
     # a bulk append, a call on another cache, then a flagged step over the appended rows

@@ -42,3 +42,21 @@ def test_kernels_are_found():
 def test_waits_before_it_releases(name):
     body = KERNELS[name]
     assert 0 <= body.find("pdl_wait()") < body.find("pdl_launch_dependents()")
+
+
+def test_split_of_a_ready_step_waits_in_every_thread():
+    # its producer starts without a wait; it waits before the stages that the step ahead may write and, in any case,
+    # before the CTA's release, which counts with the first thread that gets there
+    body = KERNELS["decode_split_kernel"]
+    producer = body[body.index("if (warp == kConsumerWarps)"):body.index("for (int k = max(0, kbase - Lay::kStages)")]
+    assert producer.count("pdl_wait()") == 2
+    assert re.search(r"pdl_wait\(\);\s*if \(lane == 0\) \{\s*$", producer)
+    consumers = body[body.index("for (int k = max(0, kbase - Lay::kStages)"):]
+    assert consumers.index("pdl_wait()") < consumers.index("while (remaining > 0")
+
+
+def test_a_merge_called_on_its_own_releases_late():
+    # anything may lie between kvq8_decode_split and kvq8_decode_combine
+    text = open(os.path.join(CSRC, "abi.cu")).read()
+    combine = text[text.index("kvq8_status kvq8_decode_combine("):text.index("kvq8_status kvq8_decode_attn(")]
+    assert "p.release_early = 0;" in combine
