@@ -191,3 +191,52 @@ def test_wide_table(gpu_lib):
     before, wsum = _sums(case, 4)
     _run(case, wsum)
     _check_sums(case, before, wsum.cpu().numpy())
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("shape", ["rise", "fall", "waves"])
+def test_many_records_per_unit(gpu_lib, G, shape):
+    # a unit cut into more than 32 records, whose maxima rise, fall, or do both from one to the next
+    rng = np.random.default_rng(860 + G)
+    lens = [30001, 70]
+    u = rng.standard_normal((G, 128)).astype(np.float32)
+    q = np.stack([4 * u, 4 * u])
+    L = lens[0]
+    t = np.arange(L) / L
+    lift = {"rise": t, "fall": 1 - t, "waves": 0.5 + 0.5 * np.sin(40 * t)}[shape]
+    k = 0.3 * rng.standard_normal((2, L, 1, 128)) + 0.35 * lift[None, :, None, None] * u.sum(0)
+    k, v = k.astype(np.float32), rng.standard_normal((2, L, 1, 128)).astype(np.float32)
+    nb = 2 * ((L + 255) // 256)
+    table = rng.permutation(nb).astype(np.int32).reshape(2, -1)
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    cache, table_d, lens_d = kvq8.alloc_cache(nb, 1), d(table), d(np.array(lens, np.int32))
+    kvq8.quantize_append(d(k), d(v), torch.zeros(2, dtype=torch.int32, device="cuda"), table_d, cache)
+    wsum, out = kvq8.alloc_weight_sum(nb, 1), torch.full((2, G, 128), float("nan"), device="cuda")
+    ws = kvq8.alloc_weights_workspace(2, G, 1, table.shape[1])
+    ws.fill_(255)
+    kvq8.decode_attn_weights(d(q), cache, table_d, lens_d, out, wsum, ws)
+    got, sums = out.cpu().numpy(), wsum.cpu().numpy()
+    records = ws[:8].view(torch.int32)[1].item()             # the first unit's (first CTA, number) in the workspace
+    assert records > 64
+    for b, n in enumerate(lens):
+        rows = ref.unit_rows(k[b, :n, 0], v[b, :n, 0])
+        assert_close(got[b], ref.decode(q[b], *rows), f"sequence {b}")
+        p, most = ref.weights(q[b], *rows[:2])
+        assert most <= 64
+        i = np.arange(n)
+        assert np.all(np.abs(sums[table[b, i // 256], 0, i % 256] - p) <= 1e-4 * p + 1e-30)
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_output_of_many_units_of_two_heads(gpu_lib, step):
+    # the grid of two CTAs per SM, against the plain decode over the same cache
+    lens = np.random.default_rng(7).integers(1, 3000, 40)
+    lens[5] = 0
+    cfg = wl.Workload("s", 846, batch=40, nqh=8, nkv=4)
+    case = (StepCase if step else Case)(cfg, lens=lens)
+    got = _run(case, kvq8.alloc_weight_sum(case.num_blocks, 4), step=step)
+    assert_close(got, case.decode(), "against the plain decode")
+    for b in (0, 17, 39):
+        rows = ref.unit_rows(*wl.unit_kv(cfg, b, 3, int(lens[b])), step)
+        assert_close(got[b, 6:], ref.decode(case.q[b, 6:], *rows), f"sequence {b}")
+    assert not got[5].any() and case.status_bits() == 0
