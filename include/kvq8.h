@@ -371,11 +371,13 @@ kvq8_status kvq8_selftest_bounded_wait(uint32_t *dev_status, uint64_t timeout_ns
 /*
  * Rounding in the operators from here to kvq8_norm_rope_append: where
  * kvq8_quantize_append, kvq8_quantize_q and kvq8_decode_step divide, these
- * multiply by rounded reciprocals (cheaper, and as near to the exact quotient
- * to half a step): a row's scale is max|v| * (1/127), a query block's factor
- * 127 * (1/qm), 1/127 and 1/qm rounded to fp32.  A scale may differ from the
- * other rule's in its last bit, and a code by one where its value lies within
- * a few 2^-24 of a border; everything else is as there.
+ * multiply by reciprocals rounded to fp32, as elementary tensor operations
+ * evaluate x / 127 and 127 / x: a row's scale is max|v| * (1/127), off by at
+ * most 0.56 units in its last place (a division 0.5; one scale in twenty
+ * differs), a query block's factor 127 * (1/qm), off by at most 1.5 (one in
+ * four differs).  So a row's scale may differ in its last bit from what those
+ * calls store for it, and a code by one where its value lies within 3 * 2^-24
+ * of itself of a border; everything else is as there.
  */
 
 /*

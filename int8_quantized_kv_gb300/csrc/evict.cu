@@ -540,10 +540,12 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
     if (blocks > 2147483647 || units > 2147483647 / 8) return cudaErrorInvalidConfiguration;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // Small tables: CTAs of 128 threads, eight to an SM.  Else 512 threads, two
+    // Small tables: CTAs of 128 threads, eight to an SM up to 768 tokens and six
+    // at 2048 (24 KiB of counts and the keys each).  Else 512 threads, two
     // to an SM (1024 leave room for one: 224 units of 8192 tokens then took two
     // rounds), and where that leaves SMs idle, clusters of up to eight CTAs per
-    // unit with at least 8192 tokens each.  (Whole calls: 32 units of 131072
+    // unit with at least 8192 tokens each, the table's width taken for the
+    // lengths, which the host does not know.  (Whole calls: 32 units of 131072
     // tokens 363 -> 202 us, 32 of 32768 91 -> 66, 18 of 24000 53 -> 45; with
     // 2048 tokens per CTA the cluster's barriers cost more than they save: 64
     // units of 8192 44 -> 49, 32 of 32768 76.)
