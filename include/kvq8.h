@@ -97,6 +97,7 @@ typedef enum kvq8_status {
 #define KVQ8_DEV_BAD_POSITION 0x4u   /* append position start_pos[b]+i outside the block table */
 #define KVQ8_DEV_TIMEOUT 0x8u        /* an internal pipeline wait gave up (never expected); the
                                         affected results are unspecified */
+#define KVQ8_DEV_BAD_GROUPS 0x20u    /* group_starts does not cut the batch into groups (kvq8_decode_attn_shared) */
 #define KVQ8_DEV_NONFINITE 0x10u     /* a K/V row, a 4-bit group or a query 32-block held a NaN
                                         or an infinity and was quantised as zeros (see below) */
 
@@ -565,6 +566,132 @@ kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, i
                                   int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
                                   float *weight_sum, float *q_out,
                                   uint32_t *dev_status, void *stream);
+
+/* ------------------------------------------------- prompt attention --- */
+
+/*
+ * kvq8_prompt_attn -- attention of several query tokens per sequence over the
+ * int8 cache, each over the tokens up to its own position: a prompt or a part
+ * of one, or drafted tokens to be verified.  Their own K and V rows are in the
+ * cache already (kvq8_quantize_append, kvq8_norm_rope_append).  Query token i
+ * of sequence b stands at position start_pos[b] + i and gets what
+ * kvq8_decode_attn computes for it at a context of start_pos[b] + i + 1 tokens.
+ *
+ *   q          rows of `q_dtype` (KVQ8_DTYPE_*): the heads of a token lie side
+ *              by side ([nqh][hd]); token i of sequence b is row b * n_new + i,
+ *              rows q_stride elements apart.  kvq8_norm_rope_append's q_out is
+ *              fp32 with q_stride = nqh * hd
+ *   start_pos  int32 [batch]: position of each sequence's first query token
+ *   n_tokens   int32 [batch], or NULL: query tokens i >= n_tokens[b] are
+ *              padding: nothing is read or written for them
+ *   out        rows of `out_dtype`, out_stride elements apart, not overlapping
+ *              q; computed in fp32 and rounded once.  (For bf16 the softmax
+ *              weights enter the sum rounded to 11 bits, otherwise to 22.)
+ *   workspace  at least kvq8_prompt_workspace_bytes(...) bytes, otherwise as
+ *              kvq8_decode_attn
+ * Pointers 16-byte aligned, strides multiples of 16 bytes and at least
+ * nqh * hd.  A query token whose position lies outside the block table is
+ * flagged KVQ8_DEV_BAD_POSITION and attends the tokens that the table has (none
+ * before position 0: its row is 0).  Tokens whose block id is outside the pool
+ * are skipped and flagged.  batch * n_new * nqh is below 2^31, else
+ * KVQ8_ERR_UNSUPPORTED.
+ */
+size_t kvq8_prompt_workspace_bytes(int batch, int n_new, int nqh, int nkv, int hd, int max_blocks,
+                                   int block_size);
+
+kvq8_status kvq8_prompt_attn(const void *q, int q_dtype, int64_t q_stride,
+                             int batch, int n_new, int nqh, int nkv, int hd,
+                             const int8_t *k_pool, const int8_t *v_pool,
+                             const float *k_scale, const float *v_scale,
+                             int num_blocks, const int32_t *block_table,
+                             int max_blocks, int block_size,
+                             const int32_t *start_pos, const int32_t *n_tokens, float sm_scale,
+                             void *out, int out_dtype, int64_t out_stride,
+                             void *workspace, size_t workspace_bytes,
+                             uint32_t *dev_status, void *stream);
+
+/* ------------------------------------------ decode over shared prefixes --- */
+
+/*
+ * kvq8_decode_attn_shared -- kvq8_decode_attn for a batch whose rows share
+ * their first tokens in groups: rows group_starts[g] .. group_starts[g + 1] - 1
+ * hold the same tokens at the positions t < shared_lens[g].  These are read
+ * once for the whole group (through the block-table row of one of them: the
+ * first whose context has all of them), and each row's own tokens, from
+ * shared_lens[g] on, through its own block-table row, whose blocks that hold
+ * shared tokens only are not looked at.  A prefix may end inside a block; the
+ * rows' own blocks then hold their own tokens behind it.
+ *
+ *   n_groups      groups in the batch, 1 <= n_groups <= 65535; a group may be
+ *                 empty.  (Layers that are folded into the batch are groups of
+ *                 their own)
+ *   group_starts  int32 [n_groups + 1]: 0 = group_starts[0] <= ... <=
+ *                 group_starts[n_groups] = batch.  Otherwise flagged
+ *                 KVQ8_DEV_BAD_GROUPS, and every row is decoded from its own
+ *                 block-table row alone
+ *   shared_lens   int32 [n_groups], >= 0 (below 0: taken as 0 and flagged
+ *                 KVQ8_DEV_BAD_CTX_LEN).  A row whose ctx_lens[b] is smaller
+ *                 attends the first ctx_lens[b] shared tokens
+ *   workspace     at least kvq8_shared_workspace_bytes(...) bytes, otherwise as
+ *                 kvq8_decode_attn
+ * Other arguments as kvq8_decode_attn.
+ *
+ * kvq8_decode_step_shared -- the same as one decode step: appends k_new, v_new
+ * at position ctx_lens[b] - 1 as kvq8_decode_step does, then attends.  The new
+ * token counts as the row's own, however large shared_lens[g].
+ */
+size_t kvq8_shared_workspace_bytes(int batch, int n_groups, int nqh, int nkv, int hd, int max_blocks,
+                                   int block_size);
+
+kvq8_status kvq8_decode_attn_shared(const float *q, int batch, int nqh, int nkv, int hd,
+                                    const int8_t *k_pool, const int8_t *v_pool,
+                                    const float *k_scale, const float *v_scale,
+                                    int num_blocks, const int32_t *block_table,
+                                    int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, int n_groups,
+                                    const int32_t *group_starts, const int32_t *shared_lens,
+                                    float sm_scale, float *out,
+                                    void *workspace, size_t workspace_bytes,
+                                    uint32_t *dev_status, void *stream);
+
+kvq8_status kvq8_decode_step_shared(const float *q, const float *k_new, const float *v_new,
+                                    int batch, int nqh, int nkv, int hd,
+                                    int8_t *k_pool, int8_t *v_pool, float *k_scale, float *v_scale,
+                                    int num_blocks, const int32_t *block_table,
+                                    int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, int n_groups,
+                                    const int32_t *group_starts, const int32_t *shared_lens,
+                                    float sm_scale, float *out,
+                                    void *workspace, size_t workspace_bytes,
+                                    uint32_t *dev_status, void *stream);
+
+/* ------------------------------------------------- reading the cache back --- */
+
+/*
+ * kvq8_read -- the K and V rows of given positions as the values their codes
+ * stand for, code * scale in fp32, rounded once to `dtype`: what another
+ * kernel, or a copy outside the pool, needs of a cached stretch.
+ *
+ *   start_pos, n_tokens   token i of sequence b is position start_pos[b] + i;
+ *              n_tokens int32 [batch], or NULL: rows i >= n_tokens[b] are left
+ *              as they are
+ *   k_out, v_out  rows of `dtype` (KVQ8_DTYPE_*): the heads of a token lie side
+ *              by side ([nkv][hd]); token i of sequence b is row b * n_new + i,
+ *              rows k_stride (v_stride) elements apart.  Pointers 16-byte
+ *              aligned, strides multiples of 16 bytes and at least nkv * hd.
+ *              Either may be NULL: its rows are not read
+ * Rows whose position is outside the block table, or whose block id is outside
+ * the pool, are left as they are and flagged (KVQ8_DEV_BAD_POSITION,
+ * KVQ8_DEV_BAD_BLOCK_ID).  batch == 0 or n_new == 0 is a no-op.
+ */
+kvq8_status kvq8_read(int batch, int n_new, int nkv, int hd,
+                      const int8_t *k_pool, const int8_t *v_pool,
+                      const float *k_scale, const float *v_scale,
+                      int num_blocks, const int32_t *block_table,
+                      int max_blocks, int block_size,
+                      const int32_t *start_pos, const int32_t *n_tokens,
+                      void *k_out, void *v_out, int dtype, int64_t k_stride, int64_t v_stride,
+                      uint32_t *dev_status, void *stream);
 
 /* -------------------------------------------- 4-bit cache (NEXT row) --- */
 

@@ -568,6 +568,241 @@ kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, i
     return KVQ8_OK;
 }
 
+// ------------------------------------------ prompts, shared prefixes, reading --
+
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+static bool dtype_known(int dtype) {
+    return dtype == KVQ8_DTYPE_F32 || dtype == KVQ8_DTYPE_BF16 || dtype == KVQ8_DTYPE_F16;
+}
+
+// Rows of `width` elements of a type, `stride` apart, every one 16-byte aligned.
+static bool stride_ok(int64_t stride, int64_t width, int dtype) {
+    return stride >= width && stride % (dtype == KVQ8_DTYPE_F32 ? 4 : 8) == 0;
+}
+
+// Workspace of a tile kernel: its directory, then (M, S) and the accumulator of
+// `rows` rows.
+struct TileWorkspace {
+    size_t dir, ml, acc, bytes;
+};
+static TileWorkspace tile_workspace(size_t dirs, size_t rows) {
+    TileWorkspace w;
+    w.dir = 0;
+    w.ml = up256(dirs * sizeof(int4));
+    w.acc = w.ml + up256(rows * 2 * sizeof(float));
+    w.bytes = w.acc + up256(rows * kHD * sizeof(float));
+    return w;
+}
+
+static void place_tile_workspace(const TileWorkspace &w, void *base, TileParams *p) {
+    p->ws_dir = (int4 *)((char *)base + w.dir);
+    p->ws_ml = (float *)((char *)base + w.ml);
+    p->ws_acc = (float *)((char *)base + w.acc);
+}
+
+static TileWorkspace prompt_workspace() {
+    return tile_workspace(kMaxTileCtas, (size_t)kMaxTileCtas * 2 * kTileRows);
+}
+
+size_t kvq8_prompt_workspace_bytes(int batch, int n_new, int nqh, int nkv, int hd, int max_blocks,
+                                   int block_size) {
+    if (check_shape(hd, block_size) != KVQ8_OK || check_heads(nqh, nkv) != KVQ8_OK) return 0;
+    if (batch < 0 || n_new < 0 || max_blocks <= 0 || max_blocks > 2147483647 / kBS || batch > kMaxGridYZ) return 0;
+    if ((int64_t)batch * n_new > 2147483647 / nqh) return 0;
+    return prompt_workspace().bytes;
+}
+
+kvq8_status kvq8_prompt_attn(const void *q, int q_dtype, int64_t q_stride, int batch, int n_new, int nqh, int nkv,
+                             int hd, const int8_t *k_pool, const int8_t *v_pool, const float *k_scale,
+                             const float *v_scale, int num_blocks, const int32_t *block_table, int max_blocks,
+                             int block_size, const int32_t *start_pos, const int32_t *n_tokens, float sm_scale,
+                             void *out, int out_dtype, int64_t out_stride, void *workspace,
+                             size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    kvq8_status st = check_shape(hd, block_size);
+    if (st != KVQ8_OK) return st;
+    if ((st = check_heads(nqh, nkv)) != KVQ8_OK) return st;
+    if (batch < 0 || n_new < 0 || num_blocks <= 0 || max_blocks <= 0) return KVQ8_ERR_INVALID_ARG;
+    if (max_blocks > 2147483647 / kBS || batch > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
+    if (!dtype_known(q_dtype) || !dtype_known(out_dtype)) return KVQ8_ERR_UNSUPPORTED;
+    if (!isfinite(sm_scale)) return KVQ8_ERR_INVALID_ARG;
+    if ((int64_t)batch * n_new > 2147483647 / nqh) return KVQ8_ERR_UNSUPPORTED;
+    if (batch == 0 || n_new == 0) return KVQ8_OK;
+    if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !block_table || !start_pos || !out)
+        return KVQ8_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scale, 16) ||
+        !aligned(v_scale, 16) || !aligned(block_table, 4) || !aligned(start_pos, 4) || !aligned(n_tokens, 4) ||
+        !aligned(out, 16))
+        return KVQ8_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)nqh * kHD;
+    if (!stride_ok(q_stride, width, q_dtype) || !stride_ok(out_stride, width, out_dtype)) return KVQ8_ERR_INVALID_ARG;
+    const TileWorkspace w = prompt_workspace();
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.bytes) return KVQ8_ERR_WORKSPACE;
+    TileParams p = {};
+    p.q = q;
+    p.q_dtype = q_dtype;
+    p.q_stride = q_stride;
+    p.batch = batch;
+    p.n_new = n_new;
+    p.nqh = nqh;
+    p.nkv = nkv;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_blocks = num_blocks;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    p.dev_status = dev_status;
+    p.start_pos = start_pos;
+    p.n_tokens = n_tokens;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.out_stride = out_stride;
+    place_tile_workspace(w, workspace, &p);
+    return launch_prompt(p, nqh / nkv, (cudaStream_t)stream) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+}
+
+// The prefix part's workspace, behind the plain decode's and the tails.
+static TileWorkspace shared_workspace(int batch, int nqh) {
+    const size_t rows = (size_t)batch * nqh;
+    return tile_workspace(rows, rows + (size_t)kMaxTileCtas * kTileRows);
+}
+
+size_t kvq8_shared_workspace_bytes(int batch, int n_groups, int nqh, int nkv, int hd, int max_blocks,
+                                   int block_size) {
+    const size_t base = kvq8_decode_workspace_bytes(batch, nqh, nkv, hd, max_blocks, block_size);
+    if (!base || n_groups < 0 || n_groups > kMaxGridYZ || (int64_t)batch * nqh > 2147483647 - kMaxTileCtas * kTileRows)
+        return 0;
+    return base + up256((size_t)batch * sizeof(int32_t)) + shared_workspace(batch, nqh).bytes;
+}
+
+static kvq8_status run_shared(const float *q, const float *k_new, const float *v_new, bool step, int batch, int nqh,
+                              int nkv, int hd, const int8_t *k_pool, const int8_t *v_pool, const float *k_scale,
+                              const float *v_scale, int num_blocks, const int32_t *block_table, int max_blocks,
+                              int block_size, const int32_t *ctx_lens, int n_groups, const int32_t *group_starts,
+                              const int32_t *shared_lens, float sm_scale, float *out, void *workspace,
+                              size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    kvq8_status st = check_decode_args(q, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale,
+                                       num_blocks, block_table, max_blocks, block_size, ctx_lens);
+    if (st != KVQ8_OK) return st;
+    if (n_groups < 0 || (batch > 0 && n_groups == 0)) return KVQ8_ERR_INVALID_ARG;
+    if (n_groups > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
+    if (batch == 0) return KVQ8_OK;
+    if ((int64_t)batch * nqh > 2147483647 - kMaxTileCtas * kTileRows) return KVQ8_ERR_UNSUPPORTED;
+    if (!out || !aligned(out, 16) || !isfinite(sm_scale)) return KVQ8_ERR_INVALID_ARG;
+    if (!group_starts || !shared_lens || !aligned(group_starts, 4) || !aligned(shared_lens, 4))
+        return KVQ8_ERR_INVALID_ARG;
+    if (step && (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))) return KVQ8_ERR_INVALID_ARG;
+    DecodeParams d;
+    DecodePlan plan;
+    st = fill_decode_params(q, batch, nqh, nkv, k_pool, v_pool, k_scale, v_scale, num_blocks, block_table,
+                            max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &d, &plan);
+    if (st != KVQ8_OK) return st;
+    const size_t tails = plan.bytes, tiles = tails + up256((size_t)batch * sizeof(int32_t));
+    const TileWorkspace w = shared_workspace(batch, nqh);
+    if (workspace_bytes < tiles + w.bytes) return KVQ8_ERR_WORKSPACE;
+    TileParams p = {};
+    p.q = q;
+    p.q_dtype = KVQ8_DTYPE_F32;
+    p.q_stride = (int64_t)nqh * kHD;
+    p.batch = batch;
+    p.n_new = 1;
+    p.nqh = nqh;
+    p.nkv = nkv;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_blocks = num_blocks;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.sm_scale_log2 = d.sm_scale_log2;
+    p.dev_status = dev_status;
+    p.ctx_lens = ctx_lens;
+    p.group_starts = group_starts;
+    p.shared_lens = shared_lens;
+    p.n_groups = n_groups;
+    p.step = step ? 1 : 0;
+    p.ws_tail = (int32_t *)((char *)workspace + tails);
+    place_tile_workspace(w, (char *)workspace + tiles, &p);
+    d.out = out;
+    d.k_new = k_new;
+    d.v_new = v_new;
+    d.windows = p.ws_tail;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (launch_shared_prefix(p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    if (launch_decode_tail_split(d, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    if (launch_shared_merge(d, p, plan.group, s) != cudaSuccess) return KVQ8_ERR_CUDA;
+    return KVQ8_OK;
+}
+
+kvq8_status kvq8_decode_attn_shared(const float *q, int batch, int nqh, int nkv, int hd, const int8_t *k_pool,
+                                    const int8_t *v_pool, const float *k_scale, const float *v_scale,
+                                    int num_blocks, const int32_t *block_table, int max_blocks, int block_size,
+                                    const int32_t *ctx_lens, int n_groups, const int32_t *group_starts,
+                                    const int32_t *shared_lens, float sm_scale, float *out, void *workspace,
+                                    size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    return run_shared(q, nullptr, nullptr, false, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale, num_blocks,
+                      block_table, max_blocks, block_size, ctx_lens, n_groups, group_starts, shared_lens, sm_scale,
+                      out, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq8_status kvq8_decode_step_shared(const float *q, const float *k_new, const float *v_new, int batch, int nqh,
+                                    int nkv, int hd, int8_t *k_pool, int8_t *v_pool, float *k_scale,
+                                    float *v_scale, int num_blocks, const int32_t *block_table, int max_blocks,
+                                    int block_size, const int32_t *ctx_lens, int n_groups,
+                                    const int32_t *group_starts, const int32_t *shared_lens, float sm_scale,
+                                    float *out, void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                                    void *stream) {
+    return run_shared(q, k_new, v_new, true, batch, nqh, nkv, hd, k_pool, v_pool, k_scale, v_scale, num_blocks,
+                      block_table, max_blocks, block_size, ctx_lens, n_groups, group_starts, shared_lens, sm_scale,
+                      out, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq8_status kvq8_read(int batch, int n_new, int nkv, int hd, const int8_t *k_pool, const int8_t *v_pool,
+                      const float *k_scale, const float *v_scale, int num_blocks, const int32_t *block_table,
+                      int max_blocks, int block_size, const int32_t *start_pos, const int32_t *n_tokens,
+                      void *k_out, void *v_out, int dtype, int64_t k_stride, int64_t v_stride,
+                      uint32_t *dev_status, void *stream) {
+    const kvq8_status st = check_shape(hd, block_size);
+    if (st != KVQ8_OK) return st;
+    if (batch < 0 || n_new < 0 || nkv <= 0 || num_blocks <= 0 || max_blocks <= 0) return KVQ8_ERR_INVALID_ARG;
+    if (max_blocks > 2147483647 / kBS || batch > kMaxGridYZ || nkv > kMaxGridYZ) return KVQ8_ERR_UNSUPPORTED;
+    if (!dtype_known(dtype)) return KVQ8_ERR_UNSUPPORTED;
+    if (batch == 0 || n_new == 0) return KVQ8_OK;
+    if ((!k_out && !v_out) || !block_table || !start_pos) return KVQ8_ERR_INVALID_ARG;
+    if ((k_out && (!k_pool || !k_scale)) || (v_out && (!v_pool || !v_scale))) return KVQ8_ERR_INVALID_ARG;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+        !aligned(block_table, 4) || !aligned(start_pos, 4) || !aligned(n_tokens, 4) || !aligned(k_out, 16) ||
+        !aligned(v_out, 16))
+        return KVQ8_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)nkv * kHD;
+    if ((k_out && !stride_ok(k_stride, width, dtype)) || (v_out && !stride_ok(v_stride, width, dtype)))
+        return KVQ8_ERR_INVALID_ARG;
+    ReadParams p;
+    p.batch = batch;
+    p.n_new = n_new;
+    p.nkv = nkv;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_blocks = num_blocks;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.start_pos = start_pos;
+    p.n_tokens = n_tokens;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.dtype = dtype;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.dev_status = dev_status;
+    return launch_read(p, (cudaStream_t)stream) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+}
+
 kvq8_status kvq8_evict(int batch, int nkv, int hd, int8_t *k_pool, int8_t *v_pool, float *k_scale,
                        float *v_scale, float *weight_sum, int num_blocks, const int32_t *block_table,
                        int max_blocks, int block_size, const int32_t *ctx_lens, int keep, int n_first,

@@ -120,13 +120,16 @@ __device__ __forceinline__ int clamp_len(int L, int cap) { return max(0, min(L, 
 enum SplitMode {
     kWhole = 0,      // every token of the span
     kWindowed = 1,   // tokens t < sinks or t >= L - windows[b]
-    kScored = 2      // every token, and its scores (base 2) are written to ws_scores
+    kScored = 2,     // every token, and its scores (base 2) are written to ws_scores
+    kTail = 3        // tokens t >= windows[b] (here the row's first token behind its shared prefix)
 };
+// The windowed and scored decodes round with reciprocal factors (include/kvq8.h).
+constexpr bool recip_rule(int mode) { return mode == kWindowed || mode == kScored; }
 
 // The tokens of sequence b that this launch decodes: [x, y) in stages of 64
 // from x on, after `ns` stages from token 0 on (kWindowed: the first tokens).
 // x is a multiple of 64.  Tokens of these stages from min(sinks, lo) to lo are
-// masked (kWindowed; lo = 0 otherwise).
+// masked (kWindowed, kTail; lo = 0 otherwise).
 struct SeqSpan {
     int x, y, ns, lo;
 };
@@ -145,6 +148,10 @@ __device__ __forceinline__ SeqSpan seq_span(const DecodeParams &p, int b, int ca
         const int ns = p.sinks / kStageTok + (p.sinks % kStageTok ? 1 : 0);
         if (ns >= x / kStageTok) return {0, L, 0, lo};
         return {x, L, ns, lo};
+    }
+    if (kMode == kTail) {
+        const int lo = max(0, min(L, p.windows[b]));
+        return {lo < L ? lo / kStageTok * kStageTok : L, L, 0, lo};
     }
     const int s = (kMixed && p.first_q8_block) ? min(L, max(0, min(p.first_q8_block[b], cap / kBS)) * kBS) : 0;
     return {s, L, 0, 0};
@@ -524,7 +531,7 @@ decode_split_kernel(DecodeParams p) {
 #pragma unroll
             for (int i = 0; i < kQRows; ++i) {
                 const int g = warp + i * kConsumerWarps;
-                if (g < G) quantize_q_vals_warp<kMode != kWhole>(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
+                if (g < G) quantize_q_vals_warp<recip_rule(kMode)>(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
             }
             named_barrier_sync(1, kConsumerWarps * 32);
             if (remaining > seg_n) {   // the next segment's unit follows this one
@@ -571,13 +578,17 @@ decode_split_kernel(DecodeParams p) {
                             nxk = reinterpret_cast<const float4 *>(p.k_new + src)[lane];
                             nxv = reinterpret_cast<const float4 *>(p.v_new + src)[lane];
                         }
-                        append_new_token<kMode != kWhole>(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
+                        append_new_token<recip_rule(kMode)>(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
                     }
                     const int ta = lane, tb = lane + 32;
                     bool va = ta < nvalid, vb = tb < nvalid;
                     if (kMode == kWindowed) {
                         va &= t0 + ta < p.sinks || t0 + ta >= sp.lo;
                         vb &= t0 + tb < p.sinks || t0 + tb >= sp.lo;
+                    }
+                    if (kMode == kTail) {
+                        va &= t0 + ta >= sp.lo;
+                        vb &= t0 + tb >= sp.lo;
                     }
 
                     // ---- segment 2a: int32 block dots, lane = token ----
@@ -715,7 +726,7 @@ decode_split_kernel(DecodeParams p) {
                         for (int i = 0; i < 8; ++i) bl[i] = 0u;
                     }
                     // the stage's offset correction, one tile shared by all dims
-                    // (the windowed and scored splits take the offset off the
+                    // (the windowed, scored and tail splits take the offset off the
                     // codes themselves instead, and add each stage's product to
                     // the accumulator in fp32: the tensor cores cut off what an
                     // accumulator cannot hold, which next to the offset's share

@@ -131,7 +131,8 @@ struct DecodeParams {
     // merge: 1 when it follows its own split in the stream (it releases the next
     // kernel before its wait), 0 when other kernels may lie between
     int release_early;
-    // sliding window with first tokens (windowed split only)
+    // sliding window with first tokens (windowed split only); the tail split of a
+    // shared decode: each row's first token behind the shared ones
     const int32_t *windows;       // [batch]
     int sinks;
     // accumulated attention weights (scored split and its merge only)
@@ -177,6 +178,67 @@ struct NormRopeParams {
 };
 cudaError_t launch_norm_rope_append(const NormRopeParams &p, cudaStream_t s);
 cudaError_t launch_rope_table(const double *inv_freq, int64_t n_pos, float *table, cudaStream_t s);
+
+// ------------------------------- query rows over a cached stretch (tiles) --
+// A tile is up to kTileRows query rows (token, query head) that share a kv head
+// and a stretch of cached tokens: of a prompt (rows of consecutive tokens, each
+// over the tokens up to its own position), or of the batch rows that share a
+// prefix.  Row n of a tile is token n / G, head n % G of the kv head.
+constexpr int kTileRows = 128;
+constexpr int kMaxTileCtas = 160;     // upper bound of the tile kernels' grid
+struct TileParams {
+    const void *q;                // rows of q_dtype; q_stride elements from one token to the next
+    int q_dtype;
+    int64_t q_stride;
+    int batch, n_new, nqh, nkv;   // n_new: query tokens per sequence (prompt)
+    const int8_t *k_pool, *v_pool;
+    const float *k_scale, *v_scale;
+    int num_blocks;
+    const int32_t *block_table;
+    int max_blocks;
+    float sm_scale_log2;
+    uint32_t *dev_status;
+    // prompt
+    const int32_t *start_pos, *n_tokens;
+    void *out;                    // rows of out_dtype, out_stride apart
+    int out_dtype;
+    int64_t out_stride;
+    // shared prefix
+    const int32_t *ctx_lens, *group_starts, *shared_lens;
+    int n_groups;
+    int step;                     // 1: the token at ctx_lens[b] - 1 is the row's own
+    int32_t *ws_tail;             // [batch]: the row's first token behind the shared ones
+    // partial results.  Prompt: CTA c's rows at c * 2 * kTileRows (a tile that it
+    // goes on with) and kTileRows later (a tile that it begins and another ends),
+    // ws_dir[c] says of which tile the latter is.  Shared prefix: row x of the
+    // batch * nqh rows, ordered by (group, kv head, row), by CTA c at
+    // x + c * kTileRows; ws_dir[x of a tile's first row] = (first CTA, their count).
+    int4 *ws_dir;
+    float *ws_ml;                 // [..][2]: running max M (base 2), sum S
+    float *ws_acc;                // [..][128]
+};
+cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s);
+cudaError_t launch_shared_prefix(const TileParams &p, int group, cudaStream_t s);
+// The split over every row's own tokens (d.windows = ws_tail), and the merge of
+// both parts into d.out.
+cudaError_t launch_decode_tail_split(const DecodeParams &d, int group, cudaStream_t s);
+cudaError_t launch_shared_merge(const DecodeParams &d, const TileParams &p, int group, cudaStream_t s);
+
+// ------------------------------------------------------------ reading back --
+struct ReadParams {
+    int batch, n_new, nkv;
+    const int8_t *k_pool, *v_pool;
+    const float *k_scale, *v_scale;
+    int num_blocks;
+    const int32_t *block_table;
+    int max_blocks;
+    const int32_t *start_pos, *n_tokens;
+    void *k_out, *v_out;          // rows of dtype, or null
+    int dtype;
+    int64_t k_stride, v_stride;
+    uint32_t *dev_status;
+};
+cudaError_t launch_read(const ReadParams &p, cudaStream_t s);
 
 // --------------------------------------------------------------- eviction --
 struct EvictParams {

@@ -22,6 +22,7 @@ NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024   # KVQ8_NOALLOC_SCRATCH_BYTES in kvq8.
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA = range(5)
 STEP_CACHE_READY = 0x1   # KVQ8_STEP_CACHE_READY
 DEV_BAD_BLOCK_ID, DEV_BAD_CTX_LEN, DEV_BAD_POSITION, DEV_TIMEOUT, DEV_NONFINITE = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_GROUPS = 0x20
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -90,6 +91,15 @@ SIGNATURES = {
     "kvq8_rope_table": (_I, [_P, _I, _I, _P, _P]),
     "kvq8_norm_rope_append": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P,
                                    _P, ctypes.c_uint32, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "kvq8_prompt_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "kvq8_prompt_attn": (_I, [_P, _I, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _F, _P, _I,
+                              _I64, _P, _SZ, _P, _P]),
+    "kvq8_shared_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "kvq8_decode_attn_shared": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _F, _P, _P,
+                                     _SZ, _P, _P]),
+    "kvq8_decode_step_shared": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _F,
+                                     _P, _P, _SZ, _P, _P]),
+    "kvq8_read": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _I64, _I64, _P, _P]),
 }
 
 _lib = None
@@ -715,6 +725,145 @@ def norm_rope_append(q, k, v, q_weight, k_weight, eps: float, rope_table, start_
         _ptr(n_tokens), ROPE_PAIRS if interleaved else 0, start_pos.data_ptr(), block_table.data_ptr(), max_blocks,
         BLOCK_SIZE, nb, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
         _ptr(weight_sum), q_out.data_ptr(), _ptr(dev_status), _stream_on(stream, dev)))
+
+
+# --------------------------------------- prompts, shared prefixes, reading back ---
+def _dtype_code(what: str, t) -> int:
+    torch = _torch()
+    kind = t.dtype
+    if kind is torch.float32:
+        return DTYPE_F32
+    if kind is torch.bfloat16:
+        return DTYPE_BF16
+    if kind is torch.float16:
+        return DTYPE_F16
+    raise ValueError(f"{what}: expected fp32, bf16 or fp16, got {kind}")
+
+
+def _need_rows(dev: int, *wanted):
+    """Each (name, tensor, shape): token rows of this shape on the device, as _token_stride takes them."""
+    for what, t, shape in wanted:
+        if t.shape != shape or t.get_device() != dev:
+            raise ValueError(f"{what}: expected {list(shape)} on the current device (cuda:{dev}), got {list(t.shape)} "
+                             f"on device {t.get_device()}")
+
+
+def prompt_workspace_bytes(batch: int, n_new: int, nqh: int, nkv: int, max_blocks: int) -> int:
+    return int(load().kvq8_prompt_workspace_bytes(batch, n_new, nqh, nkv, HEAD_DIM, max_blocks, BLOCK_SIZE))
+
+
+def alloc_prompt_workspace(batch: int, n_new: int, nqh: int, nkv: int, max_blocks: int, device="cuda"):
+    n = prompt_workspace_bytes(batch, n_new, nqh, nkv, max_blocks)
+    if n == 0:
+        raise ValueError("unsupported prompt sizes")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def prompt_attn(q, cache: KVCache, block_table, start_pos, out, workspace, n_tokens=None,
+                sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """Attention of query tokens q [batch][n_new][nqh][128] (fp32, bf16 or fp16;
+    possibly part of a packed projection) at the positions start_pos[b] + i, each
+    over the cached tokens up to its own position; their K and V rows are in the
+    cache already.  n_tokens int32 [batch] (None: no padding): rows i >=
+    n_tokens[b] are neither read nor written.  out: as q, of any of the three
+    types; workspace from alloc_prompt_workspace."""
+    i32 = _torch().int32
+    nb, nkv, wants = _cache_wants(cache)
+    batch, n_new, nqh, _ = q.shape
+    max_blocks = block_table.shape[1]
+    wants += [("block_table", block_table, i32, (batch, max_blocks)), ("start_pos", start_pos, i32, (batch,)),
+              ("workspace", workspace, _torch().uint8, (workspace.shape[0],))]
+    if n_tokens is not None:
+        wants.append(("n_tokens", n_tokens, i32, (batch,)))
+    if dev_status is not None:
+        wants.append(("dev_status", dev_status, i32, (1,)))
+    dev = _need(*wants)
+    shape = (batch, n_new, nqh, HEAD_DIM)
+    _need_rows(dev, ("q", q, shape), ("out", out, shape))
+    _check("kvq8_prompt_attn", load().kvq8_prompt_attn(
+        q.data_ptr(), _dtype_code("q", q), _token_stride("q", q, batch, n_new, nqh), batch, n_new, nqh, nkv, HEAD_DIM,
+        cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), nb,
+        block_table.data_ptr(), max_blocks, BLOCK_SIZE, start_pos.data_ptr(), _ptr(n_tokens),
+        SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _dtype_code("out", out),
+        _token_stride("out", out, batch, n_new, nqh), workspace.data_ptr(), workspace.shape[0], _ptr(dev_status),
+        _stream_on(stream, dev)))
+
+
+def shared_workspace_bytes(batch: int, n_groups: int, nqh: int, nkv: int, max_blocks: int) -> int:
+    return int(load().kvq8_shared_workspace_bytes(batch, n_groups, nqh, nkv, HEAD_DIM, max_blocks, BLOCK_SIZE))
+
+
+def alloc_shared_workspace(batch: int, n_groups: int, nqh: int, nkv: int, max_blocks: int, device="cuda"):
+    n = shared_workspace_bytes(batch, n_groups, nqh, nkv, max_blocks)
+    if n == 0:
+        raise ValueError("unsupported decode sizes")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def _shared(fn, q, k_new, v_new, cache, block_table, ctx_lens, group_starts, shared_lens, out, workspace, sm_scale,
+            dev_status, stream):
+    i32 = _torch().int32
+    dev, lead = _decode_lead(q, k_new, v_new, cache, block_table, ctx_lens, out, workspace, dev_status, None, None)
+    n_groups = shared_lens.shape[0]
+    _need(("group_starts", group_starts, i32, (n_groups + 1,)), ("shared_lens", shared_lens, i32, (n_groups,)))
+    st = getattr(load(), fn)(*lead, n_groups, group_starts.data_ptr(), shared_lens.data_ptr(),
+                             SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), workspace.data_ptr(),
+                             workspace.shape[0], _ptr(dev_status), _stream_on(stream, dev))
+    if st != OK:
+        raise Kvq8Error(fn, st)
+
+
+def decode_attn_shared(q, cache: KVCache, block_table, ctx_lens, group_starts, shared_lens, out, workspace,
+                       sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_attn for rows that share their first tokens in groups: rows
+    group_starts[g] .. group_starts[g + 1] - 1 (int32 [n_groups + 1], from 0 to
+    batch) hold the same tokens at the positions below shared_lens[g] (int32
+    [n_groups]), which are read once for the group; workspace from
+    alloc_shared_workspace."""
+    _shared("kvq8_decode_attn_shared", q, None, None, cache, block_table, ctx_lens, group_starts, shared_lens, out,
+            workspace, sm_scale, dev_status, stream)
+
+
+def decode_step_shared(q, k_new, v_new, cache: KVCache, block_table, ctx_lens, group_starts, shared_lens, out,
+                       workspace, sm_scale: Optional[float] = None, dev_status=None, stream=None):
+    """decode_step (append k_new/v_new at ctx_lens-1, then attend) over shared
+    prefixes as decode_attn_shared takes them."""
+    _shared("kvq8_decode_step_shared", q, k_new, v_new, cache, block_table, ctx_lens, group_starts, shared_lens, out,
+            workspace, sm_scale, dev_status, stream)
+
+
+def read_cache(cache: KVCache, block_table, start_pos, k_out, v_out, n_tokens=None, dev_status=None, stream=None):
+    """The K and V rows of the positions start_pos[b] + i as the values their
+    codes stand for, into k_out, v_out [batch][n][nkv][128] (of one type: fp32,
+    bf16 or fp16; either may be None).  n_tokens int32 [batch] (None: all n):
+    rows i >= n_tokens[b] are left as they are."""
+    i32 = _torch().int32
+    nb, nkv, wants = _cache_wants(cache)
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("read_cache: neither k_out nor v_out")
+    batch, n_new = some.shape[:2]
+    max_blocks = block_table.shape[1]
+    wants += [("block_table", block_table, i32, (batch, max_blocks)), ("start_pos", start_pos, i32, (batch,))]
+    if n_tokens is not None:
+        wants.append(("n_tokens", n_tokens, i32, (batch,)))
+    if dev_status is not None:
+        wants.append(("dev_status", dev_status, i32, (1,)))
+    dev = _need(*wants)
+    strides = []
+    for what, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            strides.append(nkv * HEAD_DIM)
+            continue
+        _need_rows(dev, (what, t, (batch, n_new, nkv, HEAD_DIM)))
+        if t.dtype is not some.dtype:
+            raise ValueError(f"{what}: expected {some.dtype}, got {t.dtype}")
+        strides.append(_token_stride(what, t, batch, n_new, nkv))
+    _check("kvq8_read", load().kvq8_read(
+        batch, n_new, nkv, HEAD_DIM, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+        cache[3].data_ptr(), nb, block_table.data_ptr(), max_blocks, BLOCK_SIZE, start_pos.data_ptr(),
+        _ptr(n_tokens), _ptr(k_out), _ptr(v_out), _dtype_code("k_out", some), *strides, _ptr(dev_status),
+        _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------ 4-bit cache ---
