@@ -208,6 +208,8 @@ struct TileParams {
     int n_groups;
     int step;                     // 1: the token at ctx_lens[b] - 1 is the row's own
     int32_t *ws_tail;             // [batch]: the row's first token behind the shared ones
+    int4 *ws_group;               // [n_groups]: (first row, rows, row read through, shared tokens)
+    int tile_rows;                // rows of a tile (set with the launch)
     // partial results.  Prompt: CTA c's rows at c * 2 * kTileRows (a tile that it
     // goes on with) and kTileRows later (a tile that it begins and another ends),
     // ws_dir[c] says of which tile the latter is.  Shared prefix: row x of the
@@ -218,7 +220,7 @@ struct TileParams {
     float *ws_acc;                // [..][128]
 };
 cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s);
-cudaError_t launch_shared_prefix(const TileParams &p, int group, cudaStream_t s);
+cudaError_t launch_shared_prefix(TileParams &p, int group, cudaStream_t s);
 // The split over every row's own tokens (d.windows = ws_tail), and the merge of
 // both parts into d.out.
 cudaError_t launch_decode_tail_split(const DecodeParams &d, int group, cudaStream_t s);
