@@ -194,34 +194,56 @@ __device__ __forceinline__ uint32_t mma_word(int n, bool n_major) {
     return 1u << 4 | (n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
-// D (tensor memory, 128 x n) (+)= A (tensor memory, 128 x 16) B (shared memory, n x 16).
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool accumulate) {
+// D (tensor memory, 128 x n) (+)= A (tensor memory, 128 x 128 halves: eight steps of 8 columns) B (shared memory, n x
+// 128: steps 256 bytes apart), issued by the lane that has `lead` set; the whole warp comes here, so that the
+// operands' arithmetic stays in uniform registers (one lane alone takes twice as long per step).
+__device__ __forceinline__ void mma_k128(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool accumulate, bool lead) {
+#define KVQ8_MMA_STEP "add.u32 ta, ta, 8;\n\tadd.s64 tb, tb, 16;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, r;\n\t"
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, q, r;\n\t.reg .b32 ta;\n\t.reg .b64 tb;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.eq.u32 r, %0, %0;\n\t"
+        "mov.b32 ta, %1;\n\tmov.b64 tb, %2;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, q;\n\t"
+        KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP "}" ::"r"(d),
+        "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate), "r"((uint32_t)lead)
+        : "memory");
+#undef KVQ8_MMA_STEP
+}
+
+// One arrival on the mbarrier when the leading lane's MMAs so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"((uint32_t)lead)
         : "memory");
 }
 
-// One arrival on the mbarrier when this thread's MMAs so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Columns of this warp's lanes.  (A load's registers hold their values after tmem_wait_ld; the caller orders what
+// uses them behind it.)
+#define KVQ8_R8(r) "=f"((r)[0]), "=f"((r)[1]), "=f"((r)[2]), "=f"((r)[3]), "=f"((r)[4]), "=f"((r)[5]), "=f"((r)[6]), "=f"((r)[7])
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : KVQ8_R8(r) : "r"(addr));
 }
-
-// Eight columns of this warp's lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&r)[8]) {
-    uint32_t v[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(addr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(v[i]);
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : KVQ8_R8(r), KVQ8_R8(r + 8)
+        : "r"(addr));
 }
+#undef KVQ8_R8
 
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // Shared-memory writes of this thread become visible to the async proxy (MMA operands).

@@ -42,42 +42,53 @@ namespace kvq8 {
 namespace {
 
 constexpr int kTok = 128;                       // tokens per stage
-constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 16, kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kThreads = 256 + kSoftmaxThreads;
 constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
 constexpr int kCoreRow = 2048;                  // bytes between cores along the rows (16 cores of 128 B along k)
-constexpr uint64_t kLimitNs = 2000000000ull;
+constexpr uint64_t kLimitNs = 2000000000ull;      // bounds of the waits: two seconds
+constexpr long long kLimitTicks = 4000000000ll;
 // A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^8 and 2^9 when M is set; M moves
 // when P would pass 2^15.9 (fp16 ends below 2^16).
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
 constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this when M is set (rows of zeros do)
-// registers per thread of the four warpgroups: copies and MMAs, operands, softmax (2); their sum is what the
-// launch holds (4 * 128)
-constexpr int kRegsIssue = 64, kRegsOperand = 96, kRegsSoftmax = 176;
-static_assert(kRegsIssue + kRegsOperand + 2 * kRegsSoftmax == 4 * 128, "the launch's registers");
-// columns of tensor memory
+// Registers per thread: what the launch holds, and what the warpgroups (copies, MMAs and queries; operands; four of
+// softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory leaves it no L1.
+constexpr int kLaunchRegs = 80, kRegsIssue = 64, kRegsOperand = 64, kRegsSoftmax = 88;
+static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs, "registers");
+constexpr int kQBatch = 2;                      // query rows that a warp prepares at a time
+// columns of tensor memory, all of which is the CTA's (so that it begins at address 0)
 constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = 384;
 
-// Rows per tile and shared memory: Q (high, low), P (high, low), the ring.
-template <bool kWide, bool kLow>
+// Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
+template <int kRows, bool kLow>
 struct Lay {
-    static constexpr int kRows = kWide ? 128 : 64;
+    static constexpr bool kWide = kRows > 64;   // the parts are two products; else columns of one
     static constexpr int kQ = kRows * 2 * kHD * 2;
     static constexpr int kP = kRows * (kLow ? 2 : 1) * kTok * 2;
     static constexpr int oQ = 0;
     static constexpr int oP = kQ;
     static constexpr int oMisc = oP + kP;
-    static constexpr int kMisc = 12288;
+    static constexpr int kMisc = 13312;
     static constexpr int oRing = oMisc + kMisc;
     static constexpr int kSlots = (232448 - oRing) / kSlotBytes < 8 ? (232448 - oRing) / kSlotBytes : 8;
     static constexpr int kBytes = oRing + kSlots * kSlotBytes;
     static_assert(kSlots >= 4, "ring too shallow");
 };
 
+// One tile's stages of one CTA.
+struct Part {
+    int stages, off, end, rows;                 // (stages 0: no more)
+    int lead, head, token, direct;              // block-table row, kv head, first token, whether out is written
+    long long rec;                              // first record row
+};
+
 struct Misc {
     uint64_t full[8], empty[8];                 // ring slots
     uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2], sc_ready[4];
-    // (two, since the operand warps may be two tiles ahead of the softmax's)
+    uint64_t part_ready[4];
+    // (two, since the queries may be two tiles ahead of the softmax)
     uint64_t q_ready[2];
     uint64_t s_full, s_free, p_ready, pv_done, q_free, o_free, all_done;
     long long warp_tot[kThreads / 32];
@@ -87,35 +98,43 @@ struct Misc {
     uint32_t tmem;
     int skip[8];                                // slot: its block id is outside the pool
     int bad[4];                                 // stage (mod 4): the same
-    int lim_min[2];
+    int lim_min[4][2];                          // tile (mod 4)
+    // what concerns a tile is kept four deep: the queries of tile x + 3 are prepared when QK of x + 2 is done, so
+    // when the softmax has left tile x
+    alignas(16) Part part[4];
+    alignas(16) int lim[4][kTileRows];          // tile (mod 4), row: tokens below
+    alignas(16) float gain[4][kTileRows];       // tile (mod 4), row: power of two of the query's operand
     alignas(16) float2 scale[4][kTok];          // stage (mod 4): (K scale * sm_scale, V scale)
-    alignas(16) float2 col[2 * kTileRows];      // per row: (score factor, -M)
-    alignas(16) int lim[kTileRows];             // per row: tokens below
-    alignas(16) float alpha[kTileRows];
+    alignas(16) float ref[kTileRows];           // per row: -M
+    alignas(16) float shift[kTileRows];         // per row: M before - M now, or the output's factor
     alignas(16) float wave[4][kTileRows];       // per warp and row: maxima, sums
-    float factor[2][kTileRows];                 // per tile (mod 2) and row: power of two of the query's operand
+    long long dst[kTileRows];                   // per row: where its output or record starts
 };
-static_assert(sizeof(Misc) <= 12288, "misc");
+static_assert(sizeof(Misc) <= 13312, "misc");
 
+// Bounded like every wait here, by clock ticks.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *ms, uint32_t *status) {
     const uint32_t a = smem_addr(bar);
     if (mbar_try_wait(a, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(a, parity)) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(a, parity)) return true;
         if (ms->abort) return false;
-        if (global_timer_ns() - t0 > kLimitNs) {
+        if (clock64() - t0 > kLimitTicks) {
             ms->abort = 1;
             flag_status(status, KVQ8_DEV_TIMEOUT);
             return false;
         }
     }
-    return true;
 }
 
 // The same by all lanes of a warp, together again behind it.
-__device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, Misc *ms, uint32_t *status) {
-    wait_bar(bar, parity, ms, status);
-    __syncwarp();
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Misc *ms, uint32_t *status) {
+    const bool ok = wait_bar(bar, parity, ms, status);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // The tiles in their order: (sequence or group, kv head, rows).
@@ -193,36 +212,51 @@ __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t &lo, uint32_
 
 // 32 bytes of codes (two 16-byte chunks) into 16 columns of this lane.
 __device__ __forceinline__ void put_codes(uint32_t tmem, uint4 x, uint4 y) {
-    uint32_t v[8];
+    uint32_t v[16];
     codes_to_half2(x.x, v[0], v[1]);
     codes_to_half2(x.y, v[2], v[3]);
     codes_to_half2(x.z, v[4], v[5]);
     codes_to_half2(x.w, v[6], v[7]);
-    tmem_st8(tmem, v);
-    codes_to_half2(y.x, v[0], v[1]);
-    codes_to_half2(y.y, v[2], v[3]);
-    codes_to_half2(y.z, v[4], v[5]);
-    codes_to_half2(y.w, v[6], v[7]);
-    tmem_st8(tmem + 8, v);
+    codes_to_half2(y.x, v[8], v[9]);
+    codes_to_half2(y.y, v[10], v[11]);
+    codes_to_half2(y.z, v[12], v[13]);
+    codes_to_half2(y.w, v[14], v[15]);
+    tmem_st16(tmem, v);
 }
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
 
-// Floats as integers of the same order, so that one redux gives a maximum.
-__device__ __forceinline__ float warp_top(float x) {
-    int k = __float_as_int(x);
-    k ^= (k >> 31) & 0x7fffffff;
-    k = __reduce_max_sync(0xffffffffu, k);
-    k ^= (k >> 31) & 0x7fffffff;
-    return __int_as_float(k);
+// Floats as integers of the same order (and back), so that one redux gives a maximum.
+__device__ __forceinline__ int ordered(int k) { return k ^ ((k >> 31) & 0x7fffffff); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
-template <bool kShared, bool kWide, bool kLow>
+template <bool kShared, int kRows, bool kLow>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_kernel(TileParams p, int lg) {
-    using L = Lay<kWide, kLow>;
+    using L = Lay<kRows, kLow>;
+    constexpr bool kWide = L::kWide;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *ms = reinterpret_cast<Misc *>(smem + L::oMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -233,32 +267,34 @@ tile_kernel(TileParams p, int lg) {
             mbar_init(smem_addr(&ms->empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&ms->q_ready[i]), 4);
+            mbar_init(smem_addr(&ms->q_ready[i]), 2);
             mbar_init(smem_addr(&ms->k_ready[i]), 4);
             mbar_init(smem_addr(&ms->k_free[i]), 1);
             mbar_init(smem_addr(&ms->v_ready[i]), 4);
             mbar_init(smem_addr(&ms->v_free[i]), 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&ms->sc_ready[i]), 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&ms->sc_ready[i]), 4);
+            mbar_init(smem_addr(&ms->part_ready[i]), 1);
+        }
         mbar_init(smem_addr(&ms->s_full), 1);
-        mbar_init(smem_addr(&ms->s_free), 8);
-        mbar_init(smem_addr(&ms->p_ready), 8);
+        mbar_init(smem_addr(&ms->s_free), kSoftmaxWarps);
+        mbar_init(smem_addr(&ms->p_ready), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->pv_done), 1);
         mbar_init(smem_addr(&ms->q_free), 1);
-        mbar_init(smem_addr(&ms->o_free), 8);
+        mbar_init(smem_addr(&ms->o_free), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->all_done), 1);
         fence_mbar_init();
         ms->abort = 0;
         ms->s0 = 0;
         ms->r0 = 0;
-        ms->lim_min[0] = ms->lim_min[1] = 0x7fffffff;
     }
     if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), 512);
     pdl_wait();
     pdl_launch_dependents();   // (the next kernel's CTAs find no registers here before this one leaves)
     // ---- this CTA's share: stages [lo, hi) of the sequence of all tiles' stages ----
-    Walk<kShared> w(p, lg, L::kRows);
-    const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + L::kRows - 1) / L::kRows);
+    Walk<kShared> w(p, lg, kRows);
+    const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + kRows - 1) / kRows);
     const int seqs = kShared ? p.n_groups : p.batch;
     const long long items = (long long)seqs * per_seq;   // (sequence, tile of one kv head), or group
     const long long per = (items + kThreads - 1) / kThreads;
@@ -272,6 +308,7 @@ tile_kernel(TileParams p, int lg) {
     };
     long long mine = 0;
     int s, r;
+#pragma unroll 1
     for (long long i = i_lo; i < i_hi; ++i) mine += item(i, s, r);
     long long incl = mine;
 #pragma unroll
@@ -284,6 +321,7 @@ tile_kernel(TileParams p, int lg) {
     __syncthreads();
     tc_fence_after();
     long long excl = incl - mine, total = 0;
+#pragma unroll 1
     for (int k = 0; k < kThreads / 32; ++k) {
         if (k < warp) excl += ms->warp_tot[k];
         total += ms->warp_tot[k];
@@ -298,10 +336,10 @@ tile_kernel(TileParams p, int lg) {
         hi = (long long)(c + 1) * Tq + ((long long)(c + 1) * Tr) / C;
     }
     if (!kShared && tid == 0) p.ws_dir[c] = make_int4(0, 0, 0, 0);
-    const uint32_t tmem = ms->tmem;
     int off = 0;
     if (hi > lo) {   // (uniform over the CTA)
         long long acc = excl;
+#pragma unroll 1
         for (long long i = i_lo; i < i_hi; ++i) {
             const long long v = item(i, s, r);
             if (r == 0 && acc * p.nkv <= lo) atomicMax(&ms->s0, s);
@@ -311,6 +349,7 @@ tile_kernel(TileParams p, int lg) {
         __syncthreads();
         const int s0 = ms->s0;
         acc = excl;
+#pragma unroll 1
         for (long long i = i_lo; i < i_hi; ++i) {
             const long long v = item(i, s, r);
             if (r == 0 && s == s0) ms->base = acc;
@@ -328,6 +367,7 @@ tile_kernel(TileParams p, int lg) {
             off = (int)(rem % w.stages(0));
         } else {
             acc = excl;
+#pragma unroll 1
             for (long long i = i_lo; i < i_hi; ++i) {
                 const long long v = item(i, s, r);
                 if (s == s0 && v > 0 && acc - base <= rem) atomicMax(&ms->r0, r);
@@ -336,6 +376,7 @@ tile_kernel(TileParams p, int lg) {
             __syncthreads();
             w.r = ms->r0;
             acc = excl;
+#pragma unroll 1
             for (long long i = i_lo; i < i_hi; ++i) {
                 const long long v = item(i, s, r);
                 if (s == s0 && r == w.r) ms->end = rem - (acc - base);
@@ -347,12 +388,6 @@ tile_kernel(TileParams p, int lg) {
         }
         w.h = h0;
     }
-    long long left = hi - lo;
-    // `part` stages of tile (w.s, w.h, w.r) from stage `off` on are this CTA's
-#define KVQ8_FOR_TILES                                                                                    \
-    for (int part = 0, seg = 0; left > 0 && !(seg > 0 && w.s >= seqs);                                   \
-         left -= part, off = 0, ++seg, w.next(seqs))                                                       \
-        if (part = (int)min(left, (long long)(w.stages(w.r) - off)), true)
 
     if (warp < 4) {
         regs_shrink<kRegsIssue>();
@@ -360,12 +395,17 @@ tile_kernel(TileParams p, int lg) {
             // ============================ copies ============================
             int g = 0;   // granules so far: K and V of every stage
             bool stop = false;
-            KVQ8_FOR_TILES {
-                const int end = w.end(w.r);
-                const int32_t *row = p.block_table + (size_t)w.lead * p.max_blocks;
+#pragma unroll 1
+            for (int seg = 0; !stop; ++seg) {
+                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+                const Part &part = ms->part[seg & 3];
+                const int n = part.stages, first = part.off, end = part.end, h = part.head;
+                if (n == 0) break;
+                const int32_t *row = p.block_table + (size_t)part.lead * p.max_blocks;
                 int tbl_base = -1, tbl = -1;
-                for (int j = 0; j < part && !stop; ++j, g += 2) {
-                    const int t0 = (off + j) * kTok, lb = t0 / kBS;
+#pragma unroll 1
+                for (int j = 0; j < n && !stop; ++j, g += 2) {
+                    const int t0 = (first + j) * kTok, lb = t0 / kBS;
                     if (tbl_base < 0 || lb >= tbl_base + 32) {
                         tbl_base = lb;
                         tbl = lb + lane < p.max_blocks ? row[lb + lane] : -1;
@@ -374,9 +414,10 @@ tile_kernel(TileParams p, int lg) {
                     if (lane == 0) {
                         const bool any = t0 < end, ok = any && phys >= 0 && phys < p.num_blocks;
                         if (any && !ok) flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
-                        const size_t tile = ok ? (size_t)phys * p.nkv + w.h : 0;
+                        const size_t tile = ok ? (size_t)phys * p.nkv + h : 0;
                         const int slot0 = t0 % kBS;
-                        for (int v = 0; v < 2 && !stop; ++v) {
+#pragma unroll 1
+                        for (int v = 0; v < 2; ++v) {
                             const int at = (g + v) % L::kSlots;
                             if (!wait_bar(&ms->empty[at], (((g + v) / L::kSlots) & 1) ^ 1, ms, p.dev_status)) {
                                 stop = true;
@@ -400,7 +441,6 @@ tile_kernel(TileParams p, int lg) {
                     }
                     stop = __shfl_sync(0xffffffffu, (int)stop, 0) != 0;
                 }
-                if (stop) break;
             }
             // no copy may still be in flight when the CTA exits (a stopped ring: whichever the slots were given last)
             if (lane == 0) {
@@ -410,122 +450,172 @@ tile_kernel(TileParams p, int lg) {
             __syncwarp();
         } else if (warp == 1) {
             // ============================= MMAs =============================
-            if (lane == 0) {
-                const uint32_t q0 = smem_addr(smem + L::oQ), p0 = smem_addr(smem + L::oP);
-                int j = 0;   // stages so far
-                KVQ8_FOR_TILES {
-                    const int n = (w.tile_rows(w.r) + 15) & ~15;
-                    const uint32_t word_q = mma_word(kWide ? n : 2 * n, false);
-                    const uint32_t word_p = mma_word(kWide || !kLow ? n : 2 * n, true);
-                    wait_bar(&ms->q_ready[seg & 1], (seg >> 1) & 1, ms, p.dev_status);
-                    for (int i = 0; i <= part; ++i) {
-                        if (i < part) {
-                            const int x = j + i;
-                            wait_bar(&ms->k_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
-                            wait_bar(&ms->s_free, (x & 1) ^ 1, ms, p.dev_status);
-                            tc_fence_after();
-                            const uint32_t a = tmem + kColK + (x & 1) * 64;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_tmem_a(tmem + kColS, a + 8 * k, core_desc(q0 + k * 256, 128, kCoreRow), word_q, k > 0);
-                            if (kWide) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_tmem_a(tmem + kColS, a + 8 * k,
-                                               core_desc(q0 + L::kRows / 8 * kCoreRow + k * 256, 128, kCoreRow), word_q, true);
-                            }
-                            mma_commit(smem_addr(&ms->k_free[x & 1]));
-                            mma_commit(smem_addr(&ms->s_full));
-                            if (i == part - 1) mma_commit(smem_addr(&ms->q_free));
-                        }
-                        if (i > 0) {
-                            const int x = j + i - 1;
-                            wait_bar(&ms->v_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
-                            if (i == 1) wait_bar(&ms->o_free, (seg & 1) ^ 1, ms, p.dev_status);
-                            wait_bar(&ms->p_ready, x & 1, ms, p.dev_status);
-                            tc_fence_after();
-                            const uint32_t a = tmem + kColV + (x & 1) * 64;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_tmem_a(tmem + kColO, a + 8 * k, core_desc(p0 + k * 256, 128, kCoreRow), word_p, i > 1 || k > 0);
-                            if (kWide && kLow) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_tmem_a(tmem + kColO, a + 8 * k,
-                                               core_desc(p0 + L::kRows / 8 * kCoreRow + k * 256, 128, kCoreRow), word_p, true);
-                            }
-                            mma_commit(smem_addr(&ms->v_free[x & 1]));
-                            mma_commit(smem_addr(&ms->pv_done));
+            const bool lead = lane == 0;
+            const uint64_t q_hi = core_desc(smem_addr(smem + L::oQ), 128, kCoreRow);
+            const uint64_t p_hi = core_desc(smem_addr(smem + L::oP), 128, kCoreRow);
+            constexpr uint64_t kLowPart = kRows / 8 * kCoreRow / 16;
+            const uint32_t word_q = mma_word(kWide ? kRows : 2 * kRows, false);
+            const uint32_t word_p = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
+            int x = 0;   // stages so far
+#pragma unroll 1
+            for (int seg = 0;; ++seg) {
+                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+                const int n = ms->part[seg & 3].stages;
+                if (n == 0) break;
+                wait_warp(&ms->q_ready[seg & 1], (seg >> 1) & 1, ms, p.dev_status);
+#pragma unroll 1
+                for (int i = 0; i <= n; ++i, ++x) {
+                    if (i < n) {
+                        wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
+                        wait_warp(&ms->s_free, (x & 1) ^ 1, ms, p.dev_status);
+                        tc_fence_after();
+                        mma_k128(kColS, kColK + (x & 1) * 64, q_hi, word_q, false, lead);
+                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, q_hi + kLowPart, word_q, true, lead);
+                        mma_commit(smem_addr(&ms->s_full), lead);
+                        mma_commit(smem_addr(&ms->k_free[x & 1]), lead);
+                        if (i == n - 1) mma_commit(smem_addr(&ms->q_free), lead);
+                    }
+                    if (i > 0) {
+                        const int y = x - 1;
+                        wait_warp(&ms->v_ready[y & 1], (y >> 1) & 1, ms, p.dev_status);
+                        if (i == 1) wait_warp(&ms->o_free, (seg & 1) ^ 1, ms, p.dev_status);
+                        wait_warp(&ms->p_ready, y & 1, ms, p.dev_status);
+                        tc_fence_after();
+                        mma_k128(kColO, kColV + (y & 1) * 64, p_hi, word_p, i > 1, lead);
+                        if (kWide && kLow) mma_k128(kColO, kColV + (y & 1) * 64, p_hi + kLowPart, word_p, true, lead);
+                        mma_commit(smem_addr(&ms->pv_done), lead);
+                        mma_commit(smem_addr(&ms->v_free[y & 1]), lead);
+                    }
+                }
+                --x;   // (n + 1 rounds)
+            }
+            mma_commit(smem_addr(&ms->all_done), lead);
+            mbar_wait_bounded(smem_addr(&ms->all_done), 0, kLimitNs);
+            __syncwarp();
+        } else {
+            // ================== the tiles' order and their queries ==================
+            long long left = hi - lo;
+            unsigned char *at = smem + L::oQ + (lane >> 1) * 128 + (lane & 1) * 8;
+            auto put = [&](int k, __half2 a, __half2 b) {
+                *reinterpret_cast<uint2 *>(at + (k >> 3) * kCoreRow + (k & 7) * 16) = make_uint2(half2_bits(a), half2_bits(b));
+            };
+#pragma unroll 1
+            for (int seg = 0;; ++seg) {
+                Part &part = ms->part[seg & 3];
+                const int stages = left > 0 ? w.stages(w.r) : 0;
+                const int n = (int)min(left, (long long)(stages - off));
+                const int rows = left > 0 ? w.tile_rows(w.r) : 0;
+                if (warp == 2 && lane == 0) {
+                    part.stages = n;
+                    if (n > 0) {
+                        const bool whole = n == stages;
+                        const long long x = (long long)w.first * p.nqh + (long long)w.h * w.rows + (long long)w.r * kRows;
+                        part.off = off;
+                        part.end = w.end(w.r);
+                        part.rows = rows;
+                        part.lead = w.lead;
+                        part.head = w.h;
+                        part.token = (int)w.token(w.r, 0);
+                        part.direct = !kShared && whole;
+                        part.rec = kShared ? x + (long long)c * kTileRows : ((long long)c * 2 + (off == 0 ? 1 : 0)) * kTileRows;
+                        if (off == 0) {   // the CTAs c .. that hold this tile's records
+                            const int cnt = (int)(((hi - left + stages) * C + T - 1) / T) - c;
+                            if (kShared) p.ws_dir[x] = make_int4(c, whole ? 1 : cnt, 0, 0);
+                            else if (!whole) p.ws_dir[c] = make_int4(cnt, w.s, w.h, w.r);
                         }
                     }
-                    j += part;
+                    mbar_arrive(smem_addr(&ms->part_ready[seg & 3]));
                 }
-                mma_commit(smem_addr(&ms->all_done));
-                mbar_wait_bounded(smem_addr(&ms->all_done), 0, kLimitNs);
+                if (n == 0) break;
+                // the tile's queries: high and low parts of code * scale, in units of a power of two per row
+                if (!wait_warp(&ms->q_free, (seg & 1) ^ 1, ms, p.dev_status)) break;
+                int least = 0x7fffffff;
+                for (int i = (warp - 2) * 32 + lane; i < kRows; i += 64) {
+                    int lim = 0x7fffffff;
+                    if (i < rows) {
+                        bool bad;
+                        lim = w.limit(w.r, i, bad);
+                        if (bad) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+                    }
+                    ms->lim[seg & 3][i] = lim;
+                    least = min(least, lim);
+                }
+                least = __reduce_min_sync(0xffffffffu, least);
+                if (lane == 0) ms->lim_min[seg & 3][warp - 2] = least;
+#pragma unroll 1
+                for (int i0 = warp - 2; i0 < kRows; i0 += 2 * kQBatch) {
+                    // lane l: dims 4l .. 4l + 3, a 32-block is eight lanes; the rule of quantize_q_vals_warp
+                    float4 xs[kQBatch];
+#pragma unroll
+                    for (int k = 0; k < kQBatch; ++k) {
+                        const int i = i0 + 2 * k;
+                        xs[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i < rows) xs[k] = load4(p.q, p.q_dtype, w.token(w.r, i) * p.q_stride + (int64_t)w.head(i) * kHD + 4 * lane);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kQBatch; ++k) {
+                        const int i = i0 + 2 * k;
+                        float4 x = xs[k];
+                        uint32_t m = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
+                                         max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
+#pragma unroll
+                        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        if (m >= 0x7f800000u) {
+                            x = make_float4(0.f, 0.f, 0.f, 0.f);
+                            m = 0;
+                            flag_status(p.dev_status, KVQ8_DEV_NONFINITE);
+                        }
+                        float qm = __uint_as_float(m);
+                        if (qm < 1e-6f) qm = 1.0f;
+                        const float iq = __fdiv_rn(127.0f, qm), qs = __fmul_rn(qm, KVQ8_INV127);
+                        auto value = [&](float v) { return __fmul_rn((float)max(-128, min(127, __float2int_rn(__fmul_rn(v, iq)))), qs); };
+                        x = make_float4(value(x.x), value(x.y), value(x.z), value(x.w));
+                        // exponent of the row's largest value: the row is scaled to below 2^11
+                        int e = max(max(__float_as_int(x.x) & 0x7fffffff, __float_as_int(x.y) & 0x7fffffff),
+                                    max(__float_as_int(x.z) & 0x7fffffff, __float_as_int(x.w) & 0x7fffffff));
+                        e = max(-100, (__reduce_max_sync(0xffffffffu, e) >> 23) - 127 - 10);
+                        const float down = exp2_int(-e);
+                        x = make_float4(x.x * down, x.y * down, x.z * down, x.w * down);
+                        const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
+                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                        put(i, h0, h1);
+                        put(i + kRows, __floats2half2_rn(x.x - f0.x, x.y - f0.y), __floats2half2_rn(x.z - f1.x, x.w - f1.y));
+                        if (lane == 0) ms->gain[seg & 3][i] = exp2_int(e);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ms->q_ready[seg & 1]));
+                left -= n;
+                off = 0;
+                if (left > 0) w.next(seqs);
             }
-            __syncwarp();
         }
     } else if (warp < 8) {
         regs_shrink<kRegsOperand>();
         // ========================= operands =========================
         const int quad = warp & 3, row = 32 * quad + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         int j = 0;
-        KVQ8_FOR_TILES {
-            // the tile's queries: high and low parts of code * scale, in units of a power of two per row
-            const int rows = w.tile_rows(w.r), n = (rows + 15) & ~15;
-            wait_warp(&ms->q_free, (seg & 1) ^ 1, ms, p.dev_status);
-            for (int i = quad; i < n; i += 4) {
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < rows) x = load4(p.q, p.q_dtype, w.token(w.r, i) * p.q_stride + (int64_t)w.head(i) * kHD + 4 * lane);
-                // lane l: dims 4l .. 4l + 3, a 32-block is eight lanes; the rule of quantize_q_vals_warp
-                uint32_t m = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
-                                 max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (m >= 0x7f800000u) {
-                    x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    m = 0;
-                    if ((lane & 7) == 0) flag_status(p.dev_status, KVQ8_DEV_NONFINITE);
-                }
-                float qm = __uint_as_float(m);
-                if (qm < 1e-6f) qm = 1.0f;
-                const float iq = __fdiv_rn(127.0f, qm), qs = __fmul_rn(qm, KVQ8_INV127);
-                auto value = [&](float v) { return __fmul_rn((float)max(-128, min(127, __float2int_rn(__fmul_rn(v, iq)))), qs); };
-                x = make_float4(value(x.x), value(x.y), value(x.z), value(x.w));
-                // exponent of the row's largest value: the row is scaled to below 2^11
-                int e = max(max(__float_as_int(x.x) & 0x7fffffff, __float_as_int(x.y) & 0x7fffffff),
-                            max(__float_as_int(x.z) & 0x7fffffff, __float_as_int(x.w) & 0x7fffffff));
-                e = max(-100, (__reduce_max_sync(0xffffffffu, e) >> 23) - 127 - 10);
-                const float down = exp2_int(-e);
-                x = make_float4(x.x * down, x.y * down, x.z * down, x.w * down);
-                const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
-                const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                const __half2 l0 = __floats2half2_rn(x.x - f0.x, x.y - f0.y), l1 = __floats2half2_rn(x.z - f1.x, x.w - f1.y);
-                unsigned char *at = smem + L::oQ + (lane >> 1) * 128 + (lane & 1) * 8;
-                auto put = [&](int k, __half2 a, __half2 b) {
-                    *reinterpret_cast<uint2 *>(at + (k >> 3) * kCoreRow + (k & 7) * 16) = make_uint2(half2_bits(a), half2_bits(b));
-                };
-                put(i, h0, h1);
-                put(i + (kWide ? L::kRows : n), l0, l1);
-                if (lane == 0) ms->factor[seg & 1][i] = exp2_int(e);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ms->q_ready[seg & 1]));
-            const int end = w.end(w.r);
-            for (int i = 0; i < part; ++i, ++j) {
+#pragma unroll 1
+        for (int seg = 0;; ++seg) {
+            if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+            const Part &part = ms->part[seg & 3];
+            const int n = part.stages;
+            if (n == 0) break;
+            // tokens of the tile behind this lane's in its first stage
+            int behind = part.end - part.off * kTok - row;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++j, behind -= kTok) {
                 const uint32_t par = (j >> 1) & 1;
                 // K: lane = token, the row's chunk c stands at c ^ (token & 7)
                 int g = 2 * j, at = g % L::kSlots;
                 const unsigned char *st = smem + L::oRing + at * kSlotBytes;
                 wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms, p.dev_status);
                 const int skip = ms->skip[at];
-                const int t = (off + i) * kTok + row;
                 const float *scales = reinterpret_cast<const float *>(st + kCodeBytes);
-                const bool real = !skip && t < end;
-                const float ks = real ? scales[row] * p.sm_scale_log2 : 0.0f, vs = real ? scales[kTok + row] : 0.0f;
-                ms->scale[j & 3][row] = make_float2(ks, vs);
+                const bool real = !skip && behind > 0;
+                ms->scale[j & 3][row] = make_float2(real ? scales[row] * p.sm_scale_log2 : 0.0f, real ? scales[kTok + row] : 0.0f);
                 if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
@@ -539,8 +629,8 @@ tile_kernel(TileParams p, int lg) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_addr(&ms->empty[at]));
                     mbar_arrive(smem_addr(&ms->k_ready[j & 1]));
+                    mbar_arrive(smem_addr(&ms->empty[at]));
                 }
                 // V: lane = dim; two 64-token quarters of 64 bytes.  Lanes 2 apart start at
                 // another chunk, so that eight lanes' 16-byte reads hit all banks, and turn
@@ -552,7 +642,7 @@ tile_kernel(TileParams p, int lg) {
                 wait_warp(&ms->v_free[j & 1], par ^ 1, ms, p.dev_status);
                 tc_fence_after();
                 const int turn = (lane >> 1) & 3;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 2; ++q) {
                     const uint4 *vr = reinterpret_cast<const uint4 *>(st + q * kTileVQuarter + row * kStageTok);
                     uint4 a[4], b[4];
@@ -569,150 +659,140 @@ tile_kernel(TileParams p, int lg) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_addr(&ms->empty[at]));
                     mbar_arrive(smem_addr(&ms->v_ready[j & 1]));
+                    mbar_arrive(smem_addr(&ms->empty[at]));
                 }
             }
         }
     } else {
         regs_grow<kRegsSoftmax>();
         // ========================== softmax ==========================
-        constexpr int kCols = L::kRows / 2;   // a warp's share of the rows
-        constexpr int kBar = 1, kN = 256;
-        const int quad = warp & 3, half = (warp - 8) >> 2, st = tid - 256;
+        constexpr int kCols = kRows / 4;      // a warp's rows
+        // the four warps of a share of the rows see to it by themselves
+        const int quad = warp & 3, share = (warp - 8) >> 2, c0 = share * kCols, st = tid & 127;
+        const int bar = 1 + share;
         const int row = 32 * quad + lane;     // token of the stage (scores), dim (output)
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        unsigned char *prow = smem + L::oP + row * 16;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        unsigned char *prow = smem + L::oP + (c0 >> 3) * kCoreRow + row * 16;
         int j = 0;
-        KVQ8_FOR_TILES {
-            const int rows = w.tile_rows(w.r), n = (rows + 15) & ~15;
-            const int nh = n / 2, c0 = half * nh;   // this warp: rows c0 .. c0 + nh - 1
+#pragma unroll 1
+        for (int seg = 0;; ++seg) {
+            const bool ok = wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status);
+            // (the four warps stop together, or a barrier would wait for the one that left)
+            if (barrier_any(bar, 128, !ok)) break;
+            const int n = ms->part[seg & 3].stages;
+            if (n == 0) break;
             wait_warp(&ms->q_ready[seg & 1], (seg >> 1) & 1, ms, p.dev_status);
-            if (st < n) {
-                int lim = 0x7fffffff;
-                if (st < rows) {
-                    bool bad;
-                    lim = w.limit(w.r, st, bad);
-                    if (bad) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-                    atomicMin(&ms->lim_min[seg & 1], lim);
-                }
-                ms->lim[st] = lim;
-                ms->col[st] = make_float2(ms->factor[seg & 1][st], INFINITY);
-            }
-            named_barrier_sync(kBar, kN);
-            const int lim_min = ms->lim_min[seg & 1];
-            if (st == 0) ms->lim_min[(seg & 1) ^ 1] = 0x7fffffff;
+            if (st < kCols) ms->ref[c0 + st] = 0.0f;
+            const int lim_min = min(ms->lim_min[seg & 3][0], ms->lim_min[seg & 3][1]);
+            const float *gain = ms->gain[seg & 3] + c0;
+            named_barrier_sync(bar, 128);
             float sum[kCols];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-            for (int i = 0; i < part; ++i, ++j) {
-                const int buf = j & 3;
-                wait_warp(&ms->sc_ready[buf], (j >> 2) & 1, ms, p.dev_status);
-                const float2 sc = ms->scale[buf][row];
-                const bool bad = ms->bad[buf] != 0;
-                const int t0 = (off + i) * kTok;
-                const int tok = bad ? 0x7fffffff : t0 + row;
-                const bool masked = bad || t0 + kTok > lim_min;   // some row does not see all of the stage
-                const float vs_log2 = fmaxf(__log2f(sc.y), kTinyScaleLog2);
+            for (int k = 0; k < kCols; ++k) sum[k] = 0.0f;
+            bool fresh = true;   // no row has a reference yet
+            int t0 = ms->part[seg & 3].off * kTok;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
+                wait_warp(&ms->sc_ready[j & 3], (j >> 2) & 1, ms, p.dev_status);
+                const float2 sc = ms->scale[j & 3][row];
+                const bool bad = ms->bad[j & 3] != 0;
                 wait_warp(&ms->s_full, j & 1, ms, p.dev_status);
                 tc_fence_after();
+                // scores of this thread's token, relative to the references
                 float t[kCols];
-                // scores of this thread's token, relative to the running maxima
-                auto scores = [&](bool relative) {
+                if constexpr (kWide) {
+                    tmem_ld16(lanes + kColS + c0, t);
+                    tmem_ld16(lanes + kColS + c0 + 16, t + 16);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < kCols / 8; ++k) {
-                        if (8 * k < nh) {
-                            float x[8], y[8];
-                            tmem_ld8(lanes + kColS + c0 + 8 * k, x);
-                            if (!kWide) tmem_ld8(lanes + kColS + n + c0 + 8 * k, y);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) t[8 * k + q] = x[q];
-                            if (!kWide) {
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int q = 0; q < 8; ++q) {
-                                    asm volatile("" : "+f"(t[8 * k + q]), "+f"(y[q]));
-                                    t[8 * k + q] += y[q];
-                                }
-                            }
-                        }
+                    for (int k = 0; k < kCols; ++k) asm volatile("" : "+f"(t[k]));
+                } else {
+                    float low[kCols];
+                    if constexpr (kCols == 16) {
+                        tmem_ld16(lanes + kColS + c0, t);
+                        tmem_ld16(lanes + kColS + kRows + c0, low);
+                    } else {
+                        tmem_ld8(lanes + kColS + c0, t);
+                        tmem_ld8(lanes + kColS + kRows + c0, low);
                     }
-                    if (kWide) {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < kCols; ++q) asm volatile("" : "+f"(t[q]));
-                    }
-#pragma unroll
-                    for (int k = 0; k < kCols / 2; ++k) {
-                        if (2 * k < nh) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&ms->col[c0 + 2 * k]);
-                            t[2 * k] = fmaf(t[2 * k] * sc.x, f.x, relative ? f.y : 0.0f);
-                            t[2 * k + 1] = fmaf(t[2 * k + 1] * sc.x, f.z, relative ? f.w : 0.0f);
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < kCols / 4; ++k) {
-                            if (4 * k < nh) {
-                                const int4 f = *reinterpret_cast<const int4 *>(&ms->lim[c0 + 4 * k]);
-                                if (tok >= f.x) t[4 * k] = -INFINITY;
-                                if (tok >= f.y) t[4 * k + 1] = -INFINITY;
-                                if (tok >= f.z) t[4 * k + 2] = -INFINITY;
-                                if (tok >= f.w) t[4 * k + 3] = -INFINITY;
-                            }
-                        }
-                    }
-                };
-                scores(true);
-                const float most = kPMaxLog2 - vs_log2;
-                bool raise = false;
-#pragma unroll
-                for (int k = 0; k < kCols / 8; ++k) {
-                    if (8 * k < nh) {
-                        float top = t[8 * k];
-#pragma unroll
-                        for (int q = 1; q < 8; ++q) top = fmaxf(top, t[8 * k + q]);
-                        raise |= top > most;
-                    }
-                }
-                bool p_free = i == 0;   // the product before this one is done
-                if (barrier_any(kBar, kN, raise)) {
-                    // move the references that are too low, by whole numbers
-                    scores(false);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < kCols; ++k) {
-                        if (k < nh) {
-                            const float top = warp_top(t[k] + vs_log2);
-                            if (lane == (k & 31)) ms->wave[quad][c0 + k] = top;
-                        }
+                        asm volatile("" : "+f"(t[k]), "+f"(low[k]));
+                        t[k] += low[k];
                     }
-                    named_barrier_sync(kBar, kN);
-                    if (st < n) {
-                        const float top = fmaxf(fmaxf(ms->wave[0][st], ms->wave[1][st]), fmaxf(ms->wave[2][st], ms->wave[3][st]));
-                        const float old = -ms->col[st].y;
-                        float now = old;
-                        if (top > old + kPMaxLog2) now = ceilf(top) - kPTopLog2;   // (also the first time: old is -inf)
-                        ms->col[st].y = -now;
-                        ms->alpha[st] = old == -INFINITY ? 0.0f : ex2_approx(old - now);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ms->s_free));
+                float top = -INFINITY;
+                {
+                    const float2 ks = make_float2(sc.x, sc.x);
+#pragma unroll
+                    for (int q = 0; q < kCols; q += 4) {
+                        const float4 g = *reinterpret_cast<const float4 *>(gain + q);
+                        const float4 m = *reinterpret_cast<const float4 *>(ms->ref + c0 + q);
+                        const float2 a = fma2(mul2(make_float2(t[q], t[q + 1]), ks), make_float2(g.x, g.y), make_float2(m.x, m.y));
+                        const float2 b = fma2(mul2(make_float2(t[q + 2], t[q + 3]), ks), make_float2(g.z, g.w), make_float2(m.z, m.w));
+                        t[q] = a.x;
+                        t[q + 1] = a.y;
+                        t[q + 2] = b.x;
+                        t[q + 3] = b.y;
                     }
-                    named_barrier_sync(kBar, kN);
-                    if (!p_free) {
-                        wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+                }
+                if (bad || t0 + kTok > lim_min) {   // some row does not see all of the stage
+                    const int tok = bad ? 0x7fffffff : t0 + row;
+#pragma unroll
+                    for (int q = 0; q < kCols; q += 4) {
+                        const int4 f = *reinterpret_cast<const int4 *>(ms->lim[seg & 3] + c0 + q);
+                        t[q] = tok >= f.x ? -INFINITY : t[q];
+                        t[q + 1] = tok >= f.y ? -INFINITY : t[q + 1];
+                        t[q + 2] = tok >= f.z ? -INFINITY : t[q + 2];
+                        t[q + 3] = tok >= f.w ? -INFINITY : t[q + 3];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) top = fmaxf(top, t[k]);
+                const float vs_log2 = fmaxf(__log2f(sc.y), kTinyScaleLog2);
+                // the product before this one is done: P's room is free, the accumulator at rest
+                if (i > 0) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+                if (barrier_any(bar, 128, fresh || top > kPMaxLog2 - vs_log2)) {
+                    // move the references of rows whose P would leave fp16's range (at first: of all), by whole
+                    // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
+                    // stage of one leaves the rows fresh
+                    int mine = 0;
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k) {
+                        const int m = __reduce_max_sync(0xffffffffu, ordered(__float_as_int(t[k] + vs_log2)));
+                        if (lane == k) mine = m;
+                    }
+                    if (lane < kCols) ms->wave[quad][c0 + lane] = __int_as_float(ordered(mine));
+                    named_barrier_sync(bar, 128);
+                    if (st < kCols) {
+                        const int x = c0 + st;
+                        const float most = fmaxf(fmaxf(ms->wave[0][x], ms->wave[1][x]), fmaxf(ms->wave[2][x], ms->wave[3][x]));
+                        const bool move = fresh ? most > -INFINITY : most > kPMaxLog2;
+                        const float by = move ? kPTopLog2 - ceilf(most) : 0.0f;
+                        ms->ref[x] += by;
+                        ms->shift[x] = by;
+                    }
+                    named_barrier_sync(bar, 128);
+                    if (i > 0 && !fresh) {
                         tc_fence_after();
-                        p_free = true;
 #pragma unroll 1
-                        for (int part_lo = 0; part_lo < (!kWide && kLow ? 2 : 1); ++part_lo) {
+                        for (int x = 0; x < (!kWide && kLow ? 2 : 1); ++x) {
 #pragma unroll 1
-                            for (int k = 0; k < nh; k += 8) {
-                                const uint32_t at = lanes + kColO + part_lo * n + c0 + k;
-                                float x[8];
+                            for (int k = 0; k < kCols; k += 8) {
+                                const uint32_t at = lanes + kColO + x * kRows + c0 + k;
+                                float o[8];
                                 uint32_t v[8];
-                                tmem_ld8(at, x);
+                                tmem_ld8(at, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int q = 0; q < 8; ++q) {
-                                    asm volatile("" : "+f"(x[q]));
-                                    v[q] = __float_as_uint(x[q] * ms->alpha[c0 + k + q]);
+                                    asm volatile("" : "+f"(o[q]));
+                                    v[q] = __float_as_uint(o[q] * ex2_approx(ms->shift[c0 + k + q]));
                                 }
                                 tmem_st8(at, v);
                             }
@@ -720,41 +800,37 @@ tile_kernel(TileParams p, int lg) {
                         tmem_wait_st();
                     }
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k)
-                        if (k < nh) sum[k] *= ms->alpha[c0 + k];
-                    scores(true);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ms->s_free));
-                // weights, and P = weight * V scale in high and low parts
-                const float pvs = sc.y;
-                uint32_t hi[kCols / 2], lo[kLow ? kCols / 2 : 1];
-#pragma unroll
-                for (int k = 0; k < kCols / 2; ++k) {
-                    if (2 * k < nh) {
-                        const float w0 = ex2_approx(t[2 * k]), w1 = ex2_approx(t[2 * k + 1]);
-                        sum[2 * k] += w0;
-                        sum[2 * k + 1] += w1;
-                        const float x0 = w0 * pvs, x1 = w1 * pvs;
-                        const __half2 a = __floats2half2_rn(x0, x1);
-                        hi[k] = half2_bits(a);
-                        if (kLow) {
-                            const float2 f = __half22float2(a);
-                            lo[k] = half2_bits(__floats2half2_rn(x0 - f.x, x1 - f.y));
-                        }
+                    for (int k = 0; k < kCols; ++k) {
+                        const float by = ms->shift[c0 + k];
+                        t[k] += by;
+                        if (!fresh) sum[k] *= ex2_approx(by);
                     }
+                    fresh = fresh && bad;
                 }
-                if (!p_free) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+                // weights, and P = weight * V scale in high and low parts
+                {
+                    const float2 vs = make_float2(sc.y, sc.y);
 #pragma unroll
-                for (int k = 0; k < kCols / 8; ++k) {
-                    if (8 * k < nh) {
-                        const int core = (c0 >> 3) + k;
-                        *reinterpret_cast<uint4 *>(prow + core * kCoreRow) =
-                            make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                    for (int k = 0; k < kCols; k += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int x = k + 2 * q;
+                            const float2 e = make_float2(ex2_approx(t[x]), ex2_approx(t[x + 1]));
+                            const float2 s2 = add2(make_float2(sum[x], sum[x + 1]), e);
+                            sum[x] = s2.x;
+                            sum[x + 1] = s2.y;
+                            const float2 v = mul2(e, vs);
+                            const __half2 a = __floats2half2_rn(v.x, v.y);
+                            hi[q] = half2_bits(a);
+                            if (kLow) {
+                                const float2 d = fma2(__half22float2(a), make_float2(-1.f, -1.f), v);
+                                lo[q] = half2_bits(__floats2half2_rn(d.x, d.y));
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(prow + (k >> 3) * kCoreRow) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         if (kLow)
-                            *reinterpret_cast<uint4 *>(prow + (core + (kWide ? L::kRows / 8 : n / 8)) * kCoreRow) =
-                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                            *reinterpret_cast<uint4 *>(prow + ((k + kRows) >> 3) * kCoreRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 fence_async_smem();
@@ -763,53 +839,51 @@ tile_kernel(TileParams p, int lg) {
                 if (lane == 0) mbar_arrive(smem_addr(&ms->p_ready));
             }
             // ---- the tile's end: row sums over the tokens, then the output or a record ----
-            // (each step adds the halves of the rows that a lane keeps and gives away: lane l ends with rows
-            // l * kCols / 32 ..)
+            // (each step adds the halves of the rows that a lane keeps and gives away; the last ones, with one row
+            // left, add the lanes of that row)
 #pragma unroll
             for (int o = 16, cnt = kCols / 2; o > 0; o >>= 1, cnt >>= 1) {
+                if (cnt > 0) {
 #pragma unroll
-                for (int k = 0; k < cnt; ++k) {
-                    const bool up = lane & o;
-                    const float give = up ? sum[k] : sum[k + cnt], keep = up ? sum[k + cnt] : sum[k];
-                    sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    for (int k = 0; k < cnt; ++k) {
+                        const bool up = lane & o;
+                        const float give = up ? sum[k] : sum[k + cnt], keep = up ? sum[k + cnt] : sum[k];
+                        sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                } else {
+                    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kCols / 32; ++k) {
-                const int x = lane * (kCols / 32) + k;
-                if (x < nh) ms->wave[quad][c0 + x] = sum[k];
-            }
-            named_barrier_sync(kBar, kN);
-            const bool whole = off == 0 && part == w.stages(w.r);
-            const bool direct = !kShared && whole;
-            // first record row of this part
-            long long rec;
-            if (kShared) rec = (long long)w.first * p.nqh + (long long)w.h * w.rows + (long long)w.r * L::kRows + (long long)c * kTileRows;
-            else rec = ((long long)c * 2 + (off == 0 ? 1 : 0)) * kTileRows;
-            if (st < n) {
-                const float S = ms->wave[0][st] + ms->wave[1][st] + ms->wave[2][st] + ms->wave[3][st];
-                ms->alpha[st] = direct ? (S > 0.0f ? 1.0f / S : 0.0f) : 1.0f;
-                if (!direct && st < rows) {
-                    const float2 ml = make_float2(-ms->col[st].y, S);
-                    *reinterpret_cast<float2 *>(p.ws_ml + (rec + st) * 2) = ml;
+            const Part &part = ms->part[seg & 3];
+            const bool direct = part.direct != 0;
+            ms->wave[quad][c0 + lane / (32 / kCols)] = sum[0];   // the row that this lane ended with
+            named_barrier_sync(bar, 128);
+            if (st < kCols) {
+                const int x = c0 + st;
+                const float S = ms->wave[0][x] + ms->wave[1][x] + ms->wave[2][x] + ms->wave[3][x];
+                ms->shift[x] = direct ? (S > 0.0f ? 1.0f / S : 0.0f) : 1.0f;
+                long long dst = -1;
+                if (x < part.rows) {
+                    if (direct) {
+                        dst = ((long long)part.token + (x >> lg)) * p.out_stride +
+                              (long long)((part.head << lg) + (x & ((1 << lg) - 1))) * kHD;
+                    } else {
+                        dst = (part.rec + x) * kHD;
+                        *reinterpret_cast<float2 *>(p.ws_ml + (part.rec + x) * 2) = make_float2(-ms->ref[x], S);
+                    }
                 }
+                ms->dst[x] = dst;
             }
-            if (st == 0 && !whole && off == 0) {
-                // the CTAs c .. that hold this tile's records
-                const int cnt = (int)(((hi - left + w.stages(w.r)) * C + T - 1) / T) - c;
-                if (!kShared) p.ws_dir[c] = make_int4(cnt, w.s, w.h, w.r);
-                else p.ws_dir[rec - (long long)c * kTileRows] = make_int4(c, cnt, 0, 0);
-            } else if (kShared && st == 0 && whole) {
-                p.ws_dir[rec - (long long)c * kTileRows] = make_int4(c, 1, 0, 0);
-            }
-            named_barrier_sync(kBar, kN);
+            named_barrier_sync(bar, 128);
             wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
             tc_fence_after();
+            void *to = direct ? p.out : p.ws_acc;
+            const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
 #pragma unroll 1
-            for (int k = 0; k < nh; k += 8) {
+            for (int k = 0; k < kCols; k += 8) {
                 float x[8], y[8];
                 tmem_ld8(lanes + kColO + c0 + k, x);
-                if (!kWide && kLow) tmem_ld8(lanes + kColO + n + c0 + k, y);
+                if (!kWide && kLow) tmem_ld8(lanes + kColO + kRows + c0 + k, y);
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -818,11 +892,12 @@ tile_kernel(TileParams p, int lg) {
                         asm volatile("" : "+f"(y[q]));
                         x[q] += y[q];
                     }
-                    const int i = c0 + k + q;
-                    if (i >= rows) continue;
-                    const float v = x[q] * ms->alpha[i];
-                    if (direct) store1(p.out, p.out_dtype, w.token(w.r, i) * p.out_stride + (int64_t)w.head(i) * kHD + row, v);
-                    else p.ws_acc[(rec + i) * kHD + row] = v;
+                    const long long dst = ms->dst[c0 + k + q];
+                    const float v = x[q] * ms->shift[c0 + k + q];
+                    if (dst >= 0) {
+                        if (type == KVQ8_DTYPE_F32) static_cast<float *>(to)[dst + row] = v;
+                        else store1(to, type, dst + row, v);
+                    }
                 }
             }
             tc_fence_before();
@@ -833,8 +908,7 @@ tile_kernel(TileParams p, int lg) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
-#undef KVQ8_FOR_TILES
+    if (warp == 1) tmem_dealloc(0, 512);
 }
 
 // What the tile kernel needs to know of the groups: (first row, rows, the row
@@ -940,7 +1014,7 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, in
 
 int tile_ctas() { return min(device_sm_count(), kMaxTileCtas); }
 
-template <bool kShared, bool kWide, bool kLow>
+template <bool kShared, int kRows, bool kLow>
 cudaError_t launch_tiles(const TileParams &p, int lg, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
     const int ctas = tile_ctas();
@@ -950,14 +1024,14 @@ cudaError_t launch_tiles(const TileParams &p, int lg, cudaStream_t s) {
         [] {
             // the warpgroups trade registers within the launch's own: it must hold what they come to
             cudaFuncAttributes a;
-            cudaError_t e = cudaFuncGetAttributes(&a, tile_kernel<kShared, kWide, kLow>);
+            cudaError_t e = cudaFuncGetAttributes(&a, tile_kernel<kShared, kRows, kLow>);
             if (e != cudaSuccess) return e;
-            if (a.numRegs != 128) return cudaErrorInvalidConfiguration;
-            return cudaFuncSetAttribute(tile_kernel<kShared, kWide, kLow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        Lay<kWide, kLow>::kBytes);
+            if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+            return cudaFuncSetAttribute(tile_kernel<kShared, kRows, kLow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        Lay<kRows, kLow>::kBytes);
         },
         [&] {
-            return launch_dependent(tile_kernel<kShared, kWide, kLow>, dim3(ctas), kThreads, Lay<kWide, kLow>::kBytes, s, p, lg);
+            return launch_dependent(tile_kernel<kShared, kRows, kLow>, dim3(ctas), kThreads, Lay<kRows, kLow>::kBytes, s, p, lg);
         });
 }
 
@@ -969,25 +1043,30 @@ int log2_of(int x) {
 
 }  // namespace
 
-// Tiles of 128 rows where a sequence (or, on average, a group) has more than 64.
+// Rows per tile: the most that a sequence (on average, a group) has, up to 128.
+static int rows_of(int64_t rows) { return rows > 64 ? 128 : rows > 32 ? 64 : 32; }
+
 cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
-    const int lg = log2_of(group);
-    const bool wide = ((int64_t)p.n_new << lg) > 64, low = p.out_dtype != KVQ8_DTYPE_BF16;
-    const cudaError_t e = wide ? (low ? launch_tiles<false, true, true>(p, lg, s) : launch_tiles<false, true, false>(p, lg, s))
-                               : (low ? launch_tiles<false, false, true>(p, lg, s) : launch_tiles<false, false, false>(p, lg, s));
+    const int lg = log2_of(group), rows = rows_of((int64_t)p.n_new << lg);
+    cudaError_t e;
+    if (p.out_dtype == KVQ8_DTYPE_BF16)
+        e = rows == 128 ? launch_tiles<false, 128, false>(p, lg, s)
+            : rows == 64 ? launch_tiles<false, 64, false>(p, lg, s) : launch_tiles<false, 32, false>(p, lg, s);
+    else
+        e = rows == 128 ? launch_tiles<false, 128, true>(p, lg, s)
+            : rows == 64 ? launch_tiles<false, 64, true>(p, lg, s) : launch_tiles<false, 32, true>(p, lg, s);
     if (e != cudaSuccess) return e;
-    const int rows = wide ? 128 : 64;
     return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
 }
 
 cudaError_t launch_shared_prefix(TileParams &p, int group, cudaStream_t s) {
     const int lg = log2_of(group);
-    const bool wide = ((int64_t)p.batch << lg) > 64 * (int64_t)p.n_groups;
-    p.tile_rows = wide ? 128 : 64;
+    p.tile_rows = rows_of((((int64_t)p.batch << lg) + p.n_groups - 1) / p.n_groups);
     const int blocks = min((p.n_groups + kPlanWarps - 1) / kPlanWarps, 304);
     const cudaError_t e = launch_dependent(shared_plan_kernel, dim3(blocks), kPlanWarps * 32, 0, s, p);
     if (e != cudaSuccess) return e;
-    return wide ? launch_tiles<true, true, true>(p, lg, s) : launch_tiles<true, false, true>(p, lg, s);
+    return p.tile_rows == 128 ? launch_tiles<true, 128, true>(p, lg, s)
+           : p.tile_rows == 64 ? launch_tiles<true, 64, true>(p, lg, s) : launch_tiles<true, 32, true>(p, lg, s);
 }
 
 }  // namespace kvq8
