@@ -29,9 +29,9 @@ shared_merge_kernel(DecodeParams d, TileParams t, int G) {
     };
     if (own > 0) {
         const int grp = group_of_row(t.group_starts, t.n_groups, b);
-        const int b0 = t.group_starts[grp], rows = (t.group_starts[grp + 1] - b0) * G;
-        const int n = (b - b0) * G + g;                                     // row of the (group, kv head)
-        const int64_t x0 = (int64_t)b0 * t.nqh + (int64_t)h * rows;
+        const int b0 = t.group_starts[grp];
+        const int n = (b - b0) * G + g;                                     // row of the (kv head, group)
+        const int64_t x0 = ((int64_t)h * t.batch + b0) * G;
         const int4 dir = t.ws_dir[x0 + n / t.tile_rows * t.tile_rows];
         for (int c = 0; c < dir.y; ++c) {
             const int64_t r = x0 + n + (int64_t)(dir.x + c) * kTileRows;

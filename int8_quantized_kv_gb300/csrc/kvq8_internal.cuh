@@ -213,7 +213,7 @@ struct TileParams {
     // partial results.  Prompt: CTA c's rows at c * 2 * kTileRows (a tile that it
     // goes on with) and kTileRows later (a tile that it begins and another ends),
     // ws_dir[c] says of which tile the latter is.  Shared prefix: row x of the
-    // batch * nqh rows, ordered by (group, kv head, row), by CTA c at
+    // batch * nqh rows, ordered by (kv head, batch row, head), by CTA c at
     // x + c * kTileRows; ws_dir[x of a tile's first row] = (first CTA, their count).
     int4 *ws_dir;
     float *ws_ml;                 // [..][2]: running max M (base 2), sum S

@@ -57,7 +57,6 @@ constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this 
 // softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory leaves it no L1.
 constexpr int kLaunchRegs = 80, kRegsIssue = 64, kRegsOperand = 64, kRegsSoftmax = 88;
 static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs, "registers");
-constexpr int kQBatch = 2;                      // query rows that a warp prepares at a time
 // columns of tensor memory, all of which is the CTA's (so that it begins at address 0)
 constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = 384;
 
@@ -87,20 +86,15 @@ struct Part {
 struct Misc {
     uint64_t full[8], empty[8];                 // ring slots
     uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2], sc_ready[4];
-    uint64_t part_ready[4];
-    // (two, since the queries may be two tiles ahead of the softmax)
-    uint64_t q_ready[2];
-    uint64_t s_full, s_free, p_ready, pv_done, q_free, o_free, all_done;
+    uint64_t part_ready[4], part_free[4];
+    uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done;
     long long warp_tot[kThreads / 32];
-    long long base, end;
-    int s0, r0;
+    int s0, r0, off;
     volatile int abort;
     uint32_t tmem;
     int skip[8];                                // slot: its block id is outside the pool
     int bad[4];                                 // stage (mod 4): the same
-    int lim_min[4][2];                          // tile (mod 4)
-    // what concerns a tile is kept four deep: the queries of tile x + 3 are prepared when QK of x + 2 is done, so
-    // when the softmax has left tile x
+    int lim_min[4];                             // tile (mod 4)
     alignas(16) Part part[4];
     alignas(16) int lim[4][kTileRows];          // tile (mod 4), row: tokens below
     alignas(16) float gain[4][kTileRows];       // tile (mod 4), row: power of two of the query's operand
@@ -108,7 +102,7 @@ struct Misc {
     alignas(16) float ref[kTileRows];           // per row: -M
     alignas(16) float shift[kTileRows];         // per row: M before - M now, or the output's factor
     alignas(16) float wave[4][kTileRows];       // per warp and row: maxima, sums
-    long long dst[kTileRows];                   // per row: where its output or record starts
+    char *dst[kTileRows];                       // per row: where its output or record starts (null: nowhere)
 };
 static_assert(sizeof(Misc) <= 13312, "misc");
 
@@ -137,7 +131,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Misc *
     return __all_sync(0xffffffffu, ok);
 }
 
-// The tiles in their order: (sequence or group, kv head, rows).
+// The tiles in their order: (kv head, sequence or group, rows).
 template <bool kShared>
 struct Walk {
     const TileParams &p;
@@ -189,15 +183,17 @@ struct Walk {
         return kShared ? first + i : (long long)s * p.n_new + i;
     }
     __device__ int head(int n) const { return (h << lg) + (n & ((1 << lg) - 1)); }
+    // (there is one behind: the caller counts)
     __device__ void next(int count) {
         if (++r < tiles()) return;
         r = 0;
-        if (++h < p.nkv) return;
-        h = 0;
-        for (++s; s < count; ++s) {
+        do {
+            if (++s == count) {
+                s = 0;
+                ++h;
+            }
             load(s);
-            if (rows > 0) return;
-        }
+        } while (rows == 0);
     }
 };
 
@@ -228,8 +224,31 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 x) { return *reinterpret_
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
 
-// Floats as integers of the same order (and back), so that one redux gives a maximum.
-__device__ __forceinline__ int ordered(int k) { return k ^ ((k >> 31) & 0x7fffffff); }
+// Combines 2 * kCount values per lane over the warp: each step combines the half of the values that a lane keeps with
+// the other lane's, from lanes kLanes apart on, then (one value left) all lanes of that value.  Lane l ends with value
+// l / (32 / count) of `count` values that the first step (16 lanes apart) began with.
+template <int kCount, int kLanes, typename Op>
+__device__ __forceinline__ void halve(float *v, int lane, Op op) {
+    if constexpr (kLanes > 0) {
+        if constexpr (kCount > 0) {
+#pragma unroll
+            for (int k = 0; k < kCount; ++k) {
+                const bool up = lane & kLanes;
+                const float give = up ? v[k] : v[k + kCount], keep = up ? v[k + kCount] : v[k];
+                v[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, kLanes));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], kLanes));
+        }
+        halve<kCount / 2, kLanes / 2>(v, lane, op);
+    }
+}
+
+// a / b for positive b; in 32 bits where that does.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 31) == 0) return (int)a / (int)b;
+    return a / b;
+}
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -267,7 +286,6 @@ tile_kernel(TileParams p, int lg) {
             mbar_init(smem_addr(&ms->empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&ms->q_ready[i]), 2);
             mbar_init(smem_addr(&ms->k_ready[i]), 4);
             mbar_init(smem_addr(&ms->k_free[i]), 1);
             mbar_init(smem_addr(&ms->v_ready[i]), 4);
@@ -276,18 +294,18 @@ tile_kernel(TileParams p, int lg) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&ms->sc_ready[i]), 4);
             mbar_init(smem_addr(&ms->part_ready[i]), 1);
+            mbar_init(smem_addr(&ms->part_free[i]), kSoftmaxWarps);
         }
         mbar_init(smem_addr(&ms->s_full), 1);
         mbar_init(smem_addr(&ms->s_free), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->p_ready), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->pv_done), 1);
+        mbar_init(smem_addr(&ms->q_ready), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->q_free), 1);
         mbar_init(smem_addr(&ms->o_free), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->all_done), 1);
         fence_mbar_init();
         ms->abort = 0;
-        ms->s0 = 0;
-        ms->r0 = 0;
     }
     if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), 512);
     pdl_wait();
@@ -296,97 +314,69 @@ tile_kernel(TileParams p, int lg) {
     Walk<kShared> w(p, lg, kRows);
     const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + kRows - 1) / kRows);
     const int seqs = kShared ? p.n_groups : p.batch;
-    const long long items = (long long)seqs * per_seq;   // (sequence, tile of one kv head), or group
-    const long long per = (items + kThreads - 1) / kThreads;
-    const long long i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
-    auto item = [&](long long i, int &s, int &r) {
-        s = (int)(i / per_seq);
-        r = (int)(i % per_seq);
+    const int items = seqs * per_seq;   // (sequence, tile of one kv head), or group
+    const int per = (items + kThreads - 1) / kThreads;
+    const int i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
+    auto item = [&](int i) {   // its stages, for one kv head
+        const int s = i / per_seq, r = i - s * per_seq;
         w.load(s);
-        if (kShared) return (long long)w.tiles() * w.stages(0) * (w.rows > 0);
-        return r < w.tiles() ? (long long)w.stages(r) : 0ll;
+        w.r = r;
+        return kShared ? (w.rows > 0 ? (long long)w.tiles() * w.stages(0) : 0) : r < w.tiles() ? w.stages(r) : 0;
     };
     long long mine = 0;
-    int s, r;
 #pragma unroll 1
-    for (long long i = i_lo; i < i_hi; ++i) mine += item(i, s, r);
-    long long incl = mine;
+    for (int i = i_lo; i < i_hi; ++i) mine += item(i);
+    long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    if (lane == 31) ms->warp_tot[warp] = incl;
+    if (lane == 31) ms->warp_tot[warp] = before;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long excl = incl - mine, total = 0;
+    before -= mine;
+    long long total = 0;   // stages of one kv head
 #pragma unroll 1
     for (int k = 0; k < kThreads / 32; ++k) {
-        if (k < warp) excl += ms->warp_tot[k];
-        total += ms->warp_tot[k];
+        const long long v = ms->warp_tot[k];
+        if (k < warp) before += v;
+        total += v;
     }
     const long long T = total * p.nkv;
     const int C = (int)min((long long)gridDim.x, T);
-    long long lo = 0, hi = 0;
-    if (c < C) {
-        const long long Tq = T / C;
-        const int Tr = (int)(T - Tq * C);
-        lo = (long long)c * Tq + ((long long)c * Tr) / C;
-        hi = (long long)(c + 1) * Tq + ((long long)(c + 1) * Tr) / C;
-    }
     if (!kShared && tid == 0) p.ws_dir[c] = make_int4(0, 0, 0, 0);
+    long long lo = 0, hi = 0;
     int off = 0;
-    if (hi > lo) {   // (uniform over the CTA)
-        long long acc = excl;
+    if (c < C) {   // (uniform over the CTA)
+        const long long Tq = divide(T, C);
+        const int Tr = (int)(T - Tq * C);
+        lo = (long long)c * Tq + (c * Tr) / C;
+        hi = (long long)(c + 1) * Tq + ((c + 1) * Tr) / C;
+        const int h = (int)divide(lo, total);
+        const long long rem = lo - h * total;
+        // the item that holds stage lo says so
 #pragma unroll 1
-        for (long long i = i_lo; i < i_hi; ++i) {
-            const long long v = item(i, s, r);
-            if (r == 0 && acc * p.nkv <= lo) atomicMax(&ms->s0, s);
-            acc += v;
-        }
-        if (tid == 0) ms->end = total;
-        __syncthreads();
-        const int s0 = ms->s0;
-        acc = excl;
-#pragma unroll 1
-        for (long long i = i_lo; i < i_hi; ++i) {
-            const long long v = item(i, s, r);
-            if (r == 0 && s == s0) ms->base = acc;
-            if (r == 0 && s == s0 + 1) ms->end = acc;
-            acc += v;
+        for (int i = i_lo; i < i_hi && before <= rem; ++i) {
+            const long long v = item(i);
+            if (rem < before + v) {
+                ms->s0 = w.s;
+                ms->r0 = w.r;
+                ms->off = (int)(rem - before);
+            }
+            before += v;
         }
         __syncthreads();
-        const long long base = ms->base, W = ms->end - base;
-        long long rem = lo - base * p.nkv;
-        const int h0 = (int)(rem / W);
-        rem -= h0 * W;
+        off = ms->off;
+        w.load(ms->s0);
+        w.h = h;
+        w.r = ms->r0;
         if (kShared) {
-            w.load(s0);
-            w.r = (int)(rem / w.stages(0));
-            off = (int)(rem % w.stages(0));
-        } else {
-            acc = excl;
-#pragma unroll 1
-            for (long long i = i_lo; i < i_hi; ++i) {
-                const long long v = item(i, s, r);
-                if (s == s0 && v > 0 && acc - base <= rem) atomicMax(&ms->r0, r);
-                acc += v;
-            }
-            __syncthreads();
-            w.r = ms->r0;
-            acc = excl;
-#pragma unroll 1
-            for (long long i = i_lo; i < i_hi; ++i) {
-                const long long v = item(i, s, r);
-                if (s == s0 && r == w.r) ms->end = rem - (acc - base);
-                acc += v;
-            }
-            __syncthreads();
-            off = (int)ms->end;
-            w.load(s0);
+            const int n = w.stages(0);
+            w.r = off / n;
+            off -= w.r * n;
         }
-        w.h = h0;
     }
 
     if (warp < 4) {
@@ -462,7 +452,7 @@ tile_kernel(TileParams p, int lg) {
                 if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
                 const int n = ms->part[seg & 3].stages;
                 if (n == 0) break;
-                wait_warp(&ms->q_ready[seg & 1], (seg >> 1) & 1, ms, p.dev_status);
+                wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
 #pragma unroll 1
                 for (int i = 0; i <= n; ++i, ++x) {
                     if (i < n) {
@@ -492,24 +482,34 @@ tile_kernel(TileParams p, int lg) {
             mma_commit(smem_addr(&ms->all_done), lead);
             mbar_wait_bounded(smem_addr(&ms->all_done), 0, kLimitNs);
             __syncwarp();
-        } else {
-            // ================== the tiles' order and their queries ==================
+        } else if (warp == 2) {
+            // ======================= the tiles' order =======================
             long long left = hi - lo;
-            unsigned char *at = smem + L::oQ + (lane >> 1) * 128 + (lane & 1) * 8;
-            auto put = [&](int k, __half2 a, __half2 b) {
-                *reinterpret_cast<uint2 *>(at + (k >> 3) * kCoreRow + (k & 7) * 16) = make_uint2(half2_bits(a), half2_bits(b));
-            };
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
+                if (!wait_warp(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms, p.dev_status)) break;
                 Part &part = ms->part[seg & 3];
                 const int stages = left > 0 ? w.stages(w.r) : 0;
                 const int n = (int)min(left, (long long)(stages - off));
-                const int rows = left > 0 ? w.tile_rows(w.r) : 0;
-                if (warp == 2 && lane == 0) {
-                    part.stages = n;
-                    if (n > 0) {
+                if (n > 0) {
+                    const int rows = w.tile_rows(w.r);
+                    int least = 0x7fffffff;
+#pragma unroll 1
+                    for (int i = lane; i < kRows; i += 32) {
+                        int lim = 0x7fffffff;
+                        if (i < rows) {
+                            bool bad;
+                            lim = w.limit(w.r, i, bad);
+                            if (bad) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+                        }
+                        ms->lim[seg & 3][i] = lim;
+                        least = min(least, lim);
+                    }
+                    least = __reduce_min_sync(0xffffffffu, least);
+                    if (lane == 0) {
                         const bool whole = n == stages;
-                        const long long x = (long long)w.first * p.nqh + (long long)w.h * w.rows + (long long)w.r * kRows;
+                        const long long x = (((long long)w.h * p.batch + w.first) << lg) + (long long)w.r * kRows;
+                        ms->lim_min[seg & 3] = least;
                         part.off = off;
                         part.end = w.end(w.r);
                         part.rows = rows;
@@ -524,68 +524,13 @@ tile_kernel(TileParams p, int lg) {
                             else if (!whole) p.ws_dir[c] = make_int4(cnt, w.s, w.h, w.r);
                         }
                     }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    part.stages = n;
                     mbar_arrive(smem_addr(&ms->part_ready[seg & 3]));
                 }
                 if (n == 0) break;
-                // the tile's queries: high and low parts of code * scale, in units of a power of two per row
-                if (!wait_warp(&ms->q_free, (seg & 1) ^ 1, ms, p.dev_status)) break;
-                int least = 0x7fffffff;
-                for (int i = (warp - 2) * 32 + lane; i < kRows; i += 64) {
-                    int lim = 0x7fffffff;
-                    if (i < rows) {
-                        bool bad;
-                        lim = w.limit(w.r, i, bad);
-                        if (bad) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
-                    }
-                    ms->lim[seg & 3][i] = lim;
-                    least = min(least, lim);
-                }
-                least = __reduce_min_sync(0xffffffffu, least);
-                if (lane == 0) ms->lim_min[seg & 3][warp - 2] = least;
-#pragma unroll 1
-                for (int i0 = warp - 2; i0 < kRows; i0 += 2 * kQBatch) {
-                    // lane l: dims 4l .. 4l + 3, a 32-block is eight lanes; the rule of quantize_q_vals_warp
-                    float4 xs[kQBatch];
-#pragma unroll
-                    for (int k = 0; k < kQBatch; ++k) {
-                        const int i = i0 + 2 * k;
-                        xs[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (i < rows) xs[k] = load4(p.q, p.q_dtype, w.token(w.r, i) * p.q_stride + (int64_t)w.head(i) * kHD + 4 * lane);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kQBatch; ++k) {
-                        const int i = i0 + 2 * k;
-                        float4 x = xs[k];
-                        uint32_t m = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
-                                         max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
-#pragma unroll
-                        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if (m >= 0x7f800000u) {
-                            x = make_float4(0.f, 0.f, 0.f, 0.f);
-                            m = 0;
-                            flag_status(p.dev_status, KVQ8_DEV_NONFINITE);
-                        }
-                        float qm = __uint_as_float(m);
-                        if (qm < 1e-6f) qm = 1.0f;
-                        const float iq = __fdiv_rn(127.0f, qm), qs = __fmul_rn(qm, KVQ8_INV127);
-                        auto value = [&](float v) { return __fmul_rn((float)max(-128, min(127, __float2int_rn(__fmul_rn(v, iq)))), qs); };
-                        x = make_float4(value(x.x), value(x.y), value(x.z), value(x.w));
-                        // exponent of the row's largest value: the row is scaled to below 2^11
-                        int e = max(max(__float_as_int(x.x) & 0x7fffffff, __float_as_int(x.y) & 0x7fffffff),
-                                    max(__float_as_int(x.z) & 0x7fffffff, __float_as_int(x.w) & 0x7fffffff));
-                        e = max(-100, (__reduce_max_sync(0xffffffffu, e) >> 23) - 127 - 10);
-                        const float down = exp2_int(-e);
-                        x = make_float4(x.x * down, x.y * down, x.z * down, x.w * down);
-                        const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
-                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                        put(i, h0, h1);
-                        put(i + kRows, __floats2half2_rn(x.x - f0.x, x.y - f0.y), __floats2half2_rn(x.z - f1.x, x.w - f1.y));
-                        if (lane == 0) ms->gain[seg & 3][i] = exp2_int(e);
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ms->q_ready[seg & 1]));
                 left -= n;
                 off = 0;
                 if (left > 0) w.next(seqs);
@@ -622,7 +567,7 @@ tile_kernel(TileParams p, int lg) {
                 wait_warp(&ms->k_free[j & 1], par ^ 1, ms, p.dev_status);
                 tc_fence_after();
                 const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < 4; ++k)
                     put_codes(lanes + kColK + (j & 1) * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
                 tmem_wait_st();
@@ -674,17 +619,94 @@ tile_kernel(TileParams p, int lg) {
         const int row = 32 * quad + lane;     // token of the stage (scores), dim (output)
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         unsigned char *prow = smem + L::oP + (c0 >> 3) * kCoreRow + row * 16;
-        int j = 0;
-#pragma unroll 1
-        for (int seg = 0;; ++seg) {
+        // Tile seg's queries: high and low parts of code * scale, in units of a power of two per row.  False when
+        // there is no such tile (or a wait gave up: the four warps of a share go by one answer, or a barrier
+        // would wait for the one that left).
+        auto queries = [&](int seg) {
             const bool ok = wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status);
-            // (the four warps stop together, or a barrier would wait for the one that left)
-            if (barrier_any(bar, 128, !ok)) break;
+            if (barrier_any(bar, 128, !ok)) return false;
+            const Part &part = ms->part[seg & 3];
+            if (part.stages == 0) return false;
+            if (warp - 8 < kRows / 8) {
+                // eight rows to a warp: lane l has row l % 8, and of every 32-block the dims 8 (l / 8) .. + 7, a
+                // 16-byte line of an operand's core, so that eight lanes fill a core
+                const int i = (warp - 8) * 8 + (lane & 7);
+                float4 x[8];
+                const bool real = i < part.rows;
+                const int64_t src = real ? ((long long)part.token + (i >> lg)) * p.q_stride +
+                                               (int64_t)((part.head << lg) + (i & ((1 << lg) - 1))) * kHD + 8 * (lane >> 3)
+                                         : 0;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (real) x[b] = load4(p.q, p.q_dtype, src + 32 * (b >> 1) + 4 * (b & 1));
+                }
+                // the rule of quantize_q_vals_warp; |x| as bits orders as |x| does, a NaN or infinity above all
+                float top[4];
+                float most = 0.0f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 y = x[2 * b + k];
+                        m = max(max(m, max(__float_as_uint(y.x) & 0x7fffffffu, __float_as_uint(y.y) & 0x7fffffffu)),
+                                max(__float_as_uint(y.z) & 0x7fffffffu, __float_as_uint(y.w) & 0x7fffffffu));
+                    }
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m >= 0x7f800000u) {
+                        x[2 * b] = x[2 * b + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        m = 0;
+                        flag_status(p.dev_status, KVQ8_DEV_NONFINITE);
+                    }
+                    top[b] = __uint_as_float(m);
+                    if (top[b] < 1e-6f) top[b] = 1.0f;   // (codes 0)
+                    else most = fmaxf(most, top[b]);
+                }
+                // a row's values lie below 2^11 in units of 2^e
+                const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
+                const float down = exp2_int(-e);
+                wait_warp(&ms->q_free, (seg & 1) ^ 1, ms, p.dev_status);
+                unsigned char *at = smem + L::oQ + (warp - 8) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float iq = __fdiv_rn(127.0f, top[b]), unit = __fmul_rn(top[b], KVQ8_INV127) * down;
+                    const float2 unit2 = make_float2(unit, unit);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 y = x[2 * b + (k >> 1)];
+                        // round_half_even(fl(x * iq)) by a sum whose spacing is 1; |x * iq| < 127.5, so no clamp.
+                        // (The product apart: a packed product and the packed sum behind it are made one
+                        // operation of one rounding, which moves a code now and then)
+                        float2 v = k & 1 ? make_float2(__fmul_rn(y.z, iq), __fmul_rn(y.w, iq))
+                                         : make_float2(__fmul_rn(y.x, iq), __fmul_rn(y.y, iq));
+                        v = add2(add2(v, make_float2(0x1.8p23f, 0x1.8p23f)), make_float2(-0x1.8p23f, -0x1.8p23f));
+                        v = mul2(v, unit2);
+                        const __half2 h = __floats2half2_rn(v.x, v.y);
+                        hi[k] = half2_bits(h);
+                        v = fma2(__half22float2(h), make_float2(-1.f, -1.f), v);
+                        lo[k] = half2_bits(__floats2half2_rn(v.x, v.y));
+                    }
+                    *reinterpret_cast<uint4 *>(at + b * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + b * 512 + kRows / 8 * kCoreRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (lane < 8) ms->gain[seg & 3][i] = exp2_int(e);
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ms->q_ready));
+            return true;
+        };
+        int j = 0;
+        bool more = queries(0);
+#pragma unroll 1
+        for (int seg = 0; more; ++seg) {
             const int n = ms->part[seg & 3].stages;
-            if (n == 0) break;
-            wait_warp(&ms->q_ready[seg & 1], (seg >> 1) & 1, ms, p.dev_status);
+            wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
             if (st < kCols) ms->ref[c0 + st] = 0.0f;
-            const int lim_min = min(ms->lim_min[seg & 3][0], ms->lim_min[seg & 3][1]);
+            const int lim_min = ms->lim_min[seg & 3];
             const float *gain = ms->gain[seg & 3] + c0;
             named_barrier_sync(bar, 128);
             float sum[kCols];
@@ -761,13 +783,15 @@ tile_kernel(TileParams p, int lg) {
                     // move the references of rows whose P would leave fp16's range (at first: of all), by whole
                     // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
                     // stage of one leaves the rows fresh
-                    int mine = 0;
+                    float u[kCols / 2];
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k) {
-                        const int m = __reduce_max_sync(0xffffffffu, ordered(__float_as_int(t[k] + vs_log2)));
-                        if (lane == k) mine = m;
+                    for (int k = 0; k < kCols / 2; ++k) {
+                        const bool up = lane & 16;
+                        const float give = up ? t[k] : t[k + kCols / 2], keep = up ? t[k + kCols / 2] : t[k];
+                        u[k] = fmaxf(keep + vs_log2, __shfl_xor_sync(0xffffffffu, give + vs_log2, 16));
                     }
-                    if (lane < kCols) ms->wave[quad][c0 + lane] = __int_as_float(ordered(mine));
+                    halve<kCols / 4, 8>(u, lane, [](float a, float b) { return fmaxf(a, b); });
+                    ms->wave[quad][c0 + lane / (32 / kCols)] = u[0];
                     named_barrier_sync(bar, 128);
                     if (st < kCols) {
                         const int x = c0 + st;
@@ -839,21 +863,8 @@ tile_kernel(TileParams p, int lg) {
                 if (lane == 0) mbar_arrive(smem_addr(&ms->p_ready));
             }
             // ---- the tile's end: row sums over the tokens, then the output or a record ----
-            // (each step adds the halves of the rows that a lane keeps and gives away; the last ones, with one row
-            // left, add the lanes of that row)
-#pragma unroll
-            for (int o = 16, cnt = kCols / 2; o > 0; o >>= 1, cnt >>= 1) {
-                if (cnt > 0) {
-#pragma unroll
-                    for (int k = 0; k < cnt; ++k) {
-                        const bool up = lane & o;
-                        const float give = up ? sum[k] : sum[k + cnt], keep = up ? sum[k + cnt] : sum[k];
-                        sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                    }
-                } else {
-                    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-                }
-            }
+            halve<kCols / 2, 16>(sum, lane, [](float a, float b) { return a + b; });
+            more = queries(seg + 1);   // (while the last product runs)
             const Part &part = ms->part[seg & 3];
             const bool direct = part.direct != 0;
             ms->wave[quad][c0 + lane / (32 / kCols)] = sum[0];   // the row that this lane ended with
@@ -862,13 +873,14 @@ tile_kernel(TileParams p, int lg) {
                 const int x = c0 + st;
                 const float S = ms->wave[0][x] + ms->wave[1][x] + ms->wave[2][x] + ms->wave[3][x];
                 ms->shift[x] = direct ? (S > 0.0f ? 1.0f / S : 0.0f) : 1.0f;
-                long long dst = -1;
+                char *dst = nullptr;
                 if (x < part.rows) {
                     if (direct) {
-                        dst = ((long long)part.token + (x >> lg)) * p.out_stride +
-                              (long long)((part.head << lg) + (x & ((1 << lg) - 1))) * kHD;
+                        dst = static_cast<char *>(p.out) + (p.out_dtype == KVQ8_DTYPE_F32 ? 4 : 2) *
+                                  (((long long)part.token + (x >> lg)) * p.out_stride +
+                                   (long long)((part.head << lg) + (x & ((1 << lg) - 1))) * kHD);
                     } else {
-                        dst = (part.rec + x) * kHD;
+                        dst = reinterpret_cast<char *>(p.ws_acc + (part.rec + x) * kHD);
                         *reinterpret_cast<float2 *>(p.ws_ml + (part.rec + x) * 2) = make_float2(-ms->ref[x], S);
                     }
                 }
@@ -877,7 +889,6 @@ tile_kernel(TileParams p, int lg) {
             named_barrier_sync(bar, 128);
             wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
             tc_fence_after();
-            void *to = direct ? p.out : p.ws_acc;
             const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
 #pragma unroll 1
             for (int k = 0; k < kCols; k += 8) {
@@ -892,17 +903,26 @@ tile_kernel(TileParams p, int lg) {
                         asm volatile("" : "+f"(y[q]));
                         x[q] += y[q];
                     }
-                    const long long dst = ms->dst[c0 + k + q];
-                    const float v = x[q] * ms->shift[c0 + k + q];
-                    if (dst >= 0) {
-                        if (type == KVQ8_DTYPE_F32) static_cast<float *>(to)[dst + row] = v;
-                        else store1(to, type, dst + row, v);
+                    x[q] *= ms->shift[c0 + k + q];
+                }
+                if (type == KVQ8_DTYPE_F32) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (char *dst = ms->dst[c0 + k + q]) reinterpret_cast<float *>(dst)[row] = x[q];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint16_t v = !kLow ? __bfloat16_as_ushort(__float2bfloat16_rn(x[q])) : __half_as_ushort(__float2half_rn(x[q]));
+                        if (char *dst = ms->dst[c0 + k + q]) reinterpret_cast<uint16_t *>(dst)[row] = v;
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ms->o_free));
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&ms->o_free));
+                mbar_arrive(smem_addr(&ms->part_free[seg & 3]));
+            }
         }
     }
     tc_fence_before();
