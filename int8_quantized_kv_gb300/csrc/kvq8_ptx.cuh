@@ -190,7 +190,7 @@ __device__ __forceinline__ uint64_t core_desc(uint32_t addr, uint32_t k_bytes, u
 
 // Instruction word of a 128 x n MMA of fp16 operands with fp32 accumulators; A
 // is contraction-major, B too or (n_major) not.
-__device__ __forceinline__ uint32_t mma_word(int n, bool n_major) {
+__host__ __device__ constexpr uint32_t mma_word(int n, bool n_major) {
     return 1u << 4 | (n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
@@ -224,11 +224,22 @@ __device__ __forceinline__ void mma_commit(uint32_t bar, bool lead) {
 __device__ __forceinline__ void tmem_ld8(uint32_t addr, float *r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : KVQ8_R8(r) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : KVQ8_R8(r), KVQ8_R8(r + 8)
-        : "r"(addr));
+// Sixteen lanes (from addr's lane on) x 8 * kGroups columns as MMA fragments: of column group g, r[4g], r[4g + 1] are
+// lane t / 4, columns 8g + 2 (t % 4), + 1 for thread t, and r[4g + 2], r[4g + 3] the same of lane t / 4 + 8.
+template <int kGroups>
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t addr, float *r) {
+    if constexpr (kGroups == 4) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : KVQ8_R8(r), KVQ8_R8(r + 8)
+            : "r"(addr));
+    } else if constexpr (kGroups == 2) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : KVQ8_R8(r) : "r"(addr));
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                     : "r"(addr));
+    }
 }
 #undef KVQ8_R8
 
@@ -244,6 +255,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// Four 8 x 8 matrices of halves, each given as MMA fragments, to rows of 16 bytes; lane l says where row l % 8 of matrix
+// l / 8 goes.
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 
 // Shared-memory writes of this thread become visible to the async proxy (MMA operands).

@@ -11,16 +11,14 @@
 
 namespace kvq8 {
 
-// Four consecutive values of a row of `dtype` from element i (a multiple of 4).
-__device__ __forceinline__ float4 load4(const void *base, int dtype, int64_t i) {
-    if (dtype == KVQ8_DTYPE_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i);
-    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + i);
+// The four bf16 (or fp16) values in two words.
+__device__ __forceinline__ float4 widen(uint32_t a, uint32_t b, int dtype) {
     if (dtype == KVQ8_DTYPE_BF16)
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+        return make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+                           __uint_as_float(b & 0xffff0000u));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    return make_float4(x.x, x.y, y.x, y.y);
 }
 
 __device__ __forceinline__ void store1(void *base, int dtype, int64_t i, float x) {

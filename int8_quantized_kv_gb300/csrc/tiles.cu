@@ -23,8 +23,8 @@
 // the output's own rounding.
 //
 // A persistent CTA per SM takes an equal share of the (tile, 128-token stage)
-// sequence.  Warp 0 copies the stages (bulk copies into a ring), warp 1 issues
-// the MMAs, warps 4..7 turn the codes into operands and, per tile, the queries,
+// sequence.  Warp 0 copies the stages (bulk copies into a ring), warps 1 and 3 issue
+// the MMAs of scores and output, warp 2 says which tiles, warps 4..7 turn the codes into operands and, per tile, the queries,
 // warps 8..15 take the softmax: the score tile is S^T, so a thread holds one
 // token of half the tile's rows, whose row sums it keeps for itself until the
 // tile ends.  A row's weights 2^(s - M) need no exact maximum: M is set so that
@@ -87,7 +87,7 @@ struct Misc {
     uint64_t full[8], empty[8];                 // ring slots
     uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2], sc_ready[4];
     uint64_t part_ready[4], part_free[4];
-    uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done;
+    uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done[2];
     long long warp_tot[kThreads / 32];
     int s0, r0, off;
     volatile int abort;
@@ -224,12 +224,12 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 x) { return *reinterpret_
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
 
-// Combines 2 * kCount values per lane over the warp: each step combines the half of the values that a lane keeps with
-// the other lane's, from lanes kLanes apart on, then (one value left) all lanes of that value.  Lane l ends with value
-// l / (32 / count) of `count` values that the first step (16 lanes apart) began with.
+// Combines 2 * kCount values per lane over the lanes that differ in the bits from kLanes down to 4: each step combines
+// the half of the values that a lane keeps with the other lane's, then (one value left) the lanes that share it.  Of
+// `count` values that the first step (16 lanes apart) began with, lane l ends with value l / (32 / count).
 template <int kCount, int kLanes, typename Op>
 __device__ __forceinline__ void halve(float *v, int lane, Op op) {
-    if constexpr (kLanes > 0) {
+    if constexpr (kLanes >= 4) {
         if constexpr (kCount > 0) {
 #pragma unroll
             for (int k = 0; k < kCount; ++k) {
@@ -303,7 +303,8 @@ tile_kernel(TileParams p, int lg) {
         mbar_init(smem_addr(&ms->q_ready), kSoftmaxWarps);
         mbar_init(smem_addr(&ms->q_free), 1);
         mbar_init(smem_addr(&ms->o_free), kSoftmaxWarps);
-        mbar_init(smem_addr(&ms->all_done), 1);
+        mbar_init(smem_addr(&ms->all_done[0]), 1);
+        mbar_init(smem_addr(&ms->all_done[1]), 1);
         fence_mbar_init();
         ms->abort = 0;
     }
@@ -438,49 +439,51 @@ tile_kernel(TileParams p, int lg) {
                     mbar_wait_bounded(smem_addr(&ms->full[k % L::kSlots]), (k / L::kSlots) & 1, kLimitNs);
             }
             __syncwarp();
-        } else if (warp == 1) {
+        } else if (warp != 2) {
             // ============================= MMAs =============================
-            const bool lead = lane == 0;
-            const uint64_t q_hi = core_desc(smem_addr(smem + L::oQ), 128, kCoreRow);
-            const uint64_t p_hi = core_desc(smem_addr(smem + L::oP), 128, kCoreRow);
+            // warp 1: scores, warp 3: output (a warp for both leaves the tensor cores waiting for its own waits)
+            const bool lead = lane == 0, scores = warp == 1;
+            const uint64_t b = core_desc(smem_addr(smem + (scores ? L::oQ : L::oP)), 128, kCoreRow);
             constexpr uint64_t kLowPart = kRows / 8 * kCoreRow / 16;
-            const uint32_t word_q = mma_word(kWide ? kRows : 2 * kRows, false);
-            const uint32_t word_p = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
             int x = 0;   // stages so far
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
                 if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
                 const int n = ms->part[seg & 3].stages;
                 if (n == 0) break;
-                wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
+                if (scores) {
+                    wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
 #pragma unroll 1
-                for (int i = 0; i <= n; ++i, ++x) {
-                    if (i < n) {
+                    for (int i = 0; i < n; ++i, ++x) {
+                        constexpr uint32_t kWord = mma_word(kWide ? kRows : 2 * kRows, false);
                         wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
                         wait_warp(&ms->s_free, (x & 1) ^ 1, ms, p.dev_status);
                         tc_fence_after();
-                        mma_k128(kColS, kColK + (x & 1) * 64, q_hi, word_q, false, lead);
-                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, q_hi + kLowPart, word_q, true, lead);
+                        mma_k128(kColS, kColK + (x & 1) * 64, b, kWord, false, lead);
+                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, b + kLowPart, kWord, true, lead);
                         mma_commit(smem_addr(&ms->s_full), lead);
                         mma_commit(smem_addr(&ms->k_free[x & 1]), lead);
-                        if (i == n - 1) mma_commit(smem_addr(&ms->q_free), lead);
                     }
-                    if (i > 0) {
-                        const int y = x - 1;
-                        wait_warp(&ms->v_ready[y & 1], (y >> 1) & 1, ms, p.dev_status);
-                        if (i == 1) wait_warp(&ms->o_free, (seg & 1) ^ 1, ms, p.dev_status);
-                        wait_warp(&ms->p_ready, y & 1, ms, p.dev_status);
+                    mma_commit(smem_addr(&ms->q_free), lead);
+                } else {
+                    wait_warp(&ms->o_free, (seg & 1) ^ 1, ms, p.dev_status);
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i, ++x) {
+                        constexpr uint32_t kWord = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
+                        wait_warp(&ms->v_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
+                        wait_warp(&ms->p_ready, x & 1, ms, p.dev_status);
                         tc_fence_after();
-                        mma_k128(kColO, kColV + (y & 1) * 64, p_hi, word_p, i > 1, lead);
-                        if (kWide && kLow) mma_k128(kColO, kColV + (y & 1) * 64, p_hi + kLowPart, word_p, true, lead);
+                        mma_k128(kColO, kColV + (x & 1) * 64, b, kWord, i > 0, lead);
+                        if (kWide && kLow) mma_k128(kColO, kColV + (x & 1) * 64, b + kLowPart, kWord, true, lead);
                         mma_commit(smem_addr(&ms->pv_done), lead);
-                        mma_commit(smem_addr(&ms->v_free[y & 1]), lead);
+                        mma_commit(smem_addr(&ms->v_free[x & 1]), lead);
                     }
                 }
-                --x;   // (n + 1 rounds)
             }
-            mma_commit(smem_addr(&ms->all_done), lead);
-            mbar_wait_bounded(smem_addr(&ms->all_done), 0, kLimitNs);
+            // none may still run when the CTA gives its tensor memory back
+            uint64_t *done = &ms->all_done[scores ? 0 : 1];
+            mma_commit(smem_addr(done), lead);
+            mbar_wait_bounded(smem_addr(done), 0, kLimitNs);
             __syncwarp();
         } else if (warp == 2) {
             // ======================= the tiles' order =======================
@@ -616,9 +619,16 @@ tile_kernel(TileParams p, int lg) {
         // the four warps of a share of the rows see to it by themselves
         const int quad = warp & 3, share = (warp - 8) >> 2, c0 = share * kCols, st = tid & 127;
         const int bar = 1 + share;
-        const int row = 32 * quad + lane;     // token of the stage (scores), dim (output)
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        unsigned char *prow = smem + L::oP + (c0 >> 3) * kCoreRow + row * 16;
+        // Scores and P are held as MMA fragments: a thread has the tokens 32 quad + 8 m + lane / 4 (m < 4) of the
+        // stage and the rows c0 + 8 g + 2 (lane % 4) + {0, 1} (g < kGroups) of the tile, so that what concerns a
+        // row stays in registers (with a token per thread each row's reference and gain come from shared memory
+        // for every stage, which keeps the MMAs' operands waiting) and P's cores are stored as matrices.
+        constexpr int kGroups = kCols / 8, kVals = 2 * kGroups;
+        const int col = c0 + 2 * (lane & 3);                                      // + 8 g
+        const int folded = lane / (32 / kVals);                                   // of kVals values, halve() leaves this one
+        const int folded_row = c0 + 8 * (folded >> 1) + 2 * (lane & 3) + (folded & 1);
+        const uint32_t pout = smem_addr(smem + L::oP) + (c0 >> 3) * kCoreRow + quad * 512 + lane * 16;
         // Tile seg's queries: high and low parts of code * scale, in units of a power of two per row.  False when
         // there is no such tile (or a wait gave up: the four warps of a share go by one answer, or a barrier
         // would wait for the one that left).
@@ -636,10 +646,24 @@ tile_kernel(TileParams p, int lg) {
                 const int64_t src = real ? ((long long)part.token + (i >> lg)) * p.q_stride +
                                                (int64_t)((part.head << lg) + (i & ((1 << lg) - 1))) * kHD + 8 * (lane >> 3)
                                          : 0;
+                // (one test of the type around all loads: with a test in each they wait for one another)
+                if (!real) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (real) x[b] = load4(p.q, p.q_dtype, src + 32 * (b >> 1) + 4 * (b & 1));
+                    for (int b = 0; b < 8; ++b) x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                } else if (p.q_dtype == KVQ8_DTYPE_F32) {
+                    const float *row = static_cast<const float *>(p.q) + src;
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) x[b] = *reinterpret_cast<const float4 *>(row + 32 * (b >> 1) + 4 * (b & 1));
+                } else {
+                    const uint16_t *row = static_cast<const uint16_t *>(p.q) + src;
+                    uint4 y[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) y[b] = *reinterpret_cast<const uint4 *>(row + 32 * b);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        x[2 * b] = widen(y[b].x, y[b].y, p.q_dtype);
+                        x[2 * b + 1] = widen(y[b].z, y[b].w, p.q_dtype);
+                    }
                 }
                 // the rule of quantize_q_vals_warp; |x| as bits orders as |x| does, a NaN or infinity above all
                 float top[4];
@@ -707,91 +731,91 @@ tile_kernel(TileParams p, int lg) {
             wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
             if (st < kCols) ms->ref[c0 + st] = 0.0f;
             const int lim_min = ms->lim_min[seg & 3];
-            const float *gain = ms->gain[seg & 3] + c0;
             named_barrier_sync(bar, 128);
-            float sum[kCols];
+            float2 ref[kGroups], sum[kGroups];
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) sum[k] = 0.0f;
+            for (int g = 0; g < kGroups; ++g) ref[g] = sum[g] = make_float2(0.0f, 0.0f);
             bool fresh = true;   // no row has a reference yet
             int t0 = ms->part[seg & 3].off * kTok;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
                 wait_warp(&ms->sc_ready[j & 3], (j >> 2) & 1, ms, p.dev_status);
-                const float2 sc = ms->scale[j & 3][row];
+                float2 sc[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) sc[m] = ms->scale[j & 3][32 * quad + 8 * m + (lane >> 2)];
                 const bool bad = ms->bad[j & 3] != 0;
                 wait_warp(&ms->s_full, j & 1, ms, p.dev_status);
                 tc_fence_after();
-                // scores of this thread's token, relative to the references
-                float t[kCols];
+                // scores relative to the references: [pair of matrices][group][matrix of the pair][row of two]
+                float t[2][kGroups][2][2];
+                tmem_ld_fragments<kGroups>(lanes + kColS + c0, &t[0][0][0][0]);
+                tmem_ld_fragments<kGroups>(lanes + (16u << 16) + kColS + c0, &t[1][0][0][0]);
                 if constexpr (kWide) {
-                    tmem_ld16(lanes + kColS + c0, t);
-                    tmem_ld16(lanes + kColS + c0 + 16, t + 16);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k) asm volatile("" : "+f"(t[k]));
+                    for (int k = 0; k < kVals * 4; ++k) asm volatile("" : "+f"((&t[0][0][0][0])[k]));
                 } else {
-                    float low[kCols];
-                    if constexpr (kCols == 16) {
-                        tmem_ld16(lanes + kColS + c0, t);
-                        tmem_ld16(lanes + kColS + kRows + c0, low);
-                    } else {
-                        tmem_ld8(lanes + kColS + c0, t);
-                        tmem_ld8(lanes + kColS + kRows + c0, low);
-                    }
+                    float low[kVals * 4];
+                    tmem_ld_fragments<kGroups>(lanes + kColS + kRows + c0, low);
+                    tmem_ld_fragments<kGroups>(lanes + (16u << 16) + kColS + kRows + c0, low + kVals * 2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k) {
-                        asm volatile("" : "+f"(t[k]), "+f"(low[k]));
-                        t[k] += low[k];
+                    for (int k = 0; k < kVals * 4; ++k) {
+                        asm volatile("" : "+f"((&t[0][0][0][0])[k]), "+f"(low[k]));
+                        (&t[0][0][0][0])[k] += low[k];
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ms->s_free));
-                float top = -INFINITY;
-                {
-                    const float2 ks = make_float2(sc.x, sc.x);
 #pragma unroll
-                    for (int q = 0; q < kCols; q += 4) {
-                        const float4 g = *reinterpret_cast<const float4 *>(gain + q);
-                        const float4 m = *reinterpret_cast<const float4 *>(ms->ref + c0 + q);
-                        const float2 a = fma2(mul2(make_float2(t[q], t[q + 1]), ks), make_float2(g.x, g.y), make_float2(m.x, m.y));
-                        const float2 b = fma2(mul2(make_float2(t[q + 2], t[q + 3]), ks), make_float2(g.z, g.w), make_float2(m.z, m.w));
-                        t[q] = a.x;
-                        t[q + 1] = a.y;
-                        t[q + 2] = b.x;
-                        t[q + 3] = b.y;
+                for (int g = 0; g < kGroups; ++g) {
+                    const float2 gain = *reinterpret_cast<const float2 *>(&ms->gain[seg & 3][col + 8 * g]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        float *x = t[m >> 1][g][m & 1];
+                        const float2 y = fma2(mul2(make_float2(x[0], x[1]), make_float2(sc[m].x, sc[m].x)), gain, ref[g]);
+                        x[0] = y.x;
+                        x[1] = y.y;
                     }
                 }
                 if (bad || t0 + kTok > lim_min) {   // some row does not see all of the stage
-                    const int tok = bad ? 0x7fffffff : t0 + row;
 #pragma unroll
-                    for (int q = 0; q < kCols; q += 4) {
-                        const int4 f = *reinterpret_cast<const int4 *>(ms->lim[seg & 3] + c0 + q);
-                        t[q] = tok >= f.x ? -INFINITY : t[q];
-                        t[q + 1] = tok >= f.y ? -INFINITY : t[q + 1];
-                        t[q + 2] = tok >= f.z ? -INFINITY : t[q + 2];
-                        t[q + 3] = tok >= f.w ? -INFINITY : t[q + 3];
+                    for (int g = 0; g < kGroups; ++g) {
+                        const int2 lim = *reinterpret_cast<const int2 *>(&ms->lim[seg & 3][col + 8 * g]);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int tok = bad ? 0x7fffffff : t0 + 32 * quad + 8 * m + (lane >> 2);
+                            float *x = t[m >> 1][g][m & 1];
+                            if (tok >= lim.x) x[0] = -INFINITY;
+                            if (tok >= lim.y) x[1] = -INFINITY;
+                        }
                     }
                 }
+                bool raise = fresh;
+                float vs_log2[4];
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) top = fmaxf(top, t[k]);
-                const float vs_log2 = fmaxf(__log2f(sc.y), kTinyScaleLog2);
-                // the product before this one is done: P's room is free, the accumulator at rest
-                if (i > 0) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
-                if (barrier_any(bar, 128, fresh || top > kPMaxLog2 - vs_log2)) {
+                for (int m = 0; m < 4; ++m) {
+                    vs_log2[m] = fmaxf(__log2f(sc[m].y), kTinyScaleLog2);
+                    float top = fmaxf(t[m >> 1][0][m & 1][0], t[m >> 1][0][m & 1][1]);
+#pragma unroll
+                    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, fmaxf(t[m >> 1][g][m & 1][0], t[m >> 1][g][m & 1][1]));
+                    raise |= top > kPMaxLog2 - vs_log2[m];
+                }
+                bool rest = i == 0;   // the product before is done: P's room is free, the accumulator at rest
+                if (barrier_any(bar, 128, raise)) {
                     // move the references of rows whose P would leave fp16's range (at first: of all), by whole
                     // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
                     // stage of one leaves the rows fresh
-                    float u[kCols / 2];
+                    float top[kVals];
 #pragma unroll
-                    for (int k = 0; k < kCols / 2; ++k) {
-                        const bool up = lane & 16;
-                        const float give = up ? t[k] : t[k + kCols / 2], keep = up ? t[k + kCols / 2] : t[k];
-                        u[k] = fmaxf(keep + vs_log2, __shfl_xor_sync(0xffffffffu, give + vs_log2, 16));
-                    }
-                    halve<kCols / 4, 8>(u, lane, [](float a, float b) { return fmaxf(a, b); });
-                    ms->wave[quad][c0 + lane / (32 / kCols)] = u[0];
+                    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            top[2 * g + k] = fmaxf(fmaxf(t[0][g][0][k] + vs_log2[0], t[0][g][1][k] + vs_log2[1]),
+                                                   fmaxf(t[1][g][0][k] + vs_log2[2], t[1][g][1][k] + vs_log2[3]));
+                    halve<kVals / 2, 16>(top, lane, [](float a, float b) { return fmaxf(a, b); });
+                    ms->wave[quad][folded_row] = top[0];
                     named_barrier_sync(bar, 128);
                     if (st < kCols) {
                         const int x = c0 + st;
@@ -802,8 +826,10 @@ tile_kernel(TileParams p, int lg) {
                         ms->shift[x] = by;
                     }
                     named_barrier_sync(bar, 128);
-                    if (i > 0 && !fresh) {
+                    if (!rest && !fresh) {
+                        wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
                         tc_fence_after();
+                        rest = true;
 #pragma unroll 1
                         for (int x = 0; x < (!kWide && kLow ? 2 : 1); ++x) {
 #pragma unroll 1
@@ -824,38 +850,43 @@ tile_kernel(TileParams p, int lg) {
                         tmem_wait_st();
                     }
 #pragma unroll
-                    for (int k = 0; k < kCols; ++k) {
-                        const float by = ms->shift[c0 + k];
-                        t[k] += by;
-                        if (!fresh) sum[k] *= ex2_approx(by);
+                    for (int g = 0; g < kGroups; ++g) {
+                        const float2 by = *reinterpret_cast<const float2 *>(&ms->shift[col + 8 * g]);
+                        ref[g] = add2(ref[g], by);
+                        if (!fresh) sum[g] = mul2(sum[g], make_float2(ex2_approx(by.x), ex2_approx(by.y)));
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            t[m >> 1][g][m & 1][0] += by.x;
+                            t[m >> 1][g][m & 1][1] += by.y;
+                        }
                     }
                     fresh = fresh && bad;
                 }
-                // weights, and P = weight * V scale in high and low parts
-                {
-                    const float2 vs = make_float2(sc.y, sc.y);
+                // weights, and P = weight * V scale in high and low parts, kept until the product before is done
+                // (which this overlaps)
+                uint32_t hi[kGroups][4], lo[kGroups][4];
 #pragma unroll
-                    for (int k = 0; k < kCols; k += 8) {
-                        uint32_t hi[4], lo[4];
+                for (int m = 0; m < 4; ++m) {
+                    const float2 vs = make_float2(sc[m].y, sc[m].y);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int x = k + 2 * q;
-                            const float2 e = make_float2(ex2_approx(t[x]), ex2_approx(t[x + 1]));
-                            const float2 s2 = add2(make_float2(sum[x], sum[x + 1]), e);
-                            sum[x] = s2.x;
-                            sum[x + 1] = s2.y;
-                            const float2 v = mul2(e, vs);
-                            const __half2 a = __floats2half2_rn(v.x, v.y);
-                            hi[q] = half2_bits(a);
-                            if (kLow) {
-                                const float2 d = fma2(__half22float2(a), make_float2(-1.f, -1.f), v);
-                                lo[q] = half2_bits(__floats2half2_rn(d.x, d.y));
-                            }
+                    for (int g = 0; g < kGroups; ++g) {
+                        const float *x = t[m >> 1][g][m & 1];
+                        const float2 e = make_float2(ex2_approx(x[0]), ex2_approx(x[1]));
+                        sum[g] = add2(sum[g], e);
+                        const float2 v = mul2(e, vs);
+                        const __half2 a = __floats2half2_rn(v.x, v.y);
+                        hi[g][m] = half2_bits(a);
+                        if (kLow) {
+                            const float2 d = fma2(__half22float2(a), make_float2(-1.f, -1.f), v);
+                            lo[g][m] = half2_bits(__floats2half2_rn(d.x, d.y));
                         }
-                        *reinterpret_cast<uint4 *>(prow + (k >> 3) * kCoreRow) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if (kLow)
-                            *reinterpret_cast<uint4 *>(prow + ((k + kRows) >> 3) * kCoreRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
+                }
+                if (!rest) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    store_matrices(pout + g * kCoreRow, hi[g][0], hi[g][1], hi[g][2], hi[g][3]);
+                    if (kLow) store_matrices(pout + (g + kRows / 8) * kCoreRow, lo[g][0], lo[g][1], lo[g][2], lo[g][3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -863,11 +894,12 @@ tile_kernel(TileParams p, int lg) {
                 if (lane == 0) mbar_arrive(smem_addr(&ms->p_ready));
             }
             // ---- the tile's end: row sums over the tokens, then the output or a record ----
-            halve<kCols / 2, 16>(sum, lane, [](float a, float b) { return a + b; });
+            halve<kVals / 2, 16>(&sum[0].x, lane, [](float a, float b) { return a + b; });
+            ms->wave[quad][folded_row] = sum[0].x;
             more = queries(seg + 1);   // (while the last product runs)
             const Part &part = ms->part[seg & 3];
             const bool direct = part.direct != 0;
-            ms->wave[quad][c0 + lane / (32 / kCols)] = sum[0];   // the row that this lane ended with
+            const int row = 32 * quad + lane;   // dim
             named_barrier_sync(bar, 128);
             if (st < kCols) {
                 const int x = c0 + st;
