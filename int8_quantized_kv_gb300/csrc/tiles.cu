@@ -47,15 +47,14 @@ constexpr int kThreads = 256 + kSoftmaxThreads;
 constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
 constexpr int kCoreRow = 2048;                  // bytes between cores along the rows (16 cores of 128 B along k)
-constexpr uint64_t kLimitNs = 2000000000ull;      // bounds of the waits: two seconds
-constexpr long long kLimitTicks = 4000000000ll;
+constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end: two seconds
 // A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^8 and 2^9 when M is set; M moves
 // when P would pass 2^15.9 (fp16 ends below 2^16).
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
 constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this when M is set (rows of zeros do)
 // Registers per thread: what the launch holds, and what the warpgroups (copies, MMAs and queries; operands; four of
 // softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory leaves it no L1.
-constexpr int kLaunchRegs = 80, kRegsIssue = 64, kRegsOperand = 64, kRegsSoftmax = 88;
+constexpr int kLaunchRegs = 80, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
 static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs, "registers");
 // columns of tensor memory, all of which is the CTA's (so that it begins at address 0)
 constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = 384;
@@ -106,28 +105,22 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 13312, "misc");
 
-// Bounded like every wait here, by clock ticks.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *ms, uint32_t *status) {
+// Bounded like every wait here: a try sleeps up to two microseconds, and after 2^20 of them (two seconds at most) the
+// CTA gives up, its other waits with it.  Short, since the loops of all roles share the SM's instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *ms) {
     const uint32_t a = smem_addr(bar);
-    if (mbar_try_wait(a, parity)) return true;
-    const long long t0 = clock64();
+    int left = 1 << 20;
 #pragma unroll 1
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(a, parity)) return true;
+    while (!mbar_try_wait_for(a, parity, 2000u)) {
+        if (--left == 0) ms->abort = 1;
         if (ms->abort) return false;
-        if (clock64() - t0 > kLimitTicks) {
-            ms->abort = 1;
-            flag_status(status, KVQ8_DEV_TIMEOUT);
-            return false;
-        }
     }
+    return true;
 }
 
 // The same by all lanes of a warp, together again behind it.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Misc *ms, uint32_t *status) {
-    const bool ok = wait_bar(bar, parity, ms, status);
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Misc *ms) {
+    const bool ok = wait_bar(bar, parity, ms);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -388,7 +381,7 @@ tile_kernel(TileParams p, int lg) {
             bool stop = false;
 #pragma unroll 1
             for (int seg = 0; !stop; ++seg) {
-                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
                 const Part &part = ms->part[seg & 3];
                 const int n = part.stages, first = part.off, end = part.end, h = part.head;
                 if (n == 0) break;
@@ -410,7 +403,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                         for (int v = 0; v < 2; ++v) {
                             const int at = (g + v) % L::kSlots;
-                            if (!wait_bar(&ms->empty[at], (((g + v) / L::kSlots) & 1) ^ 1, ms, p.dev_status)) {
+                            if (!wait_bar(&ms->empty[at], (((g + v) / L::kSlots) & 1) ^ 1, ms)) {
                                 stop = true;
                                 break;
                             }
@@ -448,16 +441,16 @@ tile_kernel(TileParams p, int lg) {
             int x = 0;   // stages so far
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
-                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
                 const int n = ms->part[seg & 3].stages;
                 if (n == 0) break;
                 if (scores) {
-                    wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
+                    wait_warp(&ms->q_ready, seg & 1, ms);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide ? kRows : 2 * kRows, false);
-                        wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
-                        wait_warp(&ms->s_free, (x & 1) ^ 1, ms, p.dev_status);
+                        wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms);
+                        wait_warp(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
                         mma_k128(kColS, kColK + (x & 1) * 64, b, kWord, false, lead);
                         if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, b + kLowPart, kWord, true, lead);
@@ -466,12 +459,12 @@ tile_kernel(TileParams p, int lg) {
                     }
                     mma_commit(smem_addr(&ms->q_free), lead);
                 } else {
-                    wait_warp(&ms->o_free, (seg & 1) ^ 1, ms, p.dev_status);
+                    wait_warp(&ms->o_free, (seg & 1) ^ 1, ms);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
-                        wait_warp(&ms->v_ready[x & 1], (x >> 1) & 1, ms, p.dev_status);
-                        wait_warp(&ms->p_ready, x & 1, ms, p.dev_status);
+                        wait_warp(&ms->v_ready[x & 1], (x >> 1) & 1, ms);
+                        wait_warp(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
                         mma_k128(kColO, kColV + (x & 1) * 64, b, kWord, i > 0, lead);
                         if (kWide && kLow) mma_k128(kColO, kColV + (x & 1) * 64, b + kLowPart, kWord, true, lead);
@@ -490,7 +483,7 @@ tile_kernel(TileParams p, int lg) {
             long long left = hi - lo;
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
-                if (!wait_warp(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms, p.dev_status)) break;
+                if (!wait_warp(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms)) break;
                 Part &part = ms->part[seg & 3];
                 const int stages = left > 0 ? w.stages(w.r) : 0;
                 const int n = (int)min(left, (long long)(stages - off));
@@ -547,7 +540,7 @@ tile_kernel(TileParams p, int lg) {
         int j = 0;
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
-            if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status)) break;
+            if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
             const Part &part = ms->part[seg & 3];
             const int n = part.stages;
             if (n == 0) break;
@@ -559,7 +552,7 @@ tile_kernel(TileParams p, int lg) {
                 // K: lane = token, the row's chunk c stands at c ^ (token & 7)
                 int g = 2 * j, at = g % L::kSlots;
                 const unsigned char *st = smem + L::oRing + at * kSlotBytes;
-                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms, p.dev_status);
+                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
                 const int skip = ms->skip[at];
                 const float *scales = reinterpret_cast<const float *>(st + kCodeBytes);
                 const bool real = !skip && behind > 0;
@@ -567,10 +560,10 @@ tile_kernel(TileParams p, int lg) {
                 if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
-                wait_warp(&ms->k_free[j & 1], par ^ 1, ms, p.dev_status);
+                wait_warp(&ms->k_free[j & 1], par ^ 1, ms);
                 tc_fence_after();
                 const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
-#pragma unroll 2
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k)
                     put_codes(lanes + kColK + (j & 1) * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
                 tmem_wait_st();
@@ -586,8 +579,8 @@ tile_kernel(TileParams p, int lg) {
                 ++g;
                 at = g % L::kSlots;
                 st = smem + L::oRing + at * kSlotBytes;
-                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms, p.dev_status);
-                wait_warp(&ms->v_free[j & 1], par ^ 1, ms, p.dev_status);
+                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
+                wait_warp(&ms->v_free[j & 1], par ^ 1, ms);
                 tc_fence_after();
                 const int turn = (lane >> 1) & 3;
 #pragma unroll 1
@@ -633,7 +626,7 @@ tile_kernel(TileParams p, int lg) {
         // there is no such tile (or a wait gave up: the four warps of a share go by one answer, or a barrier
         // would wait for the one that left).
         auto queries = [&](int seg) {
-            const bool ok = wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms, p.dev_status);
+            const bool ok = wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms);
             if (barrier_any(bar, 128, !ok)) return false;
             const Part &part = ms->part[seg & 3];
             if (part.stages == 0) return false;
@@ -691,7 +684,7 @@ tile_kernel(TileParams p, int lg) {
                 // a row's values lie below 2^11 in units of 2^e
                 const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
                 const float down = exp2_int(-e);
-                wait_warp(&ms->q_free, (seg & 1) ^ 1, ms, p.dev_status);
+                wait_warp(&ms->q_free, (seg & 1) ^ 1, ms);
                 unsigned char *at = smem + L::oQ + (warp - 8) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -728,7 +721,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
         for (int seg = 0; more; ++seg) {
             const int n = ms->part[seg & 3].stages;
-            wait_warp(&ms->q_ready, seg & 1, ms, p.dev_status);
+            wait_warp(&ms->q_ready, seg & 1, ms);
             if (st < kCols) ms->ref[c0 + st] = 0.0f;
             const int lim_min = ms->lim_min[seg & 3];
             named_barrier_sync(bar, 128);
@@ -739,12 +732,12 @@ tile_kernel(TileParams p, int lg) {
             int t0 = ms->part[seg & 3].off * kTok;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
-                wait_warp(&ms->sc_ready[j & 3], (j >> 2) & 1, ms, p.dev_status);
+                wait_warp(&ms->sc_ready[j & 3], (j >> 2) & 1, ms);
                 float2 sc[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) sc[m] = ms->scale[j & 3][32 * quad + 8 * m + (lane >> 2)];
                 const bool bad = ms->bad[j & 3] != 0;
-                wait_warp(&ms->s_full, j & 1, ms, p.dev_status);
+                wait_warp(&ms->s_full, j & 1, ms);
                 tc_fence_after();
                 // scores relative to the references: [pair of matrices][group][matrix of the pair][row of two]
                 float t[2][kGroups][2][2];
@@ -779,7 +772,7 @@ tile_kernel(TileParams p, int lg) {
                         x[1] = y.y;
                     }
                 }
-                if (bad || t0 + kTok > lim_min) {   // some row does not see all of the stage
+                if (__builtin_expect(bad || t0 + kTok > lim_min, 0)) {   // some row does not see all of the stage
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const int2 lim = *reinterpret_cast<const int2 *>(&ms->lim[seg & 3][col + 8 * g]);
@@ -803,7 +796,7 @@ tile_kernel(TileParams p, int lg) {
                     raise |= top > kPMaxLog2 - vs_log2[m];
                 }
                 bool rest = i == 0;   // the product before is done: P's room is free, the accumulator at rest
-                if (barrier_any(bar, 128, raise)) {
+                if (__builtin_expect(barrier_any(bar, 128, raise), 0)) {
                     // move the references of rows whose P would leave fp16's range (at first: of all), by whole
                     // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
                     // stage of one leaves the rows fresh
@@ -827,7 +820,7 @@ tile_kernel(TileParams p, int lg) {
                     }
                     named_barrier_sync(bar, 128);
                     if (!rest && !fresh) {
-                        wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+                        wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
                         tc_fence_after();
                         rest = true;
 #pragma unroll 1
@@ -882,7 +875,7 @@ tile_kernel(TileParams p, int lg) {
                         }
                     }
                 }
-                if (!rest) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+                if (!rest) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     store_matrices(pout + g * kCoreRow, hi[g][0], hi[g][1], hi[g][2], hi[g][3]);
@@ -919,7 +912,7 @@ tile_kernel(TileParams p, int lg) {
                 ms->dst[x] = dst;
             }
             named_barrier_sync(bar, 128);
-            wait_warp(&ms->pv_done, (j & 1) ^ 1, ms, p.dev_status);
+            wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
             tc_fence_after();
             const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
 #pragma unroll 1
@@ -961,6 +954,7 @@ tile_kernel(TileParams p, int lg) {
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(0, 512);
+    if (tid == 0 && ms->abort) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
 }
 
 // What the tile kernel needs to know of the groups: (first row, rows, the row
