@@ -8,6 +8,7 @@
 
 #include "kvq8_device.cuh"
 #include "kvq8_internal.cuh"
+#include "kvq8_ptx.cuh"
 
 namespace kvq8 {
 
@@ -19,6 +20,12 @@ __device__ __forceinline__ float4 widen(uint32_t a, uint32_t b, int dtype) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
     return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// Brings the 128 values of a row from element i on into L2.
+__device__ __forceinline__ void prefetch_l2(const void *base, int dtype, int64_t i) {
+    const int size = dtype == KVQ8_DTYPE_F32 ? 4 : 2;
+    bulk_prefetch_l2(static_cast<const char *>(base) + i * size, kHD * size);
 }
 
 __device__ __forceinline__ void store1(void *base, int dtype, int64_t i, float x) {

@@ -42,8 +42,10 @@ namespace kvq8 {
 namespace {
 
 constexpr int kTok = 128;                       // tokens per stage
-constexpr int kSoftmaxWarps = 16, kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kThreads = 256 + kSoftmaxThreads;
+constexpr int kSoftmaxWarps = 16;
+// What a tile costs beside its stages (queries, first references, output), in stages: the CTAs' shares count it, or
+// one that gets many short tiles ends long after the others.
+constexpr int kTileCost = 4;
 constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
 constexpr int kCoreRow = 2048;                  // bytes between cores along the rows (16 cores of 128 B along k)
@@ -52,10 +54,6 @@ constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end
 // when P would pass 2^15.9 (fp16 ends below 2^16).
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
 constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this when M is set (rows of zeros do)
-// Registers per thread: what the launch holds, and what the warpgroups (copies, MMAs and queries; operands; four of
-// softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory leaves it no L1.
-constexpr int kLaunchRegs = 80, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
-static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs, "registers");
 // columns of tensor memory, all of which is the CTA's (so that it begins at address 0)
 constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = 384;
 
@@ -73,6 +71,17 @@ struct Lay {
     static constexpr int kSlots = (232448 - oRing) / kSlotBytes < 8 ? (232448 - oRing) / kSlotBytes : 8;
     static constexpr int kBytes = oRing + kSlots * kSlotBytes;
     static_assert(kSlots >= 4, "ring too shallow");
+    // Operand warps: tiles of few rows are bound by them (the softmax of a stage is short, the codes are the
+    // same), so K and V get four warps each there.
+    static constexpr int kOperandWarps = kWide ? 4 : 8;
+    static constexpr int kSoftmaxWarp0 = 4 + kOperandWarps;
+    static constexpr int kThreads = (kSoftmaxWarp0 + kSoftmaxWarps) * 32;
+    // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
+    // operands; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
+    // leaves it no L1.
+    static constexpr int kLaunchRegs = kWide ? 80 : 72, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
+    static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs || !kWide,
+                  "registers");
 };
 
 // One tile's stages of one CTA.
@@ -87,7 +96,7 @@ struct Misc {
     uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2], sc_ready[4];
     uint64_t part_ready[4], part_free[4];
     uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done[2];
-    long long warp_tot[kThreads / 32];
+    long long warp_tot[32];
     int s0, r0, off;
     volatile int abort;
     uint32_t tmem;
@@ -160,6 +169,7 @@ struct Walk {
         return (int)max(0ll, min((long long)cap, e));
     }
     __device__ int stages(int r_) const { return max(1, (end(r_) + kTok - 1) / kTok); }
+    __device__ int cost(int r_) const { return kTileCost + stages(r_); }
     // Tokens that row n of tile r_ looks at; bad: its position is outside the table.
     __device__ int limit(int r_, int n, bool &bad) const {
         const int i = (r_ * rows_per_tile + n) >> lg;
@@ -265,9 +275,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 template <bool kShared, int kRows, bool kLow>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((Lay<kRows, kLow>::kThreads), 1)
 tile_kernel(TileParams p, int lg) {
     using L = Lay<kRows, kLow>;
+    constexpr int kThreads = L::kThreads;
     constexpr bool kWide = L::kWide;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *ms = reinterpret_cast<Misc *>(smem + L::oMisc);
@@ -304,18 +315,18 @@ tile_kernel(TileParams p, int lg) {
     if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), 512);
     pdl_wait();
     pdl_launch_dependents();   // (the next kernel's CTAs find no registers here before this one leaves)
-    // ---- this CTA's share: stages [lo, hi) of the sequence of all tiles' stages ----
+    // ---- this CTA's share: [lo, hi) of the sequence of all tiles, each as long as it costs ----
     Walk<kShared> w(p, lg, kRows);
     const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + kRows - 1) / kRows);
     const int seqs = kShared ? p.n_groups : p.batch;
     const int items = seqs * per_seq;   // (sequence, tile of one kv head), or group
     const int per = (items + kThreads - 1) / kThreads;
     const int i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
-    auto item = [&](int i) {   // its stages, for one kv head
+    auto item = [&](int i) {   // its cost, for one kv head
         const int s = i / per_seq, r = i - s * per_seq;
         w.load(s);
         w.r = r;
-        return kShared ? (w.rows > 0 ? (long long)w.tiles() * w.stages(0) : 0) : r < w.tiles() ? w.stages(r) : 0;
+        return kShared ? (w.rows > 0 ? (long long)w.tiles() * w.cost(0) : 0) : r < w.tiles() ? w.cost(r) : 0;
     };
     long long mine = 0;
 #pragma unroll 1
@@ -331,7 +342,7 @@ tile_kernel(TileParams p, int lg) {
     __syncthreads();
     tc_fence_after();
     before -= mine;
-    long long total = 0;   // stages of one kv head
+    long long total = 0;   // cost of one kv head
 #pragma unroll 1
     for (int k = 0; k < kThreads / 32; ++k) {
         const long long v = ms->warp_tot[k];
@@ -342,7 +353,7 @@ tile_kernel(TileParams p, int lg) {
     const int C = (int)min((long long)gridDim.x, T);
     if (!kShared && tid == 0) p.ws_dir[c] = make_int4(0, 0, 0, 0);
     long long lo = 0, hi = 0;
-    int off = 0;
+    int off = 0;   // of the first tile: cost that lies ahead of this CTA
     if (c < C) {   // (uniform over the CTA)
         const long long Tq = divide(T, C);
         const int Tr = (int)(T - Tq * C);
@@ -350,7 +361,7 @@ tile_kernel(TileParams p, int lg) {
         hi = (long long)(c + 1) * Tq + ((c + 1) * Tr) / C;
         const int h = (int)divide(lo, total);
         const long long rem = lo - h * total;
-        // the item that holds stage lo says so
+        // the item that holds lo says so
 #pragma unroll 1
         for (int i = i_lo; i < i_hi && before <= rem; ++i) {
             const long long v = item(i);
@@ -367,14 +378,14 @@ tile_kernel(TileParams p, int lg) {
         w.h = h;
         w.r = ms->r0;
         if (kShared) {
-            const int n = w.stages(0);
+            const int n = w.cost(0);
             w.r = off / n;
             off -= w.r * n;
         }
     }
 
     if (warp < 4) {
-        regs_shrink<kRegsIssue>();
+        if constexpr (kWide) regs_shrink<L::kRegsIssue>();
         if (warp == 0) {
             // ============================ copies ============================
             int g = 0;   // granules so far: K and V of every stage
@@ -480,13 +491,21 @@ tile_kernel(TileParams p, int lg) {
             __syncwarp();
         } else if (warp == 2) {
             // ======================= the tiles' order =======================
+            // a tile's cost is kTileCost, then one for each stage: a share that ends in the former has none of it
             long long left = hi - lo;
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
+                int n = 0, stages = 0, from = 0;
+                while (left > 0) {
+                    stages = w.stages(w.r);
+                    const int until = (int)min((long long)(kTileCost + stages), off + left);   // of the tile's cost
+                    from = max(0, off - kTileCost);
+                    n = max(0, until - kTileCost) - from;
+                    if (n > 0) break;
+                    left = 0;   // (only the last tile)
+                }
                 if (!wait_warp(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms)) break;
                 Part &part = ms->part[seg & 3];
-                const int stages = left > 0 ? w.stages(w.r) : 0;
-                const int n = (int)min(left, (long long)(stages - off));
                 if (n > 0) {
                     const int rows = w.tile_rows(w.r);
                     int least = 0x7fffffff;
@@ -497,6 +516,8 @@ tile_kernel(TileParams p, int lg) {
                             bool bad;
                             lim = w.limit(w.r, i, bad);
                             if (bad) flag_status(p.dev_status, KVQ8_DEV_BAD_POSITION);
+                            // the row's query, soon to be read
+                            prefetch_l2(p.q, p.q_dtype, w.token(w.r, i) * p.q_stride + (int64_t)w.head(i) * kHD);
                         }
                         ms->lim[seg & 3][i] = lim;
                         least = min(least, lim);
@@ -506,16 +527,17 @@ tile_kernel(TileParams p, int lg) {
                         const bool whole = n == stages;
                         const long long x = (((long long)w.h * p.batch + w.first) << lg) + (long long)w.r * kRows;
                         ms->lim_min[seg & 3] = least;
-                        part.off = off;
+                        part.off = from;
                         part.end = w.end(w.r);
                         part.rows = rows;
                         part.lead = w.lead;
                         part.head = w.h;
                         part.token = (int)w.token(w.r, 0);
                         part.direct = !kShared && whole;
-                        part.rec = kShared ? x + (long long)c * kTileRows : ((long long)c * 2 + (off == 0 ? 1 : 0)) * kTileRows;
-                        if (off == 0) {   // the CTAs c .. that hold this tile's records
-                            const int cnt = (int)(((hi - left + stages) * C + T - 1) / T) - c;
+                        part.rec = kShared ? x + (long long)c * kTileRows : ((long long)c * 2 + (from == 0 ? 1 : 0)) * kTileRows;
+                        if (from == 0) {   // the CTAs c .. that hold this tile's records
+                            const long long end = hi - left - off + kTileCost + stages;
+                            const int cnt = (int)divide(end * C + T - 1, T) - c;
                             if (kShared) p.ws_dir[x] = make_int4(c, whole ? 1 : cnt, 0, 0);
                             else if (!whole) p.ws_dir[c] = make_int4(cnt, w.s, w.h, w.r);
                         }
@@ -527,16 +549,17 @@ tile_kernel(TileParams p, int lg) {
                     mbar_arrive(smem_addr(&ms->part_ready[seg & 3]));
                 }
                 if (n == 0) break;
-                left -= n;
+                left -= kTileCost + stages - off;
                 off = 0;
                 if (left > 0) w.next(seqs);
             }
         }
-    } else if (warp < 8) {
-        regs_shrink<kRegsOperand>();
+    } else if (warp < L::kSoftmaxWarp0) {
+        if constexpr (kWide) regs_shrink<L::kRegsOperand>();
         // ========================= operands =========================
         const int quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const bool keys = kWide || warp < 8, values = kWide || warp >= 8;
         int j = 0;
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
@@ -549,68 +572,71 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, behind -= kTok) {
                 const uint32_t par = (j >> 1) & 1;
-                // K: lane = token, the row's chunk c stands at c ^ (token & 7)
-                int g = 2 * j, at = g % L::kSlots;
-                const unsigned char *st = smem + L::oRing + at * kSlotBytes;
-                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
-                const int skip = ms->skip[at];
-                const float *scales = reinterpret_cast<const float *>(st + kCodeBytes);
-                const bool real = !skip && behind > 0;
-                ms->scale[j & 3][row] = make_float2(real ? scales[row] * p.sm_scale_log2 : 0.0f, real ? scales[kTok + row] : 0.0f);
-                if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
-                wait_warp(&ms->k_free[j & 1], par ^ 1, ms);
-                tc_fence_after();
-                const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k)
-                    put_codes(lanes + kColK + (j & 1) * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&ms->k_ready[j & 1]));
-                    mbar_arrive(smem_addr(&ms->empty[at]));
+                if (keys) {
+                    // K: lane = token, the row's chunk c stands at c ^ (token & 7)
+                    const int g = 2 * j, at = g % L::kSlots;
+                    const unsigned char *st = smem + L::oRing + at * kSlotBytes;
+                    wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
+                    const int skip = ms->skip[at];
+                    const float *scales = reinterpret_cast<const float *>(st + kCodeBytes);
+                    const bool real = !skip && behind > 0;
+                    ms->scale[j & 3][row] = make_float2(real ? scales[row] * p.sm_scale_log2 : 0.0f, real ? scales[kTok + row] : 0.0f);
+                    if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
+                    wait_warp(&ms->k_free[j & 1], par ^ 1, ms);
+                    tc_fence_after();
+                    const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
+#pragma unroll(kWide ? 1 : 4)
+                    for (int k = 0; k < 4; ++k)
+                        put_codes(lanes + kColK + (j & 1) * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&ms->k_ready[j & 1]));
+                        mbar_arrive(smem_addr(&ms->empty[at]));
+                    }
                 }
-                // V: lane = dim; two 64-token quarters of 64 bytes.  Lanes 2 apart start at
-                // another chunk, so that eight lanes' 16-byte reads hit all banks, and turn
-                // the four chunks back into order
-                ++g;
-                at = g % L::kSlots;
-                st = smem + L::oRing + at * kSlotBytes;
-                wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
-                wait_warp(&ms->v_free[j & 1], par ^ 1, ms);
-                tc_fence_after();
-                const int turn = (lane >> 1) & 3;
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    const uint4 *vr = reinterpret_cast<const uint4 *>(st + q * kTileVQuarter + row * kStageTok);
-                    uint4 a[4], b[4];
+                if (values) {
+                    // V: lane = dim; two 64-token quarters of 64 bytes.  Lanes 2 apart start at
+                    // another chunk, so that eight lanes' 16-byte reads hit all banks, and turn
+                    // the four chunks back into order
+                    const int g = 2 * j + 1, at = g % L::kSlots;
+                    const unsigned char *st = smem + L::oRing + at * kSlotBytes;
+                    wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
+                    wait_warp(&ms->v_free[j & 1], par ^ 1, ms);
+                    tc_fence_after();
+                    const int turn = (lane >> 1) & 3;
+#pragma unroll(kWide ? 1 : 2)
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 *vr = reinterpret_cast<const uint4 *>(st + q * kTileVQuarter + row * kStageTok);
+                        uint4 a[4], b[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) a[k] = vr[(k + turn) & 3];
+                        for (int k = 0; k < 4; ++k) a[k] = vr[(k + turn) & 3];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) b[k] = (turn & 1) ? a[(k + 3) & 3] : a[k];
+                        for (int k = 0; k < 4; ++k) b[k] = (turn & 1) ? a[(k + 3) & 3] : a[k];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) a[k] = (turn & 2) ? b[(k + 2) & 3] : b[k];
-                    put_codes(lanes + kColV + (j & 1) * 64 + 32 * q, a[0], a[1]);
-                    put_codes(lanes + kColV + (j & 1) * 64 + 32 * q + 16, a[2], a[3]);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&ms->v_ready[j & 1]));
-                    mbar_arrive(smem_addr(&ms->empty[at]));
+                        for (int k = 0; k < 4; ++k) a[k] = (turn & 2) ? b[(k + 2) & 3] : b[k];
+                        put_codes(lanes + kColV + (j & 1) * 64 + 32 * q, a[0], a[1]);
+                        put_codes(lanes + kColV + (j & 1) * 64 + 32 * q + 16, a[2], a[3]);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&ms->v_ready[j & 1]));
+                        mbar_arrive(smem_addr(&ms->empty[at]));
+                    }
                 }
             }
         }
     } else {
-        regs_grow<kRegsSoftmax>();
+        if constexpr (kWide) regs_grow<L::kRegsSoftmax>();
         // ========================== softmax ==========================
         constexpr int kCols = kRows / 4;      // a warp's rows
         // the four warps of a share of the rows see to it by themselves
-        const int quad = warp & 3, share = (warp - 8) >> 2, c0 = share * kCols, st = tid & 127;
+        const int quad = warp & 3, share = (warp - L::kSoftmaxWarp0) >> 2, c0 = share * kCols, st = tid & 127;
         const int bar = 1 + share;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         // Scores and P are held as MMA fragments: a thread has the tokens 32 quad + 8 m + lane / 4 (m < 4) of the
@@ -630,10 +656,10 @@ tile_kernel(TileParams p, int lg) {
             if (barrier_any(bar, 128, !ok)) return false;
             const Part &part = ms->part[seg & 3];
             if (part.stages == 0) return false;
-            if (warp - 8 < kRows / 8) {
+            if (warp - L::kSoftmaxWarp0 < kRows / 8) {
                 // eight rows to a warp: lane l has row l % 8, and of every 32-block the dims 8 (l / 8) .. + 7, a
                 // 16-byte line of an operand's core, so that eight lanes fill a core
-                const int i = (warp - 8) * 8 + (lane & 7);
+                const int i = (warp - L::kSoftmaxWarp0) * 8 + (lane & 7);
                 float4 x[8];
                 const bool real = i < part.rows;
                 const int64_t src = real ? ((long long)part.token + (i >> lg)) * p.q_stride +
@@ -685,7 +711,7 @@ tile_kernel(TileParams p, int lg) {
                 const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
                 const float down = exp2_int(-e);
                 wait_warp(&ms->q_free, (seg & 1) ^ 1, ms);
-                unsigned char *at = smem + L::oQ + (warp - 8) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
+                unsigned char *at = smem + L::oQ + (warp - L::kSoftmaxWarp0) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const float iq = __fdiv_rn(127.0f, top[b]), unit = __fmul_rn(top[b], KVQ8_INV127) * down;
@@ -915,7 +941,7 @@ tile_kernel(TileParams p, int lg) {
             wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
             tc_fence_after();
             const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
-#pragma unroll 1
+#pragma unroll(kWide ? 2 : 1)
             for (int k = 0; k < kCols; k += 8) {
                 float x[8], y[8];
                 tmem_ld8(lanes + kColO + c0 + k, x);
@@ -1072,12 +1098,12 @@ cudaError_t launch_tiles(const TileParams &p, int lg, cudaStream_t s) {
             cudaFuncAttributes a;
             cudaError_t e = cudaFuncGetAttributes(&a, tile_kernel<kShared, kRows, kLow>);
             if (e != cudaSuccess) return e;
-            if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+            if (Lay<kRows, kLow>::kWide && a.numRegs != Lay<kRows, kLow>::kLaunchRegs) return cudaErrorInvalidConfiguration;
             return cudaFuncSetAttribute(tile_kernel<kShared, kRows, kLow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         Lay<kRows, kLow>::kBytes);
         },
         [&] {
-            return launch_dependent(tile_kernel<kShared, kRows, kLow>, dim3(ctas), kThreads, Lay<kRows, kLow>::kBytes, s, p, lg);
+            return launch_dependent(tile_kernel<kShared, kRows, kLow>, dim3(ctas), Lay<kRows, kLow>::kThreads, Lay<kRows, kLow>::kBytes, s, p, lg);
         });
 }
 
