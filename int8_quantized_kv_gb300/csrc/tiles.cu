@@ -446,7 +446,7 @@ tile_kernel(TileParams p, int lg) {
         } else if (warp != 2) {
             // ============================= MMAs =============================
             // warp 1: scores, warp 3: output (a warp for both leaves the tensor cores waiting for its own waits)
-            const bool lead = lane == 0, scores = warp == 1;
+            const bool scores = warp == 1;
             const uint64_t b = core_desc(smem_addr(smem + (scores ? L::oQ : L::oP)), 128, kCoreRow);
             constexpr uint64_t kLowPart = kRows / 8 * kCoreRow / 16;
             int x = 0;   // stages so far
@@ -463,12 +463,12 @@ tile_kernel(TileParams p, int lg) {
                         wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms);
                         wait_warp(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
-                        mma_k128(kColS, kColK + (x & 1) * 64, b, kWord, false, lead);
-                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, b + kLowPart, kWord, true, lead);
-                        mma_commit(smem_addr(&ms->s_full), lead);
-                        mma_commit(smem_addr(&ms->k_free[x & 1]), lead);
+                        mma_k128(kColS, kColK + (x & 1) * 64, b, kWord, false);
+                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, b + kLowPart, kWord, true);
+                        mma_commit(smem_addr(&ms->s_full));
+                        mma_commit(smem_addr(&ms->k_free[x & 1]));
                     }
-                    mma_commit(smem_addr(&ms->q_free), lead);
+                    mma_commit(smem_addr(&ms->q_free));
                 } else {
                     wait_warp(&ms->o_free, (seg & 1) ^ 1, ms);
 #pragma unroll 1
@@ -477,16 +477,16 @@ tile_kernel(TileParams p, int lg) {
                         wait_warp(&ms->v_ready[x & 1], (x >> 1) & 1, ms);
                         wait_warp(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
-                        mma_k128(kColO, kColV + (x & 1) * 64, b, kWord, i > 0, lead);
-                        if (kWide && kLow) mma_k128(kColO, kColV + (x & 1) * 64, b + kLowPart, kWord, true, lead);
-                        mma_commit(smem_addr(&ms->pv_done), lead);
-                        mma_commit(smem_addr(&ms->v_free[x & 1]), lead);
+                        mma_k128(kColO, kColV + (x & 1) * 64, b, kWord, i > 0);
+                        if (kWide && kLow) mma_k128(kColO, kColV + (x & 1) * 64, b + kLowPart, kWord, true);
+                        mma_commit(smem_addr(&ms->pv_done));
+                        mma_commit(smem_addr(&ms->v_free[x & 1]));
                     }
                 }
             }
             // none may still run when the CTA gives its tensor memory back
             uint64_t *done = &ms->all_done[scores ? 0 : 1];
-            mma_commit(smem_addr(done), lead);
+            mma_commit(smem_addr(done));
             mbar_wait_bounded(smem_addr(done), 0, kLimitNs);
             __syncwarp();
         } else if (warp == 2) {
