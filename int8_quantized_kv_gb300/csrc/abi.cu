@@ -675,7 +675,7 @@ size_t kvq8_shared_workspace_bytes(int batch, int n_groups, int nqh, int nkv, in
     const size_t base = kvq8_decode_workspace_bytes(batch, nqh, nkv, hd, max_blocks, block_size);
     if (!base || n_groups < 0 || n_groups > kMaxGridYZ || (int64_t)batch * nqh > 2147483647 - kMaxTileCtas * kTileRows)
         return 0;
-    return base + up256((size_t)batch * sizeof(int32_t)) + up256((size_t)n_groups * sizeof(int4)) +
+    return base + up256((size_t)batch * 2 * sizeof(int32_t)) + up256((size_t)n_groups * sizeof(int4)) +
            shared_workspace(batch, nqh).bytes;
 }
 
@@ -701,7 +701,7 @@ static kvq8_status run_shared(const float *q, const float *k_new, const float *v
     st = fill_decode_params(q, batch, nqh, nkv, k_pool, v_pool, k_scale, v_scale, num_blocks, block_table,
                             max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &d, &plan);
     if (st != KVQ8_OK) return st;
-    const size_t tails = plan.bytes, groups = tails + up256((size_t)batch * sizeof(int32_t));
+    const size_t tails = plan.bytes, groups = tails + up256((size_t)batch * 2 * sizeof(int32_t));
     const size_t tiles = groups + up256((size_t)n_groups * sizeof(int4));
     const TileWorkspace w = shared_workspace(batch, nqh);
     if (workspace_bytes < tiles + w.bytes) return KVQ8_ERR_WORKSPACE;
@@ -728,6 +728,7 @@ static kvq8_status run_shared(const float *q, const float *k_new, const float *v
     p.n_groups = n_groups;
     p.step = step ? 1 : 0;
     p.ws_tail = (int32_t *)((char *)workspace + tails);
+    p.ws_first = p.ws_tail + batch;
     p.ws_group = (int4 *)((char *)workspace + groups);
     place_tile_workspace(w, (char *)workspace + tiles, &p);
     d.out = out;

@@ -121,7 +121,7 @@ enum SplitMode {
     kWhole = 0,      // every token of the span
     kWindowed = 1,   // tokens t < sinks or t >= L - windows[b]
     kScored = 2,     // every token, and its scores (base 2) are written to ws_scores
-    kTail = 3        // tokens t >= windows[b] (here the row's first token behind its shared prefix)
+    kTail = 3        // tokens t >= windows[b] (here the row's first token behind its shared prefix; decode_tail.cuh)
 };
 // The windowed and scored decodes round with reciprocal factors (include/kvq8.h).
 constexpr bool recip_rule(int mode) { return mode == kWindowed || mode == kScored; }
@@ -586,10 +586,6 @@ decode_split_kernel(DecodeParams p) {
                         va &= t0 + ta < p.sinks || t0 + ta >= sp.lo;
                         vb &= t0 + tb < p.sinks || t0 + tb >= sp.lo;
                     }
-                    if (kMode == kTail) {
-                        va &= t0 + ta >= sp.lo;
-                        vb &= t0 + tb >= sp.lo;
-                    }
 
                     // ---- segment 2a: int32 block dots, lane = token ----
                     int da[G][kNQB], db[G][kNQB];
@@ -726,7 +722,7 @@ decode_split_kernel(DecodeParams p) {
                         for (int i = 0; i < 8; ++i) bl[i] = 0u;
                     }
                     // the stage's offset correction, one tile shared by all dims
-                    // (the windowed, scored and tail splits take the offset off the
+                    // (the windowed and scored splits take the offset off the
                     // codes themselves instead, and add each stage's product to
                     // the accumulator in fp32: the tensor cores cut off what an
                     // accumulator cannot hold, which next to the offset's share

@@ -1,0 +1,487 @@
+// decode_tail.cuh -- the split over each row's own tokens, behind those that it
+// shares: many units (sequence, kv head) of few 64-token stages.
+//
+// decode_split.cuh's kernel gives a unit to the seven consumer warps of a CTA,
+// which pays for long contexts: of a unit of six stages each warp has one, and
+// the queries, the meeting of the warps' states and the record are paid per
+// unit and CTA (224 rows x 8 heads of 100 to 700 tokens: 80 us for what can be
+// read in 28).  Here every warp is a worker by itself: it takes an equal,
+// contiguous share of the sequence of all units' stages, copies its stages
+// (two slots of 16.5 KiB, six warps on an SM), keeps the state of its unit in
+// registers and writes the unit's record from there; queries, block ids and a
+// step's new token are loaded when the unit's first stage is asked for, two
+// stages ahead of their use.  The arithmetic of a stage is decode_split.cuh's.
+#pragma once
+
+#include "decode_split.cuh"
+
+namespace kvq8 {
+namespace {
+
+constexpr int kTailWarps = 6, kTailSlots = 2;
+
+template <int G>
+struct TailLay {
+    static constexpr int kP = (G * 2 * kPRowHalves * 2 + 15) / 16 * 16;
+    static constexpr int oSlots = 0;                                   // [warp][slot]
+    static constexpr int oP = kTailWarps * kTailSlots * kStageBytes;   // [warp]
+    static constexpr int oQCodes = oP + kTailWarps * kP;
+    static constexpr int oQScale = oQCodes + kTailWarps * G * kHD;
+    static constexpr int oFull = oQScale + kTailWarps * G * kNQB * 4;
+    static constexpr int oMisc = oFull + kTailWarps * kTailSlots * 8;
+    static constexpr int kBytes = oMisc + 256;
+    static_assert(oQScale % 16 == 0 && oFull % 8 == 0 && oMisc % 16 == 0, "alignment");
+    static_assert(kBytes <= kSmemLimit, "shared memory budget");
+};
+
+struct TailMisc {
+    long long warp_tot[kTailWarps];
+    long long base[kTailWarps];   // worker: stages ahead of its first sequence
+    int b0[kTailWarps];           // worker: that sequence
+};
+
+// One staged stage for the G query heads of a unit: the state (M, Sl, acc in units of 2^e_cur) takes in the tokens lane
+// (where va) and lane + 32 (where vb).  p_hi, p_lo: the warp's room for P.
+template <int G>
+__device__ __forceinline__ void tail_stage(const unsigned char *st, const int8_t *q_codes, const float *q_scale,
+                                             __half *p_hi, __half *p_lo, int lane, int n, int t4, bool va, bool vb, float sm_scale_log2,
+                                             float (&M)[G], float (&Sl)[G], float (&acc)[8][4], int &e_cur) {
+    const int8_t *kst = reinterpret_cast<const int8_t *>(st);
+    const int8_t *vst = kst + kStageKBytes;
+    const float *ks_st = reinterpret_cast<const float *>(st + kStageKBytes + kStageVBytes);
+    const float *vs_st = ks_st + kStageTok;
+    const int ta = lane, tb = lane + 32;
+    // n, t4: MMA fragment coordinates (lane / 4, lane % 4).
+    // P.V for G <= 4 packs P's high fp16 parts into columns 0..G-1 and its
+    // low parts into G..2G-1 of one MMA (half the MMAs); the columns' sums
+    // are added at the segment's end.  Accumulator columns 2*t4, 2*t4 + 1
+    // then belong to heads col_head0, col_head1 (for their rescaling).
+    constexpr bool kPackPV = G <= 4;
+    const int col_head0 = kPackPV ? (2 * t4) % G : 2 * t4;
+    const int col_head1 = kPackPV ? (2 * t4 + 1) % G : 2 * t4 + 1;
+    // ---- segment 2a: int32 block dots, lane = token ----
+    int da[G][kNQB], db[G][kNQB];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int q = 0; q < kNQB; ++q) { da[g][q] = 0; db[g][q] = 0; }
+#pragma unroll
+    for (int cc = 0; cc < 8; ++cc) {
+        const int4 ka = lds128(kst + ta * kHD + ((cc ^ (ta & 7)) << 4));
+        const int4 kb = lds128(kst + tb * kHD + ((cc ^ (tb & 7)) << 4));
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int4 qw = lds128(q_codes + g * kHD + cc * 16);
+            int x = da[g][cc >> 1], y = db[g][cc >> 1];
+            x = __dp4a(ka.x, qw.x, x); y = __dp4a(kb.x, qw.x, y);
+            x = __dp4a(ka.y, qw.y, x); y = __dp4a(kb.y, qw.y, y);
+            x = __dp4a(ka.z, qw.z, x); y = __dp4a(kb.z, qw.z, y);
+            x = __dp4a(ka.w, qw.w, x); y = __dp4a(kb.w, qw.w, y);
+            da[g][cc >> 1] = x;
+            db[g][cc >> 1] = y;
+        }
+    }
+    const float ksa = ks_st[ta], ksb = ks_st[tb];
+    const float vsa = va ? vs_st[ta] : 0.0f, vsb = vb ? vs_st[tb] : 0.0f;
+
+    // power-of-two unit of this stage's P: 2^e > max vs, so that
+    // p' = w * vs * 2^-e stays below 2^8 (w < 2^8, see below).  e only
+    // moves when it must grow or has become 2^12 too large.
+    const int e_need = redux_max_i32(
+        ((__float_as_int(fmaxf(vsa, vsb)) >> 23) & 0xff) - 126);  // 0 -> -126
+    int e = e_cur;
+    if (e_need > e_cur || e_need < e_cur - 12) e = max(-120, min(120, e_need));
+    const float inv = __int_as_float((127 - e) << 23);
+
+    // ---- segment 2b: scores, online softmax ----
+    float sa[G], sb[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float4 qs = *reinterpret_cast<const float4 *>(q_scale + g * kNQB);
+        float a = (float)da[g][0] * qs.x;
+        a = fmaf((float)da[g][1], qs.y, a);
+        a = fmaf((float)da[g][2], qs.z, a);
+        a = fmaf((float)da[g][3], qs.w, a);
+        float bb = (float)db[g][0] * qs.x;
+        bb = fmaf((float)db[g][1], qs.y, bb);
+        bb = fmaf((float)db[g][2], qs.z, bb);
+        bb = fmaf((float)db[g][3], qs.w, bb);
+        sa[g] = va ? a * ksa * sm_scale_log2 : -INFINITY;
+        sb[g] = vb ? bb * ksb * sm_scale_log2 : -INFINITY;
+    }
+    // The running maximum M is raised only when a score exceeds it by
+    // more than 2^kLazyLog2; below that the weights 2^(s-M) stay < 2^8
+    // and every quantity remains exact to fp32 rounding.
+    bool grow = false;
+#pragma unroll
+    for (int g = 0; g < G; ++g) grow |= fmaxf(sa[g], sb[g]) > M[g] + kLazyLog2;
+    float alpha[G];
+    bool rescale = (e != e_cur);
+    if (__any_sync(0xffffffffu, grow)) {
+        rescale = true;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float m_new = fmaxf(M[g], redux_max_f32(fmaxf(sa[g], sb[g])));
+            alpha[g] = ex2_approx(M[g] - m_new);   // 0 while M is -inf
+            M[g] = m_new;
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) alpha[g] = 1.0f;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float wa = va ? ex2_approx(sa[g] - M[g]) : 0.0f;
+        const float wb = vb ? ex2_approx(sb[g] - M[g]) : 0.0f;
+        Sl[g] = fmaf(Sl[g], alpha[g], wa + wb);
+        const float pa = wa * vsa * inv, pb = wb * vsb * inv;
+        const __half ha = __float2half_rn(pa), hb = __float2half_rn(pb);
+        p_hi[g * kPRowHalves + ta] = ha;
+        p_hi[g * kPRowHalves + tb] = hb;
+        p_lo[g * kPRowHalves + ta] = __float2half_rn(pa - __half2float(ha));
+        p_lo[g * kPRowHalves + tb] = __float2half_rn(pb - __half2float(hb));
+    }
+    if (rescale) {  // warp-uniform
+        const float two = __int_as_float((127 + max(-126, min(127, e_cur - e))) << 23);
+        float f0 = 0.0f, f1 = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (g == col_head0) f0 = alpha[g] * two;
+            if (g == col_head1) f1 = alpha[g] * two;
+        }
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            acc[mt][0] *= f0; acc[mt][1] *= f1;
+            acc[mt][2] *= f0; acc[mt][3] *= f1;
+        }
+        e_cur = e;
+    }
+    __syncwarp();
+
+    // ---- segment 2c: acc += V . P on the tensor cores ----
+    // B columns: kPackPV, head n's high part (n < G) or head n - G's
+    // low part (G <= n < 2G); else the high part of head n in
+    // bh and its low part in bl (two MMAs)
+    uint32_t bh[8], bl[8];
+    const __half *rh = kPackPV ? (n < G ? p_hi + n * kPRowHalves
+                                        : (n < 2 * G ? p_lo + (n - G) * kPRowHalves : nullptr))
+                               : (n < G ? p_hi + n * kPRowHalves : nullptr);
+    if (rh) {
+        const int4 h0 = lds128(rh + t4 * 16);
+        const int4 h1 = lds128(rh + t4 * 16 + 8);
+        bh[0] = h0.x; bh[1] = h0.y; bh[2] = h0.z; bh[3] = h0.w;
+        bh[4] = h1.x; bh[5] = h1.y; bh[6] = h1.z; bh[7] = h1.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bh[i] = 0u;
+    }
+    if (!kPackPV && n < G) {
+        const int4 l0 = lds128(p_lo + n * kPRowHalves + t4 * 16);
+        const int4 l1 = lds128(p_lo + n * kPRowHalves + t4 * 16 + 8);
+        bl[0] = l0.x; bl[1] = l0.y; bl[2] = l0.z; bl[3] = l0.w;
+        bl[4] = l1.x; bl[5] = l1.y; bl[6] = l1.z; bl[7] = l1.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bl[i] = 0u;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+        const int d = mt * 16 + n;
+        const int4 v0 = lds128(vst + d * kStageTok + t4 * 16);
+        const int4 v1 = lds128(vst + (d + 8) * kStageTok + t4 * 16);
+        const uint32_t w0[4] = {(uint32_t)v0.x, (uint32_t)v0.y, (uint32_t)v0.z, (uint32_t)v0.w};
+        const uint32_t w1[4] = {(uint32_t)v1.x, (uint32_t)v1.y, (uint32_t)v1.z, (uint32_t)v1.w};
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            uint32_t a0, a2, a1, a3;
+            codes_to_sub2(w0[s], a0, a2);
+            codes_to_sub2(w1[s], a1, a3);
+            a0 = sub2_signed(a0); a1 = sub2_signed(a1);
+            a2 = sub2_signed(a2); a3 = sub2_signed(a3);
+            mma_f16_16816(part, a0, a1, a2, a3, bh[2 * s], bh[2 * s + 1]);
+            if (!kPackPV) mma_f16_16816(part, a0, a1, a2, a3, bl[2 * s], bl[2 * s + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][i] += part[i];
+    }
+}
+
+// Where a warp is in the sequence of stages: stage j of unit (b, h), which has nb of the span sp.
+struct TailCursor {
+    int b, h, j, nb;
+    SeqSpan sp;
+    __device__ __forceinline__ void load(const DecodeParams &p, int cap) {   // the sequence b, or the next that has stages
+        for (; b < p.batch; ++b, h = 0) {
+            sp = seq_span<false, kTail>(p, b, cap);
+            nb = span_stages(sp);
+            if (nb > 0) return;
+        }
+    }
+    __device__ __forceinline__ void next_unit(const DecodeParams &p, int cap) {
+        j = 0;
+        if (++h < p.nkv) return;
+        h = 0;
+        ++b;
+        load(p, cap);
+    }
+};
+
+template <int G>
+__global__ void __launch_bounds__(kTailWarps * 32, 1)
+decode_tail_kernel(DecodeParams p) {
+    using Lay = TailLay<G>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cap = p.max_blocks * kBS;
+    TailMisc *ms = reinterpret_cast<TailMisc *>(smem + Lay::oMisc);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::oFull) + warp * kTailSlots;
+    if (lane < kTailSlots) {
+        mbar_init(smem_addr(full + lane), 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();   // (this kernel's shared memory keeps the next one's large CTAs off the SM)
+    // ---- the workers' shares of all units' stages ----
+    const int per = (p.batch + kTailWarps * 32 - 1) / (kTailWarps * 32);
+    const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int L = p.ctx_lens[b];
+        if (blockIdx.x == 0 && (L < 0 || L > cap)) flag_status(p.dev_status, KVQ8_DEV_BAD_CTX_LEN);
+        mine += (long long)p.nkv * span_stages(seq_span<false, kTail>(p, b, cap));
+    }
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) ms->warp_tot[warp] = before;
+    __syncthreads();
+    before -= mine;
+    long long T = 0;
+    for (int k = 0; k < kTailWarps; ++k) {
+        if (k < warp) before += ms->warp_tot[k];
+        T += ms->warp_tot[k];
+    }
+    // consecutive workers lie on different SMs
+    const int W = (int)min((long long)gridDim.x * kTailWarps, T);
+    auto share = [&](int worker) {   // its first stage
+        const long long q = T / W;
+        const int r = (int)(T - q * W);
+        return (long long)worker * q + ((long long)worker * r) / W;
+    };
+    if (mine > 0) {
+        for (int k = 0; k < kTailWarps; ++k) {
+            const int worker = k * gridDim.x + blockIdx.x;
+            if (worker >= W) break;
+            const long long lo = share(worker);
+            if (lo < before || lo >= before + mine) continue;
+            long long acc = before;
+            for (int b = b_lo; b < b_hi; ++b) {
+                const long long n = (long long)p.nkv * span_stages(seq_span<false, kTail>(p, b, cap));
+                if (lo < acc + n) {
+                    ms->b0[k] = b;
+                    ms->base[k] = acc;
+                    break;
+                }
+                acc += n;
+            }
+        }
+    }
+    __syncthreads();
+    const int worker = warp * gridDim.x + blockIdx.x;
+    if (worker >= W) return;
+    const long long lo = share(worker);
+    const int total = (int)(share(worker + 1) - lo);
+
+    unsigned char *slots = smem + Lay::oSlots + warp * kTailSlots * kStageBytes;
+    __half *p_hi = reinterpret_cast<__half *>(smem + Lay::oP + warp * Lay::kP), *p_lo = p_hi + G * kPRowHalves;
+    int8_t *q_codes = reinterpret_cast<int8_t *>(smem + Lay::oQCodes) + warp * G * kHD;
+    float *q_scale = reinterpret_cast<float *>(smem + Lay::oQScale) + warp * G * kNQB;
+    const int n = lane >> 2, t4 = lane & 3;   // MMA fragment coordinates
+
+    TailCursor at;   // the stage that is decoded
+    at.b = ms->b0[warp];
+    at.load(p, cap);
+    {
+        const long long rel = lo - ms->base[warp];
+        at.h = (int)(rel / at.nb);
+        at.j = (int)(rel - (long long)at.h * at.nb);
+    }
+    TailCursor ask = at;   // the stage that is copied next
+    // of the unit that is asked for: queries, new token, block ids
+    float qx[G][4];
+    float4 nxk = make_float4(0.f, 0.f, 0.f, 0.f), nxv = nxk;
+    int blk = -1, phys = -1, phys_next = -1, new_phys = -1;
+    auto enter = [&]() {
+        const float *q = p.q + ((size_t)ask.b * p.nqh + (size_t)ask.h * G) * kHD;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) qx[g][k] = q[g * kHD + 32 * k + lane];
+        if (p.k_new) {
+            const size_t src = ((size_t)ask.b * p.nkv + ask.h) * kHD;
+            nxk = reinterpret_cast<const float4 *>(p.k_new + src)[lane];
+            nxv = reinterpret_cast<const float4 *>(p.v_new + src)[lane];
+            new_phys = p.block_table[(size_t)ask.b * p.max_blocks + (ask.sp.y - 1) / kBS];
+        }
+        blk = -1;
+    };
+    const uint64_t pol = l2_evict_first_policy();
+    uint32_t skips = 0;   // bit s: slot s holds a stage whose block id is outside the pool
+    auto copy = [&](int slot) {   // the stage that is asked for, into a slot
+        const int t0 = ask.sp.x + ask.j * kStageTok, lb = t0 / kBS, quarter = (t0 / kStageTok) & 3;
+        if (lb != blk) {
+            const int32_t *row = p.block_table + (size_t)ask.b * p.max_blocks;
+            phys = blk >= 0 ? phys_next : row[lb];
+            phys_next = lb + 1 < p.max_blocks ? row[lb + 1] : -1;   // (in time for the next block)
+            blk = lb;
+        }
+        const bool ok = phys >= 0 && phys < p.num_blocks;
+        skips = ok ? skips & ~(1u << slot) : skips | 1u << slot;
+        if (lane == 0) {
+            const uint32_t bar = smem_addr(full + slot), dst = smem_addr(slots + slot * kStageBytes);
+            if (ok) {
+                const size_t tile = (size_t)phys * p.nkv + ask.h;
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                bulk_copy_g2s(dst, p.k_pool + (tile * kBS + quarter * kStageTok) * kHD, kStageKBytes, bar, pol);
+                bulk_copy_g2s(dst + kStageKBytes, p.v_pool + tile * kHD * kBS + quarter * kTileVQuarter, kStageVBytes, bar, pol);
+                bulk_copy_g2s(dst + kStageKBytes + kStageVBytes, p.k_scale + tile * kBS + quarter * kStageTok, kStageSBytes, bar, pol);
+                bulk_copy_g2s(dst + kStageKBytes + kStageVBytes + kStageSBytes, p.v_scale + tile * kBS + quarter * kStageTok,
+                              kStageSBytes, bar, pol);
+            } else {
+                flag_status(p.dev_status, KVQ8_DEV_BAD_BLOCK_ID);
+                mbar_arrive(bar);
+            }
+        }
+        ++ask.j;
+    };
+    float M[G], Sl[G], acc[8][4];
+    int e_cur = 1000;
+    bool begin = true, gave_up = false;
+    enter();
+    int asked = 0;
+    // Copies stages as long as there is a slot and the unit that is decoded ends no later than the one asked for
+    // (whose queries wait in registers): the next unit's first stage is asked for when this unit's queries are coded.
+    bool entered = true;   // the queries in registers are still to be coded
+#pragma unroll 1
+    for (int k = 0; k < total; ++k) {
+        if (begin) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                quantize_q_vals_warp(qx[g], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
+                M[g] = -INFINITY;
+                Sl[g] = 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][i] = 0.0f;
+            e_cur = 1000;
+            entered = false;
+            __syncwarp();
+        }
+        const float4 token_k = nxk, token_v = nxv;
+        const int token_phys = new_phys;
+        // (the copies ahead)
+        while (!gave_up && asked < total && asked < k + kTailSlots) {
+            if (ask.j == ask.nb) {
+                if (entered) break;
+                ask.next_unit(p, cap);
+                enter();
+                entered = true;
+            }
+            copy(asked & (kTailSlots - 1));
+            ++asked;
+        }
+        const int slot = k & (kTailSlots - 1);
+        const unsigned char *st = slots + slot * kStageBytes;
+        if (!gave_up && !mbar_wait_tries(smem_addr(full + slot), (k / kTailSlots) & 1)) {
+            gave_up = true;
+            if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
+        }
+        gave_up = __any_sync(0xffffffffu, gave_up);
+        if (!gave_up && !(skips >> slot & 1)) {
+            const int t0 = at.sp.x + at.j * kStageTok, pos = at.sp.y - 1;
+            // (a step's token: at the end of a context that the table holds)
+            if (p.k_new && pos - t0 < kStageTok && p.ctx_lens[at.b] == at.sp.y)
+                append_new_token<false>(p, at.b, at.h, pos, pos - t0, lane, const_cast<unsigned char *>(st), token_k, token_v, token_phys);
+            const bool va = t0 + lane >= at.sp.lo && t0 + lane < at.sp.y;
+            const bool vb = t0 + lane + 32 >= at.sp.lo && t0 + lane + 32 < at.sp.y;
+            tail_stage<G>(st, q_codes, q_scale, p_hi, p_lo, lane, n, t4, va, vb, p.sm_scale_log2, M, Sl, acc, e_cur);
+        }
+        __syncwarp();
+        begin = ++at.j == at.nb;
+        if (begin || k + 1 == total) {
+            // ---- the record of this worker's part of the unit ----
+            const size_t u = (size_t)at.b * p.nkv + at.h, rec = worker + u;
+            if (G <= 4) {
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    if (G == 1) {
+                        acc[mt][0] += acc[mt][1];
+                        acc[mt][2] += acc[mt][3];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[mt][i] += __shfl_xor_sync(0xffffffffu, acc[mt][i], G / 2);
+                    }
+                }
+            }
+            const float unit = __int_as_float((127 + max(-126, min(127, e_cur))) << 23);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float s = warp_sum(Sl[g]);
+                if (lane == 0) *reinterpret_cast<float2 *>(p.ws_ml + (rec * G + g) * 2) = make_float2(M[g], s);
+            }
+            float *out = p.ws_acc + rec * G * kHD + n;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = 2 * t4 + i;
+                    if (g < G) {
+                        out[g * kHD + mt * 16] = acc[mt][i] * kCodeUnit * unit;
+                        out[g * kHD + mt * 16 + 8] = acc[mt][2 + i] * kCodeUnit * unit;
+                    }
+                }
+            }
+            const int first = k + 1 - at.j;   // the unit's first stage, as a stage of this worker's
+            if (lane == 0 && first >= 0)
+                p.ws_meta[u] = make_int2(worker, (int)(((lo + first + at.nb) * W + T - 1) / T) - worker);
+            if (begin) at.next_unit(p, cap);
+        }
+    }
+    // no copy may still be in flight when the warp leaves
+    if (lane == 0) {
+        for (int k = max(0, asked - kTailSlots); k < asked; ++k)
+            mbar_wait_bounded(smem_addr(full + (k & (kTailSlots - 1))), (k / kTailSlots) & 1, kWaitTimeoutNs);
+    }
+}
+
+template <int G>
+cudaError_t launch_tail_g(const DecodeParams &p, cudaStream_t s) {
+    static std::atomic<uint64_t> configured{0};
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(min(sms, kMaxCtas / kTailWarps));   // (a record per worker: kMaxCtas of them)
+    cfg.blockDim = dim3(kTailWarps * 32);
+    cfg.dynamicSmemBytes = TailLay<G>::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_after_setting(
+        configured,
+        [] {
+            return cudaFuncSetAttribute(decode_tail_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, TailLay<G>::kBytes);
+        },
+        [&] { return cudaLaunchKernelEx(&cfg, decode_tail_kernel<G>, p); });
+}
+
+}  // namespace
+}  // namespace kvq8

@@ -208,6 +208,7 @@ struct TileParams {
     int n_groups;
     int step;                     // 1: the token at ctx_lens[b] - 1 is the row's own
     int32_t *ws_tail;             // [batch]: the row's first token behind the shared ones
+    int32_t *ws_first;            // [batch]: the first row of the row's group
     int4 *ws_group;               // [n_groups]: (first row, rows, row read through, shared tokens)
     int tile_rows;                // rows of a tile (set with the launch)
     // partial results.  Prompt: CTA c's rows at c * 2 * kTileRows (a tile that it

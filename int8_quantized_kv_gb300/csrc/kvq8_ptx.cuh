@@ -72,6 +72,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return true;
 }
 
+// Waits for a phase by up to 2^20 tries that sleep up to two microseconds each; false when they are used up.  (The
+// nanosecond timer is slow to read: a chain of short waits has this one.)
+__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity) {
+    int left = 1 << 20;
+#pragma unroll 1
+    while (!mbar_try_wait_for(bar, parity, 2000u))
+        if (--left == 0) return false;
+    return true;
+}
+
 // L2 policy for data read exactly once (the streamed KV cache).
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
     uint64_t pol;

@@ -1001,7 +1001,7 @@ shared_plan_kernel(TileParams p) {
     const int stride = gridDim.x * kPlanWarps;
     if (bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.dev_status, KVQ8_DEV_BAD_GROUPS);
-        for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.batch; b += gridDim.x * blockDim.x) p.ws_tail[b] = 0;
+        for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.batch; b += gridDim.x * blockDim.x) p.ws_tail[b] = p.ws_first[b] = 0;
         for (int g = blockIdx.x * blockDim.x + threadIdx.x; g < p.n_groups; g += gridDim.x * blockDim.x)
             p.ws_group[g] = make_int4(0, 0, 0, 0);
         return;
@@ -1013,6 +1013,7 @@ shared_plan_kernel(TileParams p) {
         for (int b = b0 + lane; b < b1; b += 32) {
             const int x = row_shared(p, b, shared, cap);
             p.ws_tail[b] = x;
+            p.ws_first[b] = b0;
             if (x > most) {
                 most = x;
                 lead = b;
