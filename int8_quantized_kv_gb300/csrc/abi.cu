@@ -51,8 +51,8 @@ kvq8_status fill_decode_params(const float *q, int batch, int nqh, int nkv,
                                const float *v_scale, int num_blocks, const int32_t *block_table,
                                int max_blocks, const int32_t *ctx_lens, float sm_scale,
                                const void *workspace, size_t workspace_bytes,
-                               uint32_t *dev_status, DecodeParams *p, DecodePlan *plan) {
-    if (!make_decode_plan(batch, nqh, nkv, max_blocks, plan)) return KVQ8_ERR_INVALID_ARG;
+                               uint32_t *dev_status, DecodeParams *p, DecodePlan *plan, int workers = kMaxCtas) {
+    if (!make_decode_plan(batch, nqh, nkv, max_blocks, plan, workers)) return KVQ8_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan->bytes)
         return KVQ8_ERR_WORKSPACE;
     char *ws = (char *)workspace;
@@ -672,10 +672,12 @@ static TileWorkspace shared_workspace(int batch, int nqh) {
 
 size_t kvq8_shared_workspace_bytes(int batch, int n_groups, int nqh, int nkv, int hd, int max_blocks,
                                    int block_size) {
-    const size_t base = kvq8_decode_workspace_bytes(batch, nqh, nkv, hd, max_blocks, block_size);
-    if (!base || n_groups < 0 || n_groups > kMaxGridYZ || (int64_t)batch * nqh > 2147483647 - kMaxTileCtas * kTileRows)
+    DecodePlan plan;
+    if (check_shape(hd, block_size) != KVQ8_OK || check_heads(nqh, nkv) != KVQ8_OK ||
+        !make_decode_plan(batch, nqh, nkv, max_blocks, &plan, kMaxTailWorkers))
         return 0;
-    return base + up256((size_t)batch * 2 * sizeof(int32_t)) + up256((size_t)n_groups * sizeof(int4)) +
+    if (n_groups < 0 || n_groups > kMaxGridYZ || (int64_t)batch * nqh > 2147483647 - kMaxTileCtas * kTileRows) return 0;
+    return plan.bytes + up256((size_t)batch * 2 * sizeof(int32_t)) + up256((size_t)n_groups * sizeof(int4)) +
            shared_workspace(batch, nqh).bytes;
 }
 
@@ -699,7 +701,8 @@ static kvq8_status run_shared(const float *q, const float *k_new, const float *v
     DecodeParams d;
     DecodePlan plan;
     st = fill_decode_params(q, batch, nqh, nkv, k_pool, v_pool, k_scale, v_scale, num_blocks, block_table,
-                            max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &d, &plan);
+                            max_blocks, ctx_lens, sm_scale, workspace, workspace_bytes, dev_status, &d, &plan,
+                            kMaxTailWorkers);
     if (st != KVQ8_OK) return st;
     const size_t tails = plan.bytes, groups = tails + up256((size_t)batch * 2 * sizeof(int32_t));
     const size_t tiles = groups + up256((size_t)n_groups * sizeof(int4));

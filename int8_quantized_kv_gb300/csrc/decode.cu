@@ -254,13 +254,13 @@ cudaError_t launch_split_g(const DecodeParams &p, cudaStream_t s) {
 
 }  // namespace
 
-bool make_decode_plan(int batch, int nqh, int nkv, int max_blocks, DecodePlan *plan) {
+bool make_decode_plan(int batch, int nqh, int nkv, int max_blocks, DecodePlan *plan, int workers) {
     if (batch < 0 || nqh <= 0 || nkv <= 0 || max_blocks <= 0 || nqh % nkv) return false;
     const int G = nqh / nkv;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     plan->group = G;
     plan->units = (int64_t)batch * nkv;
-    plan->records = kMaxCtas + plan->units;
+    plan->records = workers + plan->units;
     plan->meta_offset = 0;
     plan->ml_offset = align((size_t)plan->units * sizeof(int2));
     plan->acc_offset = plan->ml_offset + align((size_t)plan->records * G * 2 * sizeof(float));

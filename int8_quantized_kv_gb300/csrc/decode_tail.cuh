@@ -6,11 +6,14 @@
 // the queries, the meeting of the warps' states and the record are paid per
 // unit and CTA (224 rows x 8 heads of 100 to 700 tokens: 80 us for what can be
 // read in 28).  Here every warp is a worker by itself: it takes an equal,
-// contiguous share of the sequence of all units' stages, copies its stages
-// (two slots of 16.5 KiB, six warps on an SM), keeps the state of its unit in
-// registers and writes the unit's record from there; queries, block ids and a
-// step's new token are loaded when the unit's first stage is asked for, two
-// stages ahead of their use.  The arithmetic of a stage is decode_split.cuh's.
+// contiguous share of the sequence of all units' stages, keeps the state of its
+// unit in registers and writes the unit's record from there.  A stage takes a
+// lone warp some 7000 clocks, so warps count, not stages in flight: each has
+// room for one stage, whose K is overwritten with the next one's when the dot
+// products are done and whose V when the sums are, so that each copy has half a
+// stage's time (12 warps an SM with one stage each against 6 with two: 56 us -> 40).  Queries, block ids and a step's new token are loaded
+// when the unit's first stage is asked for.  The arithmetic of a stage is
+// decode_split.cuh's.
 #pragma once
 
 #include "decode_split.cuh"
@@ -18,47 +21,35 @@
 namespace kvq8 {
 namespace {
 
-constexpr int kTailWarps = 6, kTailSlots = 2;
-
 template <int G>
 struct TailLay {
+    static constexpr int kWarps = G == 8 ? 8 : 12;                     // (255 or 170 registers a thread)
     static constexpr int kP = (G * 2 * kPRowHalves * 2 + 15) / 16 * 16;
-    static constexpr int oSlots = 0;                                   // [warp][slot]
-    static constexpr int oP = kTailWarps * kTailSlots * kStageBytes;   // [warp]
-    static constexpr int oQCodes = oP + kTailWarps * kP;
-    static constexpr int oQScale = oQCodes + kTailWarps * G * kHD;
-    static constexpr int oFull = oQScale + kTailWarps * G * kNQB * 4;
-    static constexpr int oMisc = oFull + kTailWarps * kTailSlots * 8;
-    static constexpr int kBytes = oMisc + 256;
+    static constexpr int oStage = 0;                                   // [warp]
+    static constexpr int oP = kWarps * kStageBytes;                    // [warp]
+    static constexpr int oQCodes = oP + kWarps * kP;
+    static constexpr int oQScale = oQCodes + kWarps * G * kHD;
+    static constexpr int oFull = oQScale + kWarps * G * kNQB * 4;
+    static constexpr int oMisc = oFull + kWarps * 2 * 8;
+    static constexpr int kBytes = oMisc + 320;
     static_assert(oQScale % 16 == 0 && oFull % 8 == 0 && oMisc % 16 == 0, "alignment");
     static_assert(kBytes <= kSmemLimit, "shared memory budget");
 };
 
 struct TailMisc {
-    long long warp_tot[kTailWarps];
-    long long base[kTailWarps];   // worker: stages ahead of its first sequence
-    int b0[kTailWarps];           // worker: that sequence
+    long long warp_tot[12];
+    long long base[12];   // worker: stages ahead of its first sequence
+    int b0[12];           // worker: that sequence
 };
+static_assert(sizeof(TailMisc) <= 320, "misc");
 
-// One staged stage for the G query heads of a unit: the state (M, Sl, acc in units of 2^e_cur) takes in the tokens lane
-// (where va) and lane + 32 (where vb).  p_hi, p_lo: the warp's room for P.
+// Base-2 scores of a staged stage's tokens lane and lane + 32 (-inf where not va, vb) for the G query heads of a unit.
 template <int G>
-__device__ __forceinline__ void tail_stage(const unsigned char *st, const int8_t *q_codes, const float *q_scale,
-                                             __half *p_hi, __half *p_lo, int lane, int n, int t4, bool va, bool vb, float sm_scale_log2,
-                                             float (&M)[G], float (&Sl)[G], float (&acc)[8][4], int &e_cur) {
+__device__ __forceinline__ void tail_scores(const unsigned char *st, const int8_t *q_codes, const float *q_scale, int lane,
+                                            bool va, bool vb, float sm_scale_log2, float (&sa)[G], float (&sb)[G]) {
     const int8_t *kst = reinterpret_cast<const int8_t *>(st);
-    const int8_t *vst = kst + kStageKBytes;
     const float *ks_st = reinterpret_cast<const float *>(st + kStageKBytes + kStageVBytes);
-    const float *vs_st = ks_st + kStageTok;
     const int ta = lane, tb = lane + 32;
-    // n, t4: MMA fragment coordinates (lane / 4, lane % 4).
-    // P.V for G <= 4 packs P's high fp16 parts into columns 0..G-1 and its
-    // low parts into G..2G-1 of one MMA (half the MMAs); the columns' sums
-    // are added at the segment's end.  Accumulator columns 2*t4, 2*t4 + 1
-    // then belong to heads col_head0, col_head1 (for their rescaling).
-    constexpr bool kPackPV = G <= 4;
-    const int col_head0 = kPackPV ? (2 * t4) % G : 2 * t4;
-    const int col_head1 = kPackPV ? (2 * t4 + 1) % G : 2 * t4 + 1;
     // ---- segment 2a: int32 block dots, lane = token ----
     int da[G][kNQB], db[G][kNQB];
 #pragma unroll
@@ -82,19 +73,6 @@ __device__ __forceinline__ void tail_stage(const unsigned char *st, const int8_t
         }
     }
     const float ksa = ks_st[ta], ksb = ks_st[tb];
-    const float vsa = va ? vs_st[ta] : 0.0f, vsb = vb ? vs_st[tb] : 0.0f;
-
-    // power-of-two unit of this stage's P: 2^e > max vs, so that
-    // p' = w * vs * 2^-e stays below 2^8 (w < 2^8, see below).  e only
-    // moves when it must grow or has become 2^12 too large.
-    const int e_need = redux_max_i32(
-        ((__float_as_int(fmaxf(vsa, vsb)) >> 23) & 0xff) - 126);  // 0 -> -126
-    int e = e_cur;
-    if (e_need > e_cur || e_need < e_cur - 12) e = max(-120, min(120, e_need));
-    const float inv = __int_as_float((127 - e) << 23);
-
-    // ---- segment 2b: scores, online softmax ----
-    float sa[G], sb[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const float4 qs = *reinterpret_cast<const float4 *>(q_scale + g * kNQB);
@@ -109,6 +87,34 @@ __device__ __forceinline__ void tail_stage(const unsigned char *st, const int8_t
         sa[g] = va ? a * ksa * sm_scale_log2 : -INFINITY;
         sb[g] = vb ? bb * ksb * sm_scale_log2 : -INFINITY;
     }
+}
+
+// The state (M, Sl, acc in units of 2^e_cur) takes these tokens in, vsa and vsb their V scales (0 where masked).  p_hi,
+// p_lo: the warp's room for P.
+template <int G>
+__device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi, __half *p_lo, int lane, int n, int t4, bool va,
+                                          bool vb, float vsa, float vsb, const float (&sa)[G], const float (&sb)[G],
+                                          float (&M)[G], float (&Sl)[G], float (&acc)[8][4], int &e_cur) {
+    const int8_t *vst = reinterpret_cast<const int8_t *>(st) + kStageKBytes;
+    const int ta = lane, tb = lane + 32;
+    // n, t4: MMA fragment coordinates (lane / 4, lane % 4).
+    // P.V for G <= 4 packs P's high fp16 parts into columns 0..G-1 and its
+    // low parts into G..2G-1 of one MMA (half the MMAs); the columns' sums
+    // are added at the segment's end.  Accumulator columns 2*t4, 2*t4 + 1
+    // then belong to heads col_head0, col_head1 (for their rescaling).
+    constexpr bool kPackPV = G <= 4;
+    const int col_head0 = kPackPV ? (2 * t4) % G : 2 * t4;
+    const int col_head1 = kPackPV ? (2 * t4 + 1) % G : 2 * t4 + 1;
+    // power-of-two unit of this stage's P: 2^e > max vs, so that
+    // p' = w * vs * 2^-e stays below 2^8 (w < 2^8, see below).  e only
+    // moves when it must grow or has become 2^12 too large.
+    const int e_need = redux_max_i32(
+        ((__float_as_int(fmaxf(vsa, vsb)) >> 23) & 0xff) - 126);  // 0 -> -126
+    int e = e_cur;
+    if (e_need > e_cur || e_need < e_cur - 12) e = max(-120, min(120, e_need));
+    const float inv = __int_as_float((127 - e) << 23);
+
+    // ---- segment 2b: online softmax ----
     // The running maximum M is raised only when a score exceeds it by
     // more than 2^kLazyLog2; below that the weights 2^(s-M) stay < 2^8
     // and every quantity remains exact to fp32 rounding.
@@ -228,15 +234,16 @@ struct TailCursor {
 };
 
 template <int G>
-__global__ void __launch_bounds__(kTailWarps * 32, 1)
+__global__ void __launch_bounds__((TailLay<G>::kWarps * 32), 1)
 decode_tail_kernel(DecodeParams p) {
     using Lay = TailLay<G>;
+    constexpr int kTailWarps = Lay::kWarps;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cap = p.max_blocks * kBS;
     TailMisc *ms = reinterpret_cast<TailMisc *>(smem + Lay::oMisc);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::oFull) + warp * kTailSlots;
-    if (lane < kTailSlots) {
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::oFull) + warp * 2;   // of K and scales, of V
+    if (lane < 2) {
         mbar_init(smem_addr(full + lane), 1);
         fence_mbar_init();
     }
@@ -296,7 +303,8 @@ decode_tail_kernel(DecodeParams p) {
     const long long lo = share(worker);
     const int total = (int)(share(worker + 1) - lo);
 
-    unsigned char *slots = smem + Lay::oSlots + warp * kTailSlots * kStageBytes;
+    unsigned char *st = smem + Lay::oStage + warp * kStageBytes;
+    const float *vs_st = reinterpret_cast<const float *>(st + kStageKBytes + kStageVBytes) + kStageTok;
     __half *p_hi = reinterpret_cast<__half *>(smem + Lay::oP + warp * Lay::kP), *p_lo = p_hi + G * kPRowHalves;
     int8_t *q_codes = reinterpret_cast<int8_t *>(smem + Lay::oQCodes) + warp * G * kHD;
     float *q_scale = reinterpret_cast<float *>(smem + Lay::oQScale) + warp * G * kNQB;
@@ -330,24 +338,25 @@ decode_tail_kernel(DecodeParams p) {
         blk = -1;
     };
     const uint64_t pol = l2_evict_first_policy();
-    uint32_t skips = 0;   // bit s: slot s holds a stage whose block id is outside the pool
-    auto copy = [&](int slot) {   // the stage that is asked for, into a slot
-        const int t0 = ask.sp.x + ask.j * kStageTok, lb = t0 / kBS, quarter = (t0 / kStageTok) & 3;
+    bool skip = false, skip_next = false;   // the stage's block id is outside the pool
+    size_t tile = 0;
+    int quarter = 0;
+    auto copy_k = [&]() {   // K and the scales of the stage that is asked for
+        const int t0 = ask.sp.x + ask.j * kStageTok, lb = t0 / kBS;
+        quarter = (t0 / kStageTok) & 3;
         if (lb != blk) {
             const int32_t *row = p.block_table + (size_t)ask.b * p.max_blocks;
             phys = blk >= 0 ? phys_next : row[lb];
             phys_next = lb + 1 < p.max_blocks ? row[lb + 1] : -1;   // (in time for the next block)
             blk = lb;
         }
-        const bool ok = phys >= 0 && phys < p.num_blocks;
-        skips = ok ? skips & ~(1u << slot) : skips | 1u << slot;
+        skip_next = phys < 0 || phys >= p.num_blocks;
+        tile = skip_next ? 0 : (size_t)phys * p.nkv + ask.h;
         if (lane == 0) {
-            const uint32_t bar = smem_addr(full + slot), dst = smem_addr(slots + slot * kStageBytes);
-            if (ok) {
-                const size_t tile = (size_t)phys * p.nkv + ask.h;
-                mbar_arrive_expect_tx(bar, kStageBytes);
+            const uint32_t bar = smem_addr(full), dst = smem_addr(st);
+            if (!skip_next) {
+                mbar_arrive_expect_tx(bar, kStageKBytes + 2 * kStageSBytes);
                 bulk_copy_g2s(dst, p.k_pool + (tile * kBS + quarter * kStageTok) * kHD, kStageKBytes, bar, pol);
-                bulk_copy_g2s(dst + kStageKBytes, p.v_pool + tile * kHD * kBS + quarter * kTileVQuarter, kStageVBytes, bar, pol);
                 bulk_copy_g2s(dst + kStageKBytes + kStageVBytes, p.k_scale + tile * kBS + quarter * kStageTok, kStageSBytes, bar, pol);
                 bulk_copy_g2s(dst + kStageKBytes + kStageVBytes + kStageSBytes, p.v_scale + tile * kBS + quarter * kStageTok,
                               kStageSBytes, bar, pol);
@@ -356,18 +365,34 @@ decode_tail_kernel(DecodeParams p) {
                 mbar_arrive(bar);
             }
         }
-        ++ask.j;
+    };
+    auto copy_v = [&]() {   // V of the same stage
+        if (lane == 0) {
+            const uint32_t bar = smem_addr(full + 1);
+            if (!skip_next) {
+                mbar_arrive_expect_tx(bar, kStageVBytes);
+                bulk_copy_g2s(smem_addr(st + kStageKBytes), p.v_pool + tile * kHD * kBS + quarter * kTileVQuarter, kStageVBytes, bar, pol);
+            } else {
+                mbar_arrive(bar);
+            }
+        }
     };
     float M[G], Sl[G], acc[8][4];
     int e_cur = 1000;
     bool begin = true, gave_up = false;
+    auto wait = [&](int which, int k) {
+        if (!gave_up && !mbar_wait_tries(smem_addr(full + which), k & 1)) {
+            gave_up = true;
+            if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
+        }
+        gave_up = __any_sync(0xffffffffu, gave_up);
+    };
     enter();
-    int asked = 0;
-    // Copies stages as long as there is a slot and the unit that is decoded ends no later than the one asked for
-    // (whose queries wait in registers): the next unit's first stage is asked for when this unit's queries are coded.
-    bool entered = true;   // the queries in registers are still to be coded
+    copy_k();
+    copy_v();
+    int copied = 1;   // stages asked for
 #pragma unroll 1
-    for (int k = 0; k < total; ++k) {
+    for (int k = 0; k < total && !gave_up; ++k) {
         if (begin) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -380,39 +405,40 @@ decode_tail_kernel(DecodeParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][i] = 0.0f;
             e_cur = 1000;
-            entered = false;
             __syncwarp();
         }
-        const float4 token_k = nxk, token_v = nxv;
-        const int token_phys = new_phys;
-        // (the copies ahead)
-        while (!gave_up && asked < total && asked < k + kTailSlots) {
-            if (ask.j == ask.nb) {
-                if (entered) break;
-                ask.next_unit(p, cap);
-                enter();
-                entered = true;
-            }
-            copy(asked & (kTailSlots - 1));
-            ++asked;
+        skip = skip_next;
+        const int t0 = at.sp.x + at.j * kStageTok, pos = at.sp.y - 1;
+        const bool va = t0 + lane >= at.sp.lo && t0 + lane < at.sp.y;
+        const bool vb = t0 + lane + 32 >= at.sp.lo && t0 + lane + 32 < at.sp.y;
+        wait(0, k);
+        // (a step's token: at the end of a context that the table holds)
+        const bool append = p.k_new && pos - t0 < kStageTok && !skip && p.ctx_lens[at.b] == at.sp.y;
+        if (append) {
+            wait(1, k);
+            append_new_token<false>(p, at.b, at.h, pos, pos - t0, lane, st, nxk, nxv, new_phys);
+            fence_async_smem();   // (the next copies overwrite what it wrote)
+            __syncwarp();
         }
-        const int slot = k & (kTailSlots - 1);
-        const unsigned char *st = slots + slot * kStageBytes;
-        if (!gave_up && !mbar_wait_tries(smem_addr(full + slot), (k / kTailSlots) & 1)) {
-            gave_up = true;
-            if (lane == 0) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
-        }
-        gave_up = __any_sync(0xffffffffu, gave_up);
-        if (!gave_up && !(skips >> slot & 1)) {
-            const int t0 = at.sp.x + at.j * kStageTok, pos = at.sp.y - 1;
-            // (a step's token: at the end of a context that the table holds)
-            if (p.k_new && pos - t0 < kStageTok && p.ctx_lens[at.b] == at.sp.y)
-                append_new_token<false>(p, at.b, at.h, pos, pos - t0, lane, const_cast<unsigned char *>(st), token_k, token_v, token_phys);
-            const bool va = t0 + lane >= at.sp.lo && t0 + lane < at.sp.y;
-            const bool vb = t0 + lane + 32 >= at.sp.lo && t0 + lane + 32 < at.sp.y;
-            tail_stage<G>(st, q_codes, q_scale, p_hi, p_lo, lane, n, t4, va, vb, p.sm_scale_log2, M, Sl, acc, e_cur);
+        float sa[G], sb[G], vsa = 0.0f, vsb = 0.0f;
+        if (!skip) {
+            tail_scores<G>(st, q_codes, q_scale, lane, va, vb, p.sm_scale_log2, sa, sb);
+            if (va) vsa = vs_st[lane];
+            if (vb) vsb = vs_st[lane + 32];
         }
         __syncwarp();
+        if (k + 1 < total && !gave_up) {   // K's room is free
+            if (++ask.j == ask.nb) {
+                ask.next_unit(p, cap);
+                enter();
+            }
+            copy_k();
+            ++copied;
+        }
+        if (!append) wait(1, k);
+        if (!skip) tail_sums<G>(st, p_hi, p_lo, lane, n, t4, va, vb, vsa, vsb, sa, sb, M, Sl, acc, e_cur);
+        __syncwarp();
+        if (copied == k + 2) copy_v();
         begin = ++at.j == at.nb;
         if (begin || k + 1 == total) {
             // ---- the record of this worker's part of the unit ----
@@ -453,10 +479,9 @@ decode_tail_kernel(DecodeParams p) {
             if (begin) at.next_unit(p, cap);
         }
     }
-    // no copy may still be in flight when the warp leaves
-    if (lane == 0) {
-        for (int k = max(0, asked - kTailSlots); k < asked; ++k)
-            mbar_wait_bounded(smem_addr(full + (k & (kTailSlots - 1))), (k / kTailSlots) & 1, kWaitTimeoutNs);
+    // no copy may still be in flight when the warp leaves (after a wait that gave up)
+    if (gave_up && lane == 0) {
+        for (int i = 0; i < 2; ++i) mbar_wait_bounded(smem_addr(full + i), (copied - 1) & 1, kWaitTimeoutNs);
     }
 }
 
@@ -466,8 +491,8 @@ cudaError_t launch_tail_g(const DecodeParams &p, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(min(sms, kMaxCtas / kTailWarps));   // (a record per worker: kMaxCtas of them)
-    cfg.blockDim = dim3(kTailWarps * 32);
+    cfg.gridDim = dim3(min(sms, kMaxTailWorkers / TailLay<G>::kWarps));   // (a record per worker)
+    cfg.blockDim = dim3(TailLay<G>::kWarps * 32);
     cfg.dynamicSmemBytes = TailLay<G>::kBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -85,6 +85,7 @@ constexpr int kStageSBytes = kStageTok * 4;       // 256
 constexpr int kStageBytes = kStageKBytes + kStageVBytes + 2 * kStageSBytes;
 constexpr int kTileVQuarter = kHD * kStageTok;    // bytes of one V quarter
 constexpr int kMaxCtas = 1024;                    // upper bound of the split grid
+constexpr int kMaxTailWorkers = 2048;             // upper bound of decode_tail_kernel's workers (one record each)
 
 // Split-KV plan: the split kernel runs one persistent CTA per SM; the global
 // sequence of 64-token stages (units in order (sequence, kv head)) is cut into
@@ -93,10 +94,10 @@ constexpr int kMaxCtas = 1024;                    // upper bound of the split gr
 struct DecodePlan {
     int group;          // G = nqh / nkv
     int64_t units;      // batch * nkv
-    int64_t records;    // kMaxCtas + units
+    int64_t records;    // workers (kMaxCtas) + units
     size_t meta_offset, ml_offset, acc_offset, bytes;  // workspace layout
 };
-bool make_decode_plan(int batch, int nqh, int nkv, int max_blocks, DecodePlan *plan);
+bool make_decode_plan(int batch, int nqh, int nkv, int max_blocks, DecodePlan *plan, int workers = kMaxCtas);
 
 struct DecodeParams {
     const float *q;               // [batch][nqh][hd]
