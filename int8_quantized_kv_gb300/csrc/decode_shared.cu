@@ -27,7 +27,7 @@ shared_merge_kernel(DecodeParams d, TileParams t, int G) {
     const int64_t x0 = ((int64_t)h * t.batch + b0) * G;
     const int4 dir = own > 0 ? t.ws_dir[x0 + n / t.tile_rows * t.tile_rows] : make_int4(0, 0, 0, 0);
     const int shared = dir.y, count = shared + (own < L ? meta.y : 0);
-    const int64_t r1 = x0 + n + (int64_t)dir.x * kTileRows, r2 = ((int64_t)meta.x + u) * G + g;
+    const int64_t r1 = x0 + n + (int64_t)dir.x * t.tile_rows, r2 = ((int64_t)meta.x + u) * G + g;
     float m = -INFINITY, s_sum = 0.0f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kAtOnce = 4;
@@ -42,7 +42,7 @@ shared_merge_kernel(DecodeParams d, TileParams t, int G) {
             x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < count) {
                 const bool s = i < shared;
-                const int64_t r = s ? r1 + (int64_t)i * kTileRows : r2 + (int64_t)(i - shared) * G;
+                const int64_t r = s ? r1 + (int64_t)i * t.tile_rows : r2 + (int64_t)(i - shared) * G;
                 ml[k] = *reinterpret_cast<const float2 *>((s ? t.ws_ml : d.ws_ml) + r * 2);
                 x[k] = *reinterpret_cast<const float4 *>((s ? t.ws_acc : d.ws_acc) + r * kHD + 4 * lane);
             }

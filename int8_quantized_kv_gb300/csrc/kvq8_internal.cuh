@@ -186,7 +186,7 @@ cudaError_t launch_rope_table(const double *inv_freq, int64_t n_pos, float *tabl
 // over the tokens up to its own position), or of the batch rows that share a
 // prefix.  Row n of a tile is token n / G, head n % G of the kv head.
 constexpr int kTileRows = 128;
-constexpr int kMaxTileCtas = 160;     // upper bound of the tile kernels' grid
+constexpr int kMaxTileCtas = 160;     // upper bound of the tile kernels' grid (twice that for tiles of 32 rows)
 struct TileParams {
     const void *q;                // rows of q_dtype; q_stride elements from one token to the next
     int q_dtype;
@@ -212,11 +212,11 @@ struct TileParams {
     int32_t *ws_first;            // [batch]: the first row of the row's group
     int4 *ws_group;               // [n_groups]: (first row, rows, row read through, shared tokens)
     int tile_rows;                // rows of a tile (set with the launch)
-    // partial results.  Prompt: CTA c's rows at c * 2 * kTileRows (a tile that it
-    // goes on with) and kTileRows later (a tile that it begins and another ends),
+    // partial results, for tiles of R rows.  Prompt: CTA c's rows at c * 2 * R (a tile
+    // that it goes on with) and R later (a tile that it begins and another ends),
     // ws_dir[c] says of which tile the latter is.  Shared prefix: row x of the
     // batch * nqh rows, ordered by (kv head, batch row, head), by CTA c at
-    // x + c * kTileRows; ws_dir[x of a tile's first row] = (first CTA, their count).
+    // x + c * R; ws_dir[x of a tile's first row] = (first CTA, their count).
     int4 *ws_dir;
     float *ws_ml;                 // [..][2]: running max M (base 2), sum S
     float *ws_acc;                // [..][128]

@@ -42,7 +42,6 @@ namespace kvq8 {
 namespace {
 
 constexpr int kTok = 128;                       // tokens per stage
-constexpr int kSoftmaxWarps = 16;
 // What a tile costs beside its stages (queries, first references, output), in stages: the CTAs' shares count it, or
 // one that gets many short tiles ends long after the others.
 constexpr int kTileCost = 4;
@@ -54,8 +53,6 @@ constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end
 // when P would pass 2^15.9 (fp16 ends below 2^16).
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
 constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this when M is set (rows of zeros do)
-// columns of tensor memory, all of which is the CTA's (so that it begins at address 0)
-constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = 384;
 
 // Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
 template <int kRows, bool kLow>
@@ -68,19 +65,28 @@ struct Lay {
     static constexpr int oMisc = oP + kP;
     static constexpr int kMisc = 13312;
     static constexpr int oRing = oMisc + kMisc;
-    static constexpr int kSlots = (232448 - oRing) / kSlotBytes < 8 ? (232448 - oRing) / kSlotBytes : 8;
+    // Tiles of up to 32 rows: two CTAs to an SM, with half of its shared and tensor memory each.  Their stages are
+    // chains of short steps (operands, scores, softmax, output), which one CTA's warps wait through and two fill.
+    static constexpr int kCtas = kRows == 32 ? 2 : 1;
+    static constexpr int kLimit = kCtas == 2 ? 115712 : 232448;
+    static constexpr int kSlots = (kLimit - oRing) / kSlotBytes < 8 ? (kLimit - oRing) / kSlotBytes : 8;
     static constexpr int kBytes = oRing + kSlots * kSlotBytes;
     static_assert(kSlots >= 4, "ring too shallow");
-    // Operand warps: tiles of few rows are bound by them (the softmax of a stage is short, the codes are the
-    // same), so K and V get four warps each there.
-    static constexpr int kOperandWarps = kWide ? 4 : 8;
+    // columns of tensor memory: kBufs of K's operand and of V's, scores, output
+    static constexpr int kBufs = kCtas == 2 ? 1 : 2, kColumns = 512 / kCtas;
+    static constexpr int kColK = 0, kColV = 64 * kBufs, kColS = 128 * kBufs, kColO = kColS + (kWide ? kRows : 2 * kRows);
+    static_assert(kColO + (kWide ? kRows : 2 * kRows) <= kColumns, "tensor memory");
+    // Operand warps: in tiles of 64 rows K and V get four warps each, since the softmax of a stage is short there and
+    // the codes are the same.
+    static constexpr int kOperandWarps = kRows == 64 ? 8 : 4;
+    static constexpr int kSoftmaxWarps = kCtas == 2 ? 8 : 16;
     static constexpr int kSoftmaxWarp0 = 4 + kOperandWarps;
     static constexpr int kThreads = (kSoftmaxWarp0 + kSoftmaxWarps) * 32;
     // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
     // operands; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
     // leaves it no L1.
-    static constexpr int kLaunchRegs = kWide ? 80 : 72, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
-    static_assert(kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs || !kWide,
+    static constexpr int kLaunchRegs = 80, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
+    static_assert(!kWide || kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs,
                   "registers");
 };
 
@@ -99,7 +105,7 @@ struct Misc {
     long long warp_tot[32];
     int s0, r0, off;
     volatile int abort;
-    uint32_t tmem;
+    uint32_t tmem;                              // address of the CTA's columns
     int skip[8];                                // slot: its block id is outside the pool
     int bad[4];                                 // stage (mod 4): the same
     int lim_min[4];                             // tile (mod 4)
@@ -275,10 +281,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 template <bool kShared, int kRows, bool kLow>
-__global__ void __launch_bounds__((Lay<kRows, kLow>::kThreads), 1)
+__global__ void __launch_bounds__((Lay<kRows, kLow>::kThreads), (Lay<kRows, kLow>::kCtas))
 tile_kernel(TileParams p, int lg) {
     using L = Lay<kRows, kLow>;
-    constexpr int kThreads = L::kThreads;
+    constexpr int kThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps, kBufs = L::kBufs;
     constexpr bool kWide = L::kWide;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *ms = reinterpret_cast<Misc *>(smem + L::oMisc);
@@ -312,7 +318,7 @@ tile_kernel(TileParams p, int lg) {
         fence_mbar_init();
         ms->abort = 0;
     }
-    if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), 512);
+    if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), L::kColumns);
     pdl_wait();
     pdl_launch_dependents();   // (the next kernel's CTAs find no registers here before this one leaves)
     // ---- this CTA's share: [lo, hi) of the sequence of all tiles, each as long as it costs ----
@@ -341,6 +347,8 @@ tile_kernel(TileParams p, int lg) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (a CTA that has all columns has them from 0 on)
+    const uint32_t tmem = L::kColumns == 512 ? 0 : ms->tmem;
     before -= mine;
     long long total = 0;   // cost of one kv head
 #pragma unroll 1
@@ -460,13 +468,15 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide ? kRows : 2 * kRows, false);
-                        wait_warp(&ms->k_ready[x & 1], (x >> 1) & 1, ms);
+                        const int buf = x % kBufs;
+                        const uint32_t d = tmem + L::kColS, a = tmem + L::kColK + buf * 64;
+                        wait_warp(&ms->k_ready[buf], (x / kBufs) & 1, ms);
                         wait_warp(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
-                        mma_k128(kColS, kColK + (x & 1) * 64, b, kWord, false);
-                        if (kWide) mma_k128(kColS, kColK + (x & 1) * 64, b + kLowPart, kWord, true);
+                        mma_k128(d, a, b, kWord, false);
+                        if (kWide) mma_k128(d, a, b + kLowPart, kWord, true);
                         mma_commit(smem_addr(&ms->s_full));
-                        mma_commit(smem_addr(&ms->k_free[x & 1]));
+                        mma_commit(smem_addr(&ms->k_free[buf]));
                     }
                     mma_commit(smem_addr(&ms->q_free));
                 } else {
@@ -474,13 +484,15 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
-                        wait_warp(&ms->v_ready[x & 1], (x >> 1) & 1, ms);
+                        const int buf = x % kBufs;
+                        const uint32_t d = tmem + L::kColO, a = tmem + L::kColV + buf * 64;
+                        wait_warp(&ms->v_ready[buf], (x / kBufs) & 1, ms);
                         wait_warp(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
-                        mma_k128(kColO, kColV + (x & 1) * 64, b, kWord, i > 0);
-                        if (kWide && kLow) mma_k128(kColO, kColV + (x & 1) * 64, b + kLowPart, kWord, true);
+                        mma_k128(d, a, b, kWord, i > 0);
+                        if (kWide && kLow) mma_k128(d, a, b + kLowPart, kWord, true);
                         mma_commit(smem_addr(&ms->pv_done));
-                        mma_commit(smem_addr(&ms->v_free[x & 1]));
+                        mma_commit(smem_addr(&ms->v_free[buf]));
                     }
                 }
             }
@@ -534,7 +546,7 @@ tile_kernel(TileParams p, int lg) {
                         part.head = w.h;
                         part.token = (int)w.token(w.r, 0);
                         part.direct = !kShared && whole;
-                        part.rec = kShared ? x + (long long)c * kTileRows : ((long long)c * 2 + (from == 0 ? 1 : 0)) * kTileRows;
+                        part.rec = kShared ? x + (long long)c * kRows : ((long long)c * 2 + (from == 0 ? 1 : 0)) * kRows;
                         if (from == 0) {   // the CTAs c .. that hold this tile's records
                             const long long end = hi - left - off + kTileCost + stages;
                             const int cnt = (int)divide(end * C + T - 1, T) - c;
@@ -558,8 +570,8 @@ tile_kernel(TileParams p, int lg) {
         if constexpr (kWide) regs_shrink<L::kRegsOperand>();
         // ========================= operands =========================
         const int quad = warp & 3, row = 32 * quad + lane;
-        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const bool keys = kWide || warp < 8, values = kWide || warp >= 8;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        const bool keys = L::kOperandWarps == 4 || warp < 8, values = L::kOperandWarps == 4 || warp >= 8;
         int j = 0;
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
@@ -571,7 +583,8 @@ tile_kernel(TileParams p, int lg) {
             int behind = part.end - part.off * kTok - row;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, behind -= kTok) {
-                const uint32_t par = (j >> 1) & 1;
+                const int buf = j % kBufs;
+                const uint32_t par = (j / kBufs) & 1;
                 if (keys) {
                     // K: lane = token, the row's chunk c stands at c ^ (token & 7)
                     const int g = 2 * j, at = g % L::kSlots;
@@ -584,17 +597,17 @@ tile_kernel(TileParams p, int lg) {
                     if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
-                    wait_warp(&ms->k_free[j & 1], par ^ 1, ms);
+                    wait_warp(&ms->k_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
 #pragma unroll(kWide ? 1 : 4)
                     for (int k = 0; k < 4; ++k)
-                        put_codes(lanes + kColK + (j & 1) * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
+                        put_codes(lanes + L::kColK + buf * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(smem_addr(&ms->k_ready[j & 1]));
+                        mbar_arrive(smem_addr(&ms->k_ready[buf]));
                         mbar_arrive(smem_addr(&ms->empty[at]));
                     }
                 }
@@ -605,7 +618,7 @@ tile_kernel(TileParams p, int lg) {
                     const int g = 2 * j + 1, at = g % L::kSlots;
                     const unsigned char *st = smem + L::oRing + at * kSlotBytes;
                     wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
-                    wait_warp(&ms->v_free[j & 1], par ^ 1, ms);
+                    wait_warp(&ms->v_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const int turn = (lane >> 1) & 3;
 #pragma unroll(kWide ? 1 : 2)
@@ -618,14 +631,14 @@ tile_kernel(TileParams p, int lg) {
                         for (int k = 0; k < 4; ++k) b[k] = (turn & 1) ? a[(k + 3) & 3] : a[k];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) a[k] = (turn & 2) ? b[(k + 2) & 3] : b[k];
-                        put_codes(lanes + kColV + (j & 1) * 64 + 32 * q, a[0], a[1]);
-                        put_codes(lanes + kColV + (j & 1) * 64 + 32 * q + 16, a[2], a[3]);
+                        put_codes(lanes + L::kColV + buf * 64 + 32 * q, a[0], a[1]);
+                        put_codes(lanes + L::kColV + buf * 64 + 32 * q + 16, a[2], a[3]);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(smem_addr(&ms->v_ready[j & 1]));
+                        mbar_arrive(smem_addr(&ms->v_ready[buf]));
                         mbar_arrive(smem_addr(&ms->empty[at]));
                     }
                 }
@@ -634,11 +647,11 @@ tile_kernel(TileParams p, int lg) {
     } else {
         if constexpr (kWide) regs_grow<L::kRegsSoftmax>();
         // ========================== softmax ==========================
-        constexpr int kCols = kRows / 4;      // a warp's rows
+        constexpr int kCols = kRows / (kSoftmaxWarps / 4);   // a warp's rows
         // the four warps of a share of the rows see to it by themselves
         const int quad = warp & 3, share = (warp - L::kSoftmaxWarp0) >> 2, c0 = share * kCols, st = tid & 127;
         const int bar = 1 + share;
-        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         // Scores and P are held as MMA fragments: a thread has the tokens 32 quad + 8 m + lane / 4 (m < 4) of the
         // stage and the rows c0 + 8 g + 2 (lane % 4) + {0, 1} (g < kGroups) of the tile, so that what concerns a
         // row stays in registers (with a token per thread each row's reference and gain come from shared memory
@@ -767,16 +780,16 @@ tile_kernel(TileParams p, int lg) {
                 tc_fence_after();
                 // scores relative to the references: [pair of matrices][group][matrix of the pair][row of two]
                 float t[2][kGroups][2][2];
-                tmem_ld_fragments<kGroups>(lanes + kColS + c0, &t[0][0][0][0]);
-                tmem_ld_fragments<kGroups>(lanes + (16u << 16) + kColS + c0, &t[1][0][0][0]);
+                tmem_ld_fragments<kGroups>(lanes + L::kColS + c0, &t[0][0][0][0]);
+                tmem_ld_fragments<kGroups>(lanes + (16u << 16) + L::kColS + c0, &t[1][0][0][0]);
                 if constexpr (kWide) {
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < kVals * 4; ++k) asm volatile("" : "+f"((&t[0][0][0][0])[k]));
                 } else {
                     float low[kVals * 4];
-                    tmem_ld_fragments<kGroups>(lanes + kColS + kRows + c0, low);
-                    tmem_ld_fragments<kGroups>(lanes + (16u << 16) + kColS + kRows + c0, low + kVals * 2);
+                    tmem_ld_fragments<kGroups>(lanes + L::kColS + kRows + c0, low);
+                    tmem_ld_fragments<kGroups>(lanes + (16u << 16) + L::kColS + kRows + c0, low + kVals * 2);
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < kVals * 4; ++k) {
@@ -853,7 +866,7 @@ tile_kernel(TileParams p, int lg) {
                         for (int x = 0; x < (!kWide && kLow ? 2 : 1); ++x) {
 #pragma unroll 1
                             for (int k = 0; k < kCols; k += 8) {
-                                const uint32_t at = lanes + kColO + x * kRows + c0 + k;
+                                const uint32_t at = lanes + L::kColO + x * kRows + c0 + k;
                                 float o[8];
                                 uint32_t v[8];
                                 tmem_ld8(at, o);
@@ -944,8 +957,8 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll(kWide ? 2 : 1)
             for (int k = 0; k < kCols; k += 8) {
                 float x[8], y[8];
-                tmem_ld8(lanes + kColO + c0 + k, x);
-                if (!kWide && kLow) tmem_ld8(lanes + kColO + kRows + c0 + k, y);
+                tmem_ld8(lanes + L::kColO + c0 + k, x);
+                if (!kWide && kLow) tmem_ld8(lanes + L::kColO + kRows + c0 + k, y);
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -979,7 +992,7 @@ tile_kernel(TileParams p, int lg) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(0, 512);
+    if (warp == 1) tmem_dealloc(tmem, L::kColumns);
     if (tid == 0 && ms->abort) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
 }
 
@@ -1042,7 +1055,7 @@ prompt_merge_kernel(TileParams p, int lg, int rows_per_tile) {
     const int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
     if (i >= w.tile_rows(w.r)) return;
     // record k: of CTA c + k; the first one is c's own second place
-    auto at = [&](int k) { return ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * kTileRows + i; };
+    auto at = [&](int k) { return ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * rows_per_tile + i; };
     float m = -INFINITY;
     for (int k = lane; k < dir.x; k += 32) m = fmaxf(m, p.ws_ml[at(k) * 2]);
     m = warp_max(m);
@@ -1085,12 +1098,13 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, in
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-int tile_ctas() { return min(device_sm_count(), kMaxTileCtas); }
+// CTAs of a launch: as many as the SMs hold.
+int tile_ctas(int rows) { return min(device_sm_count(), kMaxTileCtas) * (rows == 32 ? Lay<32, true>::kCtas : 1); }
 
 template <bool kShared, int kRows, bool kLow>
 cudaError_t launch_tiles(const TileParams &p, int lg, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
-    const int ctas = tile_ctas();
+    const int ctas = tile_ctas(kRows);
     if (ctas <= 0) return cudaErrorInvalidDevice;
     return launch_after_setting(
         configured,
@@ -1129,7 +1143,7 @@ cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
         e = rows == 128 ? launch_tiles<false, 128, true>(p, lg, s)
             : rows == 64 ? launch_tiles<false, 64, true>(p, lg, s) : launch_tiles<false, 32, true>(p, lg, s);
     if (e != cudaSuccess) return e;
-    return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
+    return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(rows), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
 }
 
 cudaError_t launch_shared_prefix(TileParams &p, int group, cudaStream_t s) {
