@@ -49,10 +49,10 @@ constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
 constexpr int kCoreRow = 2048;                  // bytes between cores along the rows (16 cores of 128 B along k)
 constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end: two seconds
-// A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^8 and 2^9 when M is set; M moves
-// when P would pass 2^15.9 (fp16 ends below 2^16).
+// A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^7 and 2^9 when M is set; M moves
+// when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
-constexpr float kTinyScaleLog2 = -60.0f;        // V scales below count as this when M is set (rows of zeros do)
+constexpr int kTinyScaleLog2 = -60;             // V scales below count as this (rows of zeros do)
 
 // Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
 template <int kRows, bool kLow>
@@ -99,7 +99,7 @@ struct Part {
 
 struct Misc {
     uint64_t full[8], empty[8];                 // ring slots
-    uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2], sc_ready[4];
+    uint64_t k_ready[2], k_free[2], v_ready[2], v_free[2];
     uint64_t part_ready[4], part_free[4];
     uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done[2];
     long long warp_tot[32];
@@ -253,6 +253,17 @@ __device__ __forceinline__ void halve(float *v, int lane, Op op) {
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The least whole number above log2 of a V scale (kTinyScaleLog2 at least), by its exponent bits.
+__device__ __forceinline__ float exponent_above(float scale) {
+    return __int_as_float(max(__float_as_int(scale) >> 23, kTinyScaleLog2 + 126) | 0x4b000000) - (0x1p23f + 126.0f);
+}
+
 // a / b for positive b; in 32 bits where that does.
 __device__ __forceinline__ long long divide(long long a, long long b) {
     if (((a | b) >> 31) == 0) return (int)a / (int)b;
@@ -302,7 +313,6 @@ tile_kernel(TileParams p, int lg) {
             mbar_init(smem_addr(&ms->v_free[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_addr(&ms->sc_ready[i]), 4);
             mbar_init(smem_addr(&ms->part_ready[i]), 1);
             mbar_init(smem_addr(&ms->part_free[i]), kSoftmaxWarps);
         }
@@ -595,8 +605,6 @@ tile_kernel(TileParams p, int lg) {
                     const bool real = !skip && behind > 0;
                     ms->scale[j & 3][row] = make_float2(real ? scales[row] * p.sm_scale_log2 : 0.0f, real ? scales[kTok + row] : 0.0f);
                     if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ms->sc_ready[j & 3]));
                     wait_warp(&ms->k_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
@@ -771,13 +779,12 @@ tile_kernel(TileParams p, int lg) {
             int t0 = ms->part[seg & 3].off * kTok;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
-                wait_warp(&ms->sc_ready[j & 3], (j >> 2) & 1, ms);
+                wait_warp(&ms->s_full, j & 1, ms);   // (the scales were there before the scores' operand)
+                tc_fence_after();
                 float2 sc[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) sc[m] = ms->scale[j & 3][32 * quad + 8 * m + (lane >> 2)];
                 const bool bad = ms->bad[j & 3] != 0;
-                wait_warp(&ms->s_full, j & 1, ms);
-                tc_fence_after();
                 // scores relative to the references: [pair of matrices][group][matrix of the pair][row of two]
                 float t[2][kGroups][2][2];
                 tmem_ld_fragments<kGroups>(lanes + L::kColS + c0, &t[0][0][0][0]);
@@ -825,21 +832,21 @@ tile_kernel(TileParams p, int lg) {
                     }
                 }
                 bool raise = fresh;
-                float vs_log2[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    vs_log2[m] = fmaxf(__log2f(sc[m].y), kTinyScaleLog2);
-                    float top = fmaxf(t[m >> 1][0][m & 1][0], t[m >> 1][0][m & 1][1]);
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, fmaxf(t[m >> 1][g][m & 1][0], t[m >> 1][g][m & 1][1]));
-                    raise |= top > kPMaxLog2 - vs_log2[m];
+                    for (int g = 0; g < kGroups; ++g) top = max3(top, t[m >> 1][g][m & 1][0], t[m >> 1][g][m & 1][1]);
+                    raise |= top > kPMaxLog2 - exponent_above(sc[m].y);
                 }
                 bool rest = i == 0;   // the product before is done: P's room is free, the accumulator at rest
                 if (__builtin_expect(barrier_any(bar, 128, raise), 0)) {
                     // move the references of rows whose P would leave fp16's range (at first: of all), by whole
                     // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
                     // stage of one leaves the rows fresh
-                    float top[kVals];
+                    float top[kVals], vs_log2[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) vs_log2[m] = exponent_above(sc[m].y);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
