@@ -186,7 +186,7 @@ cudaError_t launch_rope_table(const double *inv_freq, int64_t n_pos, float *tabl
 // over the tokens up to its own position), or of the batch rows that share a
 // prefix.  Row n of a tile is token n / G, head n % G of the kv head.
 constexpr int kTileRows = 128;
-constexpr int kMaxTileCtas = 160;     // upper bound of the tile kernels' grid (twice that for tiles of 32 rows)
+constexpr int kMaxTileCtas = 160;     // upper bound of the tile kernels' grid
 struct TileParams {
     const void *q;                // rows of q_dtype; q_stride elements from one token to the next
     int q_dtype;

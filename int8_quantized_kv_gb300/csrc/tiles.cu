@@ -48,6 +48,9 @@ constexpr int kTileCost = 4;
 constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
 constexpr int kCoreRow = 2048;                  // bytes between cores along the rows (16 cores of 128 B along k)
+constexpr int kLimit = 232448;                  // bytes of shared memory
+constexpr int kColumns = 512;                   // of tensor memory: all
+constexpr int kSoftmaxWarp0 = 12;               // warps before: 4 for copies, MMAs and order, 4 for K's operands, 4 for V's
 constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end: two seconds
 // A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^7 and 2^9 when M is set; M moves
 // when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
@@ -65,28 +68,21 @@ struct Lay {
     static constexpr int oMisc = oP + kP;
     static constexpr int kMisc = 13312;
     static constexpr int oRing = oMisc + kMisc;
-    // Tiles of up to 32 rows: two CTAs to an SM, with half of its shared and tensor memory each.  Their stages are
-    // chains of short steps (operands, scores, softmax, output), which one CTA's warps wait through and two fill.
-    static constexpr int kCtas = kRows == 32 ? 2 : 1;
-    static constexpr int kLimit = kCtas == 2 ? 115712 : 232448;
     static constexpr int kSlots = (kLimit - oRing) / kSlotBytes < 8 ? (kLimit - oRing) / kSlotBytes : 8;
     static constexpr int kBytes = oRing + kSlots * kSlotBytes;
     static_assert(kSlots >= 4, "ring too shallow");
-    // columns of tensor memory: kBufs of K's operand and of V's, scores, output
-    static constexpr int kBufs = kCtas == 2 ? 1 : 2, kColumns = 512 / kCtas;
-    static constexpr int kColK = 0, kColV = 64 * kBufs, kColS = 128 * kBufs, kColO = kColS + (kWide ? kRows : 2 * kRows);
+    // columns of tensor memory: two of K's operand and of V's, scores, output
+    static constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = kColS + (kWide ? kRows : 2 * kRows);
     static_assert(kColO + (kWide ? kRows : 2 * kRows) <= kColumns, "tensor memory");
-    // Operand warps: in tiles of 64 rows K and V get four warps each, since the softmax of a stage is short there and
-    // the codes are the same.
-    static constexpr int kOperandWarps = kRows == 64 ? 8 : 4;
-    static constexpr int kSoftmaxWarps = kCtas == 2 ? 8 : 16;
-    static constexpr int kSoftmaxWarp0 = 4 + kOperandWarps;
+    // Softmax warps: as many as fill the SM's registers, but for tiles of 32 rows, where a warp of sixteen would have
+    // 8 rows (8 prompts of 5 tokens x 32 heads: 33.1 us with sixteen, 32.2 us with eight).
+    static constexpr int kSoftmaxWarps = kRows == 32 ? 8 : 16;
     static constexpr int kThreads = (kSoftmaxWarp0 + kSoftmaxWarps) * 32;
     // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
-    // operands; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
+    // K's operands; V's; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
     // leaves it no L1.
-    static constexpr int kLaunchRegs = 80, kRegsIssue = 48, kRegsOperand = 48, kRegsSoftmax = 96;
-    static_assert(!kWide || kRegsIssue + kRegsOperand + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs,
+    static constexpr int kLaunchRegs = 72, kRegsOther = 40, kRegsSoftmax = 96;
+    static_assert(!kWide || kSoftmaxWarp0 / 4 * kRegsOther + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs,
                   "registers");
 };
 
@@ -105,7 +101,7 @@ struct Misc {
     long long warp_tot[32];
     int s0, r0, off;
     volatile int abort;
-    uint32_t tmem;                              // address of the CTA's columns
+    uint32_t tmem;                              // address of the columns
     int skip[8];                                // slot: its block id is outside the pool
     int bad[4];                                 // stage (mod 4): the same
     int lim_min[4];                             // tile (mod 4)
@@ -291,11 +287,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+// a - b, b in fp16
+__device__ __forceinline__ float minus(float a, __half b) {
+    float d;
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(__half_as_ushort(b)), "h"((unsigned short)0xbc00), "f"(a));
+    return d;
+}
+
 template <bool kShared, int kRows, bool kLow>
-__global__ void __launch_bounds__((Lay<kRows, kLow>::kThreads), (Lay<kRows, kLow>::kCtas))
+__global__ void __launch_bounds__((Lay<kRows, kLow>::kThreads), 1)
 tile_kernel(TileParams p, int lg) {
     using L = Lay<kRows, kLow>;
-    constexpr int kThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps, kBufs = L::kBufs;
+    constexpr int kThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
     constexpr bool kWide = L::kWide;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *ms = reinterpret_cast<Misc *>(smem + L::oMisc);
@@ -328,7 +331,7 @@ tile_kernel(TileParams p, int lg) {
         fence_mbar_init();
         ms->abort = 0;
     }
-    if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), L::kColumns);
+    if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), kColumns);
     pdl_wait();
     pdl_launch_dependents();   // (the next kernel's CTAs find no registers here before this one leaves)
     // ---- this CTA's share: [lo, hi) of the sequence of all tiles, each as long as it costs ----
@@ -357,8 +360,7 @@ tile_kernel(TileParams p, int lg) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // (a CTA that has all columns has them from 0 on)
-    const uint32_t tmem = L::kColumns == 512 ? 0 : ms->tmem;
+    constexpr uint32_t tmem = 0;   // (who has all columns has them from 0 on)
     before -= mine;
     long long total = 0;   // cost of one kv head
 #pragma unroll 1
@@ -403,7 +405,7 @@ tile_kernel(TileParams p, int lg) {
     }
 
     if (warp < 4) {
-        if constexpr (kWide) regs_shrink<L::kRegsIssue>();
+        if constexpr (kWide) regs_shrink<L::kRegsOther>();
         if (warp == 0) {
             // ============================ copies ============================
             int g = 0;   // granules so far: K and V of every stage
@@ -478,9 +480,9 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide ? kRows : 2 * kRows, false);
-                        const int buf = x % kBufs;
+                        const int buf = x & 1;
                         const uint32_t d = tmem + L::kColS, a = tmem + L::kColK + buf * 64;
-                        wait_warp(&ms->k_ready[buf], (x / kBufs) & 1, ms);
+                        wait_warp(&ms->k_ready[buf], (x >> 1) & 1, ms);
                         wait_warp(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
                         mma_k128(d, a, b, kWord, false);
@@ -494,9 +496,9 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
-                        const int buf = x % kBufs;
+                        const int buf = x & 1;
                         const uint32_t d = tmem + L::kColO, a = tmem + L::kColV + buf * 64;
-                        wait_warp(&ms->v_ready[buf], (x / kBufs) & 1, ms);
+                        wait_warp(&ms->v_ready[buf], (x >> 1) & 1, ms);
                         wait_warp(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
                         mma_k128(d, a, b, kWord, i > 0);
@@ -576,12 +578,11 @@ tile_kernel(TileParams p, int lg) {
                 if (left > 0) w.next(seqs);
             }
         }
-    } else if (warp < L::kSoftmaxWarp0) {
-        if constexpr (kWide) regs_shrink<L::kRegsOperand>();
+    } else if (warp < kSoftmaxWarp0) {
+        if constexpr (kWide) regs_shrink<L::kRegsOther>();
         // ========================= operands =========================
         const int quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        const bool keys = L::kOperandWarps == 4 || warp < 8, values = L::kOperandWarps == 4 || warp >= 8;
         int j = 0;
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
@@ -593,9 +594,9 @@ tile_kernel(TileParams p, int lg) {
             int behind = part.end - part.off * kTok - row;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, behind -= kTok) {
-                const int buf = j % kBufs;
-                const uint32_t par = (j / kBufs) & 1;
-                if (keys) {
+                const int buf = j & 1;
+                const uint32_t par = (j >> 1) & 1;
+                if (warp < 8) {
                     // K: lane = token, the row's chunk c stands at c ^ (token & 7)
                     const int g = 2 * j, at = g % L::kSlots;
                     const unsigned char *st = smem + L::oRing + at * kSlotBytes;
@@ -608,7 +609,7 @@ tile_kernel(TileParams p, int lg) {
                     wait_warp(&ms->k_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
-#pragma unroll(kWide ? 1 : 4)
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k)
                         put_codes(lanes + L::kColK + buf * 64 + 16 * k, kr[(2 * k) ^ (lane & 7)], kr[(2 * k + 1) ^ (lane & 7)]);
                     tmem_wait_st();
@@ -618,8 +619,7 @@ tile_kernel(TileParams p, int lg) {
                         mbar_arrive(smem_addr(&ms->k_ready[buf]));
                         mbar_arrive(smem_addr(&ms->empty[at]));
                     }
-                }
-                if (values) {
+                } else {
                     // V: lane = dim; two 64-token quarters of 64 bytes.  Lanes 2 apart start at
                     // another chunk, so that eight lanes' 16-byte reads hit all banks, and turn
                     // the four chunks back into order
@@ -629,7 +629,7 @@ tile_kernel(TileParams p, int lg) {
                     wait_warp(&ms->v_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const int turn = (lane >> 1) & 3;
-#pragma unroll(kWide ? 1 : 2)
+#pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
                         const uint4 *vr = reinterpret_cast<const uint4 *>(st + q * kTileVQuarter + row * kStageTok);
                         uint4 a[4], b[4];
@@ -657,7 +657,7 @@ tile_kernel(TileParams p, int lg) {
         // ========================== softmax ==========================
         constexpr int kCols = kRows / (kSoftmaxWarps / 4);   // a warp's rows
         // the four warps of a share of the rows see to it by themselves
-        const int quad = warp & 3, share = (warp - L::kSoftmaxWarp0) >> 2, c0 = share * kCols, st = tid & 127;
+        const int quad = warp & 3, share = (warp - kSoftmaxWarp0) >> 2, c0 = share * kCols, st = tid & 127;
         const int bar = 1 + share;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         // Scores and P are held as MMA fragments: a thread has the tokens 32 quad + 8 m + lane / 4 (m < 4) of the
@@ -677,10 +677,10 @@ tile_kernel(TileParams p, int lg) {
             if (barrier_any(bar, 128, !ok)) return false;
             const Part &part = ms->part[seg & 3];
             if (part.stages == 0) return false;
-            if (warp - L::kSoftmaxWarp0 < kRows / 8) {
+            if (warp - kSoftmaxWarp0 < kRows / 8) {
                 // eight rows to a warp: lane l has row l % 8, and of every 32-block the dims 8 (l / 8) .. + 7, a
                 // 16-byte line of an operand's core, so that eight lanes fill a core
-                const int i = (warp - L::kSoftmaxWarp0) * 8 + (lane & 7);
+                const int i = (warp - kSoftmaxWarp0) * 8 + (lane & 7);
                 float4 x[8];
                 const bool real = i < part.rows;
                 const int64_t src = real ? ((long long)part.token + (i >> lg)) * p.q_stride +
@@ -732,7 +732,7 @@ tile_kernel(TileParams p, int lg) {
                 const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
                 const float down = exp2_int(-e);
                 wait_warp(&ms->q_free, (seg & 1) ^ 1, ms);
-                unsigned char *at = smem + L::oQ + (warp - L::kSoftmaxWarp0) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
+                unsigned char *at = smem + L::oQ + (warp - kSoftmaxWarp0) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const float iq = __fdiv_rn(127.0f, top[b]), unit = __fmul_rn(top[b], KVQ8_INV127) * down;
@@ -916,8 +916,7 @@ tile_kernel(TileParams p, int lg) {
                         const __half2 a = __floats2half2_rn(v.x, v.y);
                         hi[g][m] = half2_bits(a);
                         if (kLow) {
-                            const float2 d = fma2(__half22float2(a), make_float2(-1.f, -1.f), v);
-                            lo[g][m] = half2_bits(__floats2half2_rn(d.x, d.y));
+                            lo[g][m] = half2_bits(__floats2half2_rn(minus(v.x, __low2half(a)), minus(v.y, __high2half(a))));
                         }
                     }
                 }
@@ -999,7 +998,7 @@ tile_kernel(TileParams p, int lg) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, L::kColumns);
+    if (warp == 1) tmem_dealloc(tmem, kColumns);
     if (tid == 0 && ms->abort) flag_status(p.dev_status, KVQ8_DEV_TIMEOUT);
 }
 
@@ -1105,13 +1104,13 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, in
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// CTAs of a launch: as many as the SMs hold.
-int tile_ctas(int rows) { return min(device_sm_count(), kMaxTileCtas) * (rows == 32 ? Lay<32, true>::kCtas : 1); }
+// CTAs of a launch: one to an SM.
+int tile_ctas() { return min(device_sm_count(), kMaxTileCtas); }
 
 template <bool kShared, int kRows, bool kLow>
 cudaError_t launch_tiles(const TileParams &p, int lg, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
-    const int ctas = tile_ctas(kRows);
+    const int ctas = tile_ctas();
     if (ctas <= 0) return cudaErrorInvalidDevice;
     return launch_after_setting(
         configured,
@@ -1150,7 +1149,7 @@ cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
         e = rows == 128 ? launch_tiles<false, 128, true>(p, lg, s)
             : rows == 64 ? launch_tiles<false, 64, true>(p, lg, s) : launch_tiles<false, 32, true>(p, lg, s);
     if (e != cudaSuccess) return e;
-    return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(rows), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
+    return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
 }
 
 cudaError_t launch_shared_prefix(TileParams &p, int group, cudaStream_t s) {
