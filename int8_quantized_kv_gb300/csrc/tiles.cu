@@ -951,7 +951,9 @@ tile_kernel(TileParams p, int lg) {
                                    (long long)((part.head << lg) + (x & ((1 << lg) - 1))) * kHD);
                     } else {
                         dst = reinterpret_cast<char *>(p.ws_acc + (part.rec + x) * kHD);
-                        *reinterpret_cast<float2 *>(p.ws_ml + (part.rec + x) * 2) = make_float2(-ms->ref[x], S);
+                        // (a row that sees none of these tokens has no reference: the merge must not go by its 0)
+                        *reinterpret_cast<float2 *>(p.ws_ml + (part.rec + x) * 2) =
+                            make_float2(S > 0.0f ? -ms->ref[x] : -INFINITY, S);
                     }
                 }
                 ms->dst[x] = dst;

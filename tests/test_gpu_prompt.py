@@ -316,3 +316,62 @@ def test_binding_refusals(gpu_lib):
     assert e.value.status == kvq8.ERR_INVALID_ARG
     empty = kvq8.prompt_attn(c.q[:, :0], c.cache, c.table, c.start_d, c.out[:, :0], c.ws)
     assert empty is None
+
+
+@pytest.mark.parametrize("level", [-300.0, 300.0])
+def test_rows_that_see_nothing_of_a_tiles_later_part(gpu_lib, level):
+    # few tiles: every CTA has one stage of one, so the records of the stages behind a row's position hold nothing of it
+    c = Prompt([60, 0], 300, 4, 2, 59)
+    c.q.fill_(1.0)
+    c.q += 0.01 * torch.randn(c.q.shape, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    c.cache.k_pool.fill_(100)
+    c.cache.k_scale.fill_(level / (100 * 128 * ref.SM))
+    c.run()
+    c.check(what=f"level={level}")
+
+
+def test_replayed_with_other_positions(gpu_lib):
+    # positions and counts are device data: a captured call follows them
+    c = Prompt([900, 900, 900], 40, 8, 2, 61, n_tokens=[40, 40, 40])
+    c.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq8.prompt_attn(c.q, c.cache, c.table, c.start_d, c.out, c.ws, n_tokens=c.n_d, dev_status=c.status)
+    for starts, ns in (([0, 300, 12], [40, 1, 17]), ([883, 0, 0], [0, 0, 5]), ([0, 0, 0], [0, 0, 0]), ([64, 63, 900], [40, 39, 38])):
+        c.start_d.copy_(torch.tensor(starts))
+        c.n_d.copy_(torch.tensor(ns))
+        c.starts, c.ns = starts, ns
+        c.out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(what=str(starts))
+    assert c.status.item() == 0
+
+
+def test_blocks_past_32_bits(gpu_lib):
+    # a pool of more than 2^32 bytes of K, of V, and the sequence's blocks at its end
+    c = Prompt([600], 70, 8, 8, 63)
+    nb, spare = c.table.numel() + 2, 2**32 // (8 * 256 * 128)
+    big = kvq8.KVCache(*(torch.empty((spare + nb,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in c.cache))
+    for x, y in zip(big, c.cache):
+        x[spare:] = y
+    want = c.run().clone()
+    c.cache, c.table = big, c.table + spare
+    c.out.fill_(float("nan"))
+    assert torch.equal(c.run(), want)
+    assert c.status.item() == 0
+
+
+def test_most_sequences_empty(gpu_lib):
+    ns = [0] * 20000
+    ns[0], ns[9999], ns[19999] = 3, 2, 1
+    c = Prompt([5] * 20000, 3, 8, 4, 65, n_tokens=ns)
+    c.run()
+    assert c.status.item() == 0
+    assert torch.isnan(c.out.flatten(2)).all(2).sum().item() == 3 * 20000 - 6
+    pick = Prompt.__new__(Prompt)
+    pick.__dict__.update(c.__dict__)
+    for b in (0, 9999, 19999):
+        pick.starts, pick.ns, pick.table = [5], [ns[b]], c.table[b:b + 1]
+        pick.q = c.q[b:b + 1]
+        pick.check(out=c.out[b:b + 1])

@@ -97,3 +97,42 @@ def test_append_and_read_back(gpu_lib):
     step = x.abs().amax(-1, keepdim=True) / 127
     assert bool(((k - x).abs() <= step * (0.5 + 127 * 2.0 ** -22)).all())
     assert torch.equal(v, -2 * k)
+
+
+def test_blocks_past_32_bits(gpu_lib):
+    table, nb = ref.random_table(1, 3, 9)
+    cache = ref.random_cache(nb, 8, 9)
+    start = torch.tensor([70], dtype=torch.int32, device="cuda")
+    spare = 2**32 // (8 * 256 * 128)
+    big = kvq8.KVCache(*(torch.empty((spare + nb,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in cache))
+    for x, y in zip(big, cache):
+        x[spare:] = y
+    got = [torch.empty((1, 600, 8, 128), device="cuda") for _ in range(4)]
+    kvq8.read_cache(cache, table, start, got[0], got[1])
+    kvq8.read_cache(big, table + spare, start, got[2], got[3])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
+def test_captured_and_replayed_with_other_positions(gpu_lib):
+    table, nb = ref.random_table(2, 3, 11)
+    cache = ref.random_cache(nb, 2, 11)
+    start = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    ns = torch.tensor([300, 300], dtype=torch.int32, device="cuda")
+    k, v = torch.empty((2, 300, 2, 128), device="cuda"), torch.empty((2, 300, 2, 128), device="cuda")
+    kvq8.read_cache(cache, table, start, k, v, n_tokens=ns)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq8.read_cache(cache, table, start, k, v, n_tokens=ns)
+    for starts, counts in (([5, 468], [300, 300]), ([255, 16], [1, 0])):
+        start.copy_(torch.tensor(starts))
+        ns.copy_(torch.tensor(counts))
+        k.fill_(7.0)
+        v.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, (p, m) in enumerate(zip(starts, counts)):
+            assert bool((k[b, m:] == 7).all()) and bool((v[b, m:] == 9).all())
+            for h in range(2):
+                wk, wv = _want(cache, table, b, h, torch.arange(p, p + m, device="cuda"))
+                assert torch.equal(k[b, :m, h], wk) and torch.equal(v[b, :m, h], wv)

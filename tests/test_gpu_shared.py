@@ -267,3 +267,71 @@ def test_replayed_with_other_lengths(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         c.check(what=str(first))
+
+
+@pytest.mark.parametrize("level", [-300.0, 300.0])
+def test_rows_that_see_nothing_of_the_prefixs_later_part(gpu_lib, level):
+    # the rows that end early in a prefix which several CTAs share: the later records hold nothing of them
+    c = Shared([5], [1500], [1501, 100, 300, 129, 1700], 4, 2, 245)
+    c.q.fill_(1.0)
+    c.q += 0.01 * torch.randn(c.q.shape, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    c.cache.k_pool.fill_(100)
+    c.cache.k_scale.fill_(level / (100 * 128 * ref.SM))
+    c.run()
+    c.check(what=f"level={level}")
+
+
+def test_step_captured_and_replayed(gpu_lib):
+    # each replay appends the tokens that then stand in k_new, v_new, at the lengths that then stand in ctx_lens
+    c = Shared([3, 2], [300, 128], [301, 340, 500, 129, 200], 8, 2, 247, step=True)
+    graph = torch.cuda.CUDAGraph()
+    c.run()
+    with torch.cuda.graph(graph):
+        kvq8.decode_step_shared(c.q, c.k_new, c.v_new, c.cache, c.table, c.lens_d, c.starts_d, c.prefix_d, c.out, c.ws)
+    g = torch.Generator("cuda").manual_seed(7)
+    for _ in range(3):
+        c.lens_d += 1
+        c.lens = [n + 1 for n in c.lens]
+        for x in (c.q, c.k_new, c.v_new):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check()
+        for b in range(5):                                       # the token stands in the cache
+            for h in range(2):
+                k, v = ref.rows64(c.cache, c.table[b], h, torch.tensor([c.lens[b] - 1], device="cuda"))
+                for got, x in ((k, c.k_new[b, h]), (v, c.v_new[b, h])):
+                    assert (got[0] - x.double()).abs().max() <= x.abs().max().double() / 127 * 0.5001
+
+
+def test_blocks_past_32_bits(gpu_lib):
+    c = Shared([3, 2], [600, 128], [601, 640, 800, 129, 200], 8, 8, 249, step=True)
+    before = [x.clone() for x in c.cache]
+    want = c.run().clone()
+    spare = 2**32 // (8 * 256 * 128)
+    big = kvq8.KVCache(*(torch.empty((spare + x.shape[0],) + x.shape[1:], dtype=x.dtype, device="cuda") for x in c.cache))
+    for x, y in zip(big, before):
+        x[spare:] = y
+    small = c.cache
+    c.cache = big
+    c.table = torch.where(c.table >= 0, c.table + spare, c.table)
+    c.out.fill_(float("nan"))
+    assert torch.equal(c.run(), want)
+    for x, y in zip(big, small):
+        assert torch.equal(x[spare:], y)
+    assert c.status.item() == 0
+
+
+def test_two_calls_at_once(gpu_lib):
+    a = Shared([20, 5], [2000, 400], [2001 + 9 * i for i in range(20)] + [401, 500, 700, 450, 410], 8, 2, 251)
+    b = Shared([4], [3000], [3001, 3100, 3300, 3500], 16, 2, 253)
+    wa, wb = a.run().clone(), b.run().clone()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        a.out.zero_()
+        b.out.zero_()
+        torch.cuda.synchronize()
+        for x, s in ((a, sa), (b, sb)):
+            kvq8.decode_attn_shared(x.q, x.cache, x.table, x.lens_d, x.starts_d, x.prefix_d, x.out, x.ws, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
