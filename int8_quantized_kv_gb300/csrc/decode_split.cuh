@@ -123,8 +123,6 @@ enum SplitMode {
     kScored = 2,     // every token, and its scores (base 2) are written to ws_scores
     kTail = 3        // tokens t >= windows[b] (here the row's first token behind its shared prefix; decode_tail.cuh)
 };
-// The windowed and scored decodes round with reciprocal factors (include/kvq8.h).
-constexpr bool recip_rule(int mode) { return mode == kWindowed || mode == kScored; }
 
 // The tokens of sequence b that this launch decodes: [x, y) in stages of 64
 // from x on, after `ns` stages from token 0 on (kWindowed: the first tokens).
@@ -531,7 +529,7 @@ decode_split_kernel(DecodeParams p) {
 #pragma unroll
             for (int i = 0; i < kQRows; ++i) {
                 const int g = warp + i * kConsumerWarps;
-                if (g < G) quantize_q_vals_warp<recip_rule(kMode)>(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
+                if (g < G) quantize_q_vals_warp<kMode != kWhole>(qx[i], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
             }
             named_barrier_sync(1, kConsumerWarps * 32);
             if (remaining > seg_n) {   // the next segment's unit follows this one
@@ -578,7 +576,7 @@ decode_split_kernel(DecodeParams p) {
                             nxk = reinterpret_cast<const float4 *>(p.k_new + src)[lane];
                             nxv = reinterpret_cast<const float4 *>(p.v_new + src)[lane];
                         }
-                        append_new_token<recip_rule(kMode)>(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
+                        append_new_token<kMode != kWhole>(p, b, h, app_pos, tnew, lane, const_cast<unsigned char *>(st), nxk, nxv, nphys);
                     }
                     const int ta = lane, tb = lane + 32;
                     bool va = ta < nvalid, vb = tb < nvalid;

@@ -5,14 +5,15 @@
 // which pays for long contexts: of a unit of six stages each warp has one, and
 // the queries, the meeting of the warps' states and the record are paid per
 // unit and CTA (224 rows x 8 heads of 100 to 700 tokens: 80 us for what can be
-// read in 28).  Here every warp is a worker by itself: it takes an equal,
+// read in 28; here 48).  Here every warp is a worker by itself: it takes an equal,
 // contiguous share of the sequence of all units' stages, keeps the state of its
 // unit in registers and writes the unit's record from there.  A stage takes a
 // lone warp some 7000 clocks, so warps count, not stages in flight: each has
 // room for one stage, whose K is overwritten with the next one's when the dot
 // products are done and whose V when the sums are, so that each copy has half a
-// stage's time (12 warps an SM with one stage each against 6 with two: 56 us -> 40).  Queries, block ids and a step's new token are loaded
-// when the unit's first stage is asked for.  The arithmetic of a stage is
+// stage's time (12 warps an SM with one stage each against 6 with two: 48 us
+// against 56).  Queries, block ids and a step's new token are loaded when the
+// unit's first stage is asked for.  The arithmetic of a stage is
 // decode_split.cuh's.
 #pragma once
 

@@ -34,18 +34,6 @@ __device__ __forceinline__ void store1(void *base, int dtype, int64_t i, float x
     else static_cast<__half *>(base)[i] = __float2half_rn(x);
 }
 
-// The group of row b: the last g with group_starts[g] <= b (of groups that are
-// known to cut the batch).
-__device__ __forceinline__ int group_of_row(const int32_t *starts, int n_groups, int b) {
-    int lo = 0, hi = n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] <= b) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Whether group entry g (0 .. n_groups) may be part of a cut of the batch.
 __device__ __forceinline__ bool group_entry_ok(const TileParams &p, int g) {
     const int s = p.group_starts[g];

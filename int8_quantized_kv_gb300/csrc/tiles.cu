@@ -23,16 +23,29 @@
 // the output's own rounding.
 //
 // A persistent CTA per SM takes an equal share of the (tile, 128-token stage)
-// sequence.  Warp 0 copies the stages (bulk copies into a ring), warps 1 and 3 issue
-// the MMAs of scores and output, warp 2 says which tiles, warps 4..7 turn the codes into operands and, per tile, the queries,
-// warps 8..15 take the softmax: the score tile is S^T, so a thread holds one
-// token of half the tile's rows, whose row sums it keeps for itself until the
-// tile ends.  A row's weights 2^(s - M) need no exact maximum: M is set so that
-// the row's largest weight * V scale fills fp16's range, and moved only when one
-// would leave it (a factor of 2^7 or more later), which a comparison per score
-// and one barrier over the eight warps find out; maxima across lanes are formed
-// only then.  (With M from the scores alone a row that leans on tokens of small
-// V would lose P's low bits next to one large V scale.)
+// sequence.  Warp 0 copies the stages (bulk copies into a ring, K and V apart),
+// warps 1 and 3 issue the MMAs of scores and output, warp 2 says which tiles,
+// warps 4..7 turn K's codes into operands and 8..11 V's, the others (16; 8 for
+// tiles of 32 rows) take the softmax, four warps to an equal share of the rows,
+// and prepare the next tile's queries behind their last stage.  S^T and P^T move
+// as MMA fragments (tcgen05.ld 16x256b, stmatrix), so that a thread holds tokens
+// of few rows, whose references and sums stay in its registers.  A row's weights
+// 2^(s - M) need no exact maximum: M is set so that the row's largest weight * V
+// scale fills fp16's range, and moved only when one would leave it (a factor of
+// 2^7 or more later), which a comparison per token and one barrier over the four
+// warps find out; maxima across lanes are formed only then.  (With M from the
+// scores alone a row that leans on tokens of small V would lose P's low bits next
+// to one large V scale.)
+//
+// What bounds it.  Of 128 rows and fp32 outputs a stage has 32 MMAs of 128 x 128
+// x 16, 64 clocks each: 2048 clocks, of which the codes' conversion (8 warps) and
+// the softmax of 16384 scores (16 warps, about 15 instructions for two scores)
+// leave 3600 to 3700: the four schedulers issue in 65 % of all cycles, the tensor
+// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1707 us, 651 TFLOP/s
+// of the operator's own arithmetic (each product counted once).  16-bit outputs
+// skip P's low part: 4096 tokens x 16 heads 125 us, 549 TFLOP/s.  Tiles of 32
+// rows are bound by the chain copy - operand - scores - softmax - output, some
+// 1600 clocks a stage, and by 7000 clocks before the first one.
 #include <math.h>
 
 #include "kvq8_ptx.cuh"
@@ -43,7 +56,8 @@ namespace {
 
 constexpr int kTok = 128;                       // tokens per stage
 // What a tile costs beside its stages (queries, first references, output), in stages: the CTAs' shares count it, or
-// one that gets many short tiles ends long after the others.
+// one that gets many short tiles ends long after the others (4096 tokens x 16 heads: 131 us counting 3, 125 counting 4,
+// 128 counting 5).
 constexpr int kTileCost = 4;
 constexpr int kCodeBytes = kTok * kHD;          // 16 KiB of K or V codes
 constexpr int kSlotBytes = kCodeBytes + 2 * kTok * 4;   // K codes with both scales, or V codes
@@ -99,7 +113,7 @@ struct Misc {
     uint64_t part_ready[4], part_free[4];
     uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done[2];
     long long warp_tot[32];
-    int s0, r0, off;
+    int4 at0, of0;                              // the first tile: sequence, rows' tile, rows, cost ahead of this CTA; its Walk
     volatile int abort;
     uint32_t tmem;                              // address of the columns
     int skip[8];                                // slot: its block id is outside the pool
@@ -361,14 +375,15 @@ tile_kernel(TileParams p, int lg) {
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;   // (who has all columns has them from 0 on)
-    before -= mine;
-    long long total = 0;   // cost of one kv head
-#pragma unroll 1
-    for (int k = 0; k < kThreads / 32; ++k) {
-        const long long v = ms->warp_tot[k];
-        if (k < warp) before += v;
-        total += v;
+    const long long of_warp = lane < kThreads / 32 ? ms->warp_tot[lane] : 0;
+    long long upto = of_warp;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
+    const long long total = __shfl_sync(0xffffffffu, upto, 31);   // cost of one kv head
+    before += __shfl_sync(0xffffffffu, upto - of_warp, warp) - mine;
     const long long T = total * p.nkv;
     const int C = (int)min((long long)gridDim.x, T);
     if (!kShared && tid == 0) p.ws_dir[c] = make_int4(0, 0, 0, 0);
@@ -381,22 +396,27 @@ tile_kernel(TileParams p, int lg) {
         hi = (long long)(c + 1) * Tq + ((c + 1) * Tr) / C;
         const int h = (int)divide(lo, total);
         const long long rem = lo - h * total;
-        // the item that holds lo says so
+        // the thread whose item holds lo says so (one item to a thread: what it loaded still stands)
 #pragma unroll 1
         for (int i = i_lo; i < i_hi && before <= rem; ++i) {
-            const long long v = item(i);
+            const long long v = per == 1 ? mine : item(i);
             if (rem < before + v) {
-                ms->s0 = w.s;
-                ms->r0 = w.r;
-                ms->off = (int)(rem - before);
+                ms->at0 = make_int4(w.s, w.r, w.rows, (int)(rem - before));
+                ms->of0 = make_int4(w.first, w.lead, w.span, (int)w.start);
             }
             before += v;
         }
         __syncthreads();
-        off = ms->off;
-        w.load(ms->s0);
+        const int4 at0 = ms->at0, of0 = ms->of0;
+        w.s = at0.x;
         w.h = h;
-        w.r = ms->r0;
+        w.r = at0.y;
+        w.rows = at0.z;
+        off = at0.w;
+        w.first = of0.x;
+        w.lead = of0.y;
+        w.span = of0.z;
+        w.start = of0.w;
         if (kShared) {
             const int n = w.cost(0);
             w.r = off / n;
