@@ -131,9 +131,14 @@ struct Misc {
 static_assert(sizeof(Misc) <= 13312, "misc");
 
 // Bounded like every wait here: a try sleeps up to two microseconds, and after 2^20 of them (two seconds at most) the
-// CTA gives up, its other waits with it.  Short, since the loops of all roles share the SM's instruction cache.
+// CTA gives up, its other waits with it.  Short, since the loops of all roles share the SM's instruction cache.  kTest:
+// asks once before it may sleep, which takes 100 clocks less where the phase is complete already, as it often is for the
+// softmax and in tiles of up to 64 rows (8 x 5-token prompts 31.4 -> 29.5 us); in all roles of wide tiles the longer
+// code costs more (4096 tokens x 16 heads 123 -> 129 us).
+template <bool kTest>
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *ms) {
     const uint32_t a = smem_addr(bar);
+    if (kTest && mbar_test(a, parity)) return true;
     int left = 1 << 20;
 #pragma unroll 1
     while (!mbar_try_wait_for(a, parity, 2000u)) {
@@ -144,8 +149,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *m
 }
 
 // The same by all lanes of a warp, together again behind it.
+template <bool kTest>
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Misc *ms) {
-    const bool ok = wait_bar(bar, parity, ms);
+    const bool ok = wait_bar<kTest>(bar, parity, ms);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -432,7 +438,7 @@ tile_kernel(TileParams p, int lg) {
             bool stop = false;
 #pragma unroll 1
             for (int seg = 0; !stop; ++seg) {
-                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
+                if (!wait_warp<!kWide>(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
                 const Part &part = ms->part[seg & 3];
                 const int n = part.stages, first = part.off, end = part.end, h = part.head;
                 if (n == 0) break;
@@ -454,7 +460,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
                         for (int v = 0; v < 2; ++v) {
                             const int at = (g + v) % L::kSlots;
-                            if (!wait_bar(&ms->empty[at], (((g + v) / L::kSlots) & 1) ^ 1, ms)) {
+                            if (!wait_bar<!kWide>(&ms->empty[at], (((g + v) / L::kSlots) & 1) ^ 1, ms)) {
                                 stop = true;
                                 break;
                             }
@@ -492,18 +498,18 @@ tile_kernel(TileParams p, int lg) {
             int x = 0;   // stages so far
 #pragma unroll 1
             for (int seg = 0;; ++seg) {
-                if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
+                if (!wait_warp<!kWide>(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
                 const int n = ms->part[seg & 3].stages;
                 if (n == 0) break;
                 if (scores) {
-                    wait_warp(&ms->q_ready, seg & 1, ms);
+                    wait_warp<!kWide>(&ms->q_ready, seg & 1, ms);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide ? kRows : 2 * kRows, false);
                         const int buf = x & 1;
                         const uint32_t d = tmem + L::kColS, a = tmem + L::kColK + buf * 64;
-                        wait_warp(&ms->k_ready[buf], (x >> 1) & 1, ms);
-                        wait_warp(&ms->s_free, (x & 1) ^ 1, ms);
+                        wait_warp<!kWide>(&ms->k_ready[buf], (x >> 1) & 1, ms);
+                        wait_warp<!kWide>(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
                         mma_k128(d, a, b, kWord, false);
                         if (kWide) mma_k128(d, a, b + kLowPart, kWord, true);
@@ -512,14 +518,14 @@ tile_kernel(TileParams p, int lg) {
                     }
                     mma_commit(smem_addr(&ms->q_free));
                 } else {
-                    wait_warp(&ms->o_free, (seg & 1) ^ 1, ms);
+                    wait_warp<!kWide>(&ms->o_free, (seg & 1) ^ 1, ms);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++x) {
                         constexpr uint32_t kWord = mma_word(kWide || !kLow ? kRows : 2 * kRows, true);
                         const int buf = x & 1;
                         const uint32_t d = tmem + L::kColO, a = tmem + L::kColV + buf * 64;
-                        wait_warp(&ms->v_ready[buf], (x >> 1) & 1, ms);
-                        wait_warp(&ms->p_ready, x & 1, ms);
+                        wait_warp<!kWide>(&ms->v_ready[buf], (x >> 1) & 1, ms);
+                        wait_warp<!kWide>(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
                         mma_k128(d, a, b, kWord, i > 0);
                         if (kWide && kLow) mma_k128(d, a, b + kLowPart, kWord, true);
@@ -548,7 +554,7 @@ tile_kernel(TileParams p, int lg) {
                     if (n > 0) break;
                     left = 0;   // (only the last tile)
                 }
-                if (!wait_warp(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms)) break;
+                if (!wait_warp<!kWide>(&ms->part_free[seg & 3], ((seg >> 2) & 1) ^ 1, ms)) break;
                 Part &part = ms->part[seg & 3];
                 if (n > 0) {
                     const int rows = w.tile_rows(w.r);
@@ -606,7 +612,7 @@ tile_kernel(TileParams p, int lg) {
         int j = 0;
 #pragma unroll 1
         for (int seg = 0;; ++seg) {
-            if (!wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
+            if (!wait_warp<!kWide>(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms)) break;
             const Part &part = ms->part[seg & 3];
             const int n = part.stages;
             if (n == 0) break;
@@ -620,13 +626,13 @@ tile_kernel(TileParams p, int lg) {
                     // K: lane = token, the row's chunk c stands at c ^ (token & 7)
                     const int g = 2 * j, at = g % L::kSlots;
                     const unsigned char *st = smem + L::oRing + at * kSlotBytes;
-                    wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
+                    wait_warp<!kWide>(&ms->full[at], (g / L::kSlots) & 1, ms);
                     const int skip = ms->skip[at];
                     const float *scales = reinterpret_cast<const float *>(st + kCodeBytes);
                     const bool real = !skip && behind > 0;
                     ms->scale[j & 3][row] = make_float2(real ? scales[row] * p.sm_scale_log2 : 0.0f, real ? scales[kTok + row] : 0.0f);
                     if (lane == 0 && quad == 0) ms->bad[j & 3] = skip;
-                    wait_warp(&ms->k_free[buf], par ^ 1, ms);
+                    wait_warp<!kWide>(&ms->k_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const uint4 *kr = reinterpret_cast<const uint4 *>(st + row * kHD);
 #pragma unroll 1
@@ -645,8 +651,8 @@ tile_kernel(TileParams p, int lg) {
                     // the four chunks back into order
                     const int g = 2 * j + 1, at = g % L::kSlots;
                     const unsigned char *st = smem + L::oRing + at * kSlotBytes;
-                    wait_warp(&ms->full[at], (g / L::kSlots) & 1, ms);
-                    wait_warp(&ms->v_free[buf], par ^ 1, ms);
+                    wait_warp<!kWide>(&ms->full[at], (g / L::kSlots) & 1, ms);
+                    wait_warp<!kWide>(&ms->v_free[buf], par ^ 1, ms);
                     tc_fence_after();
                     const int turn = (lane >> 1) & 3;
 #pragma unroll 1
@@ -693,7 +699,7 @@ tile_kernel(TileParams p, int lg) {
         // there is no such tile (or a wait gave up: the four warps of a share go by one answer, or a barrier
         // would wait for the one that left).
         auto queries = [&](int seg) {
-            const bool ok = wait_warp(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms);
+            const bool ok = wait_warp<!kWide>(&ms->part_ready[seg & 3], (seg >> 2) & 1, ms);
             if (barrier_any(bar, 128, !ok)) return false;
             const Part &part = ms->part[seg & 3];
             if (part.stages == 0) return false;
@@ -751,7 +757,7 @@ tile_kernel(TileParams p, int lg) {
                 // a row's values lie below 2^11 in units of 2^e
                 const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
                 const float down = exp2_int(-e);
-                wait_warp(&ms->q_free, (seg & 1) ^ 1, ms);
+                wait_warp<!kWide>(&ms->q_free, (seg & 1) ^ 1, ms);
                 unsigned char *at = smem + L::oQ + (warp - kSoftmaxWarp0) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -788,7 +794,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll 1
         for (int seg = 0; more; ++seg) {
             const int n = ms->part[seg & 3].stages;
-            wait_warp(&ms->q_ready, seg & 1, ms);
+            wait_warp<!kWide>(&ms->q_ready, seg & 1, ms);
             if (st < kCols) ms->ref[c0 + st] = 0.0f;
             const int lim_min = ms->lim_min[seg & 3];
             named_barrier_sync(bar, 128);
@@ -799,7 +805,7 @@ tile_kernel(TileParams p, int lg) {
             int t0 = ms->part[seg & 3].off * kTok;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
-                wait_warp(&ms->s_full, j & 1, ms);   // (the scales were there before the scores' operand)
+                wait_warp<true>(&ms->s_full, j & 1, ms);   // (the scales were there before the scores' operand)
                 tc_fence_after();
                 float2 sc[4];
 #pragma unroll
@@ -886,7 +892,7 @@ tile_kernel(TileParams p, int lg) {
                     }
                     named_barrier_sync(bar, 128);
                     if (!rest && !fresh) {
-                        wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
+                        wait_warp<!kWide>(&ms->pv_done, (j & 1) ^ 1, ms);
                         tc_fence_after();
                         rest = true;
 #pragma unroll 1
@@ -940,7 +946,7 @@ tile_kernel(TileParams p, int lg) {
                         }
                     }
                 }
-                if (!rest) wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
+                if (!rest) wait_warp<true>(&ms->pv_done, (j & 1) ^ 1, ms);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     store_matrices(pout + g * kCoreRow, hi[g][0], hi[g][1], hi[g][2], hi[g][3]);
@@ -979,7 +985,7 @@ tile_kernel(TileParams p, int lg) {
                 ms->dst[x] = dst;
             }
             named_barrier_sync(bar, 128);
-            wait_warp(&ms->pv_done, (j & 1) ^ 1, ms);
+            wait_warp<!kWide>(&ms->pv_done, (j & 1) ^ 1, ms);
             tc_fence_after();
             const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
 #pragma unroll(kWide ? 2 : 1)
