@@ -41,11 +41,13 @@
 // x 16, 64 clocks each: 2048 clocks, of which the codes' conversion (8 warps) and
 // the softmax of 16384 scores (16 warps, about 15 instructions for two scores)
 // leave 3600 to 3700: the four schedulers issue in 65 % of all cycles, the tensor
-// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1707 us, 651 TFLOP/s
-// of the operator's own arithmetic (each product counted once).  16-bit outputs
-// skip P's low part: 4096 tokens x 16 heads 125 us, 549 TFLOP/s.  Tiles of 32
-// rows are bound by the chain copy - operand - scores - softmax - output, some
-// 1600 clocks a stage, and by 7000 clocks before the first one.
+// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.72 ms, 650 TFLOP/s
+// of the operator's own arithmetic (each product counted once); 4096 tokens x 16
+// heads in bf16, without P's low part: 123 us, 560 TFLOP/s.  Tiles of 32 rows
+// take some 2200 clocks a stage, of which the MMAs are 512 and the bytes 700 (at
+// the copy rate): the warps of seven roles draw on the instruction caches, so
+// that longer loops (unrolled operands), more warps (16 for the operands, two
+// groups of softmax warps in turn, two CTAs per SM) all came out slower.
 #include <math.h>
 
 #include "kvq8_ptx.cuh"
@@ -1164,12 +1166,15 @@ int log2_of(int x) {
 
 }  // namespace
 
-// Rows per tile: the most that a sequence (on average, a group) has, up to 128.
+// Rows per tile: the most that a sequence (on average, a group) has, up to 128, since a stage's time grows with its
+// tile's rows, and each further tile turns the same codes into operands again.  8 sequences behind 4000 tokens, G = 4,
+// with tiles of 32, 64 and 128 rows: 20 rows 29, 35, 45 us; 64 rows 46, 36, 47 us; 128 rows 74, 55, 52 us.
 static int rows_of(int64_t rows) { return rows > 64 ? 128 : rows > 32 ? 64 : 32; }
 
 cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
     const int lg = log2_of(group), rows = rows_of((int64_t)p.n_new << lg);
     cudaError_t e;
+    // (without P's low part, which bf16 outputs would not show: 4096 tokens x 16 heads 130 us, with it 150)
     if (p.out_dtype == KVQ8_DTYPE_BF16)
         e = rows == 128 ? launch_tiles<false, 128, false>(p, lg, s)
             : rows == 64 ? launch_tiles<false, 64, false>(p, lg, s) : launch_tiles<false, 32, false>(p, lg, s);
