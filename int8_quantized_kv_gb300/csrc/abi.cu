@@ -602,7 +602,7 @@ static void place_tile_workspace(const TileWorkspace &w, void *base, TileParams 
 }
 
 static TileWorkspace prompt_workspace() {
-    return tile_workspace(kMaxTileCtas, (size_t)kMaxTileCtas * 2 * kTileRows);
+    return tile_workspace(kMaxTileCtas, (size_t)kMaxTileCtas * 3 * kTileRows);
 }
 
 size_t kvq8_prompt_workspace_bytes(int batch, int n_new, int nqh, int nkv, int hd, int max_blocks,

@@ -212,9 +212,10 @@ struct TileParams {
     int32_t *ws_first;            // [batch]: the first row of the row's group
     int4 *ws_group;               // [n_groups]: (first row, rows, row read through, shared tokens)
     int tile_rows;                // rows of a tile (set with the launch)
-    // partial results, for tiles of R rows.  Prompt: CTA c's rows at c * 2 * R (a tile
+    // partial results, for tiles of R rows.  Prompt: CTA c's rows at c * 3 * R (a tile
     // that it goes on with) and R later (a tile that it begins and another ends),
-    // ws_dir[c] says of which tile the latter is.  Shared prefix: row x of the
+    // ws_dir[c] says of which tile the latter is; 2 R later the totals of a tile that
+    // it has alone.  Shared prefix: row x of the
     // batch * nqh rows, ordered by (kv head, batch row, head), by CTA c at
     // x + c * R; ws_dir[x of a tile's first row] = (first CTA, their count).
     int4 *ws_dir;

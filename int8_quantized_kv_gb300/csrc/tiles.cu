@@ -94,6 +94,12 @@ struct Lay {
     // 8 rows (8 prompts of 5 tokens x 32 heads: 33.1 us with sixteen, 32.2 us with eight).
     static constexpr int kSoftmaxWarps = kRows == 32 ? 8 : 16;
     static constexpr int kThreads = (kSoftmaxWarp0 + kSoftmaxWarps) * 32;
+    // Stages whose outputs add up in tensor memory.  The tensor cores cut off what leaves an accumulator's 24 bits, always
+    // downwards in size, so that a long sum shrinks (2e-4 of the output over 130560 tokens): after a run of stages it is
+    // added, in fp32 and rounded, to a total in the workspace, and begins anew.  The shorter the run, the nearer to the
+    // 64-bit result and the more often 64 KB per tile of 128 rows go out.  bf16 outputs need none of it: over 256 stages
+    // the cut is a thirtieth of their rounding.
+    static constexpr int kRun = !kLow ? 256 : kWide ? 12 : 8;
     // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
     // K's operands; V's; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
     // leaves it no L1.
@@ -280,6 +286,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The least whole number above log2 of a V scale (kTinyScaleLog2 at least), by its exponent bits.
 __device__ __forceinline__ float exponent_above(float scale) {
     return __int_as_float(max(__float_as_int(scale) >> 23, kTinyScaleLog2 + 126) | 0x4b000000) - (0x1p23f + 126.0f);
+}
+
+// A total's element, which one thread alone has to do with: what it asks for in turn happens in turn.
+__device__ __forceinline__ void store_relaxed(float *at, float x) {
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ void add_relaxed(float *at, float x) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ float load_relaxed(const float *at) {
+    float x;
+    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(x) : "l"(at) : "memory");
+    return x;
 }
 
 // a / b for positive b; in 32 bits where that does.
@@ -513,8 +532,9 @@ tile_kernel(TileParams p, int lg) {
                         wait_warp<!kWide>(&ms->k_ready[buf], (x >> 1) & 1, ms);
                         wait_warp<!kWide>(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
-                        mma_k128(d, a, b, kWord, false);
-                        if (kWide) mma_k128(d, a, b + kLowPart, kWord, true);
+                        // (low parts first: what they add to is small yet, and little is cut off)
+                        if (kWide) mma_k128(d, a, b + kLowPart, kWord, false);
+                        mma_k128(d, a, b, kWord, kWide);
                         mma_commit(smem_addr(&ms->s_full));
                         mma_commit(smem_addr(&ms->k_free[buf]));
                     }
@@ -529,7 +549,7 @@ tile_kernel(TileParams p, int lg) {
                         wait_warp<!kWide>(&ms->v_ready[buf], (x >> 1) & 1, ms);
                         wait_warp<!kWide>(&ms->p_ready, x & 1, ms);
                         tc_fence_after();
-                        mma_k128(d, a, b, kWord, i > 0);
+                        mma_k128(d, a, b, kWord, i % L::kRun != 0);
                         if (kWide && kLow) mma_k128(d, a, b + kLowPart, kWord, true);
                         mma_commit(smem_addr(&ms->pv_done));
                         mma_commit(smem_addr(&ms->v_free[buf]));
@@ -586,7 +606,7 @@ tile_kernel(TileParams p, int lg) {
                         part.head = w.h;
                         part.token = (int)w.token(w.r, 0);
                         part.direct = !kShared && whole;
-                        part.rec = kShared ? x + (long long)c * kRows : ((long long)c * 2 + (from == 0 ? 1 : 0)) * kRows;
+                        part.rec = kShared ? x + (long long)c * kRows : ((long long)c * 3 + (whole ? 2 : from == 0 ? 1 : 0)) * kRows;
                         if (from == 0) {   // the CTAs c .. that hold this tile's records
                             const long long end = hi - left - off + kTileCost + stages;
                             const int cnt = (int)divide(end * C + T - 1, T) - c;
@@ -791,6 +811,21 @@ tile_kernel(TileParams p, int lg) {
             if (lane == 0) mbar_arrive(smem_addr(&ms->q_ready));
             return true;
         };
+        // the outputs of eight rows from c0 + k on, dim 32 quad + lane
+        auto read_output = [&](int k, float (&x)[8]) {
+            float y[8];
+            tmem_ld8(lanes + L::kColO + c0 + k, x);
+            if (!kWide && kLow) tmem_ld8(lanes + L::kColO + kRows + c0 + k, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                asm volatile("" : "+f"(x[q]));
+                if (!kWide && kLow) {
+                    asm volatile("" : "+f"(y[q]));
+                    x[q] += y[q];
+                }
+            }
+        };
         int j = 0;
         bool more = queries(0);
 #pragma unroll 1
@@ -805,6 +840,9 @@ tile_kernel(TileParams p, int lg) {
             for (int g = 0; g < kGroups; ++g) ref[g] = sum[g] = make_float2(0.0f, 0.0f);
             bool fresh = true;   // no row has a reference yet
             int t0 = ms->part[seg & 3].off * kTok;
+            // where the totals of tiles of more than one run are kept, the record's place: of row c0, this thread's dim
+            // (asked for when needed: a register less in the stages)
+            auto totals = [&] { return p.ws_acc + (ms->part[seg & 3].rec + c0) * kHD + 32 * quad + lane; };
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, t0 += kTok) {
                 wait_warp<true>(&ms->s_full, j & 1, ms);   // (the scales were there before the scores' operand)
@@ -916,6 +954,14 @@ tile_kernel(TileParams p, int lg) {
                         }
                         tmem_wait_st();
                     }
+                    if (i > L::kRun && !fresh) {
+                        float *const total = totals();
+                        const int rows = ms->part[seg & 3].rows;
+#pragma unroll 1
+                        for (int k = 0; k < kCols && c0 + k < rows; ++k)
+                            if (ms->shift[c0 + k] != 0.0f)
+                                store_relaxed(total + k * kHD, load_relaxed(total + k * kHD) * ex2_approx(ms->shift[c0 + k]));
+                    }
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const float2 by = *reinterpret_cast<const float2 *>(&ms->shift[col + 8 * g]);
@@ -949,6 +995,22 @@ tile_kernel(TileParams p, int lg) {
                     }
                 }
                 if (!rest) wait_warp<true>(&ms->pv_done, (j & 1) ^ 1, ms);
+                if (i % L::kRun == 0 && i > 0) {   // a run's end
+                    tc_fence_after();
+                    float *const total = totals();
+                    const int rows = ms->part[seg & 3].rows - c0;
+#pragma unroll 1
+                    for (int k = 0; k < kCols; k += 8) {
+                        float o[8];
+                        read_output(k, o);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (k + q >= rows) continue;
+                            if (i > L::kRun) add_relaxed(total + (k + q) * kHD, o[q]);
+                            else store_relaxed(total + (k + q) * kHD, o[q]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     store_matrices(pout + g * kCoreRow, hi[g][0], hi[g][1], hi[g][2], hi[g][3]);
@@ -990,22 +1052,23 @@ tile_kernel(TileParams p, int lg) {
             wait_warp<!kWide>(&ms->pv_done, (j & 1) ^ 1, ms);
             tc_fence_after();
             const int type = direct ? p.out_dtype : KVQ8_DTYPE_F32;
+            float *const total = totals();
 #pragma unroll(kWide ? 2 : 1)
             for (int k = 0; k < kCols; k += 8) {
-                float x[8], y[8];
-                tmem_ld8(lanes + L::kColO + c0 + k, x);
-                if (!kWide && kLow) tmem_ld8(lanes + L::kColO + kRows + c0 + k, y);
-                tmem_wait_ld();
+                float x[8];
+                read_output(k, x);
+                if (direct && n > L::kRun) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    asm volatile("" : "+f"(x[q]));
-                    if (!kWide && kLow) {
-                        asm volatile("" : "+f"(y[q]));
-                        x[q] += y[q];
-                    }
-                    x[q] *= ms->shift[c0 + k + q];
+                    for (int q = 0; q < 8; ++q)
+                        if (c0 + k + q < part.rows) x[q] += load_relaxed(total + (k + q) * kHD);
                 }
-                if (type == KVQ8_DTYPE_F32) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] *= ms->shift[c0 + k + q];
+                if (!direct && n > L::kRun) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (c0 + k + q < part.rows) add_relaxed(total + (k + q) * kHD, x[q]);
+                } else if (type == KVQ8_DTYPE_F32) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         if (char *dst = ms->dst[c0 + k + q]) reinterpret_cast<float *>(dst)[row] = x[q];
@@ -1091,7 +1154,7 @@ prompt_merge_kernel(TileParams p, int lg, int rows_per_tile) {
     const int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
     if (i >= w.tile_rows(w.r)) return;
     // record k: of CTA c + k; the first one is c's own second place
-    auto at = [&](int k) { return ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * rows_per_tile + i; };
+    auto at = [&](int k) { return ((long long)(c + k) * 3 + (k == 0 ? 1 : 0)) * rows_per_tile + i; };
     float m = -INFINITY;
     for (int k = lane; k < dir.x; k += 32) m = fmaxf(m, p.ws_ml[at(k) * 2]);
     m = warp_max(m);

@@ -375,3 +375,62 @@ def test_most_sequences_empty(gpu_lib):
         pick.starts, pick.ns, pick.table = [5], [ns[b]], c.table[b:b + 1]
         pick.q = c.q[b:b + 1]
         pick.check(out=c.out[b:b + 1])
+
+
+# 160 tiles of each height, so that every CTA has some 450 stages of a tile.
+LONG_RUNS = [(20, 2), (20, 12), (5, 128)]
+# Outputs of values of one sign.  A step of the tensor cores cuts off less than 2^-23 of its accumulator, which grows evenly
+# over a run of at most 12 stages of 16 steps: 12 * 16 / 2 * 2^-23; queries, weights and the runs' sum: 2^-18.
+LONG_TOL = 96 * 2.0 ** -23 + 2.0 ** -18
+
+
+def _long(batch, n_new, seed, out):
+    c = Prompt([60000 + 7 * b for b in range(batch)], n_new, 32, 8, seed, out=out)
+    c.cache.v_pool.abs_()
+    return c
+
+
+def _check_long(c, tol, what):
+    for b in (0, c.batch - 1):
+        for i in (0, c.n_new - 1):
+            L = c.starts[b] + i + 1
+            for h in (0, 7):
+                k, v = ref.rows64(c.cache, c.table[b], h, torch.arange(L, device="cuda"))
+                rows = c.q[b, i, 4 * h:4 * h + 4]
+                want, _ = ref.attend(rows, k, v, torch.full((4,), L, device="cuda"))
+                half = torch.finfo(c.out.dtype).eps / 2
+                r = ((c.out[b, i, 4 * h:4 * h + 4].double() - want).abs() / want).max().item()
+                assert r <= tol + half, f"{what} b={b} i={i} h={h}: {r:.3g} off, {tol + half:.3g} allowed"
+
+
+@pytest.mark.parametrize("batch,n_new", LONG_RUNS)
+def test_long_sums_do_not_shrink(gpu_lib, batch, n_new):
+    # even weights: each output is the mean of 60000 values, which one accumulator would cut by 1e-4
+    for out in (torch.float32, torch.float16) if n_new == 128 else (torch.float32,):
+        c = _long(batch, n_new, 67, out)
+        c.q.zero_()
+        c.run()
+        _check_long(c, LONG_TOL, str(out))
+
+
+@pytest.mark.parametrize("batch,n_new", LONG_RUNS)
+def test_totals_move_with_their_references(gpu_lib, batch, n_new):
+    # the last 300 tokens weigh 2^8 times as much as the others, which are still two fifths of the output
+    c = _long(batch, n_new, 69, torch.float32)
+    c.q.fill_(1.0)
+    for b, p in enumerate(c.starts):
+        t = torch.arange(p + n_new, device="cuda")
+        blk, s = c.table[b].long()[t // 256], t % 256
+        c.cache.k_pool[blk, :, s] = 100
+        c.cache.k_scale[blk, :, s] = ((t >= p - 300).float() * 8 / (100 * 128 * ref.SM * ref.LOG2E))[:, None]
+    c.run()
+    # (scores of 8 in size: 2 * 2^-19 * 8 of ln 2 each)
+    _check_long(c, LONG_TOL + 16 * 2.0 ** -19, "cliff")
+
+
+def test_long_sums_in_bf16(gpu_lib):
+    # the weights' 11 bits and the cut of up to 256 stages, both far below bf16's half step
+    c = _long(5, 128, 71, torch.bfloat16)
+    c.q.zero_()
+    c.run()
+    _check_long(c, 2.0 ** -11 + 256 * 8 / 2 * 2.0 ** -23 + 2.0 ** -18, "bf16")

@@ -13,13 +13,13 @@ pytestmark = pytest.mark.gpu
 class Shared:
     """sizes[g] rows in group g, prefix[g] tokens shared, lens[b] tokens in each row."""
 
-    def __init__(self, sizes, prefix, lens, nqh, nkv, seed, step=False, size=1.5, spread=None):
+    def __init__(self, sizes, prefix, lens, nqh, nkv, seed, step=False, size=1.5, spread=None, table=None):
         self.batch, self.nqh, self.nkv, self.step = sum(sizes), nqh, nkv, step
         self.sizes, self.prefix, self.lens = sizes, prefix, lens
         self.first = [sum(sizes[:g]) for g in range(len(sizes))]
         self.group = [g for g, m in enumerate(sizes) for _ in range(m)]
         self.mb = max(1, max(max(lens, default=1), max(prefix, default=1)) // 256 + 1)
-        table, nb = ref.random_table(self.batch, self.mb, seed)
+        table, nb = table or ref.random_table(self.batch, self.mb, seed)
         self.cache = ref.random_cache(nb, nkv, seed, spread)
         # a row's whole blocks below the prefix are nobody's (its own entries are not looked at), but in the row
         # that the prefix is read through: the first one that has all of it, else the longest
@@ -335,3 +335,27 @@ def test_two_calls_at_once(gpu_lib):
             kvq8.decode_attn_shared(x.q, x.cache, x.table, x.lens_d, x.starts_d, x.prefix_d, x.out, x.ws, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
+
+
+@pytest.mark.parametrize("rows", [4, 16, 32])
+def test_long_sums_do_not_shrink(gpu_lib, rows):
+    # 20 groups x 8 heads, so that every CTA has some 450 stages of a tile; even weights and values of one sign: each output
+    # is the mean of 60000 values.  A step of the tensor cores cuts off less than 2^-23 of its accumulator, which grows evenly
+    # over at most 12 stages of 16 steps; weights and sums 2^-18
+    prefix = 60000
+    mb = prefix // 256 + 1                                       # only the blocks that are looked at, or 640 rows need 147 GB
+    table = torch.full((20 * rows, mb), -1, dtype=torch.int32, device="cuda")
+    table[:, -1] = 20 * mb + torch.arange(20 * rows)
+    table[::rows] = torch.arange(20 * mb, dtype=torch.int32, device="cuda").reshape(20, mb)
+    c = Shared([rows] * 20, [prefix] * 20, [prefix + 1 + b % 5 for b in range(20 * rows)], 32, 8, 255,
+               table=(table, 20 * mb + 20 * rows))
+    c.cache.v_pool.abs_()
+    c.q.zero_()
+    c.run()
+    for b in (0, 20 * rows - 1):
+        for h in (0, 7):
+            k1, v1 = ref.rows64(c.cache, c.table[c.lead[c.group[b]]], h, torch.arange(prefix, device="cuda"))
+            k2, v2 = ref.rows64(c.cache, c.table[b], h, torch.arange(prefix, c.lens[b], device="cuda"))
+            want = torch.cat([v1, v2]).mean(0)
+            r = ((c.out[b, 4 * h:4 * h + 4].double() - want).abs() / want).max().item()
+            assert r <= 96 * 2.0 ** -23 + 2.0 ** -18, f"b={b} h={h}: {r:.3g} off"
