@@ -2,7 +2,8 @@
 // stand for: code * scale in fp32, rounded once to the output's type.
 //
 // Traffic bounds it: 264 B of cache and 2 * 128 values of output per (token, kv
-// head).  A warp takes the 16 slots of a tile that one 16-byte access of a V
+// head); 8 x 4096 tokens x 8 heads to fp32 in 55.8 us (6.0 TB/s, 49.8 at the copy
+// rate), 18000 tokens to bf16 in 22.3 (16.5).  A warp takes the 16 slots of a tile that one 16-byte access of a V
 // row (dim-major per 64 slots) covers: lane l holds the codes of dims 4l..4l+3
 // of all 16 tokens, V as one 16-byte load per dim turned by byte permutes, K as
 // one word per token (the row's chunk j stands at j ^ (slot & 7)), so that every

@@ -38,16 +38,17 @@
 // to one large V scale.)
 //
 // What bounds it.  Of 128 rows and fp32 outputs a stage has 32 MMAs of 128 x 128
-// x 16, 64 clocks each: 2048 clocks, of which the codes' conversion (8 warps) and
-// the softmax of 16384 scores (16 warps, about 15 instructions for two scores)
-// leave 3600 to 3700: the four schedulers issue in 65 % of all cycles, the tensor
-// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.72 ms, 650 TFLOP/s
+// x 16, 64 clocks each: 2048 clocks.  The codes' conversion (8 warps) and the
+// softmax of 16384 scores (16 warps, about 15 instructions for two scores) make
+// them 3600 to 3700: the four schedulers issue in 69 % of all cycles, the tensor
+// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
 // of the operator's own arithmetic (each product counted once); 4096 tokens x 16
-// heads in bf16, without P's low part: 123 us, 560 TFLOP/s.  Tiles of 32 rows
-// take some 2200 clocks a stage, of which the MMAs are 512 and the bytes 700 (at
-// the copy rate): the warps of seven roles draw on the instruction caches, so
-// that longer loops (unrolled operands), more warps (16 for the operands, two
-// groups of softmax warps in turn, two CTAs per SM) all came out slower.
+// heads in bf16, without P's low part: 128 us, 537 TFLOP/s.  Tiles of 32 rows
+// take some 2100 clocks a stage, of which the MMAs are 512 and the bytes 1400 (at
+// the copy rate; 28 layers x 8 heads of 4096 tokens: 62 us, 36 at that rate): the
+// warps of seven roles draw on the instruction caches, so that longer loops
+// (unrolled operands) and more warps (16 for the operands, two groups of softmax
+// warps in turn, two CTAs per SM) all came out slower.
 #include <math.h>
 
 #include "kvq8_ptx.cuh"
