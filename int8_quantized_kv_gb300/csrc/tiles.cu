@@ -1153,27 +1153,43 @@ prompt_merge_kernel(TileParams p, int lg, int rows_per_tile) {
     w.h = dir.z;
     w.r = dir.w;
     const int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-    if (i >= w.tile_rows(w.r)) return;
     // record k: of CTA c + k; the first one is c's own second place
     auto at = [&](int k) { return ((long long)(c + k) * 3 + (k == 0 ? 1 : 0)) * rows_per_tile + i; };
-    float m = -INFINITY;
-    for (int k = lane; k < dir.x; k += 32) m = fmaxf(m, p.ws_ml[at(k) * 2]);
-    m = warp_max(m);
-    float S = 0.0f;
+    // four at a time, and asked for before the tile's rows are known (rows behind them are anything, and go nowhere)
+    float m = -INFINITY, S = 0.0f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
-#pragma unroll 4
-        for (int k = 0; k < dir.x; ++k) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + at(k) * 2);
-            const float4 x = *reinterpret_cast<const float4 *>(p.ws_acc + at(k) * kHD + 4 * lane);
-            const float f = ex2_approx(ml.x - m);
-            S = fmaf(ml.y, f, S);
-            a.x = fmaf(x.x, f, a.x);
-            a.y = fmaf(x.y, f, a.y);
-            a.z = fmaf(x.z, f, a.z);
-            a.w = fmaf(x.w, f, a.w);
+    constexpr int kAtOnce = 4;
+    for (int k0 = 0; k0 < dir.x; k0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 x[kAtOnce];
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < dir.x) {
+                ml[k] = *reinterpret_cast<const float2 *>(p.ws_ml + at(k0 + k) * 2);
+                x[k] = *reinterpret_cast<const float4 *>(p.ws_acc + at(k0 + k) * kHD + 4 * lane);
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+        if (top == -INFINITY) continue;
+        const float f_old = ex2_approx(m - top);   // 0 while m is -inf
+        S *= f_old;
+        a = make_float4(a.x * f_old, a.y * f_old, a.z * f_old, a.w * f_old);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const float f = ex2_approx(ml[k].x - top);
+            S = fmaf(ml[k].y, f, S);
+            a.x = fmaf(x[k].x, f, a.x);
+            a.y = fmaf(x[k].y, f, a.y);
+            a.z = fmaf(x[k].z, f, a.z);
+            a.w = fmaf(x[k].w, f, a.w);
+        }
+        m = top;
     }
+    if (i >= w.tile_rows(w.r)) return;
     const float inv = S > 0.0f ? 1.0f / S : 0.0f;
     const int64_t o = w.token(w.r, i) * p.out_stride + (int64_t)w.head(i) * kHD + 4 * lane;
     store1(p.out, p.out_dtype, o, a.x * inv);
