@@ -1,6 +1,6 @@
 // decode_shared.cu -- the decode of a batch whose rows share their first tokens
-// in groups: the split over each row's own tokens (decode_split.cuh, kTail) and
-// the merge of its partial results with those of the shared tokens.
+// in groups: the split over each row's own tokens (decode_tail.cuh) and the merge
+// of its partial results with those of the shared tokens.
 #include "decode_tail.cuh"
 #include "tile_rows.cuh"
 

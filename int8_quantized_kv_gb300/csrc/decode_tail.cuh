@@ -14,7 +14,8 @@
 // stage's time (12 warps an SM with one stage each against 6 with two: 48 us
 // against 56).  Queries, block ids and a step's new token are loaded when the
 // unit's first stage is asked for.  The arithmetic of a stage is
-// decode_split.cuh's.
+// decode_split.cuh's.  The kernel starts on the SMs that the tile kernel ahead has
+// left and waits for it at its own end (28 layers' step 119.7 -> 110.7 us).
 #pragma once
 
 #include "decode_split.cuh"
@@ -248,8 +249,9 @@ decode_tail_kernel(DecodeParams p) {
         mbar_init(smem_addr(full + lane), 1);
         fence_mbar_init();
     }
-    pdl_wait();
-    pdl_launch_dependents();   // (this kernel's shared memory keeps the next one's large CTAs off the SM)
+    // No wait here: nothing below reads what the tile kernel ahead writes, and what is ahead of that kernel (the plan's
+    // ws_tail among it) was done when its CTAs let this kernel start.  The CTAs begin on the SMs that it has left, and
+    // each waits for it before it leaves itself, so that the merge behind finds both done.
     // ---- the workers' shares of all units' stages ----
     const int per = (p.batch + kTailWarps * 32 - 1) / (kTailWarps * 32);
     const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);
@@ -300,7 +302,10 @@ decode_tail_kernel(DecodeParams p) {
     }
     __syncthreads();
     const int worker = warp * gridDim.x + blockIdx.x;
-    if (worker >= W) return;
+    if (worker >= W) {
+        pdl_wait();
+        return;
+    }
     const long long lo = share(worker);
     const int total = (int)(share(worker + 1) - lo);
 
@@ -484,6 +489,8 @@ decode_tail_kernel(DecodeParams p) {
     if (gave_up && lane == 0) {
         for (int i = 0; i < 2; ++i) mbar_wait_bounded(smem_addr(full + i), (copied - 1) & 1, kWaitTimeoutNs);
     }
+    pdl_wait();
+    pdl_launch_dependents();
 }
 
 template <int G>

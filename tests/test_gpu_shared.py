@@ -359,3 +359,54 @@ def test_long_sums_do_not_shrink(gpu_lib, rows):
             want = torch.cat([v1, v2]).mean(0)
             r = ((c.out[b, 4 * h:4 * h + 4].double() - want).abs() / want).max().item()
             assert r <= 96 * 2.0 ** -23 + 2.0 ** -18, f"b={b} h={h}: {r:.3g} off"
+
+
+def test_ready_steps_between_shared_ones(gpu_lib):
+    # a step with the cache declared ready may start while the call ahead of it runs: what that call appended is there all
+    # the same, and the other way round; captured, replayed over a cache whose new slots were overwritten, bit for bit
+    batch, nkv, G, L0, n, prefix = 6, 2, 4, 330, 8, 300
+    g = torch.Generator("cuda").manual_seed(257)
+    rows = lambda *s: torch.randn((*s, 128), generator=g, device="cuda")  # noqa: E731
+    old_k, old_v = rows(batch, L0, nkv), rows(batch, L0, nkv)
+    for x in (old_k, old_v):
+        x[1:4, :prefix], x[5, :prefix] = x[0, :prefix], x[4, :prefix]
+    k, v = rows(n, batch, nkv), 5 * rows(n, batch, nkv)
+    q = (k[:, :, :, None] + 0.3 * rows(n, batch, nkv, G)).flatten(2, 3).contiguous()   # along the new tokens' keys
+    table, nb = ref.random_table(batch, 2, 257)
+    cache = kvq8.alloc_cache(nb, nkv, "cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens = [i32(*[L0 + i + 1] * batch) for i in range(n)]
+    starts, shared, zero, status = i32(0, 4, 6), i32(prefix, prefix), i32(*[0] * batch), i32(0)
+    ws, wd = kvq8.alloc_shared_workspace(batch, 2, nkv * G, nkv, 2), kvq8.alloc_workspace(batch, nkv * G, nkv, 2)
+    out = torch.empty_like(q)
+
+    def reset():
+        for x, y in zip(cache, (99, -99, 0.5, 9.0)):
+            x.fill_(y)
+        out.fill_(float("nan"))
+        kvq8.quantize_append(old_k, old_v, zero, table, cache)
+        torch.cuda.synchronize()
+
+    def steps(ready, sync):
+        for i in range(n):
+            args = (q[i], k[i], v[i], cache, table, lens[i])
+            if i % 2:
+                kvq8.decode_step(*args, out[i], wd, dev_status=status, cache_ready=ready)
+            else:
+                kvq8.decode_step_shared(*args, starts, shared, out[i], ws, dev_status=status)
+            if sync:
+                torch.cuda.synchronize()
+
+    reset()
+    steps(False, True)
+    want, want_cache = out.clone(), [x.clone() for x in cache]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps(True, False)
+    for _ in range(20):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all(torch.equal(x, y) for x, y in zip(cache, want_cache))
+    assert status.item() == 0
