@@ -26,7 +26,7 @@
 // sequence.  Warp 0 copies the stages (bulk copies into a ring, K and V apart),
 // warps 1 and 3 issue the MMAs of scores and output, warp 2 says which tiles,
 // warps 4..7 turn K's codes into operands and 8..11 V's, the others (16; 8 for
-// tiles of 32 rows) take the softmax, four warps to an equal share of the rows,
+// tiles of 32 rows, 4 for 16) take the softmax, four warps to an equal share of the rows,
 // and prepare the next tile's queries behind their last stage.  S^T and P^T move
 // as MMA fragments (tcgen05.ld 16x256b, stmatrix), so that a thread holds tokens
 // of few rows, whose references and sums stay in its registers.  A row's weights
@@ -91,9 +91,10 @@ struct Lay {
     // columns of tensor memory: two of K's operand and of V's, scores, output
     static constexpr int kColK = 0, kColV = 128, kColS = 256, kColO = kColS + (kWide ? kRows : 2 * kRows);
     static_assert(kColO + (kWide ? kRows : 2 * kRows) <= kColumns, "tensor memory");
-    // Softmax warps: as many as fill the SM's registers, but for tiles of 32 rows, where a warp of sixteen would have
-    // 8 rows (8 prompts of 5 tokens x 32 heads: 33.1 us with sixteen, 32.2 us with eight).
-    static constexpr int kSoftmaxWarps = kRows == 32 ? 8 : 16;
+    // Softmax warps: as many as fill the SM's registers, but for tiles of up to 32 rows, where a warp of sixteen would
+    // have 8 rows or fewer (8 prompts of 5 tokens x 32 heads, 20 rows: 33.1 us with sixteen, 32.2 us with eight; later
+    // 31.0 with eight, 32.9 with four).
+    static constexpr int kSoftmaxWarps = kRows == 16 ? 4 : kRows == 32 ? 8 : 16;
     static constexpr int kThreads = (kSoftmaxWarp0 + kSoftmaxWarps) * 32;
     // Stages whose outputs add up in tensor memory.  The tensor cores cut off what leaves an accumulator's 24 bits, always
     // downwards in size, so that a long sum shrinks (2e-4 of the output over 130560 tokens): after a run of stages it is
@@ -1248,8 +1249,9 @@ int log2_of(int x) {
 
 // Rows per tile: the most that a sequence (on average, a group) has, up to 128, since a stage's time grows with its
 // tile's rows, and each further tile turns the same codes into operands again.  8 sequences behind 4000 tokens, G = 4,
-// with tiles of 32, 64 and 128 rows: 20 rows 29, 35, 45 us; 64 rows 46, 36, 47 us; 128 rows 74, 55, 52 us.
-static int rows_of(int64_t rows) { return rows > 64 ? 128 : rows > 32 ? 64 : 32; }
+// with tiles of 32, 64 and 128 rows: 20 rows 29, 35, 45 us; 64 rows 46, 36, 47 us; 128 rows 74, 55, 52 us; of 16 and
+// 32 rows: 8 rows 23.8, 26.7 us.
+static int rows_of(int64_t rows) { return rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16; }
 
 cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
     const int lg = log2_of(group), rows = rows_of((int64_t)p.n_new << lg);
@@ -1257,10 +1259,10 @@ cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
     // (without P's low part, which bf16 outputs would not show: 4096 tokens x 16 heads 130 us, with it 150)
     if (p.out_dtype == KVQ8_DTYPE_BF16)
         e = rows == 128 ? launch_tiles<false, 128, false>(p, lg, s)
-            : rows == 64 ? launch_tiles<false, 64, false>(p, lg, s) : launch_tiles<false, 32, false>(p, lg, s);
+            : rows == 64 ? launch_tiles<false, 64, false>(p, lg, s) : rows == 32 ? launch_tiles<false, 32, false>(p, lg, s) : launch_tiles<false, 16, false>(p, lg, s);
     else
         e = rows == 128 ? launch_tiles<false, 128, true>(p, lg, s)
-            : rows == 64 ? launch_tiles<false, 64, true>(p, lg, s) : launch_tiles<false, 32, true>(p, lg, s);
+            : rows == 64 ? launch_tiles<false, 64, true>(p, lg, s) : rows == 32 ? launch_tiles<false, 32, true>(p, lg, s) : launch_tiles<false, 16, true>(p, lg, s);
     if (e != cudaSuccess) return e;
     return launch_dependent(prompt_merge_kernel, dim3(tile_ctas(), rows / kMergeWarps), kMergeWarps * 32, 0, s, p, lg, rows);
 }
@@ -1272,7 +1274,7 @@ cudaError_t launch_shared_prefix(TileParams &p, int group, cudaStream_t s) {
     const cudaError_t e = launch_dependent(shared_plan_kernel, dim3(blocks), kPlanWarps * 32, 0, s, p);
     if (e != cudaSuccess) return e;
     return p.tile_rows == 128 ? launch_tiles<true, 128, true>(p, lg, s)
-           : p.tile_rows == 64 ? launch_tiles<true, 64, true>(p, lg, s) : launch_tiles<true, 32, true>(p, lg, s);
+           : p.tile_rows == 64 ? launch_tiles<true, 64, true>(p, lg, s) : p.tile_rows == 32 ? launch_tiles<true, 32, true>(p, lg, s) : launch_tiles<true, 16, true>(p, lg, s);
 }
 
 }  // namespace kvq8
