@@ -43,12 +43,13 @@
 // them 3600 to 3700: the four schedulers issue in 69 % of all cycles, the tensor
 // cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
 // of the operator's own arithmetic (each product counted once); 4096 tokens x 16
-// heads in bf16, without P's low part: 128 us, 537 TFLOP/s.  Tiles of 32 rows
-// take some 2100 clocks a stage, of which the MMAs are 512 and the bytes 1400 (at
-// the copy rate; 28 layers x 8 heads of 4096 tokens: 62 us, 36 at that rate): the
-// warps of seven roles draw on the instruction caches, so that longer loops
-// (unrolled operands) and more warps (16 for the operands, two groups of softmax
-// warps in turn, two CTAs per SM) all came out slower.
+// heads in bf16, without P's low part: 127 us, 541 TFLOP/s.  Tiles of 32 rows
+// take some 2100 clocks a stage, of 16 rows 1900, of which the MMAs are 512 (272)
+// and the bytes 1400 (at the copy rate; 28 layers x 8 heads of 4096 tokens, 16
+// rows: 57 us, 36 at that rate): the warps of seven roles draw on the instruction
+// caches, so that longer loops (unrolled operands) and more warps (16 for the
+// operands, two groups of softmax warps in turn, two CTAs per SM) all came out
+// slower, and fewer (four of softmax for 16 rows) faster.
 #include <math.h>
 
 #include "kvq8_ptx.cuh"
