@@ -73,7 +73,8 @@ constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end
 // A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^7 and 2^9 when M is set; M moves
 // when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
-constexpr int kTinyScaleLog2 = -60;             // V scales below count as this (rows of zeros do)
+// V scales below count as this (rows of zeros do).  Not lower: weights of up to 2^(15.9 + 90) still add up, a million of them.
+constexpr int kTinyScaleLog2 = -90;
 
 // Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
 template <int kRows, bool kLow>

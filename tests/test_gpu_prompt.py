@@ -434,3 +434,26 @@ def test_long_sums_in_bf16(gpu_lib):
     c.q.zero_()
     c.run()
     _check_long(c, 2.0 ** -11 + 256 * 8 / 2 * 2.0 ** -23 + 2.0 ** -18, "bf16")
+
+
+@pytest.mark.parametrize("by", [-85, 85])
+@pytest.mark.parametrize("n_new", [2, 10, 90])
+def test_values_of_any_size(gpu_lib, by, n_new):
+    c = Prompt([700, 0, 130], n_new, 8, 2, 73, spread=3.0)
+    c.cache.v_scale.mul_(2.0 ** by)
+    c.run()
+    c.check(what=f"2^{by}")
+
+
+def test_rows_of_zeros_among_the_values(gpu_lib):
+    # their scale is 0: they count in the sum alone; first all of them, then every third
+    for n_new in (2, 90):
+        c = Prompt([700, 0], n_new, 8, 2, 75)
+        for b in range(2):
+            t = torch.arange(c.starts[b] + n_new, device="cuda")
+            t = t[(t < 300) | (t % 3 == 0)]
+            blk, s = c.table[b].long()[t // 256], t % 256
+            c.cache.v_scale[blk, :, s] = 0.0
+            c.cache.v_pool[blk, :, s // 64, :, s % 64] = 0
+        c.run()
+        c.check()

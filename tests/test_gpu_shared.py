@@ -410,3 +410,12 @@ def test_ready_steps_between_shared_ones(gpu_lib):
         assert torch.equal(out, want)
         assert all(torch.equal(x, y) for x, y in zip(cache, want_cache))
     assert status.item() == 0
+
+
+@pytest.mark.parametrize("by", [-85, 85])
+def test_values_of_any_size(gpu_lib, by):
+    c = Shared([3, 20, 9], [300, 700, 256], [301 + 3 * i for i in range(3)] + [701 + 30 * i for i in range(20)] +
+               [257 + i for i in range(9)], 8, 2, 259, spread=3.0)
+    c.cache.v_scale.mul_(2.0 ** by)
+    c.run()
+    c.check(what=f"2^{by}")
