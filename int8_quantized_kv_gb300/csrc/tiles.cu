@@ -43,7 +43,7 @@
 // them 3600 to 3700: the four schedulers issue in 69 % of all cycles, the tensor
 // cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
 // of the operator's own arithmetic (each product counted once); 4096 tokens x 16
-// heads in bf16, without P's low part: 127 us, 541 TFLOP/s.  Tiles of 32 rows
+// heads in bf16, without P's low part: 117 us, 585 TFLOP/s.  Tiles of 32 rows
 // take some 2100 clocks a stage, of 16 rows 1900, of which the MMAs are 512 (272)
 // and the bytes 1400 (at the copy rate; 28 layers x 8 heads of 4096 tokens, 16
 // rows: 57 us, 36 at that rate): the warps of seven roles draw on the instruction
@@ -85,7 +85,7 @@ struct Lay {
     static constexpr int oQ = 0;
     static constexpr int oP = kQ;
     static constexpr int oMisc = oP + kP;
-    static constexpr int kMisc = 13312;
+    static constexpr int kMisc = 13824;
     static constexpr int oRing = oMisc + kMisc;
     static constexpr int kSlots = (kLimit - oRing) / kSlotBytes < 8 ? (kLimit - oRing) / kSlotBytes : 8;
     static constexpr int kBytes = oRing + kSlots * kSlotBytes;
@@ -134,13 +134,15 @@ struct Misc {
     alignas(16) Part part[4];
     alignas(16) int lim[4][kTileRows];          // tile (mod 4), row: tokens below
     alignas(16) float gain[4][kTileRows];       // tile (mod 4), row: power of two of the query's operand
+    float common[4][4];                         // tile (mod 4), share of a wide tile: its rows' gain, 0 where they differ
+    int2 spread[16];                            // warp: largest and smallest exponent of its rows' queries
     alignas(16) float2 scale[4][kTok];          // stage (mod 4): (K scale * sm_scale, V scale)
     alignas(16) float ref[kTileRows];           // per row: -M
     alignas(16) float shift[kTileRows];         // per row: M before - M now, or the output's factor
     alignas(16) float wave[4][kTileRows];       // per warp and row: maxima, sums
     char *dst[kTileRows];                       // per row: where its output or record starts (null: nowhere)
 };
-static_assert(sizeof(Misc) <= 13312, "misc");
+static_assert(sizeof(Misc) <= 13824, "misc");
 
 // Bounded like every wait here: a try sleeps up to two microseconds, and after 2^20 of them (two seconds at most) the
 // CTA gives up, its other waits with it.  Short, since the loops of all roles share the SM's instruction cache.  kTest:
@@ -781,7 +783,25 @@ tile_kernel(TileParams p, int lg) {
                     else most = fmaxf(most, top[b]);
                 }
                 // a row's values lie below 2^11 in units of 2^e
-                const int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
+                int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
+                if constexpr (kWide) {
+                    // one unit for the share's rows (prepared by its four warps) where the largest is at most 2^12 times
+                    // the smallest, which leaves the small ones 22 bits still: a multiplication less per pair of scores (4096
+                    // tokens x 16 heads in bf16 127 -> 117 us; fp32 outputs as before)
+                    const int most_e = __reduce_max_sync(0xffffffffu, e);
+                    const int least_e = __reduce_min_sync(0xffffffffu, most > 0.0f ? e : 127);
+                    if (lane == 0) ms->spread[4 * share + quad] = make_int2(most_e, least_e);
+                    named_barrier_sync(bar, 128);
+                    int2 all = ms->spread[4 * share];
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) {
+                        const int2 y = ms->spread[4 * share + k];
+                        all = make_int2(max(all.x, y.x), min(all.y, y.y));
+                    }
+                    const bool even = all.x - all.y <= 12;
+                    if (even) e = all.x;
+                    if (st == 0) ms->common[seg & 3][share] = even ? exp2_int(all.x) : 0.0f;
+                }
                 const float down = exp2_int(-e);
                 wait_warp<!kWide>(&ms->q_free, (seg & 1) ^ 1, ms);
                 unsigned char *at = smem + L::oQ + (warp - kSoftmaxWarp0) * kCoreRow + (lane >> 3) * 128 + (lane & 7) * 16;
@@ -843,6 +863,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) ref[g] = sum[g] = make_float2(0.0f, 0.0f);
             bool fresh = true;   // no row has a reference yet
+            const float common = kWide ? ms->common[seg & 3][share] : 0.0f;
             int t0 = ms->part[seg & 3].off * kTok;
             // where the totals of tiles of more than one run are kept, the record's place: of row c0, this thread's dim
             // (asked for when needed: a register less in the stages)
@@ -877,15 +898,42 @@ tile_kernel(TileParams p, int lg) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ms->s_free));
+                if constexpr (kWide) {
+                    if (__builtin_expect(common == 0.0f, 0)) {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const float2 gain = *reinterpret_cast<const float2 *>(&ms->gain[seg & 3][col + 8 * g]);
+                        for (int g = 0; g < kGroups; ++g) {
+                            const float2 gain = *reinterpret_cast<const float2 *>(&ms->gain[seg & 3][col + 8 * g]);
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        float *x = t[m >> 1][g][m & 1];
-                        const float2 y = fma2(mul2(make_float2(x[0], x[1]), make_float2(sc[m].x, sc[m].x)), gain, ref[g]);
-                        x[0] = y.x;
-                        x[1] = y.y;
+                            for (int m = 0; m < 4; ++m) {
+                                t[m >> 1][g][m & 1][0] *= gain.x;
+                                t[m >> 1][g][m & 1][1] *= gain.y;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) sc[m].x *= common;
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            float *x = t[m >> 1][g][m & 1];
+                            const float2 y = fma2(make_float2(x[0], x[1]), make_float2(sc[m].x, sc[m].x), ref[g]);
+                            x[0] = y.x;
+                            x[1] = y.y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        const float2 gain = *reinterpret_cast<const float2 *>(&ms->gain[seg & 3][col + 8 * g]);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            float *x = t[m >> 1][g][m & 1];
+                            const float2 y = fma2(mul2(make_float2(x[0], x[1]), make_float2(sc[m].x, sc[m].x)), gain, ref[g]);
+                            x[0] = y.x;
+                            x[1] = y.y;
+                        }
                     }
                 }
                 if (__builtin_expect(bad || t0 + kTok > lim_min, 0)) {   // some row does not see all of the stage

@@ -457,3 +457,24 @@ def test_rows_of_zeros_among_the_values(gpu_lib):
             c.cache.v_pool[blk, :, s // 64, :, s % 64] = 0
         c.run()
         c.check()
+
+
+@pytest.mark.parametrize("spread", [6, 11, 13, 40])
+def test_rows_of_one_tile_of_any_size(gpu_lib, spread):
+    # queries of 2^-spread .. 1 beside each other, rows of zeros among them, in tiles of 128 rows (which take one unit for
+    # rows of like size), and one row whose scores leave all others' far behind
+    c = Prompt([150, 600], 70, 8, 2, 77)
+    g = torch.Generator("cuda").manual_seed(79)
+    c.q *= torch.exp2(-spread * torch.rand((2, 70, 8, 1), generator=g, device="cuda"))
+    c.q[0, 5], c.q[1, 40, 3] = 0.0, 0.0
+    c.run()
+    c.check(what=f"spread={spread}")
+    c.q[1, 20, 2] *= 2.0 ** 60
+    c.run()
+    keep = torch.ones(2, 70, 8, dtype=torch.bool, device="cuda")
+    keep[1, 20, 2] = False
+    want = c.out.clone()
+    c.q[1, 20, 2] = 0.0
+    c.run()
+    d = (c.out - want)[keep]
+    assert torch.isfinite(want).all() and d.abs().max().item() <= 2.0 ** -17 * want.abs().max().item()
