@@ -40,7 +40,7 @@
 // What bounds it.  Of 128 rows and fp32 outputs a stage has 32 MMAs of 128 x 128
 // x 16, 64 clocks each: 2048 clocks.  The codes' conversion (8 warps) and the
 // softmax of 16384 scores (16 warps, about 15 instructions for two scores) make
-// them 3600 to 3700: the four schedulers issue in 69 % of all cycles, the tensor
+// them 3600 to 3700: the four schedulers issue in 64 % of all cycles, the tensor
 // cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
 // of the operator's own arithmetic (each product counted once); 4096 tokens x 16
 // heads in bf16, without P's low part: 117 us, 585 TFLOP/s.  Tiles of 32 rows
