@@ -586,7 +586,9 @@ kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, i
  *              padding: nothing is read or written for them
  *   out        rows of `out_dtype`, out_stride elements apart, not overlapping
  *              q; computed in fp32 and rounded once.  (For bf16 the softmax
- *              weights enter the sum rounded to 11 bits, otherwise to 22.)
+ *              weights enter the sum rounded to 11 bits, otherwise to 22.
+ *              Where V scales reach 2^x, weights below 2^-(134 - x) of a row's
+ *              largest count as 0: below 2^-40 up to scales of 2^94)
  *   workspace  at least kvq8_prompt_workspace_bytes(...) bytes, otherwise as
  *              kvq8_decode_attn
  * Pointers 16-byte aligned, strides multiples of 16 bytes and at least

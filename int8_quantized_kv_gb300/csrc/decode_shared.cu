@@ -50,13 +50,15 @@ shared_merge_kernel(DecodeParams d, TileParams t, int G) {
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
         if (top == -INFINITY) continue;
-        const float f_old = ex2_approx(m - top);   // 0 while m is -inf
-        s_sum *= f_old;
+        const float2 old = pow2_parts(m - top);   // 0 while m is -inf
+        const float f_old = old.x * old.y;
+        s_sum = s_sum * old.x * old.y;
         a = make_float4(a.x * f_old, a.y * f_old, a.z * f_old, a.w * f_old);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const float f = ex2_approx(ml[k].x - top);
-            s_sum = fmaf(ml[k].y, f, s_sum);
+            const float2 part = pow2_parts(ml[k].x - top);
+            const float f = part.x * part.y;
+            s_sum = fmaf(ml[k].y * part.x, part.y, s_sum);
             a.x = fmaf(x[k].x, f, a.x);
             a.y = fmaf(x[k].y, f, a.y);
             a.z = fmaf(x[k].z, f, a.z);

@@ -34,6 +34,13 @@ __device__ __forceinline__ void store1(void *base, int dtype, int64_t i, float x
     else static_cast<__half *>(base)[i] = __float2half_rn(x);
 }
 
+// 2^d (d <= 0) as two factors, each a normal number where 2^d alone need not be: the sums of weights that it is for reach
+// 2^126 (tiles.cu), and what is left of them after a move by more than 2^-126 still counts.
+__device__ __forceinline__ float2 pow2_parts(float d) {
+    const float whole = floorf(0.5f * fmaxf(d, -252.0f));
+    return make_float2(ex2_approx(whole), ex2_approx(d - whole));   // (0 for d = -inf)
+}
+
 // Whether group entry g (0 .. n_groups) may be part of a cut of the batch.
 __device__ __forceinline__ bool group_entry_ok(const TileParams &p, int g) {
     const int s = p.group_starts[g];

@@ -74,6 +74,7 @@ constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end
 // when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
 // V scales below count as this (rows of zeros do).  Not lower: weights of up to 2^(15.9 + 90) still add up, a million of them.
+// (Where V scales reach 2^x, weights below 2^-(134 - x) of a row's largest are lost: below fp32's normal numbers.)
 constexpr int kTinyScaleLog2 = -90;
 
 // Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
@@ -1018,7 +1019,10 @@ tile_kernel(TileParams p, int lg) {
                     for (int g = 0; g < kGroups; ++g) {
                         const float2 by = *reinterpret_cast<const float2 *>(&ms->shift[col + 8 * g]);
                         ref[g] = add2(ref[g], by);
-                        if (!fresh) sum[g] = mul2(sum[g], make_float2(ex2_approx(by.x), ex2_approx(by.y)));
+                        if (!fresh) {
+                            const float2 fx = pow2_parts(by.x), fy = pow2_parts(by.y);
+                            sum[g] = mul2(mul2(sum[g], make_float2(fx.x, fy.x)), make_float2(fx.y, fy.y));
+                        }
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             t[m >> 1][g][m & 1][0] += by.x;
@@ -1226,13 +1230,15 @@ prompt_merge_kernel(TileParams p, int lg, int rows_per_tile) {
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
         if (top == -INFINITY) continue;
-        const float f_old = ex2_approx(m - top);   // 0 while m is -inf
-        S *= f_old;
+        const float2 old = pow2_parts(m - top);   // 0 while m is -inf
+        const float f_old = old.x * old.y;
+        S = S * old.x * old.y;
         a = make_float4(a.x * f_old, a.y * f_old, a.z * f_old, a.w * f_old);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const float f = ex2_approx(ml[k].x - top);
-            S = fmaf(ml[k].y, f, S);
+            const float2 part = pow2_parts(ml[k].x - top);
+            const float f = part.x * part.y;
+            S = fmaf(ml[k].y * part.x, part.y, S);
             a.x = fmaf(x[k].x, f, a.x);
             a.y = fmaf(x[k].y, f, a.y);
             a.z = fmaf(x[k].z, f, a.z);

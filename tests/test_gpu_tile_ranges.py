@@ -1,0 +1,110 @@
+"""Prompts and shared prefixes at the ends of what their inputs may be: rows of zeros among
+the values beside values of any size."""
+import pytest
+import torch
+
+import tile_ref as ref
+from test_gpu_prompt import Prompt
+from test_gpu_shared import Shared
+
+pytestmark = pytest.mark.gpu
+
+# New query tokens per sequence with four heads to a kv head: tiles of 16, 32, 64 and 128 rows.
+HEIGHTS = [3, 6, 12, 40]
+
+
+def _places(blocks, t):
+    return blocks.long()[t // 256], t % 256
+
+
+def _zeros(cache, blocks, t):
+    blk, s = _places(blocks, t)
+    cache.v_scale[blk, :, s] = 0.0
+    cache.v_pool[blk, :, s // 64, :, s % 64] = 0
+
+
+def _larger(cache, blocks, t, by):
+    blk, s = _places(blocks, t)
+    cache.v_scale[blk, :, s] *= 2.0 ** by
+
+
+def _mixed_values(cache, blocks, n, by, where):
+    """Tokens [0, n): rows of zeros before, behind or between rows 2^by times as large as drawn."""
+    t = torch.arange(n, device="cuda")
+    zero = {"first": t < n // 2, "last": t >= n // 2, "between": (t // 150) % 2 == 0}[where]
+    _zeros(cache, blocks, t[zero])
+    _larger(cache, blocks, t[~zero], by)
+
+
+@pytest.mark.parametrize("where", ["first", "last", "between"])
+@pytest.mark.parametrize("by", [-40, 40, 44, 85])
+@pytest.mark.parametrize("n_new", HEIGHTS)
+def test_prompt_rows_of_zeros_beside_values_of_any_size(gpu_lib, n_new, by, where):
+    # a tile shared by many CTAs (each has a stage or two, so the records differ), and tiles that a CTA has whole
+    for starts, size in (([700], 0.0), ([700, 333], 1.5), ([400 + 3 * i for i in range(90)], 0.0)):
+        c = Prompt(starts, n_new, 8, 2, 301, size=size)
+        for b, p in enumerate(starts):
+            _mixed_values(c.cache, c.table[b], p + n_new, by, where)
+        c.run()
+        for b in range(0, len(starts), 17):
+            one = Prompt.__new__(Prompt)
+            one.__dict__.update(c.__dict__)
+            one.starts, one.ns, one.q, one.table = c.starts[b:b + 1], c.ns[b:b + 1], c.q[b:b + 1], c.table[b:b + 1]
+            one.check(out=c.out[b:b + 1], what=f"2^{by} {where} size={size} of {len(starts)}")
+
+
+@pytest.mark.parametrize("where", ["first", "last", "between"])
+@pytest.mark.parametrize("by", [-40, 40, 85])
+@pytest.mark.parametrize("rows", HEIGHTS)
+def test_shared_rows_of_zeros_beside_values_of_any_size(gpu_lib, rows, by, where):
+    # in the prefix, and the rows' own tokens of the other kind: zeros behind large values, and the other way round
+    for size, own in ((0.0, "zeros"), (1.5, "large"), (0.0, "as drawn")):
+        prefix = 900
+        c = Shared([rows], [prefix], [prefix + 1 + (5 * i) % 70 for i in range(rows)], 8, 2, 303, size=size)
+        _mixed_values(c.cache, c.table[c.lead[0]], prefix, by, where)
+        for b in range(rows):
+            t = torch.arange(prefix, c.lens[b], device="cuda")
+            if own == "zeros":
+                _zeros(c.cache, c.table[b], t)
+            elif own == "large":
+                _larger(c.cache, c.table[b], t, by)
+        c.run()
+        c.check(what=f"2^{by} {where} size={size} own={own}")
+
+
+def test_shared_prefix_of_zeros_and_large_values_of_the_rows_own(gpu_lib):
+    # the records of the prefix and of the rows' own tokens far apart, either way
+    for prefix_by, own_by in ((None, 60), (60, None), (-85, 60), (85, -60)):
+        c = Shared([6, 20], [700, 300], [701 + 7 * i for i in range(6)] + [301 + 3 * i for i in range(20)], 8, 2, 305, size=0.0)
+        for b in range(c.batch):
+            p = c.prefix[c.group[b]]
+            if b == c.lead[c.group[b]]:
+                t = torch.arange(p, device="cuda")
+                _zeros(c.cache, c.table[b], t) if prefix_by is None else _larger(c.cache, c.table[b], t, prefix_by)
+            t = torch.arange(p, c.lens[b], device="cuda")
+            _zeros(c.cache, c.table[b], t) if own_by is None else _larger(c.cache, c.table[b], t, own_by)
+        c.run()
+        c.check(what=f"prefix {prefix_by}, own {own_by}")
+
+
+@pytest.mark.parametrize("n_new", HEIGHTS)
+@pytest.mark.parametrize("many", [False, True])
+def test_many_rows_of_zeros_below_large_values_of_higher_scores(gpu_lib, n_new, many):
+    # 4000 rows of zeros, then 100 rows of values near 2^36 whose scores are 10 higher (base 2): the zeros still take
+    # 4000 / (4000 + 100 * 2^10) of the weight
+    starts = [4100] * (90 if many else 1)
+    c = Prompt(starts, n_new, 8, 2, 307)
+    c.q.fill_(1.0)
+    for b in range(len(starts)):
+        t = torch.arange(4100 + n_new, device="cuda")
+        blk, s = _places(c.table[b], t)
+        c.cache.k_pool[blk, :, s] = 100
+        c.cache.k_scale[blk, :, s] = ((t >= 4000).float() * 10 / (100 * 128 * ref.SM * ref.LOG2E))[:, None]
+        _zeros(c.cache, c.table[b], t[:4000])
+        _larger(c.cache, c.table[b], t[4000:], 36)
+    c.run()
+    for b in {0, len(starts) - 1}:
+        one = Prompt.__new__(Prompt)
+        one.__dict__.update(c.__dict__)
+        one.starts, one.ns, one.q, one.table = c.starts[b:b + 1], c.ns[b:b + 1], c.q[b:b + 1], c.table[b:b + 1]
+        one.check(out=c.out[b:b + 1])
