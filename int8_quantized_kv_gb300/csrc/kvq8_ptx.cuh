@@ -233,15 +233,17 @@ __host__ __device__ constexpr uint32_t mma_word(int n, bool n_major) {
 // D (tensor memory, 128 x n) (+)= A (tensor memory, 128 x 128 halves: eight steps of 8 columns) B (shared memory, n x
 // 128: steps 256 bytes apart).  The whole warp comes here and elects the lane that issues, so that the operands stay in
 // uniform registers: a step takes 31 clocks to issue (17 to run, for n = 32), with a lane chosen by its number 67.
+// kDown: what D held counts 2^-kDown of itself (0 .. 15).
+template <int kDown = 0>
 __device__ __forceinline__ void mma_k128(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool accumulate) {
 #define KVQ8_MMA_STEP "add.u32 ta, ta, 8;\n\tadd.s64 tb, tb, 16;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, r;\n\t"
     asm volatile(
         "{\n\t.reg .pred p, q, r;\n\t.reg .b32 ta;\n\t.reg .b64 tb;\n\t"
         "elect.sync _|p, 0xffffffff;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.eq.u32 r, %0, %0;\n\t"
         "mov.b32 ta, %1;\n\tmov.b64 tb, %2;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], tb, %3, q, %5;\n\t"
         KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP KVQ8_MMA_STEP "}" ::"r"(d),
-        "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate), "n"(kDown)
         : "memory");
 #undef KVQ8_MMA_STEP
 }

@@ -19,6 +19,8 @@
 // (22 bits).  Of a tile of up to 64 rows both parts are columns of one product
 // (A from tensor memory feeds at most 128 columns per 64 cycles, so the second
 // part is free); of up to 128 rows they are two products into one accumulator.
+// (The query's low part counts 2^-11 of itself, in the addition of the columns
+// or as the first product's result enters the second.)
 // bf16 outputs take P's high part alone: 11 bits of each weight, an eighth of
 // the output's own rounding.
 //
@@ -70,6 +72,9 @@ constexpr int kLimit = 232448;                  // bytes of shared memory
 constexpr int kColumns = 512;                   // of tensor memory: all
 constexpr int kSoftmaxWarp0 = 12;               // warps before: 4 for copies, MMAs and order, 4 for K's operands, 4 for V's
 constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end: two seconds
+// The query's low parts are held 2^11 times as large as they are: at half a step of the high part at most, they end
+// below fp16's largest, and parts of small values keep their bits.
+constexpr int kQLowBits = 11;
 // A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^7 and 2^9 when M is set; M moves
 // when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
 constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
@@ -314,6 +319,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
     return a / b;
 }
 
+// The exponent of the unit in which a positive value lies in [2^14, 2^15).
+__device__ __forceinline__ int unit_exponent(float x) { return (__float_as_int(x) >> 23) - 127 - 14; }
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -540,8 +548,12 @@ tile_kernel(TileParams p, int lg) {
                         wait_warp<!kWide>(&ms->s_free, (x & 1) ^ 1, ms);
                         tc_fence_after();
                         // (low parts first: what they add to is small yet, and little is cut off)
-                        if (kWide) mma_k128(d, a, b + kLowPart, kWord, false);
-                        mma_k128(d, a, b, kWord, kWide);
+                        if constexpr (kWide) {
+                            mma_k128(d, a, b + kLowPart, kWord, false);
+                            mma_k128<kQLowBits>(d, a, b, kWord, true);
+                        } else {
+                            mma_k128(d, a, b, kWord, false);
+                        }
                         mma_commit(smem_addr(&ms->s_full));
                         mma_commit(smem_addr(&ms->k_free[buf]));
                     }
@@ -762,7 +774,7 @@ tile_kernel(TileParams p, int lg) {
                 }
                 // the rule of quantize_q_vals_warp; |x| as bits orders as |x| does, a NaN or infinity above all
                 float top[4];
-                float most = 0.0f;
+                float most = 0.0f, least = INFINITY;   // of the blocks that are not zeros
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     uint32_t m = 0;
@@ -781,16 +793,21 @@ tile_kernel(TileParams p, int lg) {
                     }
                     top[b] = __uint_as_float(m);
                     if (top[b] < 1e-6f) top[b] = 1.0f;   // (codes 0)
-                    else most = fmaxf(most, top[b]);
+                    else {
+                        most = fmaxf(most, top[b]);
+                        least = fminf(least, top[b]);
+                    }
                 }
-                // a row's values lie below 2^11 in units of 2^e
-                int e = max(-100, (__float_as_int(most) >> 23) - 127 - 10);
+                // A row's values lie below 2^15 in units of 2^e (fp16 ends below 2^16).  The low parts, in units 2^11 times
+                // smaller, leave out 2^-36 at most: 2^-22 of a block's largest up to blocks 2^28 times smaller than the row's
+                // largest.  (A block's own size counts, not the row's: keys may be zeros everywhere else.)
+                int e = max(-100, unit_exponent(most));
                 if constexpr (kWide) {
-                    // one unit for the share's rows (prepared by its four warps) where the largest is at most 2^12 times
-                    // the smallest, which leaves the small ones 22 bits still: a multiplication less per pair of scores (4096
-                    // tokens x 16 heads in bf16 127 -> 117 us; fp32 outputs as before)
+                    // one unit for the share's rows (prepared by its four warps) where their largest block is at most 2^28 times
+                    // the smallest, by the same bound: a multiplication less per pair of scores (4096 tokens x 16 heads in bf16 127 -> 117 us;
+                    // fp32 outputs as before)
                     const int most_e = __reduce_max_sync(0xffffffffu, e);
-                    const int least_e = __reduce_min_sync(0xffffffffu, most > 0.0f ? e : 127);
+                    const int least_e = __reduce_min_sync(0xffffffffu, most > 0.0f ? unit_exponent(least) : 127);
                     if (lane == 0) ms->spread[4 * share + quad] = make_int2(most_e, least_e);
                     named_barrier_sync(bar, 128);
                     int2 all = ms->spread[4 * share];
@@ -799,7 +816,7 @@ tile_kernel(TileParams p, int lg) {
                         const int2 y = ms->spread[4 * share + k];
                         all = make_int2(max(all.x, y.x), min(all.y, y.y));
                     }
-                    const bool even = all.x - all.y <= 12;
+                    const bool even = all.x - all.y <= 27;   // (by exponents: a ratio below 2^28)
                     if (even) e = all.x;
                     if (st == 0) ms->common[seg & 3][share] = even ? exp2_int(all.x) : 0.0f;
                 }
@@ -823,7 +840,8 @@ tile_kernel(TileParams p, int lg) {
                         v = mul2(v, unit2);
                         const __half2 h = __floats2half2_rn(v.x, v.y);
                         hi[k] = half2_bits(h);
-                        v = fma2(__half22float2(h), make_float2(-1.f, -1.f), v);
+                        constexpr float kUp = 1 << kQLowBits;
+                        v = mul2(fma2(__half22float2(h), make_float2(-1.f, -1.f), v), make_float2(kUp, kUp));
                         lo[k] = half2_bits(__floats2half2_rn(v.x, v.y));
                     }
                     *reinterpret_cast<uint4 *>(at + b * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -893,7 +911,7 @@ tile_kernel(TileParams p, int lg) {
 #pragma unroll
                     for (int k = 0; k < kVals * 4; ++k) {
                         asm volatile("" : "+f"((&t[0][0][0][0])[k]), "+f"(low[k]));
-                        (&t[0][0][0][0])[k] += low[k];
+                        (&t[0][0][0][0])[k] = fmaf(low[k], 1.0f / (1 << kQLowBits), (&t[0][0][0][0])[k]);
                     }
                 }
                 tc_fence_before();

@@ -1,5 +1,5 @@
 """Prompts and shared prefixes at the ends of what their inputs may be: rows of zeros among
-the values beside values of any size."""
+the values beside values of any size, queries whose 32-blocks are of very unequal size."""
 import pytest
 import torch
 
@@ -108,3 +108,33 @@ def test_many_rows_of_zeros_below_large_values_of_higher_scores(gpu_lib, n_new, 
         one.__dict__.update(c.__dict__)
         one.starts, one.ns, one.q, one.table = c.starts[b:b + 1], c.ns[b:b + 1], c.q[b:b + 1], c.table[b:b + 1]
         one.check(out=c.out[b:b + 1])
+
+
+def _only_block(cache, blocks, n, block, nkv):
+    """K rows of the tokens [0, n): zero outside one 32-block."""
+    t = torch.arange(n, device="cuda")
+    blk, s = _places(blocks, t)
+    d = torch.arange(128, device="cuda")
+    keep = torch.zeros(128, dtype=torch.bool, device="cuda")
+    keep[32 * block:32 * block + 32] = True
+    at = ((d // 16) ^ (s[:, None] & 7)) * 16 + d % 16              # byte place of each dim
+    mask = torch.zeros((n, 128), dtype=torch.int8, device="cuda").scatter_(1, at, keep.to(torch.int8).expand(n, -1))
+    for h in range(nkv):
+        cache.k_pool[blk, h, s] *= mask
+
+
+@pytest.mark.parametrize("down,rows_apart", [(22, 0), (16, 0), (8, 10), (14, 10), (3, 40)])
+@pytest.mark.parametrize("n_new", HEIGHTS)
+def test_keys_that_meet_a_small_part_of_the_query(gpu_lib, n_new, down, rows_apart):
+    # one 32-block of each query is 2^-down of the row's largest, and the keys are zero outside it; rows of a tile up to
+    # 2^rows_apart apart.  (Rows of 2^4, so that no block falls below the query rule's 1e-6.)
+    c = Prompt([300, 0], n_new, 8, 2, 309)
+    g = torch.Generator("cuda").manual_seed(11)
+    apart = torch.randint(0, 2, (2, n_new, 8, 1), generator=g, device="cuda").float()
+    c.q *= 16.0 * torch.exp2(rows_apart * apart)
+    c.q[..., 64:96] *= 2.0 ** -down
+    for b, p in enumerate(c.starts):
+        _only_block(c.cache, c.table[b], p + n_new, 2, 2)
+    # scores of some hundreds in size for the rows of 16
+    c.run(sm_scale=ref.SM * 2.0 ** (down - 1))
+    c.check(sm=ref.SM * 2.0 ** (down - 1), what=f"2^-{down}, rows 2^{rows_apart} apart")
