@@ -251,7 +251,10 @@ decode_tail_kernel(DecodeParams p) {
     }
     // No wait here: nothing below reads what the tile kernel ahead writes, and what is ahead of that kernel (the plan's
     // ws_tail among it) was done when its CTAs let this kernel start.  The CTAs begin on the SMs that it has left, and
-    // each waits for it before it leaves itself, so that the merge behind finds both done.
+    // each waits for it before it leaves itself, so that the merge behind finds both done.  What the wait would order is
+    // ordered here: a word of the plan read at GPU scope, then a fence, so that no load below takes a line that an earlier
+    // call left in this SM's L1.
+    acquire_gpu(p.windows);
     // ---- the workers' shares of all units' stages ----
     const int per = (p.batch + kTailWarps * 32 - 1) / (kTailWarps * 32);
     const int b_lo = min(p.batch, tid * per), b_hi = min(p.batch, b_lo + per);

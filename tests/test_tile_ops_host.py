@@ -1,10 +1,14 @@
 """Host-side checks of the prompt attention, the decode over shared prefixes and the
 cache read back: every refusal returns before a launch, so this runs without a GPU."""
+import os
+import re
+
 import pytest
 
 from int8_quantized_kv_gb300 import build as kbuild
 from int8_quantized_kv_gb300 import kvq8
 
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "int8_quantized_kv_gb300", "csrc")
 FAKE = 1 << 20   # a 256-aligned non-null address that is never dereferenced
 
 
@@ -99,3 +103,15 @@ def test_read_refusals(lib):
         assert _read(lib, **{name: FAKE + 2}) == kvq8.ERR_INVALID_ARG, name
     assert _read(lib, batch=0) == kvq8.OK
     assert _read(lib, n_new=0) == kvq8.OK
+
+
+def test_the_tail_split_acquires_what_it_does_not_wait_for():
+    # it starts without the wait that would order the plan's rows, lengths, tables and queries ahead of its loads, so it
+    # acquires them itself, in every thread and ahead of the first load
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "decode_tail.cuh")).read())
+    body = text[text.index("decode_tail_kernel(DecodeParams p) {"):text.index("launch_tail_g")]
+    acquire = body.index("\n    acquire_gpu(p.windows);\n")
+    loads = re.search(r"p\.(ctx_lens|windows|block_table|q|k_new|v_new|batch)\b(?!\);)", body)
+    assert acquire < loads.start() < body.index("pdl_wait()")
+    ptx = open(os.path.join(CSRC, "kvq8_ptx.cuh")).read()
+    assert re.search(r"ld\.relaxed\.gpu\.global\.s32 [^;]*;\\n\\tfence\.acq_rel\.gpu;", ptx)
