@@ -686,7 +686,9 @@ kvq8_status kvq8_decode_step_shared(const float *q, const float *k_new, const fl
  *              Either may be NULL: its rows are not read
  * Rows whose position is outside the block table, or whose block id is outside
  * the pool, are left as they are and flagged (KVQ8_DEV_BAD_POSITION,
- * KVQ8_DEV_BAD_BLOCK_ID).  batch == 0 or n_new == 0 is a no-op.
+ * KVQ8_DEV_BAD_BLOCK_ID).  batch == 0 or n_new == 0 is a no-op.  batch * nkv *
+ * ((n_new + 30) / 16), divided downwards, is at most 2^34 - 8, else
+ * KVQ8_ERR_UNSUPPORTED.
  */
 kvq8_status kvq8_read(int batch, int n_new, int nkv, int hd,
                       const int8_t *k_pool, const int8_t *v_pool,

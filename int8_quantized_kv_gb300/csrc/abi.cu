@@ -807,6 +807,7 @@ kvq8_status kvq8_read(int batch, int n_new, int nkv, int hd, const int8_t *k_poo
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     p.dev_status = dev_status;
+    if (!read_fits(p)) return KVQ8_ERR_UNSUPPORTED;
     return launch_read(p, (cudaStream_t)stream) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
 }
 

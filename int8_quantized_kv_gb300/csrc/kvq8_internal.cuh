@@ -243,6 +243,7 @@ struct ReadParams {
     int64_t k_stride, v_stride;
     uint32_t *dev_status;
 };
+bool read_fits(const ReadParams &p);   // into one launch
 cudaError_t launch_read(const ReadParams &p, cudaStream_t s);
 
 // --------------------------------------------------------------- eviction --

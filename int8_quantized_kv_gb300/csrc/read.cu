@@ -126,13 +126,20 @@ read_kernel(ReadParams p, int groups) {
     }
 }
 
+// 16-slot groups that n_new tokens may touch, wherever the first position lies in its group.
+int64_t read_groups(int n_new) { return ((int64_t)n_new + 2 * kReadSlots - 2) / kReadSlots; }
+
+int64_t read_blocks(const ReadParams &p) {
+    // (at most 65535 * 65535 rows of 2^27 groups: below 2^63)
+    const int64_t rows = (int64_t)p.batch * p.nkv, groups = read_groups(p.n_new);
+    return (rows * groups + kReadWarps - 1) / kReadWarps;
+}
+
 template <typename T>
 cudaError_t launch_read_t(const ReadParams &p, cudaStream_t s) {
-    const int groups = (p.n_new + 2 * kReadSlots - 2) / kReadSlots;   // wherever the first position lies in its group
-    const int64_t blocks = ((int64_t)p.batch * groups * p.nkv + kReadWarps - 1) / kReadWarps;
-    if (blocks > 2147483647) return cudaErrorInvalidValue;
+    const int groups = (int)read_groups(p.n_new);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)read_blocks(p));
     cfg.blockDim = dim3(kReadWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -144,6 +151,8 @@ cudaError_t launch_read_t(const ReadParams &p, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool read_fits(const ReadParams &p) { return read_blocks(p) <= 2147483647; }
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t s) {
     switch (p.dtype) {

@@ -115,3 +115,13 @@ def test_the_tail_split_acquires_what_it_does_not_wait_for():
     assert acquire < loads.start() < body.index("pdl_wait()")
     ptx = open(os.path.join(CSRC, "kvq8_ptx.cuh")).read()
     assert re.search(r"ld\.relaxed\.gpu\.global\.s32 [^;]*;\\n\\tfence\.acq_rel\.gpu;", ptx)
+
+
+def test_read_takes_no_more_rows_than_one_launch_has_warps_for(lib):
+    # 65535 * 65535 * 2^27 tasks at most; a count that passed 31 bits would make a small grid of it.  (Without a GPU what
+    # passes the checks fails at its launch.)
+    top = 2**31 - 1
+    for bad in (dict(n_new=top, batch=256, nkv=1, k_s=128, v_s=128), dict(n_new=top, batch=65535, nkv=8, k_s=1024, v_s=1024),
+                dict(n_new=2**30, batch=2048, nkv=2), dict(n_new=top, batch=65535, nkv=65535, k_s=2**23, v_s=2**23),
+                dict(n_new=top - 29, batch=128, nkv=1, k_s=128, v_s=128)):
+        assert _read(lib, **bad) == kvq8.ERR_UNSUPPORTED, bad
