@@ -131,7 +131,7 @@ struct Misc {
     uint64_t part_ready[4], part_free[4];
     uint64_t s_full, s_free, p_ready, pv_done, q_ready, q_free, o_free, all_done[2];
     long long warp_tot[32];
-    int4 at0, of0;                              // the first tile: sequence, rows' tile, rows, cost ahead of this CTA; its Walk
+    int4 at0, of0;                              // the first tile: sequence, rows' tile, rows, its cost ahead of this CTA; its Walk
     volatile int abort;
     uint32_t tmem;                              // address of the columns
     int skip[8];                                // slot: its block id is outside the pool
@@ -443,7 +443,13 @@ tile_kernel(TileParams p, int lg) {
         for (int i = i_lo; i < i_hi && before <= rem; ++i) {
             const long long v = per == 1 ? mine : item(i);
             if (rem < before + v) {
-                ms->at0 = make_int4(w.s, w.r, w.rows, (int)(rem - before));
+                long long at = rem - before;   // (of a group's tiles together, which may pass 31 bits)
+                if (kShared) {
+                    const int n = w.cost(0);
+                    w.r = (int)divide(at, n);
+                    at -= (long long)w.r * n;
+                }
+                ms->at0 = make_int4(w.s, w.r, w.rows, (int)at);
                 ms->of0 = make_int4(w.first, w.lead, w.span, (int)w.start);
             }
             before += v;
@@ -459,11 +465,6 @@ tile_kernel(TileParams p, int lg) {
         w.lead = of0.y;
         w.span = of0.z;
         w.start = of0.w;
-        if (kShared) {
-            const int n = w.cost(0);
-            w.r = off / n;
-            off -= w.r * n;
-        }
     }
 
     if (warp < 4) {

@@ -1,9 +1,11 @@
 """Prompts and shared prefixes at the ends of what their inputs may be: rows of zeros among
-the values beside values of any size, queries whose 32-blocks are of very unequal size."""
+the values beside values of any size, queries whose 32-blocks are of very unequal size, as
+much work in one group as 32 bits do not count."""
 import pytest
 import torch
 
 import tile_ref as ref
+from int8_quantized_kv_gb300 import kvq8
 from test_gpu_prompt import Prompt
 from test_gpu_shared import Shared
 
@@ -138,3 +140,35 @@ def test_keys_that_meet_a_small_part_of_the_query(gpu_lib, n_new, down, rows_apa
     # scores of some hundreds in size for the rows of 16
     c.run(sm_scale=ref.SM * 2.0 ** (down - 1))
     c.check(sm=ref.SM * 2.0 ** (down - 1), what=f"2^-{down}, rows 2^{rows_apart} apart")
+
+
+@pytest.mark.slow
+def test_shared_group_of_more_work_than_31_bits_count(gpu_lib):
+    # 65535 rows of 8 heads in tiles of 16 (65534 empty groups lower the average), each over 72000 stages: 2.36e9 with the
+    # tiles' own cost, so that the last tenth of the CTAs begin beyond 2^31.  Four blocks stand for the whole prefix, and
+    # equal weights make every row the mean of their values.
+    batch, G, n, blocks = 65535, 8, 36000, 5
+    prefix = n * 256
+    cache = ref.random_cache(blocks, 1, 311)
+    table = torch.full((batch, n + 1), -1, dtype=torch.int32, device="cuda")
+    table[0, :n] = torch.arange(n, device="cuda") % 4
+    table[:, n] = 4
+    starts = torch.full((batch + 1,), batch, dtype=torch.int32, device="cuda")
+    starts[0] = 0
+    shared = torch.full((batch,), prefix, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), prefix + 1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((batch, G, 128), device="cuda")
+    out = torch.full_like(q, float("nan"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = kvq8.alloc_shared_workspace(batch, batch, G, 1, n + 1)
+    kvq8.decode_attn_shared(q, cache, table, lens, starts, shared, out, ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    _, v = ref.rows64(cache, torch.arange(4, device="cuda"), 0, torch.arange(1024, device="cuda"))
+    _, last = ref.rows64(cache, torch.tensor([4], device="cuda"), 0, torch.zeros(1, device="cuda"))
+    want = (v.mean(0) * prefix + last[0]) / (prefix + 1)
+    # 9000 runs of eight stages are added to a total of 24 bits, each off by half a step (2^-25 of it) at most; within a
+    # run LONG_TOL of test_gpu_prompt, of the largest of its sums of values
+    tol = (9000 * 2.0 ** -25 + 96 * 2.0 ** -23 + 2.0 ** -18) * v.abs().mean(0).max()
+    for part in out.split(4096):
+        assert bool(((part.double() - want).abs() <= tol).all())
