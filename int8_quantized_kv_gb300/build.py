@@ -1,14 +1,17 @@
 """Builds libkvq8.so in-tree with nvcc for sm_103a (GB300).
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
-int8_quantized_kv_gb300/_build/libkvq8.so.  Rebuilds only when a source or
-header is newer than the library.  `python -m int8_quantized_kv_gb300.build`
+int8_quantized_kv_gb300/_build/libkvq8.so; what ptxas says of its kernels
+(registers, spills) is kept beside each object and checked where a kernel
+depends on it.  Rebuilds only when a source, a header or this file is newer
+than the library.  `python -m int8_quantized_kv_gb300.build`
 does the same from a shell.
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +29,20 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 
+# Kernels whose warpgroups trade registers (setmaxnreg) within what the launch holds, which is the count that the compiler
+# gives them: (mangled name, registers per thread that the shares add up to, kLaunchRegs in tiles.cu).
+TRADING = [(r"tile_kernelILb[01]ELi128E", 72)]
+
+
+def check_registers(src: str, ptxas: str) -> None:
+    """Raises where ptxas -v reports another register count for a kernel of TRADING than its shares add up to: it would be
+    refused at its launch (a share above the launch's registers would wait for ever)."""
+    for name, regs in re.findall(r"Compiling entry function '(\S+)'.*?Used (\d+) registers", ptxas, re.S):
+        for pattern, want in TRADING:
+            if re.search(pattern, name) and int(regs) != want:
+                raise RuntimeError(f"{src}: {name} has {regs} registers per thread, its warpgroups' shares need {want}")
+
+
 def _nvcc() -> str:
     cand = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(cand):
@@ -38,7 +55,7 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return [__file__] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def needs_build() -> bool:
@@ -54,16 +71,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose or ptxas_info:
-            sys.stderr.write(r.stdout + r.stderr)
+        said = r.stdout + r.stderr
+        check_registers(os.path.basename(src), said)
+        with open(obj[:-2] + ".ptxas", "w") as f:
+            f.write(said)
+        if ptxas_info:
+            sys.stderr.write(said)
+        elif verbose:
+            sys.stderr.writelines(x for x in said.splitlines(True) if "ptxas info" not in x and "bytes stack frame" not in x)
         return obj
 
     srcs = sources()

@@ -125,3 +125,18 @@ def test_read_takes_no_more_rows_than_one_launch_has_warps_for(lib):
                 dict(n_new=2**30, batch=2048, nkv=2), dict(n_new=top, batch=65535, nkv=65535, k_s=2**23, v_s=2**23),
                 dict(n_new=top - 29, batch=128, nkv=1, k_s=128, v_s=128)):
         assert _read(lib, **bad) == kvq8.ERR_UNSUPPORTED, bad
+
+
+def test_kernels_that_trade_registers_have_the_count_that_they_trade(lib):
+    # setmaxnreg draws on what the launch holds: a compiler that gives such a kernel another count fails the build, not
+    # every large prompt at its launch
+    said = open(os.path.join(kbuild.BUILD_DIR, "tiles.ptxas")).read()
+    counts = re.findall(r"Compiling entry function '(\S*tile_kernelILb[01]ELi128E\S*)'.*?Used (\d+) registers", said, re.S)
+    assert len(counts) == 3
+    want = re.search(r"kLaunchRegs = (\d+)", open(os.path.join(CSRC, "tiles.cu")).read()).group(1)
+    assert {n for _, n in counts} == {want} and [w for _, w in kbuild.TRADING] == [int(want)]
+    kbuild.check_registers("tiles.cu", said)
+    for other in (int(want) - 8, int(want) + 8):
+        with pytest.raises(RuntimeError, match="registers per thread"):
+            kbuild.check_registers("tiles.cu", said.replace(f"Used {want} registers", f"Used {other} registers"))
+    kbuild.check_registers("other.cu", "ptxas info : Compiling entry function '_Z5plainv' for 'sm_103a'\nUsed 40 registers")
