@@ -1,9 +1,10 @@
 """Prompts and shared prefixes at the ends of what their inputs may be: rows of zeros among
-the values beside values of any size, queries whose 32-blocks are of very unequal size, as
-much work in one group as 32 bits do not count."""
+the values beside values of any size, queries whose 32-blocks are of very unequal size, flat
+to one-hot weights with keys of any size, as much work in one group as 32 bits do not count."""
 import pytest
 import torch
 
+import tile_bounds
 import tile_ref as ref
 from int8_quantized_kv_gb300 import kvq8
 from test_gpu_prompt import Prompt
@@ -140,6 +141,27 @@ def test_keys_that_meet_a_small_part_of_the_query(gpu_lib, n_new, down, rows_apa
     # scores of some hundreds in size for the rows of 16
     c.run(sm_scale=ref.SM * 2.0 ** (down - 1))
     c.check(sm=ref.SM * 2.0 ** (down - 1), what=f"2^-{down}, rows 2^{rows_apart} apart")
+
+
+# (query size, spread of the cache's rows, factor of the scores): flat to one-hot weights, keys of one size and of any.
+WEIGHTS = [(1e-3, 0.0, 1.0), (1.5, 0.0, 1.0), (40.0, 0.0, 1.0), (1e3, 0.0, 1.0), (3e4, 0.0, 1.0), (1.5, 3.0, 1.0), (1.5, 12.0, 1.0),
+           (1.5, 12.0, 2.0 ** -8), (45.0, 10.0, 1.0)]
+
+
+@pytest.mark.parametrize("size,spread,factor", WEIGHTS)
+@pytest.mark.parametrize("n_new", HEIGHTS)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_prompt_weights_flat_to_one_hot(gpu_lib, out, n_new, size, spread, factor):
+    c = Prompt([200, 5, 700], n_new, 8, 2, 313, out=out, size=size, spread=spread)
+    c.run(sm_scale=ref.SM * factor)
+    for b, p in enumerate(c.starts):
+        lims = (p + 1 + torch.arange(n_new, device="cuda")).repeat_interleave(4)
+        for h in range(2):
+            k, v = ref.rows64(c.cache, c.table[b], h, torch.arange(p + n_new, device="cuda"))
+            rows = c.q[b, :, 4 * h:4 * h + 4].reshape(-1, 128)
+            want, tol, decided = tile_bounds.attend(rows, k, v, lims, ref.SM * factor, out is torch.bfloat16)
+            assert tile_bounds.sharp(want, tol, decided, 0.9)
+            tile_bounds.check(c.out[b, :, 4 * h:4 * h + 4], want, tol, f"b={b} h={h}")
 
 
 @pytest.mark.slow
