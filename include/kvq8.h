@@ -638,7 +638,8 @@ kvq8_status kvq8_prompt_attn(const void *q, int q_dtype, int64_t q_stride,
  *                 attends the first ctx_lens[b] shared tokens
  *   workspace     at least kvq8_shared_workspace_bytes(...) bytes, otherwise as
  *                 kvq8_decode_attn
- * Other arguments as kvq8_decode_attn.
+ * Other arguments as kvq8_decode_attn.  Small softmax weights where V scales are
+ * large, and 32-blocks of a query of unequal size, count as in kvq8_prompt_attn.
  *
  * kvq8_decode_step_shared -- the same as one decode step: appends k_new, v_new
  * at position ctx_lens[b] - 1 as kvq8_decode_step does, then attends.  The new

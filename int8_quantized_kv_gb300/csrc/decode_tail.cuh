@@ -13,12 +13,15 @@
 // products are done and whose V when the sums are, so that each copy has half a
 // stage's time (12 warps an SM with one stage each against 6 with two: 48 us
 // against 56).  Queries, block ids and a step's new token are loaded when the
-// unit's first stage is asked for.  The arithmetic of a stage is
-// decode_split.cuh's.  The kernel starts on the SMs that the tile kernel ahead has
+// unit's first stage is asked for.  The dot products of a stage are
+// decode_split.cuh's; the softmax goes by one reference per head for scores and V
+// scales together, as in the tile kernel, so that a token of small V scale keeps
+// its bits beside one of large V scale and little weight.  The kernel starts on the SMs that the tile kernel ahead has
 // left and waits for it at its own end (28 layers' step 119.7 -> 110.7 us).
 #pragma once
 
 #include "decode_split.cuh"
+#include "tile_rows.cuh"
 
 namespace kvq8 {
 namespace {
@@ -91,12 +94,12 @@ __device__ __forceinline__ void tail_scores(const unsigned char *st, const int8_
     }
 }
 
-// The state (M, Sl, acc in units of 2^e_cur) takes these tokens in, vsa and vsb their V scales (0 where masked).  p_hi,
-// p_lo: the warp's room for P.
+// The state (M the reference, Sl and acc relative to it) takes these tokens in, vsa and vsb their V scales (0 where
+// masked).  p_hi, p_lo: the warp's room for P.
 template <int G>
 __device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi, __half *p_lo, int lane, int n, int t4, bool va,
                                           bool vb, float vsa, float vsb, const float (&sa)[G], const float (&sb)[G],
-                                          float (&M)[G], float (&Sl)[G], float (&acc)[8][4], int &e_cur) {
+                                          float (&M)[G], float (&Sl)[G], float (&acc)[8][4]) {
     const int8_t *vst = reinterpret_cast<const int8_t *>(st) + kStageKBytes;
     const int ta = lane, tb = lane + 32;
     // n, t4: MMA fragment coordinates (lane / 4, lane % 4).
@@ -107,62 +110,44 @@ __device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi,
     constexpr bool kPackPV = G <= 4;
     const int col_head0 = kPackPV ? (2 * t4) % G : 2 * t4;
     const int col_head1 = kPackPV ? (2 * t4 + 1) % G : 2 * t4 + 1;
-    // power-of-two unit of this stage's P: 2^e > max vs, so that
-    // p' = w * vs * 2^-e stays below 2^8 (w < 2^8, see below).  e only
-    // moves when it must grow or has become 2^12 too large.
-    const int e_need = redux_max_i32(
-        ((__float_as_int(fmaxf(vsa, vsb)) >> 23) & 0xff) - 126);  // 0 -> -126
-    int e = e_cur;
-    if (e_need > e_cur || e_need < e_cur - 12) e = max(-120, min(120, e_need));
-    const float inv = __int_as_float((127 - e) << 23);
-
     // ---- segment 2b: online softmax ----
-    // The running maximum M is raised only when a score exceeds it by
-    // more than 2^kLazyLog2; below that the weights 2^(s-M) stay < 2^8
-    // and every quantity remains exact to fp32 rounding.
+    const float ea = exponent_above(vsa), eb = exponent_above(vsb);
     bool grow = false;
 #pragma unroll
-    for (int g = 0; g < G; ++g) grow |= fmaxf(sa[g], sb[g]) > M[g] + kLazyLog2;
-    float alpha[G];
-    bool rescale = (e != e_cur);
+    for (int g = 0; g < G; ++g) grow |= fmaxf(sa[g] + ea, sb[g] + eb) > M[g] + kPMaxLog2;
     if (__any_sync(0xffffffffu, grow)) {
-        rescale = true;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float m_new = fmaxf(M[g], redux_max_f32(fmaxf(sa[g], sb[g])));
-            alpha[g] = ex2_approx(M[g] - m_new);   // 0 while M is -inf
-            M[g] = m_new;
-        }
-    } else {
-#pragma unroll
-        for (int g = 0; g < G; ++g) alpha[g] = 1.0f;
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const float wa = va ? ex2_approx(sa[g] - M[g]) : 0.0f;
-        const float wb = vb ? ex2_approx(sb[g] - M[g]) : 0.0f;
-        Sl[g] = fmaf(Sl[g], alpha[g], wa + wb);
-        const float pa = wa * vsa * inv, pb = wb * vsb * inv;
-        const __half ha = __float2half_rn(pa), hb = __float2half_rn(pb);
-        p_hi[g * kPRowHalves + ta] = ha;
-        p_hi[g * kPRowHalves + tb] = hb;
-        p_lo[g * kPRowHalves + ta] = __float2half_rn(pa - __half2float(ha));
-        p_lo[g * kPRowHalves + tb] = __float2half_rn(pb - __half2float(hb));
-    }
-    if (rescale) {  // warp-uniform
-        const float two = __int_as_float((127 + max(-126, min(127, e_cur - e))) << 23);
         float f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (g == col_head0) f0 = alpha[g] * two;
-            if (g == col_head1) f1 = alpha[g] * two;
+            const float top = redux_max_f32(fmaxf(sa[g] + ea, sb[g] + eb));
+            float f = 1.0f;
+            if (top > M[g] + kPMaxLog2) {
+                const float to = ceilf(top) - kPTopLog2;
+                const float2 part = pow2_parts(M[g] - to);   // 0 while M is -inf
+                Sl[g] = Sl[g] * part.x * part.y;
+                f = part.x * part.y;
+                M[g] = to;
+            }
+            if (g == col_head0) f0 = f;
+            if (g == col_head1) f1 = f;
         }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             acc[mt][0] *= f0; acc[mt][1] *= f1;
             acc[mt][2] *= f0; acc[mt][3] *= f1;
         }
-        e_cur = e;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float wa = va ? ex2_approx(sa[g] - M[g]) : 0.0f;
+        const float wb = vb ? ex2_approx(sb[g] - M[g]) : 0.0f;
+        Sl[g] += wa + wb;
+        const float pa = wa * vsa, pb = wb * vsb;
+        const __half ha = __float2half_rn(pa), hb = __float2half_rn(pb);
+        p_hi[g * kPRowHalves + ta] = ha;
+        p_hi[g * kPRowHalves + tb] = hb;
+        p_lo[g * kPRowHalves + ta] = __float2half_rn(pa - __half2float(ha));
+        p_lo[g * kPRowHalves + tb] = __float2half_rn(pb - __half2float(hb));
     }
     __syncwarp();
 
@@ -387,7 +372,6 @@ decode_tail_kernel(DecodeParams p) {
         }
     };
     float M[G], Sl[G], acc[8][4];
-    int e_cur = 1000;
     bool begin = true, gave_up = false;
     auto wait = [&](int which, int k) {
         if (!gave_up && !mbar_wait_tries(smem_addr(full + which), k & 1)) {
@@ -413,7 +397,6 @@ decode_tail_kernel(DecodeParams p) {
             for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][i] = 0.0f;
-            e_cur = 1000;
             __syncwarp();
         }
         skip = skip_next;
@@ -445,7 +428,7 @@ decode_tail_kernel(DecodeParams p) {
             ++copied;
         }
         if (!append) wait(1, k);
-        if (!skip) tail_sums<G>(st, p_hi, p_lo, lane, n, t4, va, vb, vsa, vsb, sa, sb, M, Sl, acc, e_cur);
+        if (!skip) tail_sums<G>(st, p_hi, p_lo, lane, n, t4, va, vb, vsa, vsb, sa, sb, M, Sl, acc);
         __syncwarp();
         if (copied == k + 2) copy_v();
         begin = ++at.j == at.nb;
@@ -464,7 +447,6 @@ decode_tail_kernel(DecodeParams p) {
                     }
                 }
             }
-            const float unit = __int_as_float((127 + max(-126, min(127, e_cur))) << 23);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const float s = warp_sum(Sl[g]);
@@ -477,8 +459,8 @@ decode_tail_kernel(DecodeParams p) {
                 for (int i = 0; i < 2; ++i) {
                     const int g = 2 * t4 + i;
                     if (g < G) {
-                        out[g * kHD + mt * 16] = acc[mt][i] * kCodeUnit * unit;
-                        out[g * kHD + mt * 16 + 8] = acc[mt][2 + i] * kCodeUnit * unit;
+                        out[g * kHD + mt * 16] = acc[mt][i] * kCodeUnit;
+                        out[g * kHD + mt * 16 + 8] = acc[mt][2 + i] * kCodeUnit;
                     }
                 }
             }

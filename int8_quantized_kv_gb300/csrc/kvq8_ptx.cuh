@@ -98,8 +98,7 @@ __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity) {
 // What was done before *at got the value that it has (by a kernel that is over) is seen by the loads behind this, whatever
 // this SM's L1 holds of it.
 __device__ __forceinline__ void acquire_gpu(const int32_t *at) {
-    int32_t x;
-    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];\n\tfence.acq_rel.gpu;" : "=r"(x) : "l"(at) : "memory");
+    asm volatile("{\n\t.reg .s32 x;\n\tld.relaxed.gpu.global.s32 x, [%0];\n\tfence.acq_rel.gpu;\n\t}" ::"l"(at) : "memory");
 }
 
 // L2 policy for data read exactly once (the streamed KV cache).

@@ -1,6 +1,6 @@
 // tile_rows.cuh -- what the kernels over tiles of query rows (prompts, shared
-// prefixes) have in common: where a row's query lies, the groups of a shared
-// batch, rows of the three types.
+// prefixes) have in common: the reference of a row's weights, the groups of a
+// shared batch, rows of the three types.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,8 +34,20 @@ __device__ __forceinline__ void store1(void *base, int dtype, int64_t i, float x
     else static_cast<__half *>(base)[i] = __float2half_rn(x);
 }
 
+// A row's reference M: its operand P = 2^(s - M) * V scale has its maximum put between 2^7 and 2^9 when M is set; M moves
+// (up, by a whole number) when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
+constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
+// V scales below count as this (rows of zeros do).  Not lower: weights of up to 2^(15.9 + 90) still add up, a million of them.
+// (Where V scales reach 2^x, weights below 2^-(134 - x) of a row's largest are lost: below fp32's normal numbers.)
+constexpr int kTinyScaleLog2 = -90;
+
+// The least whole number above log2 of a V scale (kTinyScaleLog2 at least), by its exponent bits.
+__device__ __forceinline__ float exponent_above(float scale) {
+    return __int_as_float(max(__float_as_int(scale) >> 23, kTinyScaleLog2 + 126) | 0x4b000000) - (0x1p23f + 126.0f);
+}
+
 // 2^d (d <= 0) as two factors, each a normal number where 2^d alone need not be: the sums of weights that it is for reach
-// 2^126 (tiles.cu), and what is left of them after a move by more than 2^-126 still counts.
+// 2^126, and what is left of them after a move by more than 2^-126 still counts.
 __device__ __forceinline__ float2 pow2_parts(float d) {
     const float whole = floorf(0.5f * fmaxf(d, -252.0f));
     return make_float2(ex2_approx(whole), ex2_approx(d - whole));   // (0 for d = -inf)

@@ -75,13 +75,6 @@ constexpr uint64_t kLimitNs = 2000000000ull;    // bound of the waits at the end
 // The query's low parts are held 2^11 times as large as they are: at half a step of the high part at most, they end
 // below fp16's largest, and parts of small values keep their bits.
 constexpr int kQLowBits = 11;
-// A row's reference M: P = 2^(s - M) * V scale, whose maximum is put between 2^7 and 2^9 when M is set; M moves
-// when P might pass 2^15.9 (fp16 ends below 2^16).  (A V scale counts as the next power of two.)
-constexpr float kPTopLog2 = 9.0f, kPMaxLog2 = 15.9f;
-// V scales below count as this (rows of zeros do).  Not lower: weights of up to 2^(15.9 + 90) still add up, a million of them.
-// (Where V scales reach 2^x, weights below 2^-(134 - x) of a row's largest are lost: below fp32's normal numbers.)
-constexpr int kTinyScaleLog2 = -90;
-
 // Shared memory for tiles of kRows rows: Q (high, low), P (high, low), the ring.
 template <int kRows, bool kLow>
 struct Lay {
@@ -293,11 +286,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// The least whole number above log2 of a V scale (kTinyScaleLog2 at least), by its exponent bits.
-__device__ __forceinline__ float exponent_above(float scale) {
-    return __int_as_float(max(__float_as_int(scale) >> 23, kTinyScaleLog2 + 126) | 0x4b000000) - (0x1p23f + 126.0f);
 }
 
 // A total's element, which one thread alone has to do with: what it asks for in turn happens in turn.

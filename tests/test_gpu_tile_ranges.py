@@ -164,6 +164,21 @@ def test_prompt_weights_flat_to_one_hot(gpu_lib, out, n_new, size, spread, facto
             tile_bounds.check(c.out[b, :, 4 * h:4 * h + 4], want, tol, f"b={b} h={h}")
 
 
+@pytest.mark.parametrize("size,spread,factor", [w for w in WEIGHTS if w[2] == 1.0])
+@pytest.mark.parametrize("rows", HEIGHTS)
+def test_shared_weights_flat_to_one_hot(gpu_lib, rows, size, spread, factor):
+    c = Shared([rows], [600], [601 + (11 * i) % 150 for i in range(rows)], 8, 2, 315, size=size, spread=spread)
+    c.run()
+    for h in range(2):
+        k1, v1 = ref.rows64(c.cache, c.table[c.lead[0]], h, torch.arange(600, device="cuda"))
+        for b in range(rows):
+            k2, v2 = ref.rows64(c.cache, c.table[b], h, torch.arange(600, c.lens[b], device="cuda"))
+            want, tol, decided = tile_bounds.attend(c.q[b, 4 * h:4 * h + 4], torch.cat([k1, k2]), torch.cat([v1, v2]),
+                                                    torch.full((4,), c.lens[b], device="cuda"))
+            assert tile_bounds.sharp(want, tol, decided, 0.5)      # of four rows
+            tile_bounds.check(c.out[b, 4 * h:4 * h + 4], want, tol, f"b={b} h={h}")
+
+
 @pytest.mark.slow
 def test_shared_group_of_more_work_than_31_bits_count(gpu_lib):
     # 65535 rows of 8 heads in tiles of 16 (65534 empty groups lower the average), each over 72000 stages: 2.36e9 with the
