@@ -16,8 +16,10 @@
 // unit's first stage is asked for.  The dot products of a stage are
 // decode_split.cuh's; the softmax goes by one reference per head for scores and V
 // scales together, as in the tile kernel, so that a token of small V scale keeps
-// its bits beside one of large V scale and little weight.  The kernel starts on the SMs that the tile kernel ahead has
-// left and waits for it at its own end (28 layers' step 119.7 -> 110.7 us).
+// its bits beside one of large V scale and little weight.  The kernel starts on
+// the SMs that the tile kernel ahead has left and waits for it at its own end (28
+// layers' step 119.7 -> 110.7 us).  Spilled are 128 to 156 bytes a thread with G =
+// 1 and 8 (170 and 255 registers), 8 to 52 with 2 and 4.
 #pragma once
 
 #include "decode_split.cuh"

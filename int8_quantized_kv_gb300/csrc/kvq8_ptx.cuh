@@ -277,12 +277,9 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t addr, float *r) {
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
             : KVQ8_R8(r), KVQ8_R8(r + 8)
             : "r"(addr));
-    } else if constexpr (kGroups == 2) {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : KVQ8_R8(r) : "r"(addr));
     } else {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-                     : "r"(addr));
+        static_assert(kGroups == 2, "groups");
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : KVQ8_R8(r) : "r"(addr));
     }
 }
 #undef KVQ8_R8

@@ -11,8 +11,9 @@
 // per token for K (token-major rows), a lane per dim for V (dim-major), so the
 // codes go from the bulk-copied stage through registers (int8 -> fp16, exact)
 // into tensor memory with neither a transpose nor a second pass through shared
-// memory, and the right operands' row count is the tile's own (a multiple of
-// 16), so that few rows cost little softmax work.
+// memory, and the right operands are as narrow as the tile's height (16, 32, 64
+// or 128 rows: rows that a tile does not have are computed and dropped), so that
+// few rows cost little softmax work.
 //
 // fp32-class results from fp16 operands: the codes are exact; a query row's
 // values code * scale and the weights P enter as a high and a low fp16 part
@@ -44,7 +45,9 @@
 // softmax of 16384 scores (16 warps, about 15 instructions for two scores) make
 // them 3600 to 3700: the four schedulers issue in 64 % of all cycles, the tensor
 // cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
-// of the operator's own arithmetic (each product counted once); 4096 tokens x 16
+// of the operator's own arithmetic (each product counted once), with 4.7 GB of
+// DRAM traffic for 0.28 GB of cache (16 tiles of a kv head at different places of
+// it at a time; 36 % of DRAM's rate, which bounds nothing yet); 4096 tokens x 16
 // heads in bf16, without P's low part: 117 us, 585 TFLOP/s.  Tiles of 32 rows
 // take some 2100 clocks a stage, of 16 rows 1900, of which the MMAs are 512 (272)
 // and the bytes 1400 (at the copy rate; 28 layers x 8 heads of 4096 tokens, 16
@@ -104,8 +107,8 @@ struct Lay {
     // the cut is a thirtieth of their rounding.
     static constexpr int kRun = !kLow ? 256 : kWide ? 12 : 8;
     // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
-    // K's operands; V's; four of softmax) trade them for.  Local memory would cost more here than elsewhere: shared memory
-    // leaves it no L1.
+    // K's operands; V's; four of softmax) trade them for.  Local memory costs more here than elsewhere, since shared memory
+    // leaves it no L1: 56 to 72 bytes a thread are spilled with 128 rows, 8 to 12 with 64.  (The build checks the count.)
     static constexpr int kLaunchRegs = 72, kRegsOther = 40, kRegsSoftmax = 96;
     static_assert(!kWide || kSoftmaxWarp0 / 4 * kRegsOther + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs,
                   "registers");
@@ -377,7 +380,7 @@ tile_kernel(TileParams p, int lg) {
     }
     if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), kColumns);
     pdl_wait();
-    pdl_launch_dependents();   // (the next kernel's CTAs find no registers here before this one leaves)
+    pdl_launch_dependents();   // (the tails find no room here before this CTA leaves; a merge's CTA beside 16 rows just waits)
     // ---- this CTA's share: [lo, hi) of the sequence of all tiles, each as long as it costs ----
     Walk<kShared> w(p, lg, kRows);
     const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + kRows - 1) / kRows);
@@ -1313,7 +1316,10 @@ int log2_of(int x) {
 // Rows per tile: the most that a sequence (on average, a group) has, up to 128, since a stage's time grows with its
 // tile's rows, and each further tile turns the same codes into operands again.  8 sequences behind 4000 tokens, G = 4,
 // with tiles of 32, 64 and 128 rows: 20 rows 29, 35, 45 us; 64 rows 46, 36, 47 us; 128 rows 74, 55, 52 us; of 16 and
-// 32 rows: 8 rows 23.8, 26.7 us.
+// 32 rows: 8 rows 23.8, 26.7 us.  The counts that a tile really has are device data, which the rule does not see, so
+// sequences or groups of very unequal counts are faster in calls of their own: a prompt of 2000 tokens beside 60 single
+// tokens behind 4000 (G = 4, 8 kv heads) 349 us in one call, 110 + 107 in two; a group of 200 rows behind 8192 beside
+// 199 groups of one row behind 1024 297 us, 84 + 130 in two.
 static int rows_of(int64_t rows) { return rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16; }
 
 cudaError_t launch_prompt(const TileParams &p, int group, cudaStream_t s) {
