@@ -206,6 +206,10 @@ size_t kvq8_decode_workspace_bytes(int batch, int nqh, int nkv, int hd,
  *   with exact int32 block dots; softmax over t with a running maximum, V
  *   accumulated as int8 code * (weight * v_scale_t) in fp32; one division by
  *   the softmax sum at the end.  Sequences with ctx_lens[b] == 0 yield 0.
+ *   (weight * v_scale_t enters in two fp16 parts, in a unit that the largest
+ *   v_scale among some 64 tokens sets, whatever that token's weight: where V
+ *   rows differ in size by up to 2^6, 6e-6 of an output is lost; by 2^20, the
+ *   small ones' share may be off by some per cent.)
  *
  *   q             fp32 [batch][nqh][hd]: one query token per sequence
  *   ctx_lens      int32 [batch]: tokens 0 .. ctx_lens[b]-1 are attended
