@@ -48,7 +48,7 @@
 // of the operator's own arithmetic (each product counted once), with 4.7 GB of
 // DRAM traffic for 0.28 GB of cache (16 tiles of a kv head at different places of
 // it at a time; 36 % of DRAM's rate, which bounds nothing yet); 4096 tokens x 16
-// heads in bf16, without P's low part: 117 us, 585 TFLOP/s.  Tiles of 32 rows
+// heads in bf16, without P's low part: 119 us, 578 TFLOP/s.  Tiles of 32 rows
 // take some 2100 clocks a stage, of 16 rows 1900, of which the MMAs are 512 (272)
 // and the bytes 1400 (at the copy rate; 28 layers x 8 heads of 4096 tokens, 16
 // rows: 57 us, 36 at that rate): the warps of seven roles draw on the instruction
