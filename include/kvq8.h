@@ -592,9 +592,11 @@ kvq8_status kvq8_norm_rope_append(const void *q, const void *k, const void *v, i
  *              q; computed in fp32 and rounded once.  (For bf16 the softmax
  *              weights enter the sum rounded to 11 bits, otherwise to 22.
  *              Where V scales reach 2^x, weights below 2^-(134 - x) of a row's
- *              largest count as 0: below 2^-40 up to scales of 2^94.  The
- *              values of a query's 32-block enter with 22 bits of the block's
- *              largest, down to blocks 2^28 times smaller than the row's)
+ *              largest count as 0: below 2^-40 up to scales of 2^94; where V
+ *              rows of zeros have a row's weight, what the others add to it
+ *              below 2^-100 is lost.  The values of a query's 32-block enter
+ *              with 22 bits of the block's largest, down to blocks 2^28 times
+ *              smaller than the row's)
  *   workspace  at least kvq8_prompt_workspace_bytes(...) bytes, otherwise as
  *              kvq8_decode_attn
  * Pointers 16-byte aligned, strides multiples of 16 bytes and at least

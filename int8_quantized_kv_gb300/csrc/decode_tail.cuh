@@ -96,12 +96,12 @@ __device__ __forceinline__ void tail_scores(const unsigned char *st, const int8_
     }
 }
 
-// The state (M the reference, Sl and acc relative to it) takes these tokens in, vsa and vsb their V scales (0 where
-// masked).  p_hi, p_lo: the warp's room for P.
+// The state takes these tokens in, vsa and vsb their V scales (0 where masked): Sl and acc are relative to the reference R;
+// fresh says that there is none yet.  sa, sb: the scores, here made relative to it.  p_hi, p_lo: the warp's room for P.
 template <int G>
-__device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi, __half *p_lo, int lane, int n, int t4, bool va,
-                                          bool vb, float vsa, float vsb, const float (&sa)[G], const float (&sb)[G],
-                                          float (&M)[G], float (&Sl)[G], float (&acc)[8][4]) {
+__device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi, __half *p_lo, int lane, int n, int t4,
+                                          float vsa, float vsb, float (&sa)[G], float (&sb)[G], bool fresh,
+                                          float (&R)[G], float (&Sl)[G], float (&acc)[8][4]) {
     const int8_t *vst = reinterpret_cast<const int8_t *>(st) + kStageKBytes;
     const int ta = lane, tb = lane + 32;
     // n, t4: MMA fragment coordinates (lane / 4, lane % 4).
@@ -114,21 +114,30 @@ __device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi,
     const int col_head1 = kPackPV ? (2 * t4 + 1) % G : 2 * t4 + 1;
     // ---- segment 2b: online softmax ----
     const float ea = exponent_above(vsa), eb = exponent_above(vsb);
-    bool grow = false;
+    const float most_a = kPMaxLog2 - ea, most_b = kPMaxLog2 - eb;
+    bool grow = fresh;
 #pragma unroll
-    for (int g = 0; g < G; ++g) grow |= fmaxf(sa[g] + ea, sb[g] + eb) > M[g] + kPMaxLog2;
+    for (int g = 0; g < G; ++g) {
+        sa[g] -= R[g];
+        sb[g] -= R[g];
+        grow |= sa[g] > most_a || sb[g] > most_b;
+    }
     if (__any_sync(0xffffffffu, grow)) {
         float f0 = 0.0f, f1 = 0.0f;
+        uint32_t leapt = 0;   // (by head)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const float top = redux_max_f32(fmaxf(sa[g] + ea, sb[g] + eb));
             float f = 1.0f;
-            if (top > M[g] + kPMaxLog2) {
-                const float to = ceilf(top) - kPTopLog2;
-                const float2 part = pow2_parts(M[g] - to);   // 0 while M is -inf
+            if (fresh || top > kPMaxLog2) {
+                const float by = ceilf(top) - kPTopLog2;
+                const float2 part = fresh ? make_float2(0.0f, 0.0f) : pow2_parts(-by);
                 Sl[g] = Sl[g] * part.x * part.y;
                 f = part.x * part.y;
-                M[g] = to;
+                sa[g] -= by;
+                sb[g] -= by;
+                R[g] += by;
+                if (fabsf(by) > 0x1p20f) leapt |= 1u << g;
             }
             if (g == col_head0) f0 = f;
             if (g == col_head1) f1 = f;
@@ -138,11 +147,23 @@ __device__ __forceinline__ void tail_sums(const unsigned char *st, __half *p_hi,
             acc[mt][0] *= f0; acc[mt][1] *= f1;
             acc[mt][2] *= f0; acc[mt][3] *= f1;
         }
+        if (__builtin_expect(leapt != 0, 0)) {
+            // scores whose own rounding takes the distances that P depends on: now that they are small, they move once
+            // more, exactly (what such a head held is 0)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (leapt >> g & 1) {
+                    const float by = ceilf(redux_max_f32(fmaxf(sa[g] + ea, sb[g] + eb))) - kPTopLog2;
+                    sa[g] -= by;
+                    sb[g] -= by;
+                    R[g] += by;
+                }
+            }
+        }
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const float wa = va ? ex2_approx(sa[g] - M[g]) : 0.0f;
-        const float wb = vb ? ex2_approx(sb[g] - M[g]) : 0.0f;
+        const float wa = ex2_approx(sa[g]), wb = ex2_approx(sb[g]);   // (masked: 0)
         Sl[g] += wa + wb;
         const float pa = wa * vsa, pb = wb * vsb;
         const __half ha = __float2half_rn(pa), hb = __float2half_rn(pb);
@@ -373,8 +394,8 @@ decode_tail_kernel(DecodeParams p) {
             }
         }
     };
-    float M[G], Sl[G], acc[8][4];
-    bool begin = true, gave_up = false;
+    float R[G], Sl[G], acc[8][4];
+    bool begin = true, fresh = true, gave_up = false;
     auto wait = [&](int which, int k) {
         if (!gave_up && !mbar_wait_tries(smem_addr(full + which), k & 1)) {
             gave_up = true;
@@ -392,13 +413,13 @@ decode_tail_kernel(DecodeParams p) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 quantize_q_vals_warp(qx[g], lane, q_codes + g * kHD, q_scale + g * kNQB, p.dev_status);
-                M[g] = -INFINITY;
-                Sl[g] = 0.0f;
+                R[g] = Sl[g] = 0.0f;
             }
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][i] = 0.0f;
+            fresh = true;
             __syncwarp();
         }
         skip = skip_next;
@@ -430,7 +451,10 @@ decode_tail_kernel(DecodeParams p) {
             ++copied;
         }
         if (!append) wait(1, k);
-        if (!skip) tail_sums<G>(st, p_hi, p_lo, lane, n, t4, va, vb, vsa, vsb, sa, sb, M, Sl, acc);
+        if (!skip) {
+            tail_sums<G>(st, p_hi, p_lo, lane, n, t4, vsa, vsb, sa, sb, fresh, R, Sl, acc);
+            fresh = false;
+        }
         __syncwarp();
         if (copied == k + 2) copy_v();
         begin = ++at.j == at.nb;
@@ -452,7 +476,7 @@ decode_tail_kernel(DecodeParams p) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const float s = warp_sum(Sl[g]);
-                if (lane == 0) *reinterpret_cast<float2 *>(p.ws_ml + (rec * G + g) * 2) = make_float2(M[g], s);
+                if (lane == 0) *reinterpret_cast<float2 *>(p.ws_ml + (rec * G + g) * 2) = make_float2(s > 0.0f ? R[g] : -INFINITY, s);
             }
             float *out = p.ws_acc + rec * G * kHD + n;
 #pragma unroll

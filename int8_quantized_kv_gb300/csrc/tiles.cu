@@ -380,7 +380,7 @@ tile_kernel(TileParams p, int lg) {
     }
     if (warp == 1) tmem_alloc(smem_addr(&ms->tmem), kColumns);
     pdl_wait();
-    pdl_launch_dependents();   // (the tails find no room here before this CTA leaves; a merge's CTA beside 16 rows just waits)
+    pdl_launch_dependents();   // (the tails find no room here before this CTA leaves; what does just waits)
     // ---- this CTA's share: [lo, hi) of the sequence of all tiles, each as long as it costs ----
     Walk<kShared> w(p, lg, kRows);
     const int per_seq = kShared ? 1 : (int)((((long long)p.n_new << lg) + kRows - 1) / kRows);
@@ -973,25 +973,42 @@ tile_kernel(TileParams p, int lg) {
                     // move the references of rows whose P would leave fp16's range (at first: of all), by whole
                     // numbers.  A row that a stage hides is hidden in all stages behind, but for bad blocks: a
                     // stage of one leaves the rows fresh
-                    float top[kVals], vs_log2[4];
+                    float vs_log2[4];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) vs_log2[m] = exponent_above(sc[m].y);
+                    // the largest score + log2 V scale of row c0 + st, for the threads st < kCols
+                    auto row_tops = [&] {
+                        float top[kVals];
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
+                        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            top[2 * g + k] = fmaxf(fmaxf(t[0][g][0][k] + vs_log2[0], t[0][g][1][k] + vs_log2[1]),
-                                                   fmaxf(t[1][g][0][k] + vs_log2[2], t[1][g][1][k] + vs_log2[3]));
-                    halve<kVals / 2, 16>(top, lane, [](float a, float b) { return fmaxf(a, b); });
-                    ms->wave[quad][folded_row] = top[0];
-                    named_barrier_sync(bar, 128);
+                            for (int k = 0; k < 2; ++k)
+                                top[2 * g + k] = fmaxf(fmaxf(t[0][g][0][k] + vs_log2[0], t[0][g][1][k] + vs_log2[1]),
+                                                       fmaxf(t[1][g][0][k] + vs_log2[2], t[1][g][1][k] + vs_log2[3]));
+                        halve<kVals / 2, 16>(top, lane, [](float a, float b) { return fmaxf(a, b); });
+                        ms->wave[quad][folded_row] = top[0];
+                        named_barrier_sync(bar, 128);
+                        const int x = c0 + (st & (kCols - 1));
+                        return fmaxf(fmaxf(ms->wave[0][x], ms->wave[1][x]), fmaxf(ms->wave[2][x], ms->wave[3][x]));
+                    };
+                    // the references move by ms->shift, and what is held with them
+                    auto move = [&] {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) {
+                            const float2 by = *reinterpret_cast<const float2 *>(&ms->shift[col + 8 * g]);
+                            ref[g] = add2(ref[g], by);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                t[m >> 1][g][m & 1][0] += by.x;
+                                t[m >> 1][g][m & 1][1] += by.y;
+                            }
+                        }
+                    };
+                    float most = row_tops();
                     if (st < kCols) {
-                        const int x = c0 + st;
-                        const float most = fmaxf(fmaxf(ms->wave[0][x], ms->wave[1][x]), fmaxf(ms->wave[2][x], ms->wave[3][x]));
-                        const bool move = fresh ? most > -INFINITY : most > kPMaxLog2;
-                        const float by = move ? kPTopLog2 - ceilf(most) : 0.0f;
-                        ms->ref[x] += by;
-                        ms->shift[x] = by;
+                        const float by = (fresh ? most > -INFINITY : most > kPMaxLog2) ? kPTopLog2 - ceilf(most) : 0.0f;
+                        ms->ref[c0 + st] += by;
+                        ms->shift[c0 + st] = by;
                     }
                     named_barrier_sync(bar, 128);
                     if (!rest && !fresh) {
@@ -1025,19 +1042,29 @@ tile_kernel(TileParams p, int lg) {
                             if (ms->shift[c0 + k] != 0.0f)
                                 store_relaxed(total + k * kHD, load_relaxed(total + k * kHD) * ex2_approx(ms->shift[c0 + k]));
                     }
+                    bool far = false;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const float2 by = *reinterpret_cast<const float2 *>(&ms->shift[col + 8 * g]);
-                        ref[g] = add2(ref[g], by);
+                        far |= fmaxf(fabsf(by.x), fabsf(by.y)) > 0x1p20f;
                         if (!fresh) {
                             const float2 fx = pow2_parts(by.x), fy = pow2_parts(by.y);
                             sum[g] = mul2(mul2(sum[g], make_float2(fx.x, fy.x)), make_float2(fx.y, fy.y));
                         }
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            t[m >> 1][g][m & 1][0] += by.x;
-                            t[m >> 1][g][m & 1][1] += by.y;
+                    }
+                    move();
+                    if (__builtin_expect(barrier_any(bar, 128, far), 0)) {
+                        // Scores beyond 2^20: the distances that P depends on were lost in their rounding (from 2^26 on
+                        // P would leave fp16's range).  Now that they are small, they move once more, exactly.  (What
+                        // such a row held is 0.)
+                        most = row_tops();
+                        if (st < kCols) {
+                            const float by = fabsf(ms->shift[c0 + st]) > 0x1p20f ? kPTopLog2 - ceilf(most) : 0.0f;
+                            ms->ref[c0 + st] += by;
+                            ms->shift[c0 + st] = by;
                         }
+                        named_barrier_sync(bar, 128);
+                        move();
                     }
                     fresh = fresh && bad;
                 }

@@ -146,9 +146,11 @@ def test_keys_that_meet_a_small_part_of_the_query(gpu_lib, n_new, down, rows_apa
 # (query size, spread of the cache's rows, factor of the scores): flat to one-hot weights, keys of one size and of any.
 WEIGHTS = [(1e-3, 0.0, 1.0), (1.5, 0.0, 1.0), (40.0, 0.0, 1.0), (1e3, 0.0, 1.0), (3e4, 0.0, 1.0), (1.5, 3.0, 1.0), (1.5, 12.0, 1.0),
            (1.5, 12.0, 2.0 ** -8), (45.0, 10.0, 1.0)]
+# Scores of 2^26 and more, whose own steps are wider than the weights' range.
+HUGE = [(3e4, 12.0, 1.0), (3e4, 12.0, -1.0), (1e8, 12.0, 1.0), (1e20, 3.0, 1.0)]
 
 
-@pytest.mark.parametrize("size,spread,factor", WEIGHTS)
+@pytest.mark.parametrize("size,spread,factor", WEIGHTS + HUGE)
 @pytest.mark.parametrize("n_new", HEIGHTS)
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 def test_prompt_weights_flat_to_one_hot(gpu_lib, out, n_new, size, spread, factor):
@@ -164,7 +166,7 @@ def test_prompt_weights_flat_to_one_hot(gpu_lib, out, n_new, size, spread, facto
             tile_bounds.check(c.out[b, :, 4 * h:4 * h + 4], want, tol, f"b={b} h={h}")
 
 
-@pytest.mark.parametrize("size,spread,factor", [w for w in WEIGHTS if w[2] == 1.0])
+@pytest.mark.parametrize("size,spread,factor", [w for w in WEIGHTS + HUGE if w[2] == 1.0])
 @pytest.mark.parametrize("rows", HEIGHTS)
 def test_shared_weights_flat_to_one_hot(gpu_lib, rows, size, spread, factor):
     c = Shared([rows], [600], [601 + (11 * i) % 150 for i in range(rows)], 8, 2, 315, size=size, spread=spread)
