@@ -18,8 +18,8 @@
 // scales together, as in the tile kernel, so that a token of small V scale keeps
 // its bits beside one of large V scale and little weight.  The kernel starts on
 // the SMs that the tile kernel ahead has left and waits for it at its own end (28
-// layers' step 119.7 -> 110.7 us).  Spilled are 128 to 156 bytes a thread with G =
-// 1 and 8 (170 and 255 registers), 8 to 52 with 2 and 4.
+// layers' step 119.7 -> 110.7 us).  Spilled are 196 to 224 bytes a thread with G =
+// 1, 84 with 8, 8 to 52 with 2 and 4.
 #pragma once
 
 #include "decode_split.cuh"

@@ -108,7 +108,7 @@ struct Lay {
     static constexpr int kRun = !kLow ? 256 : kWide ? 12 : 8;
     // Registers per thread: what the launch holds, and, for wide tiles, what the warpgroups (copies, MMAs and order;
     // K's operands; V's; four of softmax) trade them for.  Local memory costs more here than elsewhere, since shared memory
-    // leaves it no L1: 56 to 72 bytes a thread are spilled with 128 rows, 8 to 12 with 64.  (The build checks the count.)
+    // leaves it no L1: 56 to 72 bytes a thread are spilled with 128 rows, 12 to 20 with 64.  (The build checks the count.)
     static constexpr int kLaunchRegs = 72, kRegsOther = 40, kRegsSoftmax = 96;
     static_assert(!kWide || kSoftmaxWarp0 / 4 * kRegsOther + kSoftmaxWarps / 4 * kRegsSoftmax <= kThreads / 128 * kLaunchRegs,
                   "registers");
