@@ -44,7 +44,7 @@
 // x 16, 64 clocks each: 2048 clocks.  The codes' conversion (8 warps) and the
 // softmax of 16384 scores (16 warps, about 15 instructions for two scores) make
 // them 3600 to 3700: the four schedulers issue in 64 % of all cycles, the tensor
-// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.81 ms, 606 TFLOP/s
+// cores run in 55 %.  512 tokens x 32 heads behind 130560: 1.80 ms, 610 TFLOP/s
 // of the operator's own arithmetic (each product counted once), with 4.7 GB of
 // DRAM traffic for 0.28 GB of cache (16 tiles of a kv head at different places of
 // it at a time; 36 % of DRAM's rate, which bounds nothing yet); 4096 tokens x 16
